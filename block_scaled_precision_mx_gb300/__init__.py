@@ -1,4 +1,5 @@
-"""GB300 (sm_103a) block-scaled quantization and GEMMs: MXFP8, MXFP4, NVFP4, DeepSeek FP8.
+"""GB300 (sm_103a) block-scaled quantization and GEMMs: MXFP8, MXFP4, NVFP4, DeepSeek FP8; and an
+8-bit key/value cache with block scales and the attention over it.
 
 Thin Python binding over the C ABI of ``libmxgb.so`` (declared in include/mx.h).
 Every function here only marshals arguments: tensors are torch CUDA tensors
@@ -10,7 +11,7 @@ Entry points (same names as the C ABI):
   mx_quantize, mx_quantize_dual, mx_gemm, nvfp4_quantize, nvfp4_gemm, fp8_blockwise_gemm,
   mx_gemm_grouped, mx_gemm_mxout, mx_scales_from_fp32_blocks, nvfp4_quantize_ex, nvfp4_quantize_2d,
   nvfp4_quantize_grouped, nvfp4_gemm_grouped, nvfp4_gemm_grouped_ex, fp8_blockwise_gemm_grouped, mx_scale_bytes,
-  nvfp4_workspace_bytes, mx_check.
+  nvfp4_workspace_bytes, mx_check, kv_block_tables, kv_cache_append, kv_attention.
 """
 from __future__ import annotations
 
@@ -28,6 +29,7 @@ E4M3, E5M2, E2M1 = 0, 1, 2
 SCALE_E8M0, SCALE_UE4M3, SCALE_FP32, SCALE_FP32_POW2 = 0, 1, 2, 3
 ROWWISE, COLWISE, BOTH = 1, 2, 3
 OUT_F32, OUT_BF16 = 0, 1
+HALF_BF16, HALF_F16 = 0, 1
 
 EXPORTS = (
     "mx_abi_version", "mx_status_string", "mx_quantize", "mx_gemm", "nvfp4_workspace_bytes",
@@ -35,7 +37,8 @@ EXPORTS = (
     "nvfp4_quantize_noalloc", "mx_quantize_dual", "mx_scales_from_fp32_blocks", "nvfp4_quantize_ex",
     "nvfp4_quantize_2d", "mx_gemm_grouped", "mx_gemm_mxout", "mx_unswizzle_scales", "mx_swizzle_scales",
     "mx_selftest_wait_timeout", "mx_gemm_mxout_ex", "nvfp4_gemm_grouped", "nvfp4_quantize_grouped",
-    "nvfp4_gemm_grouped_ex", "fp8_blockwise_gemm_grouped",
+    "nvfp4_gemm_grouped_ex", "fp8_blockwise_gemm_grouped", "kv_block_tables", "kv_cache_append",
+    "kv_attention_workspace_bytes", "kv_attention",
 )
 
 
@@ -94,6 +97,12 @@ def load():
             "fp8_blockwise_gemm_grouped": (i32, [vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, i32, i64, vp]),
             "mx_gemm_mxout_ex": (i32, [vp, vp, i32, vp, vp, i32, i64, i64, i64, i32, i32, vp, vp, i64, vp, vp, i64,
                                        vp]),
+            "kv_block_tables": (i32, [vp, i64, i64, vp, vp, vp, i64, vp, i32, i64, vp, vp, vp, vp, vp]),
+            "kv_cache_append": (i32, [vp, vp, i32, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, i32, i64, i64, i32, i32,
+                                      vp]),
+            "kv_attention_workspace_bytes": (ctypes.c_size_t, [i64, i64, i64, i64, i64, i32]),
+            "kv_attention": (i32, [vp, i32, i64, i64, i64, i64, vp, vp, vp, vp, i32, i64, i64, i32, i32, vp, i64, vp, vp,
+                                   i64, i64, ctypes.c_float, i32, i64, vp, vp, vp, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -469,6 +478,127 @@ def fp8_blockwise_gemm(qa, sa, qb, sb, M, N, K, out_dtype=OUT_BF16, out=None, st
                                    _stream(stream))
     _check(st, "fp8_blockwise_gemm")
     return out
+
+
+# ------------------------------------------------------------------ 8-bit key/value cache
+_HALF = {torch.bfloat16: HALF_BF16, torch.float16: HALF_F16}
+
+
+def _rows_of_heads(x, name):
+    """(address, type, token stride, head stride) of x[tokens][heads][head_dim], strided but for the last axis."""
+    if x.dim() != 3 or x.dtype not in _HALF:
+        raise ValueError(f"{name} must be a 3-D bf16 or fp16 tensor")
+    if not x.is_cuda or x.stride(2) != 1:
+        raise ValueError(f"{name} must be a CUDA tensor whose last axis is contiguous")
+    return x.data_ptr(), _HALF[x.dtype], x.stride(0), x.stride(1)
+
+
+def _cache_shape(k_codes, v_codes, k_scale, v_scale):
+    if k_codes.dim() != 4 or k_codes.dtype != torch.uint8 or v_codes.dtype != torch.uint8:
+        raise ValueError("codes must be uint8 [num_blocks][kv_heads][block_tokens][head_dim]")
+    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+        raise ValueError("scales must be float32 [num_blocks][kv_heads]")
+    shape = k_codes.shape
+    if v_codes.shape != shape or k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
+        raise ValueError("codes and scales of one cache must agree in shape")
+    return shape
+
+
+def _int32(**tensors):
+    for name, t in tensors.items():
+        if t.dtype != torch.int32:
+            raise ValueError(f"{name} must be int32")
+
+
+def kv_block_tables(block_tables: torch.Tensor, len_before: torch.Tensor, len_after: torch.Tensor,
+                    free_list: torch.Tensor, free_count: torch.Tensor, num_tokens: int, block_tokens: int,
+                    q_start=None, slot_map=None, positions=None, info=None, stream=None):
+    """Cache blocks for requests whose lengths go from len_before to len_after, and the new tokens'
+    places (include/mx.h, kv_block_tables).  block_tables int32 [requests][max_blocks] and free_list
+    int32 [capacity] are updated in place.  Returns (q_start int32 [requests + 1], slot_map int64
+    [num_tokens], positions int32 [num_tokens], info int32 {free blocks left, blocks missing})."""
+    _int32(block_tables=block_tables, len_before=len_before, len_after=len_after, free_list=free_list,
+           free_count=free_count)
+    if block_tables.dim() != 2 or len_before.shape != block_tables.shape[:1] or len_after.shape != len_before.shape:
+        raise ValueError("block_tables is [requests][max_blocks], the lengths are [requests]")
+    requests, max_blocks = block_tables.shape
+    dev = block_tables.device
+    if q_start is None:
+        q_start = torch.empty(requests + 1, dtype=torch.int32, device=dev)
+    if slot_map is None:
+        slot_map = torch.empty(num_tokens, dtype=torch.int64, device=dev)
+    if positions is None:
+        positions = torch.empty(num_tokens, dtype=torch.int32, device=dev)
+    if info is None:
+        info = torch.empty(2, dtype=torch.int32, device=dev)
+    _int32(q_start=q_start, positions=positions, info=info)
+    if (slot_map.dtype != torch.int64 or slot_map.numel() < num_tokens or positions.numel() < num_tokens
+            or q_start.numel() < requests + 1 or info.numel() < 2):
+        raise ValueError("q_start [requests + 1], slot_map (int64) and positions [num_tokens], info [2]")
+    st = load().kv_block_tables(_ptr(block_tables), requests, max_blocks, _ptr(len_before), _ptr(len_after),
+                                _ptr(free_list), free_list.numel(), _ptr(free_count), block_tokens, num_tokens,
+                                _ptr(q_start), _ptr(slot_map), _ptr(positions), _ptr(info), _stream(stream))
+    _check(st, "kv_block_tables")
+    return q_start, slot_map, positions, info
+
+
+def kv_cache_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_codes: torch.Tensor,
+                    v_codes: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor, elem: int = E4M3, stream=None):
+    """Quantize keys and values k, v [tokens][kv_heads][head_dim] (bf16 or fp16, slices will do) into
+    the cache at slot_map (int64), in place (include/mx.h, kv_cache_append)."""
+    k_at, half, k_st, k_sh = _rows_of_heads(k, "k")
+    v_at, v_half, v_st, v_sh = _rows_of_heads(v, "v")
+    blocks, kv_heads, block_tokens, head_dim = _cache_shape(k_codes, v_codes, k_scale, v_scale)
+    if v_half != half or v.shape != k.shape or k.shape[1:] != (kv_heads, head_dim):
+        raise ValueError("k and v must be alike, [tokens][kv_heads][head_dim] of the cache")
+    if slot_map.dtype != torch.int64 or slot_map.numel() != k.shape[0]:
+        raise ValueError("slot_map must be int64 [tokens]")
+    st = load().kv_cache_append(k_at, v_at, half, k.shape[0], k_st, k_sh, v_st, v_sh, _ptr(slot_map), _ptr(k_codes),
+                                _ptr(v_codes), _ptr(k_scale), _ptr(v_scale), elem, blocks, kv_heads, block_tokens,
+                                head_dim, _stream(stream))
+    _check(st, "kv_cache_append")
+
+
+def kv_attention_workspace_bytes(num_tokens: int, requests: int, max_q_len: int, heads: int, kv_heads: int,
+                                 head_dim: int) -> int:
+    return int(load().kv_attention_workspace_bytes(num_tokens, requests, max_q_len, heads, kv_heads, head_dim))
+
+
+def kv_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.Tensor,
+                 v_scale: torch.Tensor, block_tables: torch.Tensor, lengths: torch.Tensor, q_start: torch.Tensor,
+                 max_q_len: int, elem: int = E4M3, softmax_scale=None, causal: bool = True, window: int = 0, out=None,
+                 lse=None, workspace=None, stream=None):
+    """Attention of q [tokens][heads][head_dim] over the 8-bit cache (include/mx.h, kv_attention).
+    lengths int32 [requests]: cached tokens, the queries' own among them; q_start int32 [requests + 1];
+    softmax_scale defaults to head_dim ** -0.5.  Returns (out, like q but contiguous; lse float
+    [tokens][heads])."""
+    q_at, half, q_st, q_sh = _rows_of_heads(q, "q")
+    blocks, kv_heads, block_tokens, head_dim = _cache_shape(k_codes, v_codes, k_scale, v_scale)
+    _int32(block_tables=block_tables, lengths=lengths, q_start=q_start)
+    tokens, heads, d = q.shape
+    requests = lengths.numel()
+    if d != head_dim or block_tables.dim() != 2 or block_tables.shape[0] != requests or q_start.numel() != requests + 1:
+        raise ValueError("q [tokens][heads][head_dim], block_tables [requests][max_blocks], lengths [requests], "
+                         "q_start [requests + 1]")
+    lib = load()
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty((tokens, heads), dtype=torch.float32, device=q.device)
+    if out.shape != q.shape or out.dtype != q.dtype or lse.shape != q.shape[:2] or lse.dtype != torch.float32:
+        raise ValueError("out is shaped and typed like q, lse is float32 [tokens][heads]")
+    need = lib.kv_attention_workspace_bytes(tokens, requests, max_q_len, heads, kv_heads, head_dim)
+    if workspace is None:
+        workspace = _u8(max(16, need), q.device)
+    elif workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace must have {need} bytes")
+    st = lib.kv_attention(q_at, half, tokens, heads, q_st, q_sh, _ptr(k_codes), _ptr(v_codes), _ptr(k_scale),
+                          _ptr(v_scale), elem, blocks, kv_heads, block_tokens, head_dim, _ptr(block_tables),
+                          block_tables.shape[1], _ptr(lengths), _ptr(q_start), requests, max_q_len,
+                          head_dim ** -0.5 if softmax_scale is None else softmax_scale, int(bool(causal)), window,
+                          _ptr(out), _ptr(lse), _ptr(workspace), _stream(stream))
+    _check(st, "kv_attention")
+    return out, lse
 
 
 def mx_check(stream=None) -> int:

@@ -1,0 +1,202 @@
+// kv_api.cuh -- C ABI entry points of the 8-bit key/value cache (include/mx.h): host-side validation
+// and launches.  Included by mx_api.cu.
+#pragma once
+
+namespace {
+
+// 2^shift tokens a block, for 16, 32, 64 or 128; -1 otherwise
+int kv_block_shift(int block_tokens) {
+  return block_tokens == 16 ? 4 : block_tokens == 32 ? 5 : block_tokens == 64 ? 6 : block_tokens == 128 ? 7 : -1;
+}
+
+// shared checks of a cache's shape: code offsets within 63 bits, rows of codes within a tensor map's 31
+bool kv_cache_shape_ok(int64_t num_blocks, int64_t kv_heads, int block_tokens, int head_dim) {
+  if (num_blocks < 1 || kv_heads < 1 || kv_heads > 1024 || kv_block_shift(block_tokens) < 0) return false;
+  if (head_dim != 64 && head_dim != 128) return false;
+  return num_blocks <= 0x7FFFFFFFll / (kv_heads * block_tokens);
+}
+
+template <int FMT, bool F16, int D>
+cudaError_t kv_append_launch(const KvAppendArgs& a, bool wide, dim3 grid, cudaStream_t st) {
+  return wide ? pdl_launch(kv_append_kernel<FMT, F16, D, 4>, grid, kKvAppendThreads, 0, st, a)
+              : pdl_launch(kv_append_kernel<FMT, F16, D, 1>, grid, kKvAppendThreads, 0, st, a);
+}
+
+}  // namespace
+
+extern "C" {
+
+mx_status kv_block_tables(int32_t* block_tables, int64_t requests, int64_t max_blocks, const int32_t* len_before,
+                          const int32_t* len_after, int32_t* free_list, int64_t free_capacity,
+                          const int32_t* free_count, int block_tokens, int64_t num_tokens, int32_t* q_start,
+                          int64_t* slot_map, int32_t* positions, int32_t* info, void* stream) {
+  const int shift = kv_block_shift(block_tokens);
+  if (!block_tables || !len_before || !len_after || !free_list || !free_count || !q_start || !info || shift < 0)
+    return MX_ERR_INVALID_ARG;
+  if (num_tokens < 0 || num_tokens > 0x7FFFFFFF - 1024 || (num_tokens && (!slot_map || !positions)))
+    return MX_ERR_INVALID_ARG;
+  if (requests < 1 || requests > kKvMaxRequests || max_blocks < 1 || max_blocks > (0x7FFFFFFFll >> shift) - 1 ||
+      free_capacity < 1 || free_capacity > 0x7FFFFFFF)
+    return MX_ERR_INVALID_ARG;
+  if (!aligned(block_tables, 4) || !aligned(len_before, 4) || !aligned(len_after, 4) || !aligned(free_list, 4) ||
+      !aligned(free_count, 4) || !aligned(q_start, 4) || !aligned(slot_map, 8) || !aligned(positions, 4) ||
+      !aligned(info, 4))
+    return MX_ERR_INVALID_ARG;
+  static std::atomic<bool> attr_set[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MX_ERR_CUDA;
+  if (!attr_set[dev].load(std::memory_order_relaxed)) {
+    if (cudaFuncSetAttribute(kv_block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             3 * 4 * (kKvMaxRequests + 1)) != cudaSuccess)
+      return MX_ERR_CUDA;
+    attr_set[dev].store(true, std::memory_order_relaxed);
+  }
+  KvTablesArgs a{};
+  a.tables = block_tables;
+  a.before = len_before;
+  a.after = len_after;
+  a.free_list = free_list;
+  a.free_count = free_count;
+  a.q_start = q_start;
+  a.slots = slot_map;
+  a.positions = positions;
+  a.info = info;
+  a.requests = static_cast<int>(requests);
+  a.max_blocks = static_cast<int>(max_blocks);
+  a.capacity = static_cast<int>(free_capacity);
+  a.num_tokens = static_cast<int>(num_tokens);
+  a.shift = shift;
+  const int64_t want = (num_tokens + kKvTablesThreads - 1) / kKvTablesThreads;
+  const unsigned grid = static_cast<unsigned>(want < 1 ? 1 : want > 128 ? 128 : want);
+  if (pdl_launch(kv_block_tables_kernel, grid, kKvTablesThreads, 3 * 4 * (static_cast<size_t>(requests) + 1),
+                 as_stream(stream), a) != cudaSuccess)
+    return MX_ERR_CUDA;
+  return launch_status();
+}
+
+mx_status kv_cache_append(const void* k, const void* v, mx_half type, int64_t num_tokens, int64_t k_stride_token,
+                          int64_t k_stride_head, int64_t v_stride_token, int64_t v_stride_head,
+                          const int64_t* slot_map, void* k_codes, void* v_codes, float* k_scale, float* v_scale,
+                          mx_elem elem, int64_t num_blocks, int64_t kv_heads, int block_tokens, int head_dim,
+                          void* stream) {
+  if (num_tokens < 0 || num_tokens > 0x7FFFFFFF - 1024) return MX_ERR_INVALID_ARG;
+  if (!k_codes || !v_codes || !k_scale || !v_scale || (num_tokens && (!k || !v || !slot_map))) return MX_ERR_INVALID_ARG;
+  if (type != MX_HALF_BF16 && type != MX_HALF_F16) return MX_ERR_INVALID_ARG;
+  if (elem != MX_E4M3 && elem != MX_E5M2) return elem == MX_E2M1 ? MX_ERR_UNSUPPORTED : MX_ERR_INVALID_ARG;
+  if (!kv_cache_shape_ok(num_blocks, kv_heads, block_tokens, head_dim)) return MX_ERR_INVALID_ARG;
+  if (k_stride_token % 8 || k_stride_head % 8 || v_stride_token % 8 || v_stride_head % 8) return MX_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 8) || !aligned(k_codes, 16) || !aligned(v_codes, 16) ||
+      !aligned(k_scale, 4) || !aligned(v_scale, 4))
+    return MX_ERR_INVALID_ARG;
+  if (num_tokens == 0) return MX_OK;
+  KvAppendArgs a{};
+  a.x[0] = static_cast<const uint16_t*>(k);
+  a.x[1] = static_cast<const uint16_t*>(v);
+  a.stride_t[0] = k_stride_token;
+  a.stride_t[1] = v_stride_token;
+  a.stride_h[0] = k_stride_head;
+  a.stride_h[1] = v_stride_head;
+  a.codes[0] = static_cast<uint8_t*>(k_codes);
+  a.codes[1] = static_cast<uint8_t*>(v_codes);
+  a.scale[0] = k_scale;
+  a.scale[1] = v_scale;
+  a.slots = slot_map;
+  a.num_slots = num_blocks * block_tokens;
+  a.tokens = static_cast<int>(num_tokens);
+  a.kv_heads = static_cast<int>(kv_heads);
+  a.shift = kv_block_shift(block_tokens);
+  // A block's values of one head fit one warp's registers up to 4096 of them, else four warps'.
+  const bool wide = block_tokens * head_dim > 4096;
+  const int groups = wide ? 2 : 8;
+  const int64_t gy = (2 * kv_heads + groups - 1) / groups;
+  // Tokens looked over by a CTA: a power of two that leaves about 2048 CTAs, at most a block's tokens.
+  int chunk = 1;
+  while (chunk < block_tokens && num_tokens * gy > 2048ll * chunk) chunk *= 2;
+  a.chunk = chunk;
+  const dim3 grid(static_cast<unsigned>((num_tokens + chunk - 1) / chunk), static_cast<unsigned>(gy));
+  cudaStream_t st = as_stream(stream);
+  const bool f16 = type == MX_HALF_F16, d64 = head_dim == 64;
+  cudaError_t e;
+  if (elem == MX_E4M3)
+    e = f16 ? (d64 ? kv_append_launch<0, true, 64>(a, wide, grid, st) : kv_append_launch<0, true, 128>(a, wide, grid, st))
+            : (d64 ? kv_append_launch<0, false, 64>(a, wide, grid, st) : kv_append_launch<0, false, 128>(a, wide, grid, st));
+  else
+    e = f16 ? (d64 ? kv_append_launch<1, true, 64>(a, wide, grid, st) : kv_append_launch<1, true, 128>(a, wide, grid, st))
+            : (d64 ? kv_append_launch<1, false, 64>(a, wide, grid, st) : kv_append_launch<1, false, 128>(a, wide, grid, st));
+  if (e != cudaSuccess) return MX_ERR_CUDA;
+  return launch_status();
+}
+
+size_t kv_attention_workspace_bytes(int64_t num_tokens, int64_t requests, int64_t max_q_len, int64_t heads,
+                                    int64_t kv_heads, int head_dim) {
+  (void)num_tokens;
+  (void)requests;
+  (void)max_q_len;
+  (void)heads;
+  (void)kv_heads;
+  (void)head_dim;
+  return 16;
+}
+
+mx_status kv_attention(const void* q, mx_half type, int64_t num_tokens, int64_t heads, int64_t q_stride_token,
+                       int64_t q_stride_head, const void* k_codes, const void* v_codes, const float* k_scale,
+                       const float* v_scale, mx_elem elem, int64_t num_blocks, int64_t kv_heads, int block_tokens,
+                       int head_dim, const int32_t* block_tables, int64_t max_blocks, const int32_t* lengths,
+                       const int32_t* q_start, int64_t requests, int64_t max_q_len, float softmax_scale, int causal,
+                       int64_t window, void* out, float* lse, void* workspace, void* stream) {
+  if (num_tokens < 0 || num_tokens > 0x7FFFFFFF - 1024 || requests < 1 || requests > kKvMaxRequests)
+    return MX_ERR_INVALID_ARG;
+  if (!k_codes || !v_codes || !k_scale || !v_scale || !block_tables || !lengths || !q_start || !workspace ||
+      (num_tokens && (!q || !out || !lse)))
+    return MX_ERR_INVALID_ARG;
+  if (type != MX_HALF_BF16 && type != MX_HALF_F16) return MX_ERR_INVALID_ARG;
+  if (elem != MX_E4M3 && elem != MX_E5M2) return elem == MX_E2M1 ? MX_ERR_UNSUPPORTED : MX_ERR_INVALID_ARG;
+  if (!kv_cache_shape_ok(num_blocks, kv_heads, block_tokens, head_dim)) return MX_ERR_INVALID_ARG;
+  if (heads < 1 || heads > 65535 || heads % kv_heads) return MX_ERR_INVALID_ARG;
+  if (max_blocks < 1 || max_blocks > 0x7FFFFFFFll / block_tokens - 1) return MX_ERR_INVALID_ARG;
+  if (max_q_len < 0 || max_q_len > num_tokens || window < 0 || window > 0x7FFFFFFF) return MX_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return MX_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.f) || softmax_scale > 1e30f) return MX_ERR_INVALID_ARG;
+  if (q_stride_token % 8 || q_stride_head % 8) return MX_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_scale, 4) ||
+      !aligned(v_scale, 4) || !aligned(block_tables, 4) || !aligned(lengths, 4) || !aligned(q_start, 4) ||
+      !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16))
+    return MX_ERR_INVALID_ARG;
+  if (num_tokens == 0) return MX_OK;
+  KvAttnArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.stride_t = q_stride_token;
+  a.stride_h = q_stride_head;
+  a.k_codes = static_cast<const uint8_t*>(k_codes);
+  a.v_codes = static_cast<const uint8_t*>(v_codes);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.tables = block_tables;
+  a.lengths = lengths;
+  a.q_start = q_start;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
+  a.num_blocks = num_blocks;
+  a.tokens = static_cast<int>(num_tokens);
+  a.heads = static_cast<int>(heads);
+  a.kv_heads = static_cast<int>(kv_heads);
+  a.requests = static_cast<int>(requests);
+  a.max_blocks = static_cast<int>(max_blocks);
+  a.shift = kv_block_shift(block_tokens);
+  a.causal = causal;
+  a.window = static_cast<int>(window);
+  const dim3 grid(static_cast<unsigned>(num_tokens), static_cast<unsigned>(heads));
+  cudaStream_t st = as_stream(stream);
+  const bool f16 = type == MX_HALF_F16, d64 = head_dim == 64, e5 = elem == MX_E5M2;
+#define KV_ROWS(FMT, H, D) pdl_launch(kv_attention_rows_kernel<FMT, H, D>, grid, 128, 0, st, a)
+  const cudaError_t e = e5 ? (f16 ? (d64 ? KV_ROWS(1, true, 64) : KV_ROWS(1, true, 128))
+                                  : (d64 ? KV_ROWS(1, false, 64) : KV_ROWS(1, false, 128)))
+                           : (f16 ? (d64 ? KV_ROWS(0, true, 64) : KV_ROWS(0, true, 128))
+                                  : (d64 ? KV_ROWS(0, false, 64) : KV_ROWS(0, false, 128)));
+#undef KV_ROWS
+  if (e != cudaSuccess) return MX_ERR_CUDA;
+  return launch_status();
+}
+
+}  // extern "C"

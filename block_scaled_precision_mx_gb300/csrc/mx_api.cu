@@ -15,6 +15,8 @@
 #include "mx_gemm.cuh"
 #include "mx_gemm2.cuh"
 #include "mx_quantize.cuh"
+#include "kv_attention.cuh"
+#include "kv_cache.cuh"
 
 using namespace mxgb;
 
@@ -873,7 +875,7 @@ mx_status mx_check(void* stream) {
   if (word) {
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(g_mx_error_word, &zero, sizeof(zero)) != cudaSuccess) return MX_ERR_CUDA;
-    return (word & ~static_cast<unsigned int>(kSiteBadGroups)) ? MX_ERR_TIMEOUT : MX_ERR_INVALID_ARG;
+    return (word & ~static_cast<unsigned int>(kSiteBadGroups | kSiteBadCache)) ? MX_ERR_TIMEOUT : MX_ERR_INVALID_ARG;
   }
   return MX_OK;
 }
@@ -982,3 +984,5 @@ extern "C" mx_status nvfp4_quantize_noalloc(const void* x, int64_t rows, int64_t
              static_cast<const int64_t*>(nullptr), 1);
   return launch_status();
 }
+
+#include "kv_api.cuh"

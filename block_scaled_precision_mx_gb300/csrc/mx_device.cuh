@@ -30,6 +30,7 @@ enum WaitSite : unsigned int {
   kSiteBadGroups = 1u << 5,  // not a wait: grouped GEMM offsets that break their contract
   kSiteSelfTest = 1u << 6,   // the bounded-wait self-test (mx_selftest_wait_timeout)
   kSiteQuantLoad = 1u << 7,  // a quantizer's wait for its staged input tile
+  kSiteBadCache = 1u << 8,   // not a wait: lengths, blocks or slots of a key/value cache out of range
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

@@ -70,6 +70,7 @@ typedef enum { MX_E4M3 = 0, MX_E5M2 = 1, MX_E2M1 = 2 } mx_elem;
 typedef enum { MX_SCALE_E8M0 = 0, MX_SCALE_UE4M3 = 1, MX_SCALE_FP32 = 2, MX_SCALE_FP32_POW2 = 3 } mx_scale_fmt;
 typedef enum { MX_ROWWISE = 1, MX_COLWISE = 2, MX_BOTH = 3 } mx_layout;
 typedef enum { MX_OUT_F32 = 0, MX_OUT_BF16 = 1 } mx_out;
+typedef enum { MX_HALF_BF16 = 0, MX_HALF_F16 = 1 } mx_half;
 
 /* Version of this ABI (bumped on any signature or layout change). */
 int mx_abi_version(void);
@@ -397,10 +398,93 @@ mx_status nvfp4_quantize_noalloc(const void* x, int64_t rows, int64_t cols,
 size_t mx_scale_bytes(int64_t rows, int64_t cols, int block, int block_rows, mx_scale_fmt sfmt);
 
 /*
+ * 8-bit key/value cache.
+ *
+ * A cache keeps the keys and values of many requests in blocks of P = block_tokens tokens
+ * (16, 32, 64 or 128), as 8-bit codes with one FP32 scale for each block and kv head:
+ *   k_codes, v_codes  u8 [num_blocks][kv_heads][P][head_dim], E4M3 or E5M2, 16-byte aligned;
+ *   k_scale, v_scale  float [num_blocks][kv_heads]; a token's value is code * scale.
+ * head_dim is 64 or 128, kv_heads at most 1024, and num_blocks * kv_heads * P at most 2^31 - 1.
+ * A request's tokens are in the blocks that its row of block_tables[requests][max_blocks] (int32)
+ * names, P by P; entries past its length are not read.  requests is at most 16384.  Lengths, block
+ * numbers and slots are on the device and the host cannot see them: where they break their
+ * contract nothing is read or written out of range, and mx_check returns MX_ERR_INVALID_ARG.
+ */
+
+/*
+ * kv_block_tables -- gives requests their cache blocks and new tokens their places.
+ *
+ * len_before[r] tokens are held by the first ceil(len_before / P) entries of request r's table row;
+ * len_after[r] are to be held.  A request that shrinks (rewound, or finished with len_after = 0)
+ * puts entries ceil(len_after / P) .. on the free stack, in order; then requests that grow take
+ * blocks off its top, in request order.  free_list[free_capacity] holds the stack, free_count[1] its
+ * height.  Tables and free_list are updated in place (entries that a request gave back stay in its
+ * row, unread); free_count is only read: info[0] is the new height.
+ * The new tokens are those of requests that grow: q_start[requests + 1] their numbering, and for
+ * each, positions[num_tokens] its place in the request and slot_map[num_tokens] (int64) its slot
+ * block * P + position % P.  num_tokens may exceed their number: the rest is -1.
+ * If the stack has too few blocks nothing is moved, info[1] is how many are missing (0 otherwise),
+ * info[0] is free_count, and all slots and positions are -1.
+ * Contract: 0 <= lengths <= max_blocks * P; the stack stays within its capacity; new tokens at most
+ * num_tokens; no block is held twice.  Where it is broken nothing is moved and q_start is 0.
+ * One launch; the same inputs give the same outputs, and the same call again changes nothing.
+ */
+mx_status kv_block_tables(int32_t* block_tables, int64_t requests, int64_t max_blocks, const int32_t* len_before,
+                          const int32_t* len_after, int32_t* free_list, int64_t free_capacity,
+                          const int32_t* free_count, int block_tokens, int64_t num_tokens, int32_t* q_start,
+                          int64_t* slot_map, int32_t* positions, int32_t* info, void* stream);
+
+/*
+ * kv_cache_append -- writes new keys and values into the cache, quantizing them.
+ *
+ * k, v: num_tokens tokens of kv_heads heads of head_dim elements, bf16 or fp16, 16-byte aligned,
+ * elements contiguous, token and head strides (in elements) multiples of 8: slices of a fused
+ * projection will do.  Token t goes to slot_map[t] = block * P + offset; -1 leaves it out.
+ * Tokens that follow each other in one block are a run; a block has at most one run in a call.
+ * Scales are powers of two: 2^k, k the smallest in [-48, 48] with MAX * 2^k >= amax over the finite
+ * values (MAX 448 or 57344; 1 if amax = 0), q = RNE-satfinite(x / scale), NaN -> 0x7F.  A run that
+ * starts at offset 0 sets its block's scale from its own values.  One that starts later keeps the
+ * block's scale or, where its values need a larger one, raises it, and the codes at the offsets in
+ * front of it are rounded again to the new scale.
+ */
+mx_status kv_cache_append(const void* k, const void* v, mx_half type, int64_t num_tokens, int64_t k_stride_token,
+                          int64_t k_stride_head, int64_t v_stride_token, int64_t v_stride_head,
+                          const int64_t* slot_map, void* k_codes, void* v_codes, float* k_scale, float* v_scale,
+                          mx_elem elem, int64_t num_blocks, int64_t kv_heads, int block_tokens, int head_dim,
+                          void* stream);
+
+/* Bytes of workspace kv_attention needs for these sizes (0 if they are not supported). */
+size_t kv_attention_workspace_bytes(int64_t num_tokens, int64_t requests, int64_t max_q_len, int64_t heads,
+                                    int64_t kv_heads, int head_dim);
+
+/*
+ * kv_attention -- attention of new queries over the cache.
+ *
+ * q: num_tokens rows of heads x head_dim, bf16 or fp16, 16-byte aligned, strides as in
+ * kv_cache_append; rows q_start[r] .. q_start[r + 1] are request r's, the last of its lengths[r]
+ * cached tokens (so append first).  heads is a multiple of kv_heads; query heads g * heads / kv_heads
+ * and up share kv head g.  Row i of n stands at position p = lengths[r] - n + i and sees the tokens
+ * j < lengths[r] with j <= p if causal and j > p - window if window > 0.  No request has more than
+ * max_q_len rows.
+ *   out[num_tokens][heads][head_dim] (q's type) = softmax(softmax_scale * q k_j) v_j,
+ *   lse[num_tokens][heads] (float) = log sum_j exp(softmax_scale * q k_j).
+ * Rows that see no token, and rows from q_start[requests] on, give 0 and -inf.  NaN in tokens that a
+ * row does not see does not reach it.  workspace: kv_attention_workspace_bytes bytes, 16-byte
+ * aligned, contents free; calls that may overlap need one each.
+ * Sums and softmax statistics are FP32; the weights are rounded to FP16 for the second product.
+ */
+mx_status kv_attention(const void* q, mx_half type, int64_t num_tokens, int64_t heads, int64_t q_stride_token,
+                       int64_t q_stride_head, const void* k_codes, const void* v_codes, const float* k_scale,
+                       const float* v_scale, mx_elem elem, int64_t num_blocks, int64_t kv_heads, int block_tokens,
+                       int head_dim, const int32_t* block_tables, int64_t max_blocks, const int32_t* lengths,
+                       const int32_t* q_start, int64_t requests, int64_t max_q_len, float softmax_scale, int causal,
+                       int64_t window, void* out, float* lse, void* workspace, void* stream);
+
+/*
  * mx_check -- synchronizes `stream`, then reads and clears the library's device error word.
  * Returns MX_ERR_TIMEOUT if a kernel's bounded wait ran out since the last check,
- * MX_ERR_INVALID_ARG if the only event was a grouped GEMM whose device offsets broke their
- * contract, MX_ERR_CUDA on a pending CUDA error, MX_OK otherwise.  This is the only call that
+ * MX_ERR_INVALID_ARG if the only events were device inputs that broke their contract (a grouped
+ * GEMM's offsets, a key/value cache's lengths, blocks or slots), MX_ERR_CUDA on a pending CUDA error, MX_OK otherwise.  This is the only call that
  * synchronizes.
  */
 mx_status mx_check(void* stream);

@@ -16,6 +16,66 @@ bool kv_cache_shape_ok(int64_t num_blocks, int64_t kv_heads, int block_tokens, i
   return num_blocks <= 0x7FFFFFFFll / (kv_heads * block_tokens);
 }
 
+// 8-row tiles of the kernel for few rows: 1, 2 or 4; 0 where a kv head has more than 32 rows
+int kv_row_tiles(int64_t max_q_len, int64_t group) {
+  if (max_q_len > 32 || group > 32) return max_q_len ? 0 : 1;
+  const int64_t rows = max_q_len * group;
+  return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 0;
+}
+
+// codes as rows of head_dim bytes; a box is up to 64 tokens of one block and head
+bool kv_codes_tmap(CUtensorMap* map, const void* codes, int64_t num_blocks, int64_t kv_heads, int block_tokens,
+                   int head_dim) {
+  return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, static_cast<uint64_t>(head_dim),
+                   static_cast<uint64_t>(num_blocks * kv_heads * block_tokens), static_cast<uint64_t>(head_dim),
+                   static_cast<uint32_t>(head_dim), static_cast<uint32_t>(block_tokens < kKvTile ? block_tokens : kKvTile),
+                   head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+template <int FMT, bool F16, int D, int NT>
+mx_status kv_few_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_len, void* workspace, cudaStream_t st) {
+  using Cfg = KvFewCfg<D, NT>;
+  auto kern = kv_attention_few_kernel<FMT, F16, D, NT>;
+  static std::atomic<int> ctas[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MX_ERR_CUDA;
+  int n = ctas[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM) != cudaSuccess)
+      return MX_ERR_CUDA;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kKvFewThreads, Cfg::SMEM) != cudaSuccess || n <= 0)
+      return MX_ERR_CUDA;
+    const int sms = device_sms();
+    if (sms <= 0) return MX_ERR_CUDA;
+    n = n * sms < kKvMaxCtas ? n * sms : kKvMaxCtas;
+    ctas[dev].store(n, std::memory_order_relaxed);
+  }
+  CUtensorMap tk, tv;
+  if (!kv_codes_tmap(&tk, a.k_codes, a.num_blocks, a.kv_heads, block_tokens, D) ||
+      !kv_codes_tmap(&tv, a.v_codes, a.num_blocks, a.kv_heads, block_tokens, D))
+    return MX_ERR_CUDA;
+  const int most_q = static_cast<int>(max_q_len);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (pdl_launch(kern, n, kKvFewThreads, Cfg::SMEM, st, tk, tv, a, most_q, ws) != cudaSuccess) return MX_ERR_CUDA;
+  if (n > 1 && pdl_launch(kv_join_kernel<F16, D, NT>, n - 1, 128, 0, st, a, most_q,
+                          static_cast<const uint8_t*>(ws)) != cudaSuccess)
+    return MX_ERR_CUDA;
+  return launch_status();
+}
+
+template <int FMT, bool F16, int D>
+mx_status kv_attention_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_len, void* workspace, cudaStream_t st) {
+  switch (kv_row_tiles(max_q_len, a.heads / a.kv_heads)) {
+    case 1: return kv_few_launch<FMT, F16, D, 1>(a, block_tokens, max_q_len, workspace, st);
+    case 2: return kv_few_launch<FMT, F16, D, 2>(a, block_tokens, max_q_len, workspace, st);
+    case 4: return kv_few_launch<FMT, F16, D, 4>(a, block_tokens, max_q_len, workspace, st);
+  }
+  const dim3 grid(static_cast<unsigned>(a.tokens), static_cast<unsigned>(a.heads));
+  if (pdl_launch(kv_attention_rows_kernel<FMT, F16, D>, grid, 128, 0, st, a) != cudaSuccess) return MX_ERR_CUDA;
+  return launch_status();
+}
+
 template <int FMT, bool F16, int D>
 cudaError_t kv_append_launch(const KvAppendArgs& a, bool wide, dim3 grid, cudaStream_t st) {
   return wide ? pdl_launch(kv_append_kernel<FMT, F16, D, 4>, grid, kKvAppendThreads, 0, st, a)
@@ -129,13 +189,11 @@ mx_status kv_cache_append(const void* k, const void* v, mx_half type, int64_t nu
 
 size_t kv_attention_workspace_bytes(int64_t num_tokens, int64_t requests, int64_t max_q_len, int64_t heads,
                                     int64_t kv_heads, int head_dim) {
-  (void)num_tokens;
-  (void)requests;
-  (void)max_q_len;
-  (void)heads;
-  (void)kv_heads;
-  (void)head_dim;
-  return 16;
+  if (num_tokens < 0 || requests < 1 || max_q_len < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads) return 0;
+  if (head_dim != 64 && head_dim != 128) return 0;
+  const int nt = kv_row_tiles(max_q_len, heads / kv_heads);
+  if (!nt) return 16;
+  return sizeof(KvJob) * kKvMaxCtas + 16 + 2ull * kKvMaxCtas * (8 * nt) * (head_dim + 2) * 4;
 }
 
 mx_status kv_attention(const void* q, mx_half type, int64_t num_tokens, int64_t heads, int64_t q_stride_token,
@@ -186,17 +244,14 @@ mx_status kv_attention(const void* q, mx_half type, int64_t num_tokens, int64_t 
   a.shift = kv_block_shift(block_tokens);
   a.causal = causal;
   a.window = static_cast<int>(window);
-  const dim3 grid(static_cast<unsigned>(num_tokens), static_cast<unsigned>(heads));
   cudaStream_t st = as_stream(stream);
   const bool f16 = type == MX_HALF_F16, d64 = head_dim == 64, e5 = elem == MX_E5M2;
-#define KV_ROWS(FMT, H, D) pdl_launch(kv_attention_rows_kernel<FMT, H, D>, grid, 128, 0, st, a)
-  const cudaError_t e = e5 ? (f16 ? (d64 ? KV_ROWS(1, true, 64) : KV_ROWS(1, true, 128))
-                                  : (d64 ? KV_ROWS(1, false, 64) : KV_ROWS(1, false, 128)))
-                           : (f16 ? (d64 ? KV_ROWS(0, true, 64) : KV_ROWS(0, true, 128))
-                                  : (d64 ? KV_ROWS(0, false, 64) : KV_ROWS(0, false, 128)));
-#undef KV_ROWS
-  if (e != cudaSuccess) return MX_ERR_CUDA;
-  return launch_status();
+#define KV_ATTN(FMT, H, D) kv_attention_launch<FMT, H, D>(a, block_tokens, max_q_len, workspace, st)
+  return e5 ? (f16 ? (d64 ? KV_ATTN(1, true, 64) : KV_ATTN(1, true, 128))
+                   : (d64 ? KV_ATTN(1, false, 64) : KV_ATTN(1, false, 128)))
+            : (f16 ? (d64 ? KV_ATTN(0, true, 64) : KV_ATTN(0, true, 128))
+                   : (d64 ? KV_ATTN(0, false, 64) : KV_ATTN(0, false, 128)));
+#undef KV_ATTN
 }
 
 }  // extern "C"

@@ -109,4 +109,648 @@ __global__ void __launch_bounds__(128) kv_attention_rows_kernel(const KvAttnArgs
   if (tid == 0) a.lse[static_cast<int64_t>(t) * a.heads + head] = end > begin ? m * kLn2 + logf(l) : -INFINITY;
 }
 
+// ================================================================== few rows for each kv head
+// Queries of one request that share a kv head (query heads of the group x query tokens, at most 32 rows)
+// meet the same keys, and the cache is read once for all of them: the call is bound by the cache's
+// bytes.  What the kernel does about it:
+//
+//  * The work is the list of (request, kv head) units, each a row of 64-token tiles; all tiles of all
+//    units, in order, are cut into gridDim.x equal ranges, one for each resident CTA, whatever the
+//    lengths are.  A CTA's range is a few segments of units; a unit that one CTA has whole is finished
+//    there, else each segment leaves (O, m, l) in the workspace and kv_join_kernel joins them in order.
+//  * One warp keeps a ring of tiles in flight: TMA boxes of a block's rows of codes (128 or 64 bytes,
+//    swizzled), so a tile's codes cross the SM once, and the scales of its four 16-token slices.
+//  * Four warps take one 16-token slice of the tile each, all rows, with running (m, l, O) of their own
+//    and no barrier between them until the segment's end.  Codes become FP16 in registers, exactly.
+//      S^T (16 tokens x 8 rows) = K Q^T and O^T (16 of D x 8 rows) += V^T P^T on m16n8k16 products:
+//    the small side of both is the rows, so 8 rows cost one product's n = 8 where a 128-row tensor-memory
+//    tile would be 1/16 full; the products are 1/3 of the time the codes take to arrive.
+//    The order of d inside K Q^T, and of d among the rows of V^T, is free: each lane takes 16-byte words.
+//  * Queries become FP16 with a power of two for each row, exact to 2^-29 of the row's largest.
+//  * Softmax in base 2.  sV is folded into the exponent: p' = 2^(z + log2 sV - m), l = sum p' / sV, so
+//    the weights of all blocks are rounded to FP16 relative to the same reference m.  m is renewed when a
+//    score passes it by 8 (p' <= 2^8 stays well inside FP16), not at each new maximum.
+//  * Tiles that some row does not see whole are masked; codes there that no row sees are cleared, and
+//    NaN codes of V (0 * NaN) are taken out and put into the rows that see them.
+constexpr int kKvTile = 64;
+constexpr int kKvWarps = 4;
+constexpr int kKvFewThreads = 32 * (kKvWarps + 1);
+constexpr int kKvMaxCtas = 608;
+
+struct KvJob {  // where a range begins: the unit and its place in the list of tiles
+  long long start, end;
+  int request, head;
+};
+
+template <int D, int NT>
+struct KvFewCfg {
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int STAGES = 3;
+  static constexpr int HALF = kKvTile * D;          // codes of K, or of V, in a tile
+  static constexpr int O_STRIDE = D + 4;
+  static constexpr int OFF_O = STAGES * 2 * HALF;   // float [warps][ROWS][O_STRIDE]
+  static constexpr int OFF_ML = OFF_O + 4 * kKvWarps * ROWS * O_STRIDE;  // float2 [warps][ROWS]
+  static constexpr int OFF_Q = OFF_ML + 8 * kKvWarps * ROWS;            // uint2 [D / 16][NT][32]
+  static constexpr int OFF_QF = OFF_Q + (D / 16) * NT * 32 * 8;         // float [ROWS]
+  static constexpr int OFF_SEEN = OFF_QF + 4 * ROWS;                    // int2 [ROWS]
+  static constexpr int OFF_NAN = OFF_SEEN + 8 * ROWS;                   // u32 [ROWS][D / 32], bits of d
+  static constexpr int OFF_SC = OFF_NAN + 4 * ROWS * (D / 32);          // float4 [STAGES][4]
+  static constexpr int OFF_BAR = OFF_SC + 16 * 4 * STAGES;
+  static constexpr int SMEM = OFF_BAR + 8 * 2 * STAGES + 16 + 1024;
+  static constexpr int CTAS = NT == 1 ? 3 : 2;
+  static constexpr size_t SLOT = static_cast<size_t>(ROWS) * (D + 2) * 4;  // (O, m, l) of a segment
+};
+
+__device__ __forceinline__ void kv_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t kv_transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ float kv_exp2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t kv_pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// 0x80 in each byte that is a NaN code (E5M2: or an infinity)
+template <int FMT>
+__device__ __forceinline__ uint32_t kv_nan_bytes(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + (FMT == 0 ? 0x01010101u : 0x04040404u)) & 0x80808080u;
+}
+
+// A request as the kernels go through it.
+struct KvRequest {
+  int q0, rows_q, len, first_tile, tiles;  // tiles = 0: no queries
+};
+
+__device__ __forceinline__ KvRequest kv_request(const KvAttnArgs& a, int r, int most_q, bool tell) {
+  KvRequest v;
+  v.q0 = a.q_start[r];
+  v.rows_q = a.q_start[r + 1] - v.q0;
+  v.len = a.lengths[r];
+  const int most = a.max_blocks << a.shift;
+  if (v.rows_q < 0 || v.rows_q > most_q || v.len < 0 || v.len > most || v.q0 < 0 || v.q0 + max(v.rows_q, 0) > a.tokens) {
+    if (tell) atomicOr(&g_mx_error_word, kSiteBadCache);
+    v.rows_q = 0;
+    v.len = 0;
+  }
+  const int lo = a.window ? max(0, v.len - v.rows_q - a.window + 1) : 0;
+  v.first_tile = lo / kKvTile;
+  v.tiles = v.rows_q ? max(1, (v.len + kKvTile - 1) / kKvTile - v.first_tile) : 0;
+  return v;
+}
+
+// The place of a tile in the list of all tiles, and the walk over a range's segments.
+struct KvWalk {
+  long long pos, end, base;  // base: the place of the current unit's first tile
+  int r, h;
+  KvRequest req;
+};
+
+// Finds where this CTA's range begins and ends: every thread sums a stretch of the requests, the sums are
+// scanned, and the thread that holds the range's first tile finds its unit.  `slots` is shared memory.
+struct KvPlanSmem {
+  long long warp_sum[kKvWarps + 1];
+  long long pos, end, base, total;
+  int r, h;
+};
+__device__ __forceinline__ void kv_plan(const KvAttnArgs& a, int most_q, KvPlanSmem& sm, KvWalk& w) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.requests + kKvFewThreads - 1) / kKvFewThreads;
+  const int r0 = min(tid * per, a.requests), r1 = min(r0 + per, a.requests);
+  long long mine = 0;
+  for (int r = r0; r < r1; ++r) mine += kv_request(a, r, most_q, blockIdx.x == 0).tiles;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) sm.warp_sum[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+#pragma unroll
+  for (int i = 0; i <= kKvWarps; ++i) {
+    if (i < warp) before += sm.warp_sum[i];
+    total += sm.warp_sum[i];
+  }
+  total *= a.kv_heads;
+  before *= a.kv_heads;
+  mine *= a.kv_heads;
+  const long long pos = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
+  if (pos >= before && pos < before + mine) {
+    long long at = before;
+    for (int r = r0; r < r1; ++r) {
+      const int tiles = kv_request(a, r, most_q, false).tiles;
+      const long long all = static_cast<long long>(tiles) * a.kv_heads;
+      if (pos < at + all) {
+        sm.r = r;
+        sm.h = static_cast<int>((pos - at) / tiles);
+        sm.base = at + static_cast<long long>(sm.h) * tiles;
+        break;
+      }
+      at += all;
+    }
+  }
+  if (tid == 0) {
+    sm.pos = pos;
+    sm.end = end;
+    sm.total = total;
+  }
+  __syncthreads();
+  w.pos = sm.pos;
+  w.end = sm.end;
+  w.base = sm.base;
+  w.r = sm.r;
+  w.h = sm.h;
+  if (w.pos < sm.total) w.req = kv_request(a, w.r, most_q, false);
+}
+__device__ __forceinline__ void kv_next_unit(const KvAttnArgs& a, int most_q, KvWalk& w) {
+  w.base += w.req.tiles;
+  if (++w.h == a.kv_heads) {
+    w.h = 0;
+    while (w.pos < w.end && ++w.r < a.requests) {
+      w.req = kv_request(a, w.r, most_q, false);
+      if (w.req.tiles) break;
+    }
+  }
+}
+
+// Rows that no request has: 0 and -inf.
+__device__ __forceinline__ void kv_clear_rest(const KvAttnArgs& a, int head_dim, int first, int step) {
+  const int used = min(max(a.q_start[a.requests], 0), a.tokens);
+  const int64_t rows = static_cast<int64_t>(a.tokens - used) * a.heads, words = rows * head_dim / 8;
+  uint4* out = reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(used) * a.heads * head_dim);
+  for (int64_t i = first; i < words; i += step) out[i] = make_uint4(0, 0, 0, 0);
+  for (int64_t i = first; i < rows; i += step) a.lse[static_cast<int64_t>(used) * a.heads + i] = -INFINITY;
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t kv_pack_out(float lo, float hi) {
+  if (F16) return kv_pack_f16(lo, hi);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int FMT, bool F16, int D, int NT>
+__global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
+    kv_attention_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                            const KvAttnArgs a, int most_q, uint8_t* workspace) {
+  using Cfg = KvFewCfg<D, NT>;
+  constexpr int KS = D / 16;      // k-steps of K Q^T
+  constexpr int VW = D / 32;      // 32-bit words of V that a lane takes from each token
+  constexpr int LD = D / 4;       // elements of d that a lane takes from each key
+  extern __shared__ uint8_t kv_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(kv_smem_raw) + 1023) & ~uintptr_t(1023));
+  float* sO = reinterpret_cast<float*>(smem + Cfg::OFF_O);
+  float2* sML = reinterpret_cast<float2*>(smem + Cfg::OFF_ML);
+  uint2* sQ = reinterpret_cast<uint2*>(smem + Cfg::OFF_Q);
+  float* sQF = reinterpret_cast<float*>(smem + Cfg::OFF_QF);
+  int2* sSeen = reinterpret_cast<int2*>(smem + Cfg::OFF_SEEN);
+  uint32_t* sNan = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_NAN);
+  float4* sSC = reinterpret_cast<float4*>(smem + Cfg::OFF_SC);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);
+  uint64_t* empty = full + Cfg::STAGES;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + Cfg::STAGES);
+  __shared__ KvPlanSmem plan;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int group = a.heads / a.kv_heads;
+
+  if (tid == 0) {
+    for (int i = 0; i < Cfg::STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kKvWarps);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+  }
+  pdl_prologue();
+  KvWalk w;
+  kv_plan(a, most_q, plan, w);  // (its barriers also publish the mbarriers)
+  if (tid == 0 && w.pos < plan.total) {
+    KvJob* jobs = reinterpret_cast<KvJob*>(workspace);
+    jobs[blockIdx.x] = KvJob{w.base, w.base + w.req.tiles, w.r, w.h};
+  }
+  if (tid == 0 && blockIdx.x == 0) reinterpret_cast<long long*>(workspace + sizeof(KvJob) * kKvMaxCtas)[0] = plan.total;
+  kv_clear_rest(a, D, blockIdx.x * kKvFewThreads + tid, gridDim.x * kKvFewThreads);
+
+  if (warp == kKvWarps) {
+    // ------------------------------------------------------------------ loads
+    int stage = 0;
+    uint32_t phase = 0;
+    long issued = 0;
+    bool ok = true;
+    const int rows_box = min(1 << a.shift, kKvTile), boxes = kKvTile / rows_box;
+    while (w.pos < w.end && ok) {
+      const int t_first = static_cast<int>(w.pos - w.base);
+      const int count = static_cast<int>(min(w.end - w.pos, static_cast<long long>(w.req.tiles - t_first)));
+      const int pages = (w.req.len + (1 << a.shift) - 1) >> a.shift;
+      int held = -64;  // the page that lane 0 holds the block of
+      int block = -1;
+      float sk = 0.f, sv = 1.f;
+      for (int i = 0; i < count && ok; ++i) {
+        const int token = (w.req.first_tile + t_first + i) * kKvTile;
+        const int page = token >> a.shift;
+        if (page + boxes > held + 32) {
+          held = page;
+          block = -1;
+          sk = 0.f;
+          sv = 1.f;
+          if (held + lane < pages) {
+            block = a.tables[static_cast<int64_t>(w.r) * a.max_blocks + held + lane];
+            if (block < 0 || block >= a.num_blocks) {
+              atomicOr(&g_mx_error_word, kSiteBadCache);
+              block = -1;
+            } else {
+              const int64_t at = static_cast<int64_t>(block) * a.kv_heads + w.h;
+              sk = a.k_scale[at];
+              sv = a.v_scale[at];
+            }
+          }
+        }
+        if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, kSiteProducerEmpty)) {
+          ok = false;
+          break;
+        }
+        const int slice = lane & 3;  // lanes 0..3: the scales of the tile's 16-token slices
+        const int from = ((token + 16 * slice) >> a.shift) - held;
+        const float slice_k = __shfl_sync(0xFFFFFFFFu, sk, from), slice_v = __shfl_sync(0xFFFFFFFFu, sv, from);
+        if (lane < 4) sSC[stage * 4 + slice] = make_float4(slice_k, log2f(slice_v), 1.f / slice_v, 0.f);
+        const int box_block = __shfl_sync(0xFFFFFFFFu, block, page - held + lane < 32 ? page - held + lane : 31);
+        const bool load = lane < boxes && box_block >= 0;
+        const uint32_t loads = __popc(__ballot_sync(0xFFFFFFFFu, load));
+        if (lane == 0) mbar_arrive_expect_tx(&full[stage], loads * 2 * rows_box * D);
+        __syncwarp();
+        if (load) {
+          const int row = ((box_block * a.kv_heads + w.h) << a.shift) + (token & ((1 << a.shift) - 1));
+          uint8_t* dst = smem + stage * 2 * Cfg::HALF + lane * rows_box * D;
+          tma_load_2d(dst, &tmK, &full[stage], 0, row);
+          tma_load_2d(dst + Cfg::HALF, &tmV, &full[stage], 0, row);
+        }
+        ++issued;
+        if (++stage == Cfg::STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      w.pos += count;
+      kv_next_unit(a, most_q, w);
+    }
+    // every copy has landed before the CTA's shared memory goes
+    for (int i = 0; i < Cfg::STAGES; ++i)
+      if (issued > i)
+        mbar_drain(&full[i], static_cast<uint32_t>(((i + (issued - 1 - i) / Cfg::STAGES * Cfg::STAGES) / Cfg::STAGES) & 1),
+                   kWaitBudgetNs);
+    return;
+  }
+
+  // -------------------------------------------------------------------- products and softmax
+  const int g = lane >> 2, c = lane & 3;
+  int stage = 0;
+  uint32_t phase = 0;
+  uint8_t* slots = workspace + sizeof(KvJob) * kKvMaxCtas + 16;
+  const long long range_start = w.pos;
+  while (w.pos < w.end) {
+    const KvRequest req = w.req;
+    const int t_first = static_cast<int>(w.pos - w.base);
+    const int count = static_cast<int>(min(w.end - w.pos, static_cast<long long>(req.tiles - t_first)));
+    const int rows = req.rows_q * group;
+    const int pos0 = req.len - req.rows_q;  // the first query's position
+    // queries of n-tile `warp`, as the fragments of Q^T
+    for (int nt = warp; nt < NT; nt += kKvWarps) {
+      const int row = nt * 8 + g;
+      uint4 x[LD / 8];
+      float amax = 0.f;
+      float f[LD];
+      if (row < rows) {
+        const int qi = row / group, hg = row - qi * group;
+        const uint16_t* src = a.q + (req.q0 + qi) * a.stride_t + (w.h * group + hg) * a.stride_h + c * LD;
+#pragma unroll
+        for (int i = 0; i < LD / 8; ++i) x[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < LD / 8; ++i) x[i] = make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < LD / 8; ++i) {
+        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 y = kv_unpack2<F16>(u[j]);
+          f[8 * i + 2 * j] = y.x;
+          f[8 * i + 2 * j + 1] = y.y;
+          amax = fmaxf(amax, fmaxf(fabsf(y.x), fabsf(y.y)));
+        }
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+      // 2^e with amax 2^e in [2^14, 2^15)
+      const int e = min(14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127), 120);
+      const float mul = amax > 0.f ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : 1.f;
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+        sQ[(i * NT + nt) * 32 + lane] = make_uint2(kv_pack_f16(f[4 * i] * mul, f[4 * i + 1] * mul),
+                                                   kv_pack_f16(f[4 * i + 2] * mul, f[4 * i + 3] * mul));
+      if (c == 0) {
+        sQF[row] = a.scale_log2 / mul;
+        const int p = pos0 + (row < rows ? row / group : 0);
+        sSeen[row] = make_int2(a.window ? p - a.window + 1 : 0, a.causal ? min(req.len, p + 1) : req.len);
+      }
+    }
+    for (int i = tid; i < Cfg::ROWS * (D / 32); i += 32 * kKvWarps) sNan[i] = 0;
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kKvWarps) : "memory");
+    uint2 qf[NT == 1 ? KS : 1];
+    if (NT == 1) {
+#pragma unroll
+      for (int i = 0; i < KS; ++i) qf[i] = sQ[i * 32 + lane];
+    }
+    float m[2 * NT], l[2 * NT];
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+    }
+    float acc[2 * VW][NT][4];
+#pragma unroll
+    for (int i = 0; i < 2 * VW; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][n][j] = 0.f;
+    // what every row sees, and what any row sees
+    const int all_lo = a.window ? req.len - a.window : 0, all_hi = a.causal ? min(req.len, pos0 + 1) : req.len;
+    const int any_lo = a.window ? pos0 - a.window + 1 : 0;
+
+    for (int i = 0; i < count; ++i) {
+      const int token = (req.first_tile + t_first + i) * kKvTile;
+      const bool ok = mbar_wait(&full[stage], phase, abort_flag, kSiteMmaFull);
+      const uint8_t* sK = smem + stage * 2 * Cfg::HALF + warp * 16 * D;
+      const uint8_t* sV = sK + Cfg::HALF;
+      const float4 sc = sSC[stage * 4 + warp];
+      const bool edge = token < all_lo || token + kKvTile > all_hi;
+      const int t0 = token + 16 * warp;
+      if (ok) {
+        // S^T
+        float s[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+        uint4 ka[LD / 16], kb[LD / 16];
+#pragma unroll
+        for (int j = 0; j < LD / 16; ++j) {
+          const int at = D == 128 ? g * 128 + (((2 * c + j) ^ g) << 4) : g * 64 + ((c ^ ((g >> 1) & 3)) << 4);
+          ka[j] = *reinterpret_cast<const uint4*>(sK + at);
+          kb[j] = *reinterpret_cast<const uint4*>(sK + 8 * D + at);
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const uint4 x = ka[k / 4], y = kb[k / 4];
+          const uint32_t wa = k % 4 == 0 ? x.x : k % 4 == 1 ? x.y : k % 4 == 2 ? x.z : x.w;
+          const uint32_t wb = k % 4 == 0 ? y.x : k % 4 == 1 ? y.y : k % 4 == 2 ? y.z : y.w;
+          const uint32_t a0 = kv_codes_to_f16x2<FMT>(wa & 0xFFFFu), a2 = kv_codes_to_f16x2<FMT>(wa >> 16);
+          const uint32_t a1 = kv_codes_to_f16x2<FMT>(wb & 0xFFFFu), a3 = kv_codes_to_f16x2<FMT>(wb >> 16);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint2 b = NT == 1 ? qf[NT == 1 ? k : 0] : sQ[(k * NT + n) * 32 + lane];
+            kv_mma(s[n], a0, a1, a2, a3, b.x, b.y);
+          }
+        }
+        // z + log2 sV, the reference, the weights
+        bool past = false;
+        float mx[2 * NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[n][j] = fmaf(s[n][j], sQF[n * 8 + 2 * c + (j & 1)] * sc.x, sc.y);
+          if (edge) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int t = t0 + g + 8 * (j >> 1);
+              const int2 seen = sSeen[n * 8 + 2 * c + (j & 1)];
+              if (t < seen.x || t >= seen.y) s[n][j] = -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            mx[2 * n + e] = fmaxf(s[n][e], s[n][2 + e]);
+            past = past || mx[2 * n + e] > m[2 * n + e] + 8.f;
+          }
+        }
+        if (__any_sync(0xFFFFFFFFu, past)) {
+#pragma unroll
+          for (int j = 0; j < 2 * NT; ++j) {
+            float x = mx[j];
+            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+            x = fmaxf(x, m[j]);
+            const float keep = kv_exp2(m[j] - (x == -INFINITY ? 0.f : x));
+            m[j] = x;
+            l[j] *= keep;
+#pragma unroll
+            for (int k = 0; k < 2 * VW; ++k) {
+              acc[k][j >> 1][j & 1] *= keep;
+              acc[k][j >> 1][2 + (j & 1)] *= keep;
+            }
+          }
+        }
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float m0 = m[2 * n] == -INFINITY ? 0.f : m[2 * n], m1 = m[2 * n + 1] == -INFINITY ? 0.f : m[2 * n + 1];
+          const float p0 = kv_exp2(s[n][0] - m0), p1 = kv_exp2(s[n][1] - m1), p2 = kv_exp2(s[n][2] - m0),
+                      p3 = kv_exp2(s[n][3] - m1);
+          l[2 * n] = fmaf(p0 + p2, sc.z, l[2 * n]);
+          l[2 * n + 1] = fmaf(p1 + p3, sc.z, l[2 * n + 1]);
+          pb[n][0] = kv_transpose8x8(kv_pack_f16(p0, p1));
+          pb[n][1] = kv_transpose8x8(kv_pack_f16(p2, p3));
+        }
+        // V: tokens 2c, 2c + 1, 2c + 8, 2c + 9, this lane's D / 8 values of each
+        uint32_t v[4][VW];
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+          const int t = 2 * c + (tt & 1) + 8 * (tt >> 1);
+          if (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(sV + t * 128 + ((g ^ (t & 7)) << 4));
+            v[tt][0] = x.x;
+            v[tt][1] = x.y;
+            v[tt][VW - 2] = x.z;
+            v[tt][VW - 1] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(sV + t * 64 + (((g >> 1) ^ ((t >> 1) & 3)) << 4) + (g & 1) * 8);
+            v[tt][0] = x.x;
+            v[tt][1] = x.y;
+          }
+        }
+        if (edge) {
+          uint32_t bad = 0;
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt) {
+            const int t = t0 + 2 * c + (tt & 1) + 8 * (tt >> 1);
+#pragma unroll
+            for (int j = 0; j < VW; ++j) {
+              if (t < any_lo || t >= req.len) v[tt][j] = 0;
+              bad |= kv_nan_bytes<FMT>(v[tt][j]);
+            }
+          }
+          if (bad) {  // (rare) for each NaN: note the rows that see it, clear the code
+#pragma unroll
+            for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+              for (int j = 0; j < VW; ++j) {
+                const uint32_t x = kv_nan_bytes<FMT>(v[tt][j]);
+                v[tt][j] &= ~((x >> 7) * 0xFFu);
+                const int t = t0 + 2 * c + (tt & 1) + 8 * (tt >> 1), d = (D / 8) * g + 4 * j;
+                if (x)
+                  for (int row = 0; row < Cfg::ROWS; ++row)
+                    if (t >= sSeen[row].x && t < sSeen[row].y)
+                      atomicOr(&sNan[row * (D / 32) + (d >> 5)],
+                               ((x >> 7 & 1) | (x >> 14 & 2) | (x >> 21 & 4) | (x >> 28 & 8)) << (d & 31));
+              }
+          }
+        }
+        // O^T
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+          const uint32_t x01 = __byte_perm(v[0][j], v[1][j], 0x5140), y01 = __byte_perm(v[0][j], v[1][j], 0x7362);
+          const uint32_t x23 = __byte_perm(v[2][j], v[3][j], 0x5140), y23 = __byte_perm(v[2][j], v[3][j], 0x7362);
+          const uint32_t a0 = kv_codes_to_f16x2<FMT>(x01 & 0xFFFFu), a1 = kv_codes_to_f16x2<FMT>(x01 >> 16);
+          const uint32_t a2 = kv_codes_to_f16x2<FMT>(x23 & 0xFFFFu), a3 = kv_codes_to_f16x2<FMT>(x23 >> 16);
+          const uint32_t b0 = kv_codes_to_f16x2<FMT>(y01 & 0xFFFFu), b1 = kv_codes_to_f16x2<FMT>(y01 >> 16);
+          const uint32_t b2 = kv_codes_to_f16x2<FMT>(y23 & 0xFFFFu), b3 = kv_codes_to_f16x2<FMT>(y23 >> 16);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            kv_mma(acc[2 * j][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+            kv_mma(acc[2 * j + 1][n], b0, b1, b2, b3, pb[n][0], pb[n][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[stage]);
+      if (++stage == Cfg::STAGES) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+
+    // the four warps' (m, l, O) through shared memory
+#pragma unroll
+    for (int j = 0; j < 2 * NT; ++j) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l[j] += __shfl_xor_sync(0xFFFFFFFFu, l[j], o);
+      const int row = (j >> 1) * 8 + 2 * c + (j & 1);
+      if (g == 0) sML[warp * Cfg::ROWS + row] = make_float2(m[j], l[j]);
+#pragma unroll
+      for (int k = 0; k < VW; ++k)
+        *reinterpret_cast<float4*>(&sO[(warp * Cfg::ROWS + row) * Cfg::O_STRIDE + (D / 8) * g + 4 * k]) =
+            make_float4(acc[2 * k][j >> 1][j & 1], acc[2 * k][j >> 1][2 + (j & 1)], acc[2 * k + 1][j >> 1][j & 1],
+                        acc[2 * k + 1][j >> 1][2 + (j & 1)]);
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kKvWarps) : "memory");
+    const bool whole = count == req.tiles;
+    const int slot = w.pos == range_start ? 0 : 1;
+    float* part = reinterpret_cast<float*>(slots + (2 * blockIdx.x + slot) * Cfg::SLOT);
+    for (int i = tid; i < rows * (D / 4); i += 32 * kKvWarps) {
+      const int row = i / (D / 4), d = i % (D / 4) * 4;
+      float2 ml[kKvWarps];
+      float most = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kKvWarps; ++k) {
+        ml[k] = sML[k * Cfg::ROWS + row];
+        most = fmaxf(most, ml[k].x);
+      }
+      const float at = most == -INFINITY ? 0.f : most;
+      float sum = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kKvWarps; ++k) {
+        const float f = kv_exp2(ml[k].x - at);
+        const float4 x = *reinterpret_cast<const float4*>(&sO[(k * Cfg::ROWS + row) * Cfg::O_STRIDE + d]);
+        sum = fmaf(ml[k].y, f, sum);
+        o.x = fmaf(x.x, f, o.x);
+        o.y = fmaf(x.y, f, o.y);
+        o.z = fmaf(x.z, f, o.z);
+        o.w = fmaf(x.w, f, o.w);
+      }
+      if (const uint32_t nan = sNan[row * (D / 32) + (d >> 5)] >> (d & 31) & 15) {
+        if (nan & 1) o.x = NAN;
+        if (nan & 2) o.y = NAN;
+        if (nan & 4) o.z = NAN;
+        if (nan & 8) o.w = NAN;
+      }
+      if (whole) {
+        const int qi = row / group, hg = row - qi * group;
+        const int64_t at_row = static_cast<int64_t>(req.q0 + qi) * a.heads + w.h * group + hg;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        *reinterpret_cast<uint2*>(a.out + at_row * D + d) =
+            sum == 0.f ? make_uint2(0, 0) : make_uint2(kv_pack_out<F16>(o.x * inv, o.y * inv), kv_pack_out<F16>(o.z * inv, o.w * inv));
+        if (d == 0) a.lse[at_row] = sum == 0.f ? -INFINITY : (at + log2f(sum)) * kLn2;
+      } else {
+        *reinterpret_cast<float4*>(part + row * D + d) = o;
+        if (d == 0) *reinterpret_cast<float2*>(part + Cfg::ROWS * D + 2 * row) = make_float2(most, sum);
+      }
+    }
+    w.pos += count;
+    kv_next_unit(a, most_q, w);
+  }
+}
+
+// Joins the segments of the units that range boundaries cut.  CTA c looks at the boundary where range c
+// begins; the first boundary inside a unit takes the unit.  Segments are added in order.
+template <bool F16, int D, int NT>
+__global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int most_q, const uint8_t* workspace) {
+  pdl_prologue();
+  using Cfg = KvFewCfg<D, NT>;
+  const KvJob* jobs = reinterpret_cast<const KvJob*>(workspace);
+  const long long total = *reinterpret_cast<const long long*>(workspace + sizeof(KvJob) * kKvMaxCtas);
+  const uint8_t* slots = workspace + sizeof(KvJob) * kKvMaxCtas + 16;
+  const int c = blockIdx.x + 1, ranges = gridDim.x + 1;
+  auto begin = [&](int i) { return total * i / ranges; };
+  const long long at = begin(c);
+  if (at >= total) return;
+  const KvJob job = jobs[c];
+  if (job.start == at || begin(c - 1) > job.start) return;
+  const KvRequest req = kv_request(a, job.request, most_q, false);
+  const int group = a.heads / a.kv_heads, rows = req.rows_q * group;
+  for (int i = threadIdx.x; i < rows * (D / 4); i += 128) {
+    const int row = i / (D / 4), d = i % (D / 4) * 4;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = c - 1; k < ranges; ++k) {
+      const long long b = begin(k);
+      if (b >= job.end) break;
+      if (begin(k + 1) == b) continue;
+      const int slot = k == c - 1 && b != job.start ? 1 : 0;
+      const float* part = reinterpret_cast<const float*>(slots + (2 * k + slot) * Cfg::SLOT);
+      const float2 ml = *reinterpret_cast<const float2*>(part + Cfg::ROWS * D + 2 * row);
+      const float4 x = *reinterpret_cast<const float4*>(part + row * D + d);
+      const float most = fmaxf(m, ml.x), ref = most == -INFINITY ? 0.f : most;
+      const float f0 = kv_exp2(m - ref), f1 = kv_exp2(ml.x - ref);
+      l = l * f0 + ml.y * f1;
+      o.x = o.x * f0 + x.x * f1;
+      o.y = o.y * f0 + x.y * f1;
+      o.z = o.z * f0 + x.z * f1;
+      o.w = o.w * f0 + x.w * f1;
+      m = most;
+    }
+    const int qi = row / group, hg = row - qi * group;
+    const int64_t at_row = static_cast<int64_t>(req.q0 + qi) * a.heads + job.head * group + hg;
+    const float inv = 1.f / l;
+    *reinterpret_cast<uint2*>(a.out + at_row * D + d) =
+        l == 0.f ? make_uint2(0, 0) : make_uint2(kv_pack_out<F16>(o.x * inv, o.y * inv), kv_pack_out<F16>(o.z * inv, o.w * inv));
+    if (d == 0) a.lse[at_row] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
+  }
+}
+
 }  // namespace mxgb

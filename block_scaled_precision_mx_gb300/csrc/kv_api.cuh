@@ -193,7 +193,7 @@ size_t kv_attention_workspace_bytes(int64_t num_tokens, int64_t requests, int64_
   if (head_dim != 64 && head_dim != 128) return 0;
   const int nt = kv_row_tiles(max_q_len, heads / kv_heads);
   if (!nt) return 16;
-  return sizeof(KvJob) * kKvMaxCtas + 16 + 2ull * kKvMaxCtas * (8 * nt) * (head_dim + 2) * 4;
+  return kKvSlotsAt + 2ull * kKvMaxCtas * (8 * nt) * (head_dim + 2) * 4;
 }
 
 mx_status kv_attention(const void* q, mx_half type, int64_t num_tokens, int64_t heads, int64_t q_stride_token,

@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(128) kv_attention_rows_kernel(const KvAttnArgs
 //
 //  * The work is the list of (request, kv head) units, each a row of 64-token tiles; all tiles of all
 //    units, in order, are cut into gridDim.x equal ranges, one for each resident CTA, whatever the
-//    lengths are.  A CTA's range is a few segments of units; a unit that one CTA has whole is finished
+//    lengths are.  A range is a few segments of units; a unit that one CTA has whole is finished
 //    there, else each segment leaves (O, m, l) in the workspace and kv_join_kernel joins them in order.
 //  * One warp keeps a ring of tiles in flight: TMA boxes of a block's rows of codes (128 or 64 bytes,
 //    swizzled), so a tile's codes cross the SM once, and the scales of its four 16-token slices.
@@ -137,10 +137,12 @@ constexpr int kKvWarps = 4;
 constexpr int kKvFewThreads = 32 * (kKvWarps + 1);
 constexpr int kKvMaxCtas = 608;
 
-struct KvJob {  // where a range begins: the unit and its place in the list of tiles
-  long long start, end;
+struct KvJob {  // a range of the list, and the unit that it begins in
+  long long begin, end, unit;
   int request, head;
 };
+
+constexpr size_t kKvSlotsAt = sizeof(KvJob) * kKvMaxCtas;  // in the workspace, behind the jobs
 
 template <int D, int NT>
 struct KvFewCfg {
@@ -191,6 +193,7 @@ __device__ __forceinline__ uint32_t kv_nan_bytes(uint32_t w) {
 // A request as the kernels go through it.
 struct KvRequest {
   int q0, rows_q, len, first_tile, tiles;  // tiles = 0: no queries
+  __device__ int cost() const;
 };
 
 __device__ __forceinline__ KvRequest kv_request(const KvAttnArgs& a, int r, int most_q, bool tell) {
@@ -210,15 +213,29 @@ __device__ __forceinline__ KvRequest kv_request(const KvAttnArgs& a, int r, int 
   return v;
 }
 
-// The place of a tile in the list of all tiles, and the walk over a range's segments.
+// The list of all units' work, in 64-token tiles, is cut into equal ranges.  A unit costs its tiles and
+// kKvUnitCost more, for its queries' fetch and the join of the warps, so that many short units are not
+// one CTA's; a range that begins inside those first places begins at the unit's first tile.
+constexpr int kKvUnitCost = 3;
+
+__device__ __forceinline__ int KvRequest::cost() const { return tiles ? tiles + kKvUnitCost : 0; }
+
+// place i n-ths into a list of `total` places
+__device__ __forceinline__ long long kv_cut(long long total, int i, int n) {
+  if (total < (1 << 21)) return static_cast<unsigned>(total) * static_cast<unsigned>(i) / static_cast<unsigned>(n);
+  return total * i / n;
+}
+
+// The walk over a range's segments.
 struct KvWalk {
-  long long pos, end, base;  // base: the place of the current unit's first tile
+  long long pos, end, base;  // base: where the current unit begins in the list
   int r, h;
   KvRequest req;
+  int tile, count;  // the current segment: tiles of the unit, from the unit's first one on
 };
 
 // Finds where this CTA's range begins and ends: every thread sums a stretch of the requests, the sums are
-// scanned, and the thread that holds the range's first tile finds its unit.  `slots` is shared memory.
+// scanned, and the thread that holds the range's first place finds its unit.
 struct KvPlanSmem {
   long long warp_sum[kKvWarps + 1];
   long long pos, end, base, total;
@@ -229,7 +246,7 @@ __device__ __forceinline__ void kv_plan(const KvAttnArgs& a, int most_q, KvPlanS
   const int per = (a.requests + kKvFewThreads - 1) / kKvFewThreads;
   const int r0 = min(tid * per, a.requests), r1 = min(r0 + per, a.requests);
   long long mine = 0;
-  for (int r = r0; r < r1; ++r) mine += kv_request(a, r, most_q, blockIdx.x == 0).tiles;
+  for (int r = r0; r < r1; ++r) mine += kv_request(a, r, most_q, blockIdx.x == 0).cost();
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -247,16 +264,17 @@ __device__ __forceinline__ void kv_plan(const KvAttnArgs& a, int most_q, KvPlanS
   total *= a.kv_heads;
   before *= a.kv_heads;
   mine *= a.kv_heads;
-  const long long pos = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
+  const long long pos = kv_cut(total, blockIdx.x, gridDim.x);
   if (pos >= before && pos < before + mine) {
     long long at = before;
     for (int r = r0; r < r1; ++r) {
-      const int tiles = kv_request(a, r, most_q, false).tiles;
-      const long long all = static_cast<long long>(tiles) * a.kv_heads;
+      const int cost = kv_request(a, r, most_q, false).cost();
+      const long long all = static_cast<long long>(cost) * a.kv_heads;
       if (pos < at + all) {
         sm.r = r;
-        sm.h = static_cast<int>((pos - at) / tiles);
-        sm.base = at + static_cast<long long>(sm.h) * tiles;
+        sm.h = static_cast<int>(pos - at < (1ll << 31) ? static_cast<unsigned>(pos - at) / static_cast<unsigned>(cost)
+                                                       : (pos - at) / cost);
+        sm.base = at + static_cast<long long>(sm.h) * cost;
         break;
       }
       at += all;
@@ -264,7 +282,7 @@ __device__ __forceinline__ void kv_plan(const KvAttnArgs& a, int most_q, KvPlanS
   }
   if (tid == 0) {
     sm.pos = pos;
-    sm.end = end;
+    sm.end = kv_cut(total, blockIdx.x + 1, gridDim.x);
     sm.total = total;
   }
   __syncthreads();
@@ -275,15 +293,33 @@ __device__ __forceinline__ void kv_plan(const KvAttnArgs& a, int most_q, KvPlanS
   w.h = sm.h;
   if (w.pos < sm.total) w.req = kv_request(a, w.r, most_q, false);
 }
-__device__ __forceinline__ void kv_next_unit(const KvAttnArgs& a, int most_q, KvWalk& w) {
-  w.base += w.req.tiles;
-  if (++w.h == a.kv_heads) {
-    w.h = 0;
-    while (w.pos < w.end && ++w.r < a.requests) {
-      w.req = kv_request(a, w.r, most_q, false);
-      if (w.req.tiles) break;
+// tiles of a unit in front of place x of its cost
+__device__ __forceinline__ int kv_tiles_before(long long x, int tiles) {
+  return static_cast<int>(min(max(x - kKvUnitCost, 0ll), static_cast<long long>(tiles)));
+}
+// The next segment that has tiles, from w.pos on; false at the range's end.
+__device__ __forceinline__ bool kv_next_segment(const KvAttnArgs& a, int most_q, KvWalk& w) {
+  while (w.pos < w.end) {
+    const long long unit_end = w.base + w.req.cost();
+    if (w.pos == unit_end) {
+      w.base = unit_end;
+      if (++w.h == a.kv_heads) {
+        w.h = 0;
+        while (++w.r < a.requests) {
+          w.req = kv_request(a, w.r, most_q, false);
+          if (w.req.tiles) break;
+        }
+        if (w.r >= a.requests) return false;
+      }
+      continue;
     }
+    const long long to = min(w.end, unit_end);
+    w.tile = kv_tiles_before(w.pos - w.base, w.req.tiles);
+    w.count = kv_tiles_before(to - w.base, w.req.tiles) - w.tile;
+    w.pos = to;
+    if (w.count) return true;
   }
+  return false;
 }
 
 // Rows that no request has: 0 and -inf.
@@ -328,7 +364,7 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
 
   if (tid == 0) {
     for (int i = 0; i < Cfg::STAGES; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], 2);  // the boxes' bytes; the scales
       mbar_init(&empty[i], kKvWarps);
     }
     *abort_flag = 0;
@@ -339,74 +375,84 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
   pdl_prologue();
   KvWalk w;
   kv_plan(a, most_q, plan, w);  // (its barriers also publish the mbarriers)
-  if (tid == 0 && w.pos < plan.total) {
-    KvJob* jobs = reinterpret_cast<KvJob*>(workspace);
-    jobs[blockIdx.x] = KvJob{w.base, w.base + w.req.tiles, w.r, w.h};
-  }
-  if (tid == 0 && blockIdx.x == 0) reinterpret_cast<long long*>(workspace + sizeof(KvJob) * kKvMaxCtas)[0] = plan.total;
+  if (tid == 0) reinterpret_cast<KvJob*>(workspace)[blockIdx.x] = KvJob{w.pos, w.end, w.base, w.r, w.h};
   kv_clear_rest(a, D, blockIdx.x * kKvFewThreads + tid, gridDim.x * kKvFewThreads);
 
   if (warp == kKvWarps) {
     // ------------------------------------------------------------------ loads
+    // A chunk is up to 32 blocks of a segment: lane i holds block i and its scales, read while the chunk
+    // before it is loaded.
+    struct Chunk {
+      int token, len, h, tiles, block;
+      float sk, sv;
+    };
+    const int P = 1 << a.shift, rows_box = min(P, kKvTile), boxes = kKvTile / rows_box;
+    const int most_tiles = P > kKvTile ? 32 * P / kKvTile - 1 : 32 * P / kKvTile;  // (a segment may start inside a block)
+    int left = 0;
+    auto fetch = [&](Chunk& ch) {
+      ch.tiles = 0;
+      if (!left) {
+        if (!kv_next_segment(a, most_q, w)) return;
+        left = w.count;
+      }
+      ch.tiles = min(left, most_tiles);
+      ch.token = (w.req.first_tile + w.tile + w.count - left) * kKvTile;
+      ch.len = w.req.len;
+      ch.h = w.h;
+      left -= ch.tiles;
+      const int page = (ch.token >> a.shift) + lane;
+      ch.block = -1;
+      ch.sk = 0.f;
+      ch.sv = 1.f;
+      if (page << a.shift < ch.len) {
+        ch.block = a.tables[static_cast<int64_t>(w.r) * a.max_blocks + page];
+        if (ch.block < 0 || ch.block >= a.num_blocks) {
+          atomicOr(&g_mx_error_word, kSiteBadCache);
+          ch.block = -1;
+        } else {
+          const int64_t at = static_cast<int64_t>(ch.block) * a.kv_heads + ch.h;
+          ch.sk = a.k_scale[at];
+          ch.sv = a.v_scale[at];
+        }
+      }
+    };
     int stage = 0;
     uint32_t phase = 0;
     long issued = 0;
     bool ok = true;
-    const int rows_box = min(1 << a.shift, kKvTile), boxes = kKvTile / rows_box;
-    while (w.pos < w.end && ok) {
-      const int t_first = static_cast<int>(w.pos - w.base);
-      const int count = static_cast<int>(min(w.end - w.pos, static_cast<long long>(w.req.tiles - t_first)));
-      const int pages = (w.req.len + (1 << a.shift) - 1) >> a.shift;
-      int held = -64;  // the page that lane 0 holds the block of
-      int block = -1;
-      float sk = 0.f, sv = 1.f;
-      for (int i = 0; i < count && ok; ++i) {
-        const int token = (w.req.first_tile + t_first + i) * kKvTile;
-        const int page = token >> a.shift;
-        if (page + boxes > held + 32) {
-          held = page;
-          block = -1;
-          sk = 0.f;
-          sv = 1.f;
-          if (held + lane < pages) {
-            block = a.tables[static_cast<int64_t>(w.r) * a.max_blocks + held + lane];
-            if (block < 0 || block >= a.num_blocks) {
-              atomicOr(&g_mx_error_word, kSiteBadCache);
-              block = -1;
-            } else {
-              const int64_t at = static_cast<int64_t>(block) * a.kv_heads + w.h;
-              sk = a.k_scale[at];
-              sv = a.v_scale[at];
-            }
-          }
-        }
+    Chunk cur, next;
+    fetch(cur);
+    while (cur.tiles && ok) {
+      for (int i = 0; i < cur.tiles; ++i) {
+        const int token = cur.token + i * kKvTile, first = (token >> a.shift) - (cur.token >> a.shift);
         if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, kSiteProducerEmpty)) {
           ok = false;
           break;
         }
-        const int slice = lane & 3;  // lanes 0..3: the scales of the tile's 16-token slices
-        const int from = ((token + 16 * slice) >> a.shift) - held;
-        const float slice_k = __shfl_sync(0xFFFFFFFFu, sk, from), slice_v = __shfl_sync(0xFFFFFFFFu, sv, from);
-        if (lane < 4) sSC[stage * 4 + slice] = make_float4(slice_k, log2f(slice_v), 1.f / slice_v, 0.f);
-        const int box_block = __shfl_sync(0xFFFFFFFFu, block, page - held + lane < 32 ? page - held + lane : 31);
+        const int box_block = __shfl_sync(0xFFFFFFFFu, cur.block, min(first + lane, 31));
         const bool load = lane < boxes && box_block >= 0;
         const uint32_t loads = __popc(__ballot_sync(0xFFFFFFFFu, load));
         if (lane == 0) mbar_arrive_expect_tx(&full[stage], loads * 2 * rows_box * D);
         __syncwarp();
         if (load) {
-          const int row = ((box_block * a.kv_heads + w.h) << a.shift) + (token & ((1 << a.shift) - 1));
+          const int row = ((box_block * a.kv_heads + cur.h) << a.shift) + (token & (P - 1));
           uint8_t* dst = smem + stage * 2 * Cfg::HALF + lane * rows_box * D;
           tma_load_2d(dst, &tmK, &full[stage], 0, row);
           tma_load_2d(dst + Cfg::HALF, &tmV, &full[stage], 0, row);
         }
+        const int from = ((token + 16 * (lane & 3)) >> a.shift) - (cur.token >> a.shift);  // lanes 0..3: the slices' scales
+        const float slice_k = __shfl_sync(0xFFFFFFFFu, cur.sk, from), slice_v = __shfl_sync(0xFFFFFFFFu, cur.sv, from);
+        if (lane < 4) sSC[stage * 4 + lane] = make_float4(slice_k, log2f(slice_v), 1.f / slice_v, 0.f);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[stage]);
         ++issued;
         if (++stage == Cfg::STAGES) {
           stage = 0;
           phase ^= 1;
         }
+        if (i == min(Cfg::STAGES, cur.tiles) - 1) fetch(next);
       }
-      w.pos += count;
-      kv_next_unit(a, most_q, w);
+      cur = next;
     }
     // every copy has landed before the CTA's shared memory goes
     for (int i = 0; i < Cfg::STAGES; ++i)
@@ -420,12 +466,10 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
   const int g = lane >> 2, c = lane & 3;
   int stage = 0;
   uint32_t phase = 0;
-  uint8_t* slots = workspace + sizeof(KvJob) * kKvMaxCtas + 16;
   const long long range_start = w.pos;
-  while (w.pos < w.end) {
+  while (kv_next_segment(a, most_q, w)) {
     const KvRequest req = w.req;
-    const int t_first = static_cast<int>(w.pos - w.base);
-    const int count = static_cast<int>(min(w.end - w.pos, static_cast<long long>(req.tiles - t_first)));
+    const int count = w.count;
     const int rows = req.rows_q * group;
     const int pos0 = req.len - req.rows_q;  // the first query's position
     // queries of n-tile `warp`, as the fragments of Q^T
@@ -494,7 +538,7 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
     const int any_lo = a.window ? pos0 - a.window + 1 : 0;
 
     for (int i = 0; i < count; ++i) {
-      const int token = (req.first_tile + t_first + i) * kKvTile;
+      const int token = (req.first_tile + w.tile + i) * kKvTile;
       const bool ok = mbar_wait(&full[stage], phase, abort_flag, kSiteMmaFull);
       const uint8_t* sK = smem + stage * 2 * Cfg::HALF + warp * 16 * D;
       const uint8_t* sV = sK + Cfg::HALF;
@@ -659,8 +703,8 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
     }
     asm volatile("bar.sync 1, %0;" ::"n"(32 * kKvWarps) : "memory");
     const bool whole = count == req.tiles;
-    const int slot = w.pos == range_start ? 0 : 1;
-    float* part = reinterpret_cast<float*>(slots + (2 * blockIdx.x + slot) * Cfg::SLOT);
+    const int slot = w.base < range_start ? 0 : 1;
+    float* part = reinterpret_cast<float*>(workspace + kKvSlotsAt + (2 * blockIdx.x + slot) * Cfg::SLOT);
     for (int i = tid; i < rows * (D / 4); i += 32 * kKvWarps) {
       const int row = i / (D / 4), d = i % (D / 4) * 4;
       float2 ml[kKvWarps];
@@ -701,38 +745,54 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
         if (d == 0) *reinterpret_cast<float2*>(part + Cfg::ROWS * D + 2 * row) = make_float2(most, sum);
       }
     }
-    w.pos += count;
-    kv_next_unit(a, most_q, w);
   }
 }
 
 // Joins the segments of the units that range boundaries cut.  CTA c looks at the boundary where range c
-// begins; the first boundary inside a unit takes the unit.  Segments are added in order.
+// begins; the first boundary inside a unit takes the unit.  Segments are added in order: the range that
+// the unit begins in left its one in slot 1, the others in slot 0.
 template <bool F16, int D, int NT>
 __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int most_q, const uint8_t* workspace) {
   pdl_prologue();
   using Cfg = KvFewCfg<D, NT>;
+  __shared__ int list[kKvMaxCtas];
+  __shared__ int listed;
   const KvJob* jobs = reinterpret_cast<const KvJob*>(workspace);
-  const long long total = *reinterpret_cast<const long long*>(workspace + sizeof(KvJob) * kKvMaxCtas);
-  const uint8_t* slots = workspace + sizeof(KvJob) * kKvMaxCtas + 16;
   const int c = blockIdx.x + 1, ranges = gridDim.x + 1;
-  auto begin = [&](int i) { return total * i / ranges; };
-  const long long at = begin(c);
-  if (at >= total) return;
   const KvJob job = jobs[c];
-  if (job.start == at || begin(c - 1) > job.start) return;
+  const long long before = jobs[c - 1].begin, total = jobs[ranges - 1].end;
+  if (job.begin >= total || job.unit == job.begin || before > job.unit) return;
   const KvRequest req = kv_request(a, job.request, most_q, false);
+  const long long unit_end = job.unit + req.cost();
+  if (threadIdx.x < 32) {
+    int n = 0;
+    for (int k0 = c - 1; k0 < ranges; k0 += 32) {
+      const int k = k0 + threadIdx.x;
+      bool has = false, over = true;
+      if (k < ranges) {
+        const long long b = jobs[k].begin, e = jobs[k].end;
+        over = b >= unit_end;
+        const int from = kv_tiles_before(b - job.unit, req.tiles), to = kv_tiles_before(e - job.unit, req.tiles);
+        has = !over && to > from && to - from < req.tiles;  // (a range that has all of it has finished it)
+      }
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, has);
+      if (has) list[n + __popc(m & ((1u << threadIdx.x) - 1))] = 2 * k + (k == c - 1 ? 1 : 0);
+      n += __popc(m);
+      if (__any_sync(0xFFFFFFFFu, over)) break;
+    }
+    if (threadIdx.x == 0) listed = n;
+  }
+  __syncthreads();
+  const int n = listed;
+  if (n == 0) return;
   const int group = a.heads / a.kv_heads, rows = req.rows_q * group;
   for (int i = threadIdx.x; i < rows * (D / 4); i += 128) {
     const int row = i / (D / 4), d = i % (D / 4) * 4;
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = c - 1; k < ranges; ++k) {
-      const long long b = begin(k);
-      if (b >= job.end) break;
-      if (begin(k + 1) == b) continue;
-      const int slot = k == c - 1 && b != job.start ? 1 : 0;
-      const float* part = reinterpret_cast<const float*>(slots + (2 * k + slot) * Cfg::SLOT);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float* part = reinterpret_cast<const float*>(workspace + kKvSlotsAt + list[k] * Cfg::SLOT);
       const float2 ml = *reinterpret_cast<const float2*>(part + Cfg::ROWS * D + 2 * row);
       const float4 x = *reinterpret_cast<const float4*>(part + row * D + d);
       const float most = fmaxf(m, ml.x), ref = most == -INFINITY ? 0.f : most;

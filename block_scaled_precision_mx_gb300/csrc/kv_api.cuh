@@ -58,8 +58,38 @@ mx_status kv_few_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_len
   const int most_q = static_cast<int>(max_q_len);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   if (pdl_launch(kern, n, kKvFewThreads, Cfg::SMEM, st, tk, tv, a, most_q, ws) != cudaSuccess) return MX_ERR_CUDA;
-  if (n > 1 && pdl_launch(kv_join_kernel<F16, D, NT>, n - 1, 128, 0, st, a, most_q,
-                          static_cast<const uint8_t*>(ws)) != cudaSuccess)
+  if (n > 1 && pdl_launch(kv_join_kernel<F16, D, 8 * NT>, n - 1, 128, 0, st, a, static_cast<const uint8_t*>(ws),
+                          kKvSlotsAt) != cudaSuccess)
+    return MX_ERR_CUDA;
+  return launch_status();
+}
+
+template <int FMT, bool F16, int D>
+mx_status kv_many_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_len, void* workspace, cudaStream_t st) {
+  using Cfg = KvManyCfg<D>;
+  auto kern = kv_attention_many_kernel<FMT, F16, D>;
+  static std::atomic<bool> attr_set[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MX_ERR_CUDA;
+  if (!attr_set[dev].load(std::memory_order_relaxed)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM) != cudaSuccess)
+      return MX_ERR_CUDA;
+    attr_set[dev].store(true, std::memory_order_relaxed);
+  }
+  const int sms = device_sms();
+  if (sms <= 0) return MX_ERR_CUDA;
+  const int n = sms < kKvManyMaxCtas ? sms : kKvManyMaxCtas;
+  CUtensorMap tk, tv;
+  if (!kv_codes_tmap(&tk, a.k_codes, a.num_blocks, a.kv_heads, block_tokens, D) ||
+      !kv_codes_tmap(&tv, a.v_codes, a.num_blocks, a.kv_heads, block_tokens, D))
+    return MX_ERR_CUDA;
+  const int most_q = static_cast<int>(max_q_len);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (pdl_launch(kv_plan_kernel, 1, kKvPlanThreads, 0, st, a, most_q, n, ws) != cudaSuccess ||
+      pdl_launch(kern, n, kKvManyThreads, Cfg::SMEM, st, tk, tv, a, most_q, ws) != cudaSuccess)
+    return MX_ERR_CUDA;
+  if (n > 1 && pdl_launch(kv_join_kernel<F16, D, kKvManyRows>, dim3(n - 1, 8), 128, 0, st, a, static_cast<const uint8_t*>(ws),
+                          kv_many_slots_at(a.requests, D)) != cudaSuccess)
     return MX_ERR_CUDA;
   return launch_status();
 }
@@ -71,9 +101,7 @@ mx_status kv_attention_launch(const KvAttnArgs& a, int block_tokens, int64_t max
     case 2: return kv_few_launch<FMT, F16, D, 2>(a, block_tokens, max_q_len, workspace, st);
     case 4: return kv_few_launch<FMT, F16, D, 4>(a, block_tokens, max_q_len, workspace, st);
   }
-  const dim3 grid(static_cast<unsigned>(a.tokens), static_cast<unsigned>(a.heads));
-  if (pdl_launch(kv_attention_rows_kernel<FMT, F16, D>, grid, 128, 0, st, a) != cudaSuccess) return MX_ERR_CUDA;
-  return launch_status();
+  return kv_many_launch<FMT, F16, D>(a, block_tokens, max_q_len, workspace, st);
 }
 
 template <int FMT, bool F16, int D>
@@ -192,7 +220,8 @@ size_t kv_attention_workspace_bytes(int64_t num_tokens, int64_t requests, int64_
   if (num_tokens < 0 || requests < 1 || max_q_len < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads) return 0;
   if (head_dim != 64 && head_dim != 128) return 0;
   const int nt = kv_row_tiles(max_q_len, heads / kv_heads);
-  if (!nt) return 16;
+  if (!nt)
+    return kv_many_slots_at(requests, head_dim) + 2ull * kKvManyMaxCtas * kKvManyRows * (head_dim + 2) * 4;
   return kKvSlotsAt + 2ull * kKvMaxCtas * (8 * nt) * (head_dim + 2) * 4;
 }
 

@@ -139,7 +139,7 @@ constexpr int kKvMaxCtas = 608;
 
 struct KvJob {  // a range of the list, and the unit that it begins in
   long long begin, end, unit;
-  int request, head;
+  int tiles, head, q0, row0, rows, request, q_tile;  // rows row0 .. row0 + rows - 1 of the request's head group
 };
 
 constexpr size_t kKvSlotsAt = sizeof(KvJob) * kKvMaxCtas;  // in the workspace, behind the jobs
@@ -375,7 +375,9 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
   pdl_prologue();
   KvWalk w;
   kv_plan(a, most_q, plan, w);  // (its barriers also publish the mbarriers)
-  if (tid == 0) reinterpret_cast<KvJob*>(workspace)[blockIdx.x] = KvJob{w.pos, w.end, w.base, w.r, w.h};
+  if (tid == 0)
+    reinterpret_cast<KvJob*>(workspace)[blockIdx.x] =
+        KvJob{w.pos, w.end, w.base, w.req.tiles, w.h, w.req.q0, 0, w.req.rows_q * group, w.r, 0};
   kv_clear_rest(a, D, blockIdx.x * kKvFewThreads + tid, gridDim.x * kKvFewThreads);
 
   if (warp == kKvWarps) {
@@ -751,10 +753,10 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
 // Joins the segments of the units that range boundaries cut.  CTA c looks at the boundary where range c
 // begins; the first boundary inside a unit takes the unit.  Segments are added in order: the range that
 // the unit begins in left its one in slot 1, the others in slot 0.
-template <bool F16, int D, int NT>
-__global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int most_q, const uint8_t* workspace) {
+template <bool F16, int D, int ROWS>
+__global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, const uint8_t* workspace, size_t slots_at) {
   pdl_prologue();
-  using Cfg = KvFewCfg<D, NT>;
+  constexpr size_t kSlot = static_cast<size_t>(ROWS) * (D + 2) * 4;
   __shared__ int list[kKvMaxCtas];
   __shared__ int listed;
   const KvJob* jobs = reinterpret_cast<const KvJob*>(workspace);
@@ -762,8 +764,7 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int mo
   const KvJob job = jobs[c];
   const long long before = jobs[c - 1].begin, total = jobs[ranges - 1].end;
   if (job.begin >= total || job.unit == job.begin || before > job.unit) return;
-  const KvRequest req = kv_request(a, job.request, most_q, false);
-  const long long unit_end = job.unit + req.cost();
+  const long long unit_end = job.unit + job.tiles + kKvUnitCost;
   if (threadIdx.x < 32) {
     int n = 0;
     for (int k0 = c - 1; k0 < ranges; k0 += 32) {
@@ -772,8 +773,8 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int mo
       if (k < ranges) {
         const long long b = jobs[k].begin, e = jobs[k].end;
         over = b >= unit_end;
-        const int from = kv_tiles_before(b - job.unit, req.tiles), to = kv_tiles_before(e - job.unit, req.tiles);
-        has = !over && to > from && to - from < req.tiles;  // (a range that has all of it has finished it)
+        const int from = kv_tiles_before(b - job.unit, job.tiles), to = kv_tiles_before(e - job.unit, job.tiles);
+        has = !over && to > from && to - from < job.tiles;  // (a range that has all of it has finished it)
       }
       const uint32_t m = __ballot_sync(0xFFFFFFFFu, has);
       if (has) list[n + __popc(m & ((1u << threadIdx.x) - 1))] = 2 * k + (k == c - 1 ? 1 : 0);
@@ -785,15 +786,15 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int mo
   __syncthreads();
   const int n = listed;
   if (n == 0) return;
-  const int group = a.heads / a.kv_heads, rows = req.rows_q * group;
-  for (int i = threadIdx.x; i < rows * (D / 4); i += 128) {
+  const int group = a.heads / a.kv_heads;
+  for (int i = blockIdx.y * 128 + threadIdx.x; i < job.rows * (D / 4); i += 128 * gridDim.y) {
     const int row = i / (D / 4), d = i % (D / 4) * 4;
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int k = 0; k < n; ++k) {
-      const float* part = reinterpret_cast<const float*>(workspace + kKvSlotsAt + list[k] * Cfg::SLOT);
-      const float2 ml = *reinterpret_cast<const float2*>(part + Cfg::ROWS * D + 2 * row);
+      const float* part = reinterpret_cast<const float*>(workspace + slots_at + list[k] * kSlot);
+      const float2 ml = *reinterpret_cast<const float2*>(part + ROWS * D + 2 * row);
       const float4 x = *reinterpret_cast<const float4*>(part + row * D + d);
       const float most = fmaxf(m, ml.x), ref = most == -INFINITY ? 0.f : most;
       const float f0 = kv_exp2(m - ref), f1 = kv_exp2(ml.x - ref);
@@ -804,8 +805,8 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, int mo
       o.w = o.w * f0 + x.w * f1;
       m = most;
     }
-    const int qi = row / group, hg = row - qi * group;
-    const int64_t at_row = static_cast<int64_t>(req.q0 + qi) * a.heads + job.head * group + hg;
+    const int qi = (job.row0 + row) / group, hg = job.row0 + row - qi * group;
+    const int64_t at_row = static_cast<int64_t>(job.q0 + qi) * a.heads + job.head * group + hg;
     const float inv = 1.f / l;
     *reinterpret_cast<uint2*>(a.out + at_row * D + d) =
         l == 0.f ? make_uint2(0, 0) : make_uint2(kv_pack_out<F16>(o.x * inv, o.y * inv), kv_pack_out<F16>(o.z * inv, o.w * inv));

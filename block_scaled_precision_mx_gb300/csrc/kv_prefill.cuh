@@ -1,0 +1,707 @@
+// kv_prefill.cuh -- attention over the paged 8-bit cache for many query rows a kv head (prompts and
+// their chunks): the products are the bound, so both run on the tensor cores' own memory.
+//
+// A unit is 256 rows (query tokens x query heads of the group) of one request and kv head against the
+// tokens that any of them sees, in tiles of 128.  One CTA a SM, persistent over an equal range of all
+// units' tiles (kv_plan_kernel); a unit cut by a range boundary leaves (O, m, l) and kv_join_kernel
+// joins the pieces, as for few rows.  Roles:
+//
+//   warps 0-3, 4-7   softmax of rows 0-127 and 128-255, a row a thread.  They bring their queries into
+//                    shared memory as FP16 (a power of two for each row, exact to 2^-29 of its largest),
+//                    read S from tensor memory, write the weights back as FP16 over it, and keep m, l.
+//   warps 8-11       codes -> FP16 (exact) in the layout that the products read.
+//   warp 12          TMA: blocks' codes of K and V, tile by tile, and the scales of their 16-token slices.
+//   warp 13          products:  S_w = Q_w K^T (M = 128, N = 128, K = D),  O_w += P_w V (P from tensor memory).
+//
+// The two row halves take turns: while one's softmax runs, the other's products do.  Per tile the
+// products are 4 x 128 x 128 x D, 2048 cycles at D = 128; conversion is 32K codes, each softmax 16K
+// exponentials.  FP16 keeps every code exactly, so the only roundings are the weights' (2^-11) and FP32 sums'.
+// The codes are converted once for 256 rows and the shared-memory traffic of that (read 1, write 2, read 2
+// bytes a code and product) is what 256 rows, not 128, are for.
+//
+// As for few rows: sV is folded into the exponent, and the reference m is renewed only when a score passes
+// it by 8; the rows' O in tensor memory is then rescaled by its own thread, between two products.
+#pragma once
+
+#include "kv_attention.cuh"
+
+namespace mxgb {
+
+constexpr int kKvManyThreads = 512;
+constexpr int kKvManyTile = 128;
+constexpr int kKvManyRows = 256;
+constexpr int kKvManyScales = 8;  // tiles whose scales are kept
+constexpr int kKvPlanThreads = 512;
+constexpr int kKvManyMaxCtas = 160;
+
+template <int D>
+struct KvManyCfg {
+  static constexpr int RAW_SLOTS = 4, F16_SLOTS = 3;
+  static constexpr int RAW = kKvManyTile * D;      // codes of K or V of a tile
+  static constexpr int WIDE = 2 * RAW;             // the same in FP16; also 128 rows of Q
+  static constexpr int OFF_F16 = 2 * WIDE;
+  static constexpr int OFF_RAW = OFF_F16 + F16_SLOTS * WIDE;
+  static constexpr int OFF_SC = OFF_RAW + RAW_SLOTS * RAW;          // float4 [tiles][8 slices]
+  static constexpr int OFF_NAN = OFF_SC + kKvManyScales * 8 * 16;   // int [tiles]
+  static constexpr int OFF_BAR = OFF_NAN + 4 * kKvManyScales;
+  static constexpr int BARS = 2 * RAW_SLOTS + 2 * F16_SLOTS + 4 * 2 + kKvManyScales + 1;
+  static constexpr int SMEM = OFF_BAR + 8 * BARS + 16 + 1024;
+  static constexpr size_t SLOT = static_cast<size_t>(kKvManyRows) * (D + 2) * 4;
+  static constexpr size_t NAN_BYTES = 4 * kKvManyTile * (D / 8);    // u16 [4 tiles][128 tokens][D / 16] a CTA
+};
+
+// workspace: jobs, the requests' places (8 bytes each), NaN notes, segments
+__host__ __device__ constexpr size_t kv_many_nan_at(int64_t requests) {
+  return kKvSlotsAt + static_cast<size_t>((8 * (requests + 1) + 15) / 16 * 16);
+}
+__host__ __device__ constexpr size_t kv_many_slots_at(int64_t requests, int head_dim) {
+  return kv_many_nan_at(requests) + static_cast<size_t>(kKvManyMaxCtas) * 4 * kKvManyTile * (head_dim / 8);
+}
+
+struct KvUnit {
+  int q0, rows_q, len;                // the request
+  int row0, rows;                     // this unit's rows of its head group
+  int first_tile, tiles;
+  int any_lo, all_lo, all_hi;         // tokens from any_lo on are seen by some row; [all_lo, all_hi) by all
+  __device__ __forceinline__ int cost() const { return tiles + kKvUnitCost; }
+};
+
+__device__ __forceinline__ KvUnit kv_unit(const KvAttnArgs& a, const KvRequest& req, int group, int q_tile) {
+  KvUnit u;
+  u.q0 = req.q0;
+  u.rows_q = req.rows_q;
+  u.len = req.len;
+  u.row0 = q_tile * kKvManyRows;
+  u.rows = min(kKvManyRows, req.rows_q * group - u.row0);
+  const int p0 = req.len - req.rows_q + u.row0 / group, p1 = req.len - req.rows_q + (u.row0 + u.rows - 1) / group;
+  u.any_lo = a.window ? max(0, p0 - a.window + 1) : 0;
+  u.all_lo = a.window ? max(0, p1 - a.window + 1) : 0;
+  u.all_hi = a.causal ? min(req.len, p0 + 1) : req.len;
+  const int hi = a.causal ? min(req.len, p1 + 1) : req.len;
+  u.first_tile = u.any_lo / kKvManyTile;
+  u.tiles = max(1, (max(hi, 0) + kKvManyTile - 1) / kKvManyTile - u.first_tile);
+  return u;
+}
+__device__ __forceinline__ int kv_units_of(const KvRequest& req, int group) {
+  return (req.rows_q * group + kKvManyRows - 1) / kKvManyRows;
+}
+
+// Ranges of the list of all units (request by request, then 256 rows by 256 rows, then head by head): one
+// CTA sums the requests' costs, scans them and finds each range's first unit.  A request's units are summed
+// by a thread while they are few, by a warp otherwise.
+__global__ void __launch_bounds__(kKvPlanThreads) kv_plan_kernel(const KvAttnArgs a, int most_q, int ranges,
+                                                                 uint8_t* workspace) {
+  pdl_prologue();
+  __shared__ long long warp_sum[kKvPlanThreads / 32];
+  long long* place = reinterpret_cast<long long*>(workspace + kKvSlotsAt);  // [requests + 1]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = a.heads / a.kv_heads;
+  if (static_cast<long long>(most_q) * group <= 8 * kKvManyRows) {
+    for (int r = tid; r < a.requests; r += kKvPlanThreads) {
+      const KvRequest req = kv_request(a, r, most_q, true);
+      const int units = kv_units_of(req, group);
+      long long sum = 0;
+      for (int i = 0; i < units; ++i) sum += kv_unit(a, req, group, i).cost();
+      place[r] = sum * a.kv_heads;
+    }
+  } else {
+    for (int r = warp; r < a.requests; r += kKvPlanThreads / 32) {
+      const KvRequest req = kv_request(a, r, most_q, lane == 0);
+      const int units = kv_units_of(req, group);
+      long long sum = 0;
+      for (int i = lane; i < units; i += 32) sum += kv_unit(a, req, group, i).cost();
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+      if (lane == 0) place[r] = sum * a.kv_heads;
+    }
+  }
+  __syncthreads();
+  const int per = (a.requests + kKvPlanThreads - 1) / kKvPlanThreads;
+  const int r0 = min(tid * per, a.requests), r1 = min(r0 + per, a.requests);
+  long long mine = 0;
+  for (int r = r0; r < r1; ++r) mine += place[r];
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  long long at = incl - mine, total = 0;
+  for (int i = 0; i < kKvPlanThreads / 32; ++i) {
+    if (i < warp) at += warp_sum[i];
+    total += warp_sum[i];
+  }
+  for (int r = r0; r < r1; ++r) {
+    const long long c = place[r];
+    place[r] = at;
+    at += c;
+  }
+  if (tid == 0) place[a.requests] = total;
+  __syncthreads();
+  KvJob* jobs = reinterpret_cast<KvJob*>(workspace);
+  for (int c = tid; c < ranges; c += kKvPlanThreads) {
+    KvJob job{kv_cut(total, c, ranges), kv_cut(total, c + 1, ranges), 0, 0, 0, 0, 0, 0, 0, 0};
+    if (job.begin < total) {
+      int lo = 0, hi = a.requests;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (place[mid] <= job.begin) lo = mid;
+        else hi = mid;
+      }
+      const KvRequest req = kv_request(a, lo, most_q, false);
+      long long x = place[lo];
+      for (int q_tile = 0;; ++q_tile) {
+        const KvUnit u = kv_unit(a, req, group, q_tile);
+        const long long all = static_cast<long long>(u.cost()) * a.kv_heads;
+        if (job.begin < x + all) {
+          job.head = static_cast<int>((job.begin - x) / u.cost());
+          job.unit = x + static_cast<long long>(job.head) * u.cost();
+          job.tiles = u.tiles;
+          job.q0 = u.q0;
+          job.row0 = u.row0;
+          job.rows = u.rows;
+          job.request = lo;
+          job.q_tile = q_tile;
+          break;
+        }
+        x += all;
+      }
+    }
+    jobs[c] = job;
+  }
+}
+
+struct KvManyWalk {
+  long long pos, end, base;
+  int r, h, q_tile;
+  KvRequest req;
+  KvUnit u;
+  int tile, count;  // the current segment
+};
+__device__ __forceinline__ void kv_many_begin(const KvAttnArgs& a, int most_q, int group, const KvJob& job, KvManyWalk& w) {
+  w.pos = job.begin;
+  w.end = job.end;
+  w.base = job.unit;
+  w.r = job.request;
+  w.h = job.head;
+  w.q_tile = job.q_tile;
+  if (w.pos < w.end) {
+    w.req = kv_request(a, w.r, most_q, false);
+    w.u = kv_unit(a, w.req, group, w.q_tile);
+  }
+}
+__device__ __forceinline__ bool kv_many_next(const KvAttnArgs& a, int most_q, int group, KvManyWalk& w) {
+  while (w.pos < w.end) {
+    const long long unit_end = w.base + w.u.cost();
+    if (w.pos == unit_end) {
+      w.base = unit_end;
+      if (++w.h == a.kv_heads) {
+        w.h = 0;
+        if (++w.q_tile >= kv_units_of(w.req, group)) {
+          w.q_tile = 0;
+          do {
+            if (++w.r >= a.requests) return false;
+            w.req = kv_request(a, w.r, most_q, false);
+          } while (w.req.rows_q == 0);
+        }
+        w.u = kv_unit(a, w.req, group, w.q_tile);
+      }
+      continue;
+    }
+    const long long to = min(w.end, unit_end);
+    w.tile = kv_tiles_before(w.pos - w.base, w.u.tiles);
+    w.count = kv_tiles_before(to - w.base, w.u.tiles) - w.tile;
+    w.pos = to;
+    if (w.count) return true;
+  }
+  return false;
+}
+
+// kind::f16: FP16 operands, FP32 accumulator; B K-major or N-major
+__host__ __device__ constexpr uint32_t kv_idesc_f16(uint32_t M, uint32_t N, bool b_n_major) {
+  return (1u << 4) | (b_n_major ? 1u << 16 : 0u) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+__device__ __forceinline__ void umma_f16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void kv_regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void kv_regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
+__device__ __forceinline__ uint64_t kv_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+template <int FMT, bool F16, int D>
+__global__ void __launch_bounds__(kKvManyThreads, 1)
+    kv_attention_many_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                             const KvAttnArgs a, int most_q, uint8_t* workspace) {
+  using Cfg = KvManyCfg<D>;
+  extern __shared__ uint8_t kv_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(kv_smem_raw) + 1023) & ~uintptr_t(1023));
+  float4* sSC = reinterpret_cast<float4*>(smem + Cfg::OFF_SC);
+  volatile int* sNan = reinterpret_cast<volatile int*>(smem + Cfg::OFF_NAN);
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);
+  uint64_t* raw_empty = raw_full + Cfg::RAW_SLOTS;
+  uint64_t* f_full = raw_empty + Cfg::RAW_SLOTS;
+  uint64_t* f_empty = f_full + Cfg::F16_SLOTS;
+  uint64_t* q_full = f_empty + Cfg::F16_SLOTS;  // [2] each
+  uint64_t* s_full = q_full + 2;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = p_full + 2;
+  uint64_t* sc_full = o_full + 2;               // [kKvManyScales]
+  uint64_t* drain_bar = sc_full + kKvManyScales;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int group = a.heads / a.kv_heads;
+  if (tid == 0) {
+    for (int i = 0; i < Cfg::RAW_SLOTS; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 4);
+    }
+    for (int i = 0; i < Cfg::F16_SLOTS; ++i) {
+      mbar_init(&f_full[i], 4);
+      mbar_init(&f_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 128);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&o_full[i], 1);
+    }
+    for (int i = 0; i < kKvManyScales; ++i) mbar_init(&sc_full[i], 1);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+  }
+  if (warp == 13) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_prologue();
+  KvManyWalk w;
+  kv_many_begin(a, most_q, group, reinterpret_cast<const KvJob*>(workspace)[blockIdx.x], w);
+  const long long range_start = w.pos;
+  kv_clear_rest(a, D, blockIdx.x * kKvManyThreads + tid, gridDim.x * kKvManyThreads);
+  uint8_t* nan_notes = workspace + kv_many_nan_at(a.requests) + blockIdx.x * Cfg::NAN_BYTES;
+
+  if (warp >= 12) {
+    kv_regs_less<56>();
+    if (warp == 12) {
+      // ---------------------------------------------------------------- loads: item 2i = K, 2i + 1 = V of tile i
+      const int P = 1 << a.shift, rows_box = min(P, kKvTile), boxes = kKvManyTile / rows_box;
+      const int most_tiles = 32 * P / kKvManyTile;
+      uint32_t tiles_done = 0;
+      bool ok = true;
+      while (ok && kv_many_next(a, most_q, group, w)) {
+        for (int i0 = 0; i0 < w.count && ok; i0 += most_tiles) {  // up to 32 blocks at a time
+          const int n = min(most_tiles, w.count - i0), token0 = (w.u.first_tile + w.tile + i0) * kKvManyTile;
+          const int page = (token0 >> a.shift) + lane;
+          int block = -1;
+          float sk = 1.f, sv = 1.f;
+          if (page << a.shift < w.u.len) {
+            block = a.tables[static_cast<int64_t>(w.r) * a.max_blocks + page];
+            if (block < 0 || block >= a.num_blocks) {
+              atomicOr(&g_mx_error_word, kSiteBadCache);
+              block = -1;
+            } else {
+              const int64_t at = static_cast<int64_t>(block) * a.kv_heads + w.h;
+              sk = a.k_scale[at];
+              sv = a.v_scale[at];
+            }
+          }
+          for (int i = 0; i < n && ok; ++i, ++tiles_done) {
+            const int token = token0 + i * kKvManyTile, from = (token - token0) >> a.shift;
+            const int my = token + lane * rows_box;
+            const int box_block = __shfl_sync(0xFFFFFFFFu, block, min((my - token0) >> a.shift, 31));
+            const bool load = lane < boxes && box_block >= 0;
+            const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, load)) * rows_box * D;
+            const int slice = ((lane & 7) * 16) >> a.shift;
+            const float slice_k = __shfl_sync(0xFFFFFFFFu, sk, from + slice), slice_v = __shfl_sync(0xFFFFFFFFu, sv, from + slice);
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t item = 2 * tiles_done + half, slot = item % Cfg::RAW_SLOTS;
+              if (!mbar_wait(&raw_empty[slot], ((item / Cfg::RAW_SLOTS) & 1) ^ 1, abort_flag, kSiteProducerEmpty)) {
+                ok = false;
+                break;
+              }
+              if (lane == 0) mbar_arrive_expect_tx(&raw_full[slot], bytes);
+              __syncwarp();
+              if (load)
+                tma_load_2d(smem + Cfg::OFF_RAW + slot * Cfg::RAW + lane * rows_box * D, half ? &tmV : &tmK, &raw_full[slot], 0,
+                            ((box_block * a.kv_heads + w.h) << a.shift) + (my & (P - 1)));
+              if (half == 0) {
+                const uint32_t st = tiles_done % kKvManyScales;
+                if (lane < 8) sSC[st * 8 + lane] = make_float4(slice_k, log2f(slice_v), 1.f / slice_v, 0.f);
+                if (lane == 0) sNan[st] = 0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sc_full[st]);
+              }
+            }
+          }
+        }
+      }
+      // every copy has landed before the CTA's shared memory goes
+      const uint32_t items = 2 * tiles_done;
+      for (uint32_t i = 0; i < Cfg::RAW_SLOTS; ++i)
+        if (items > i)
+          mbar_drain(&raw_full[i], ((items - 1 - i) / Cfg::RAW_SLOTS) & 1, kWaitBudgetNs);
+    } else if (warp == 13 && lane == 0) {
+      // ---------------------------------------------------------------- products
+      constexpr uint32_t kHi = smem_desc_hi(1024, kSwizzle128B);
+      constexpr uint32_t kLoK = smem_desc_lo_lbo(16), kLoN = smem_desc_lo_lbo(kKvManyTile * 128);
+      constexpr uint32_t kIdS = kv_idesc_f16(128, kKvManyTile, false), kIdO = kv_idesc_f16(128, D, true);
+      const uint32_t q_lo = smem_u32(smem) >> 4, f_lo = smem_u32(smem + Cfg::OFF_F16) >> 4;
+      uint32_t tiles_done = 0, segments[2] = {0, 0}, weights[2] = {0, 0};
+      bool ok = true;
+      auto scores = [&](int h, uint32_t item) {  // S_h = Q_h K^T
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t at = (k / 4) * (kKvManyTile * 128 / 16) + (k % 4) * 2;
+          umma_f16_ss(tmem + h * 128, desc_from_words((q_lo + h * (Cfg::WIDE / 16) + at) | kLoK, kHi),
+                      desc_from_words((f_lo + (item % Cfg::F16_SLOTS) * (Cfg::WIDE / 16) + at) | kLoK, kHi), kIdS, k > 0);
+        }
+        umma_commit(&s_full[h]);
+      };
+      while (ok && kv_many_next(a, most_q, group, w)) {
+        const int halves = w.u.rows > 128 ? 2 : 1;
+        const uint32_t t0 = tiles_done;
+        uint32_t item = 2 * t0;
+        ok = mbar_wait(&f_full[item % Cfg::F16_SLOTS], (item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteMmaFull);
+        for (int h = 0; h < halves && ok; ++h) {
+          ok = mbar_wait(&q_full[h], segments[h]++ & 1, abort_flag, kSiteMmaFull);
+          tc_fence_after();
+          if (ok) scores(h, item);
+        }
+        if (!ok) break;
+        umma_commit(&f_empty[item % Cfg::F16_SLOTS]);
+        for (int i = 0; i < w.count && ok; ++i) {
+          const uint32_t v_item = 2 * (t0 + i) + 1, k_item = v_item + 1;
+          const uint32_t v_lo = f_lo + (v_item % Cfg::F16_SLOTS) * (Cfg::WIDE / 16);
+          const bool more = i + 1 < w.count;
+          ok = mbar_wait(&f_full[v_item % Cfg::F16_SLOTS], (v_item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteMmaFull);
+          for (int h = 0; h < halves && ok; ++h) {
+            ok = mbar_wait(&p_full[h], weights[h]++ & 1, abort_flag, kSiteMmaTmemEmpty);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < kKvManyTile / 16; ++k)  // O_h += P_h V, 16 tokens at a time
+              umma_f16_ts(tmem + 256 + h * 128, tmem + h * 128 + k * 8, desc_from_words((v_lo + k * (16 * 128 / 16)) | kLoN, kHi),
+                          kIdO, i > 0 || k > 0);
+            if (h == halves - 1) umma_commit(&f_empty[v_item % Cfg::F16_SLOTS]);
+            if (!more) {
+              umma_commit(&o_full[h]);
+              continue;
+            }
+            if (h == 0) {
+              ok = mbar_wait(&f_full[k_item % Cfg::F16_SLOTS], (k_item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteMmaFull);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            scores(h, k_item);
+            if (h == halves - 1) umma_commit(&f_empty[k_item % Cfg::F16_SLOTS]);
+          }
+        }
+        tiles_done += w.count;
+      }
+      // every product has ended before the tensor memory goes
+      umma_commit(drain_bar);
+      mbar_drain(drain_bar, 0, kWaitBudgetNs);
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------------ codes -> FP16
+    kv_regs_less<88>();
+    constexpr int CH = D / 16;        // 16-code words of a token
+    constexpr int N = CH;             // words a lane takes of an item: 32 rows x CH / 32 lanes
+    const int wq = warp - 8, tl = lane & 7;
+    uint32_t tiles_done = 0;
+    bool ok = true;
+    while (ok && kv_many_next(a, most_q, group, w)) {
+      for (int i = 0; i < w.count && ok; ++i, ++tiles_done) {
+        const int token = (w.u.first_tile + w.tile + i) * kKvManyTile;
+        const bool edge = token < w.u.all_lo || token + kKvManyTile > w.u.all_hi;
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t item = 2 * tiles_done + half, slot = item % Cfg::RAW_SLOTS, fs = item % Cfg::F16_SLOTS;
+          ok = mbar_wait(&raw_full[slot], (item / Cfg::RAW_SLOTS) & 1, abort_flag, kSiteMmaFull) &&
+               mbar_wait(&f_empty[fs], ((item / Cfg::F16_SLOTS) & 1) ^ 1, abort_flag, kSiteProducerEmpty);
+          if (!ok) break;
+          const uint8_t* src = smem + Cfg::OFF_RAW + slot * Cfg::RAW;
+          uint8_t* dst = smem + Cfg::OFF_F16 + fs * Cfg::WIDE;
+          uint4 x[N];
+#pragma unroll
+          for (int n = 0; n < N; ++n) {
+            const int row = 32 * wq + 8 * (n / (CH / 4)) + tl, word = (n % (CH / 4)) * 4 + (lane >> 3);
+            const int at = D == 128 ? row * 128 + ((word ^ (row & 7)) << 4) : row * 64 + ((word ^ ((row >> 1) & 3)) << 4);
+            x[n] = *reinterpret_cast<const uint4*>(src + at);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&raw_empty[slot]);
+          if (half && edge) {  // clear what no row sees; take NaN codes out and note them
+            uint32_t any = 0;
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+              const int row = 32 * wq + 8 * (n / (CH / 4)) + tl, word = (n % (CH / 4)) * 4 + (lane >> 3);
+              const bool out = token + row < w.u.any_lo || token + row >= w.u.len;
+              uint32_t c[4] = {x[n].x, x[n].y, x[n].z, x[n].w}, bits = 0;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if (out) c[j] = 0;
+                const uint32_t y = kv_nan_bytes<FMT>(c[j]);
+                c[j] &= ~((y >> 7) * 0xFFu);
+                bits |= ((y >> 7 & 1) | (y >> 14 & 2) | (y >> 21 & 4) | (y >> 28 & 8)) << (4 * j);
+              }
+              x[n] = make_uint4(c[0], c[1], c[2], c[3]);
+              reinterpret_cast<uint16_t*>(nan_notes)[((tiles_done & 3) * kKvManyTile + row) * CH + word] =
+                  static_cast<uint16_t>(bits);
+              any |= bits;
+            }
+            if (any) sNan[tiles_done % kKvManyScales] = 1;
+            __threadfence_block();
+          }
+#pragma unroll
+          for (int n = 0; n < N; ++n) {
+            const int row = 32 * wq + 8 * (n / (CH / 4)) + tl, word = (n % (CH / 4)) * 4 + (lane >> 3);
+            const uint32_t c[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+            uint32_t f[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              f[2 * j] = kv_codes_to_f16x2<FMT>(c[j] & 0xFFFFu);
+              f[2 * j + 1] = kv_codes_to_f16x2<FMT>(c[j] >> 16);
+            }
+            uint8_t* to = dst + (word >> 2) * (kKvManyTile * 128) + row * 128;
+            const int ch = (word & 3) * 2;
+            *reinterpret_cast<uint4*>(to + ((ch ^ (row & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
+            *reinterpret_cast<uint4*>(to + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&f_full[fs]);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax, a row a thread
+    kv_regs_more<184>();
+    const int half = warp >> 2, row = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + half * 128 + lanes, tO = tmem + 256 + half * 128 + lanes;
+    uint8_t* sQ = smem + half * Cfg::WIDE;
+    uint32_t tiles_done = 0, my_tiles = 0, segments = 0;
+    bool ok = true;
+    while (ok && kv_many_next(a, most_q, group, w)) {
+      if (half && w.u.rows <= 128) {
+        tiles_done += w.count;
+        continue;
+      }
+      const int my_row = 128 * half + row;
+      const bool live = my_row < w.u.rows;
+      const int qi = (w.u.row0 + my_row) / group, hg = w.u.row0 + my_row - qi * group;
+      const int p = w.u.len - w.u.rows_q + qi;
+      const int lo = a.window ? p - a.window + 1 : 0, hi = a.causal ? min(w.u.len, p + 1) : w.u.len;
+      float row_mul;
+      {
+        uint4 x[D / 8];
+        const uint16_t* src = a.q + (w.u.q0 + qi) * a.stride_t + (w.h * group + hg) * a.stride_h;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) x[i] = live ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 y = kv_unpack2<F16>(u[j]);
+            amax = fmaxf(amax, fmaxf(fabsf(y.x), fabsf(y.y)));
+          }
+        }
+        // 2^e with amax 2^e in [2^14, 2^15)
+        const int e = min(14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127), 120);
+        const float mul = amax > 0.f ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : 1.f;
+        row_mul = a.scale_log2 / mul;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t f[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 y = kv_unpack2<F16>(u[j]);
+            f[j] = kv_pack_f16(y.x * mul, y.y * mul);
+          }
+          *reinterpret_cast<uint4*>(sQ + (i >> 3) * (128 * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4)) =
+              make_uint4(f[0], f[1], f[2], f[3]);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&q_full[half]);
+      }
+      float m = -INFINITY, l = 0.f;
+      uint32_t nan_d[D / 32];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) nan_d[i] = 0;
+      for (int i = 0; i < w.count; ++i, ++tiles_done, ++my_tiles) {
+        const int token = (w.u.first_tile + w.tile + i) * kKvManyTile;
+        const uint32_t st = tiles_done % kKvManyScales;
+        ok = mbar_wait(&sc_full[st], (tiles_done / kKvManyScales) & 1, abort_flag, kSiteEpiTmemFull) &&
+             mbar_wait(&s_full[half], my_tiles & 1, abort_flag, kSiteEpiTmemFull);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tmem_ld_32x32b_x32(tS + 32 * j, s[j]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tmem_regs_ready(s[j]);
+        const bool edge = token < w.u.all_lo || token + kKvManyTile > w.u.all_hi;
+        if (edge) {
+#pragma unroll
+          for (int j = 0; j < 128; ++j)
+            if (token + j < lo || token + j >= hi) s[j / 32][j % 32] = 0xFF800000u;
+        }
+        float most = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          float x = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) x = fmaxf(x, __uint_as_float(s[g / 2][(g & 1) * 16 + j]));
+          const float4 sc = sSC[st * 8 + g];
+          most = fmaxf(most, fmaf(x, row_mul * sc.x, sc.y));
+        }
+        const bool past = most > m + 8.f;
+        if (__any_sync(0xFFFFFFFFu, past)) {
+          const float to = past ? most : m;
+          const float keep = kv_exp2(m - (to == -INFINITY ? 0.f : to));
+          m = to;
+          l *= keep;
+          if (i > 0) {
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              uint32_t o[16];
+              tmem_ld_32x32b_x16(tO + 16 * j, o);
+              tmem_ld_wait();
+              tmem_regs_ready16(o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * (past ? keep : 1.f));
+              tmem_st_32x32b_x16(tO + 16 * j, o);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int g = 0; g < 8; g += 2) {
+          uint32_t packed[16];
+#pragma unroll
+          for (int gg = 0; gg < 2; ++gg) {
+            const float4 sc = sSC[st * 8 + g + gg];
+            const float mul = row_mul * sc.x, add = sc.y - ref;
+            const uint64_t mul2 = pack_f32x2(mul, mul), add2 = pack_f32x2(add, add);
+            float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t* x = &s[g / 2][gg * 16 + 2 * j];
+              float z0, z1;
+              unpack_f32x2(kv_fma2(pack_f32x2(__uint_as_float(x[0]), __uint_as_float(x[1])), mul2, add2), z0, z1);
+              const float p0 = kv_exp2(z0), p1 = kv_exp2(z1);
+              sum0 += p0;
+              sum1 += p1;
+              packed[gg * 8 + j] = kv_pack_f16(p0, p1);
+            }
+            l = fmaf(sum0 + sum1, sc.z, l);
+          }
+          tmem_st_32x32b_x16(tS + g * 8, packed);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        if (edge) {  // NaN codes of V in tokens that this row sees
+          const uint32_t v_item = 2 * tiles_done + 1;
+          ok = mbar_wait(&f_full[v_item % Cfg::F16_SLOTS], (v_item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteEpiTmemFull);
+          if (!ok) break;
+          if (sNan[st]) {
+            const int j0 = max(lo - token, 0), j1 = min(hi - token, kKvManyTile);
+            for (int j = j0; j < j1; ++j) {
+              const volatile uint32_t* note =
+                  reinterpret_cast<const volatile uint32_t*>(nan_notes + ((tiles_done & 3) * kKvManyTile + j) * (D / 8));
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k) nan_d[k] |= note[k];
+            }
+          }
+        }
+        mbar_arrive(&p_full[half]);
+      }
+      if (!ok) break;
+      ok = mbar_wait(&o_full[half], segments++ & 1, abort_flag, kSiteEpiTmemFull);
+      if (!ok) break;
+      tc_fence_after();
+      const bool whole = w.count == w.u.tiles;
+      const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+      const int64_t at_row = static_cast<int64_t>(w.u.q0 + qi) * a.heads + w.h * group + hg;
+      float* part = reinterpret_cast<float*>(workspace + kv_many_slots_at(a.requests, D) +
+                                             (2 * blockIdx.x + (w.base < range_start ? 0 : 1)) * Cfg::SLOT);
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(tO + 32 * j, o);
+        tmem_ld_wait();
+        tmem_regs_ready(o);
+        float f[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) f[k] = l == 0.f ? 0.f : __uint_as_float(o[k]) * inv;
+        if (nan_d[j]) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (nan_d[j] >> k & 1) f[k] = NAN;
+        }
+        if (live && whole) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(a.out + at_row * D + 32 * j + 8 * k) =
+                make_uint4(kv_pack_out<F16>(f[8 * k], f[8 * k + 1]), kv_pack_out<F16>(f[8 * k + 2], f[8 * k + 3]),
+                           kv_pack_out<F16>(f[8 * k + 4], f[8 * k + 5]), kv_pack_out<F16>(f[8 * k + 6], f[8 * k + 7]));
+        } else if (live) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<float4*>(part + my_row * D + 32 * j + 4 * k) =
+                make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
+        }
+      }
+      if (live && whole) a.lse[at_row] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
+      else if (live) *reinterpret_cast<float2*>(part + kKvManyRows * D + 2 * my_row) = make_float2(m, l);
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 13) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace mxgb

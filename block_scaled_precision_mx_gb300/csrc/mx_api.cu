@@ -17,6 +17,7 @@
 #include "mx_quantize.cuh"
 #include "kv_attention.cuh"
 #include "kv_cache.cuh"
+#include "kv_prefill.cuh"
 
 using namespace mxgb;
 

@@ -4,6 +4,9 @@
 
 namespace {
 
+// tokens of a call, of a request and of a window: sums and differences of two stay within 32 bits
+constexpr int64_t kKvMostTokens = 1 << 30;
+
 // 2^shift tokens a block, for 16, 32, 64 or 128; -1 otherwise
 int kv_block_shift(int block_tokens) {
   return block_tokens == 16 ? 4 : block_tokens == 32 ? 5 : block_tokens == 64 ? 6 : block_tokens == 128 ? 7 : -1;
@@ -121,9 +124,9 @@ mx_status kv_block_tables(int32_t* block_tables, int64_t requests, int64_t max_b
   const int shift = kv_block_shift(block_tokens);
   if (!block_tables || !len_before || !len_after || !free_list || !free_count || !q_start || !info || shift < 0)
     return MX_ERR_INVALID_ARG;
-  if (num_tokens < 0 || num_tokens > 0x7FFFFFFF - 1024 || (num_tokens && (!slot_map || !positions)))
+  if (num_tokens < 0 || num_tokens > kKvMostTokens || (num_tokens && (!slot_map || !positions)))
     return MX_ERR_INVALID_ARG;
-  if (requests < 1 || requests > kKvMaxRequests || max_blocks < 1 || max_blocks > (0x7FFFFFFFll >> shift) - 1 ||
+  if (requests < 1 || requests > kKvMaxRequests || max_blocks < 1 || max_blocks > (kKvMostTokens >> shift) ||
       free_capacity < 1 || free_capacity > 0x7FFFFFFF)
     return MX_ERR_INVALID_ARG;
   if (!aligned(block_tables, 4) || !aligned(len_before, 4) || !aligned(len_after, 4) || !aligned(free_list, 4) ||
@@ -167,7 +170,7 @@ mx_status kv_cache_append(const void* k, const void* v, mx_half type, int64_t nu
                           const int64_t* slot_map, void* k_codes, void* v_codes, float* k_scale, float* v_scale,
                           mx_elem elem, int64_t num_blocks, int64_t kv_heads, int block_tokens, int head_dim,
                           void* stream) {
-  if (num_tokens < 0 || num_tokens > 0x7FFFFFFF - 1024) return MX_ERR_INVALID_ARG;
+  if (num_tokens < 0 || num_tokens > kKvMostTokens) return MX_ERR_INVALID_ARG;
   if (!k_codes || !v_codes || !k_scale || !v_scale || (num_tokens && (!k || !v || !slot_map))) return MX_ERR_INVALID_ARG;
   if (type != MX_HALF_BF16 && type != MX_HALF_F16) return MX_ERR_INVALID_ARG;
   if (elem != MX_E4M3 && elem != MX_E5M2) return elem == MX_E2M1 ? MX_ERR_UNSUPPORTED : MX_ERR_INVALID_ARG;
@@ -231,7 +234,7 @@ mx_status kv_attention(const void* q, mx_half type, int64_t num_tokens, int64_t 
                        int head_dim, const int32_t* block_tables, int64_t max_blocks, const int32_t* lengths,
                        const int32_t* q_start, int64_t requests, int64_t max_q_len, float softmax_scale, int causal,
                        int64_t window, void* out, float* lse, void* workspace, void* stream) {
-  if (num_tokens < 0 || num_tokens > 0x7FFFFFFF - 1024 || requests < 1 || requests > kKvMaxRequests)
+  if (num_tokens < 0 || num_tokens > kKvMostTokens || requests < 1 || requests > kKvMaxRequests)
     return MX_ERR_INVALID_ARG;
   if (!k_codes || !v_codes || !k_scale || !v_scale || !block_tables || !lengths || !q_start || !workspace ||
       (num_tokens && (!q || !out || !lse)))
@@ -240,7 +243,7 @@ mx_status kv_attention(const void* q, mx_half type, int64_t num_tokens, int64_t 
   if (elem != MX_E4M3 && elem != MX_E5M2) return elem == MX_E2M1 ? MX_ERR_UNSUPPORTED : MX_ERR_INVALID_ARG;
   if (!kv_cache_shape_ok(num_blocks, kv_heads, block_tokens, head_dim)) return MX_ERR_INVALID_ARG;
   if (heads < 1 || heads > 65535 || heads % kv_heads) return MX_ERR_INVALID_ARG;
-  if (max_blocks < 1 || max_blocks > 0x7FFFFFFFll / block_tokens - 1) return MX_ERR_INVALID_ARG;
+  if (max_blocks < 1 || max_blocks > kKvMostTokens / block_tokens) return MX_ERR_INVALID_ARG;
   if (max_q_len < 0 || max_q_len > num_tokens || window < 0 || window > 0x7FFFFFFF) return MX_ERR_INVALID_ARG;
   if (causal != 0 && causal != 1) return MX_ERR_INVALID_ARG;
   if (!(softmax_scale > 0.f) || softmax_scale > 1e30f) return MX_ERR_INVALID_ARG;
@@ -272,7 +275,7 @@ mx_status kv_attention(const void* q, mx_half type, int64_t num_tokens, int64_t 
   a.max_blocks = static_cast<int>(max_blocks);
   a.shift = kv_block_shift(block_tokens);
   a.causal = causal;
-  a.window = static_cast<int>(window);
+  a.window = static_cast<int>(window < kKvMostTokens ? window : kKvMostTokens);
   cudaStream_t st = as_stream(stream);
   const bool f16 = type == MX_HALF_F16, d64 = head_dim == 64, e5 = elem == MX_E5M2;
 #define KV_ATTN(FMT, H, D) kv_attention_launch<FMT, H, D>(a, block_tokens, max_q_len, workspace, st)

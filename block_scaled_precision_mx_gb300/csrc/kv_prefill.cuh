@@ -34,6 +34,17 @@ constexpr int kKvManyScales = 8;  // tiles whose scales are kept
 constexpr int kKvPlanThreads = 512;
 constexpr int kKvManyMaxCtas = 160;
 
+// A segment as the loading warp tells the others of it; count = 0: no more.
+struct alignas(16) KvSegment {
+  int count, token;           // tiles, and the first one's first token
+  int rows, row0, q0, rows_q; // as in KvUnit
+  int len, any_lo, all_lo, all_hi;
+  int head;
+  int part;                   // 0: the whole unit; 1 + slot: a part of it
+};
+static_assert(sizeof(KvSegment) <= 64, "a segment's place in shared memory");
+constexpr int kKvManySegments = 4;
+
 template <int D>
 struct KvManyCfg {
   static constexpr int RAW_SLOTS = 4, F16_SLOTS = 3;
@@ -44,8 +55,9 @@ struct KvManyCfg {
   static constexpr int OFF_SC = OFF_RAW + RAW_SLOTS * RAW;          // float4 [tiles][8 slices]
   static constexpr int OFF_NAN = OFF_SC + kKvManyScales * 8 * 16;   // int [tiles]
   static constexpr int OFF_BAR = OFF_NAN + 4 * kKvManyScales;
-  static constexpr int BARS = 2 * RAW_SLOTS + 2 * F16_SLOTS + 4 * 2 + kKvManyScales + 1;
-  static constexpr int SMEM = OFF_BAR + 8 * BARS + 16 + 1024;
+  static constexpr int BARS = 2 * RAW_SLOTS + 2 * F16_SLOTS + 4 * 2 + kKvManyScales + 2 * kKvManySegments + 1;
+  static constexpr int OFF_SEG = (OFF_BAR + 8 * BARS + 15) / 16 * 16;  // KvSegment [segments]
+  static constexpr int SMEM = OFF_SEG + 64 * kKvManySegments + 16 + 1024;
   static constexpr size_t SLOT = static_cast<size_t>(kKvManyRows) * (D + 2) * 4;
   static constexpr size_t NAN_BYTES = 4 * kKvManyTile * (D / 8);    // u16 [4 tiles][128 tokens][D / 16] a CTA
 };
@@ -246,14 +258,22 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void kv_regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void kv_regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+// one thread of a converged warp
+__device__ __forceinline__ bool kv_elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+  return p != 0;
+}
 
 __device__ __forceinline__ uint64_t kv_fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+__device__ __forceinline__ uint64_t kv_add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 
@@ -266,6 +286,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(kv_smem_raw) + 1023) & ~uintptr_t(1023));
   float4* sSC = reinterpret_cast<float4*>(smem + Cfg::OFF_SC);
   volatile int* sNan = reinterpret_cast<volatile int*>(smem + Cfg::OFF_NAN);
+  KvSegment* sSeg = reinterpret_cast<KvSegment*>(smem + Cfg::OFF_SEG);
   uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);
   uint64_t* raw_empty = raw_full + Cfg::RAW_SLOTS;
   uint64_t* f_full = raw_empty + Cfg::RAW_SLOTS;
@@ -275,10 +296,12 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
   uint64_t* p_full = s_full + 2;
   uint64_t* o_full = p_full + 2;
   uint64_t* sc_full = o_full + 2;               // [kKvManyScales]
-  uint64_t* drain_bar = sc_full + kKvManyScales;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  uint64_t* seg_full = sc_full + kKvManyScales; // [kKvManySegments]
+  uint64_t* seg_empty = seg_full + kKvManySegments;
+  uint64_t* drain_bar = seg_empty + kKvManySegments;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_SEG + 64 * kKvManySegments);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
   const int group = a.heads / a.kv_heads;
   if (tid == 0) {
     for (int i = 0; i < Cfg::RAW_SLOTS; ++i) {
@@ -290,12 +313,16 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
       mbar_init(&f_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 128);
+      mbar_init(&q_full[i], 4);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
+      mbar_init(&p_full[i], 4);
       mbar_init(&o_full[i], 1);
     }
     for (int i = 0; i < kKvManyScales; ++i) mbar_init(&sc_full[i], 1);
+    for (int i = 0; i < kKvManySegments; ++i) {
+      mbar_init(&seg_full[i], 1);
+      mbar_init(&seg_empty[i], 13);  // warps 0-11 and 13
+    }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -309,189 +336,212 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   pdl_prologue();
-  KvManyWalk w;
-  kv_many_begin(a, most_q, group, reinterpret_cast<const KvJob*>(workspace)[blockIdx.x], w);
-  const long long range_start = w.pos;
   kv_clear_rest(a, D, blockIdx.x * kKvManyThreads + tid, gridDim.x * kKvManyThreads);
   uint8_t* nan_notes = workspace + kv_many_nan_at(a.requests) + blockIdx.x * Cfg::NAN_BYTES;
 
-  if (warp >= 12) {
-    kv_regs_less<56>();
-    if (warp == 12) {
-      // ---------------------------------------------------------------- loads: item 2i = K, 2i + 1 = V of tile i
-      const int P = 1 << a.shift, rows_box = min(P, kKvTile), boxes = kKvManyTile / rows_box;
-      const int most_tiles = 32 * P / kKvManyTile;
-      uint32_t tiles_done = 0;
-      bool ok = true;
-      while (ok && kv_many_next(a, most_q, group, w)) {
-        for (int i0 = 0; i0 < w.count && ok; i0 += most_tiles) {  // up to 32 blocks at a time
-          const int n = min(most_tiles, w.count - i0), token0 = (w.u.first_tile + w.tile + i0) * kKvManyTile;
-          const int page = (token0 >> a.shift) + lane;
-          int block = -1;
-          float sk = 1.f, sv = 1.f;
-          if (page << a.shift < w.u.len) {
-            block = a.tables[static_cast<int64_t>(w.r) * a.max_blocks + page];
-            if (block < 0 || block >= a.num_blocks) {
-              atomicOr(&g_mx_error_word, kSiteBadCache);
-              block = -1;
-            } else {
-              const int64_t at = static_cast<int64_t>(block) * a.kv_heads + w.h;
-              sk = a.k_scale[at];
-              sv = a.v_scale[at];
-            }
+  // the next segment, for every warp but the loading one; false at the end
+  uint32_t seg = 0;
+  auto next_segment = [&](KvSegment& v) {
+    const uint32_t i = seg % kKvManySegments;
+    const bool ok = mbar_wait(&seg_full[i], (seg / kKvManySegments) & 1, abort_flag, kSiteMmaFull);
+    v = sSeg[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&seg_empty[i]);
+    ++seg;
+    return ok && v.count > 0;
+  };
+
+  if (warp == 12) {
+    // ------------------------------------------------------------------ loads: item 2i = K, 2i + 1 = V of tile i
+    KvManyWalk w;
+    kv_many_begin(a, most_q, group, reinterpret_cast<const KvJob*>(workspace)[blockIdx.x], w);
+    const long long range_start = w.pos;
+    const int P = 1 << a.shift, rows_box = min(P, kKvTile), boxes = kKvManyTile / rows_box;
+    const int most_tiles = 32 * P / kKvManyTile;
+    uint32_t tiles_done = 0;
+    bool ok = true;
+    while (ok) {
+      const bool more = kv_many_next(a, most_q, group, w);
+      const uint32_t sl = seg % kKvManySegments;
+      if (!mbar_wait(&seg_empty[sl], ((seg / kKvManySegments) & 1) ^ 1, abort_flag, kSiteProducerEmpty)) break;
+      if (lane == 0) {
+        const int part = w.count == w.u.tiles ? 0 : w.base < range_start ? 1 : 2;
+        KvSegment v{more ? w.count : 0, (w.u.first_tile + w.tile) * kKvManyTile, w.u.rows, w.u.row0, w.u.q0, w.u.rows_q,
+                    w.u.len, w.u.any_lo, w.u.all_lo, w.u.all_hi, w.h, part};
+        sSeg[sl] = v;
+        mbar_arrive(&seg_full[sl]);
+      }
+      ++seg;
+      if (!more) break;
+      for (int i0 = 0; i0 < w.count && ok; i0 += most_tiles) {  // up to 32 blocks at a time
+        const int n = min(most_tiles, w.count - i0), token0 = (w.u.first_tile + w.tile + i0) * kKvManyTile;
+        const int page = (token0 >> a.shift) + lane;
+        int block = -1;
+        float sk = 1.f, sv = 1.f;
+        if (page << a.shift < w.u.len) {
+          block = a.tables[static_cast<int64_t>(w.r) * a.max_blocks + page];
+          if (block < 0 || block >= a.num_blocks) {
+            atomicOr(&g_mx_error_word, kSiteBadCache);
+            block = -1;
+          } else {
+            const int64_t at = static_cast<int64_t>(block) * a.kv_heads + w.h;
+            sk = a.k_scale[at];
+            sv = a.v_scale[at];
           }
-          for (int i = 0; i < n && ok; ++i, ++tiles_done) {
-            const int token = token0 + i * kKvManyTile, from = (token - token0) >> a.shift;
-            const int my = token + lane * rows_box;
-            const int box_block = __shfl_sync(0xFFFFFFFFu, block, min((my - token0) >> a.shift, 31));
-            const bool load = lane < boxes && box_block >= 0;
-            const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, load)) * rows_box * D;
-            const int slice = ((lane & 7) * 16) >> a.shift;
-            const float slice_k = __shfl_sync(0xFFFFFFFFu, sk, from + slice), slice_v = __shfl_sync(0xFFFFFFFFu, sv, from + slice);
-            for (int half = 0; half < 2; ++half) {
-              const uint32_t item = 2 * tiles_done + half, slot = item % Cfg::RAW_SLOTS;
-              if (!mbar_wait(&raw_empty[slot], ((item / Cfg::RAW_SLOTS) & 1) ^ 1, abort_flag, kSiteProducerEmpty)) {
-                ok = false;
-                break;
-              }
-              if (lane == 0) mbar_arrive_expect_tx(&raw_full[slot], bytes);
+        }
+        for (int i = 0; i < n && ok; ++i, ++tiles_done) {
+          const int token = token0 + i * kKvManyTile, from = (token - token0) >> a.shift;
+          const int my = token + lane * rows_box;
+          const int box_block = __shfl_sync(0xFFFFFFFFu, block, min((my - token0) >> a.shift, 31));
+          const bool load = lane < boxes && box_block >= 0;
+          const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, load)) * rows_box * D;
+          const int slice = ((lane & 7) * 16) >> a.shift;
+          const float slice_k = __shfl_sync(0xFFFFFFFFu, sk, from + slice), slice_v = __shfl_sync(0xFFFFFFFFu, sv, from + slice);
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t item = 2 * tiles_done + half, slot = item % Cfg::RAW_SLOTS;
+            if (!mbar_wait(&raw_empty[slot], ((item / Cfg::RAW_SLOTS) & 1) ^ 1, abort_flag, kSiteProducerEmpty)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&raw_full[slot], bytes);
+            __syncwarp();
+            if (load)
+              tma_load_2d(smem + Cfg::OFF_RAW + slot * Cfg::RAW + lane * rows_box * D, half ? &tmV : &tmK, &raw_full[slot], 0,
+                          ((box_block * a.kv_heads + w.h) << a.shift) + (my & (P - 1)));
+            if (half == 0) {
+              const uint32_t st = tiles_done % kKvManyScales;
+              if (lane < 8) sSC[st * 8 + lane] = make_float4(slice_k, log2f(slice_v), 1.f / slice_v, 0.f);
+              if (lane == 0) sNan[st] = 0;
               __syncwarp();
-              if (load)
-                tma_load_2d(smem + Cfg::OFF_RAW + slot * Cfg::RAW + lane * rows_box * D, half ? &tmV : &tmK, &raw_full[slot], 0,
-                            ((box_block * a.kv_heads + w.h) << a.shift) + (my & (P - 1)));
-              if (half == 0) {
-                const uint32_t st = tiles_done % kKvManyScales;
-                if (lane < 8) sSC[st * 8 + lane] = make_float4(slice_k, log2f(slice_v), 1.f / slice_v, 0.f);
-                if (lane == 0) sNan[st] = 0;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sc_full[st]);
-              }
+              if (lane == 0) mbar_arrive(&sc_full[st]);
             }
           }
         }
       }
-      // every copy has landed before the CTA's shared memory goes
-      const uint32_t items = 2 * tiles_done;
-      for (uint32_t i = 0; i < Cfg::RAW_SLOTS; ++i)
-        if (items > i)
-          mbar_drain(&raw_full[i], ((items - 1 - i) / Cfg::RAW_SLOTS) & 1, kWaitBudgetNs);
-    } else if (warp == 13 && lane == 0) {
-      // ---------------------------------------------------------------- products
-      constexpr uint32_t kHi = smem_desc_hi(1024, kSwizzle128B);
-      constexpr uint32_t kLoK = smem_desc_lo_lbo(16), kLoN = smem_desc_lo_lbo(kKvManyTile * 128);
-      constexpr uint32_t kIdS = kv_idesc_f16(128, kKvManyTile, false), kIdO = kv_idesc_f16(128, D, true);
-      const uint32_t q_lo = smem_u32(smem) >> 4, f_lo = smem_u32(smem + Cfg::OFF_F16) >> 4;
-      uint32_t tiles_done = 0, segments[2] = {0, 0}, weights[2] = {0, 0};
-      bool ok = true;
-      auto scores = [&](int h, uint32_t item) {  // S_h = Q_h K^T
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t at = (k / 4) * (kKvManyTile * 128 / 16) + (k % 4) * 2;
-          umma_f16_ss(tmem + h * 128, desc_from_words((q_lo + h * (Cfg::WIDE / 16) + at) | kLoK, kHi),
-                      desc_from_words((f_lo + (item % Cfg::F16_SLOTS) * (Cfg::WIDE / 16) + at) | kLoK, kHi), kIdS, k > 0);
-        }
-        umma_commit(&s_full[h]);
-      };
-      while (ok && kv_many_next(a, most_q, group, w)) {
-        const int halves = w.u.rows > 128 ? 2 : 1;
-        const uint32_t t0 = tiles_done;
-        uint32_t item = 2 * t0;
-        ok = mbar_wait(&f_full[item % Cfg::F16_SLOTS], (item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteMmaFull);
+    }
+    // every copy has landed before the CTA's shared memory goes
+    const uint32_t items = 2 * tiles_done;
+    for (uint32_t i = 0; i < Cfg::RAW_SLOTS; ++i)
+      if (items > i) mbar_drain(&raw_full[i], ((items - 1 - i) / Cfg::RAW_SLOTS) & 1, kWaitBudgetNs);
+  } else if (warp == 13) {
+    // ------------------------------------------------------------------ products (the whole warp keeps step, one thread issues)
+    constexpr uint32_t kHi = smem_desc_hi(1024, kSwizzle128B);
+    constexpr uint32_t kLoK = smem_desc_lo_lbo(16), kLoN = smem_desc_lo_lbo(kKvManyTile * 128);
+    constexpr uint32_t kIdS = kv_idesc_f16(128, kKvManyTile, false), kIdO = kv_idesc_f16(128, D, true);
+    const uint32_t q_lo = (smem_u32(smem) >> 4) | kLoK, f_lo = smem_u32(smem + Cfg::OFF_F16) >> 4;
+    uint32_t tiles_done = 0, segments[2] = {0, 0}, weights[2] = {0, 0};
+    bool ok = true;
+    KvSegment v;
+    while (ok && next_segment(v)) {
+      const int count = __shfl_sync(0xFFFFFFFFu, v.count, 0), halves = v.rows > 128 ? 2 : 1;
+      for (int i = 0; i <= count && ok; ++i) {  // V of tile i - 1, then K of tile i, each for both row halves
+        const uint32_t v_item = 2 * (tiles_done + i) - 1, k_item = v_item + 1;
+        const uint32_t v_slot = v_item % Cfg::F16_SLOTS, k_slot = k_item % Cfg::F16_SLOTS;
+        if (i > 0) ok = mbar_wait(&f_full[v_slot], (v_item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteMmaFull);
+        const uint32_t v_lo = __shfl_sync(0xFFFFFFFFu, (f_lo + v_slot * (Cfg::WIDE / 16)) | kLoN, 0);
+        const uint32_t k_lo = __shfl_sync(0xFFFFFFFFu, (f_lo + k_slot * (Cfg::WIDE / 16)) | kLoK, 0);
         for (int h = 0; h < halves && ok; ++h) {
-          ok = mbar_wait(&q_full[h], segments[h]++ & 1, abort_flag, kSiteMmaFull);
-          tc_fence_after();
-          if (ok) scores(h, item);
-        }
-        if (!ok) break;
-        umma_commit(&f_empty[item % Cfg::F16_SLOTS]);
-        for (int i = 0; i < w.count && ok; ++i) {
-          const uint32_t v_item = 2 * (t0 + i) + 1, k_item = v_item + 1;
-          const uint32_t v_lo = f_lo + (v_item % Cfg::F16_SLOTS) * (Cfg::WIDE / 16);
-          const bool more = i + 1 < w.count;
-          ok = mbar_wait(&f_full[v_item % Cfg::F16_SLOTS], (v_item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteMmaFull);
-          for (int h = 0; h < halves && ok; ++h) {
+          if (i > 0) {
             ok = mbar_wait(&p_full[h], weights[h]++ & 1, abort_flag, kSiteMmaTmemEmpty);
             if (!ok) break;
             tc_fence_after();
+            if (kv_elect()) {
 #pragma unroll
-            for (int k = 0; k < kKvManyTile / 16; ++k)  // O_h += P_h V, 16 tokens at a time
-              umma_f16_ts(tmem + 256 + h * 128, tmem + h * 128 + k * 8, desc_from_words((v_lo + k * (16 * 128 / 16)) | kLoN, kHi),
-                          kIdO, i > 0 || k > 0);
-            if (h == halves - 1) umma_commit(&f_empty[v_item % Cfg::F16_SLOTS]);
-            if (!more) {
-              umma_commit(&o_full[h]);
-              continue;
+              for (int k = 0; k < kKvManyTile / 16; ++k)  // O_h += P_h V, 16 tokens at a time
+                umma_f16_ts(tmem + 256 + h * 128, tmem + h * 128 + k * 8, desc_from_words(v_lo + k * (16 * 128 / 16), kHi), kIdO,
+                            i > 1 || k > 0);
+              if (i == count) umma_commit(&o_full[h]);
+              if (h == halves - 1) umma_commit(&f_empty[v_slot]);
             }
-            if (h == 0) {
-              ok = mbar_wait(&f_full[k_item % Cfg::F16_SLOTS], (k_item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteMmaFull);
-              if (!ok) break;
-              tc_fence_after();
+            __syncwarp();
+          }
+          if (i < count) {
+            if (h == 0) ok = mbar_wait(&f_full[k_slot], (k_item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteMmaFull);
+            if (i == 0 && ok) ok = mbar_wait(&q_full[h], segments[h]++ & 1, abort_flag, kSiteMmaFull);
+            if (!ok) break;
+            tc_fence_after();
+            if (kv_elect()) {
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {  // S_h = Q_h K^T
+                const uint32_t at = (k / 4) * (kKvManyTile * 128 / 16) + (k % 4) * 2;
+                umma_f16_ss(tmem + h * 128, desc_from_words(q_lo + h * (Cfg::WIDE / 16) + at, kHi),
+                            desc_from_words(k_lo + at, kHi), kIdS, k > 0);
+              }
+              umma_commit(&s_full[h]);
+              if (h == halves - 1) umma_commit(&f_empty[k_slot]);
             }
-            scores(h, k_item);
-            if (h == halves - 1) umma_commit(&f_empty[k_item % Cfg::F16_SLOTS]);
+            __syncwarp();
           }
         }
-        tiles_done += w.count;
       }
-      // every product has ended before the tensor memory goes
+      tiles_done += count;
+    }
+    // every product has ended before the tensor memory goes
+    if (kv_elect()) {
       umma_commit(drain_bar);
       mbar_drain(drain_bar, 0, kWaitBudgetNs);
     }
-  } else if (warp >= 8) {
+    __syncwarp();
+  } else if (warp >= 8 && warp < 12) {
     // ------------------------------------------------------------------ codes -> FP16
-    kv_regs_less<88>();
-    constexpr int CH = D / 16;        // 16-code words of a token
-    constexpr int N = CH;             // words a lane takes of an item: 32 rows x CH / 32 lanes
+    constexpr int CH = D / 16;  // 16-code words of a token
     const int wq = warp - 8, tl = lane & 7;
     uint32_t tiles_done = 0;
     bool ok = true;
-    while (ok && kv_many_next(a, most_q, group, w)) {
-      for (int i = 0; i < w.count && ok; ++i, ++tiles_done) {
-        const int token = (w.u.first_tile + w.tile + i) * kKvManyTile;
-        const bool edge = token < w.u.all_lo || token + kKvManyTile > w.u.all_hi;
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t item = 2 * tiles_done + half, slot = item % Cfg::RAW_SLOTS, fs = item % Cfg::F16_SLOTS;
-          ok = mbar_wait(&raw_full[slot], (item / Cfg::RAW_SLOTS) & 1, abort_flag, kSiteMmaFull) &&
-               mbar_wait(&f_empty[fs], ((item / Cfg::F16_SLOTS) & 1) ^ 1, abort_flag, kSiteProducerEmpty);
-          if (!ok) break;
-          const uint8_t* src = smem + Cfg::OFF_RAW + slot * Cfg::RAW;
-          uint8_t* dst = smem + Cfg::OFF_F16 + fs * Cfg::WIDE;
-          uint4 x[N];
+    KvSegment v;
+    while (ok && next_segment(v)) {
+      const uint32_t items = 2 * (tiles_done + v.count);
+#pragma unroll 1
+      for (uint32_t item = 2 * tiles_done; item < items; ++item) {
+        const uint32_t slot = item % Cfg::RAW_SLOTS, fs = item % Cfg::F16_SLOTS;
+        ok = mbar_wait(&raw_full[slot], (item / Cfg::RAW_SLOTS) & 1, abort_flag, kSiteMmaFull) &&
+             mbar_wait(&f_empty[fs], ((item / Cfg::F16_SLOTS) & 1) ^ 1, abort_flag, kSiteProducerEmpty);
+        if (!ok) break;
+        uint8_t* src = smem + Cfg::OFF_RAW + slot * Cfg::RAW;
+        uint8_t* dst = smem + Cfg::OFF_F16 + fs * Cfg::WIDE;
+        // lane: row tl of 8, word lane / 8 of 4; D = 128 has two groups of 4 words
+        auto raw_at = [&](int n, int& row, int& word) {
+          row = 32 * wq + 8 * (n / (CH / 4)) + tl;
+          word = (n % (CH / 4)) * 4 + (lane >> 3);
+          return reinterpret_cast<uint4*>(src + (D == 128 ? row * 128 + ((word ^ (row & 7)) << 4)
+                                                          : row * 64 + ((word ^ ((row >> 1) & 3)) << 4)));
+        };
+        const int token = v.token + static_cast<int>(item / 2 - tiles_done) * kKvManyTile;
+        if ((item & 1) && (token < v.all_lo || token + kKvManyTile > v.all_hi)) {
+          // V of a tile that some row does not see whole: clear what no row sees; take NaN codes out and note them
+          uint32_t any = 0;
+#pragma unroll 1
+          for (int n = 0; n < CH; ++n) {
+            int row, word;
+            uint4* at = raw_at(n, row, word);
+            const uint4 x = *at;
+            const bool out = token + row < v.any_lo || token + row >= v.len;
+            uint32_t c[4] = {x.x, x.y, x.z, x.w}, bits = 0;
 #pragma unroll
-          for (int n = 0; n < N; ++n) {
-            const int row = 32 * wq + 8 * (n / (CH / 4)) + tl, word = (n % (CH / 4)) * 4 + (lane >> 3);
-            const int at = D == 128 ? row * 128 + ((word ^ (row & 7)) << 4) : row * 64 + ((word ^ ((row >> 1) & 3)) << 4);
-            x[n] = *reinterpret_cast<const uint4*>(src + at);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&raw_empty[slot]);
-          if (half && edge) {  // clear what no row sees; take NaN codes out and note them
-            uint32_t any = 0;
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-              const int row = 32 * wq + 8 * (n / (CH / 4)) + tl, word = (n % (CH / 4)) * 4 + (lane >> 3);
-              const bool out = token + row < w.u.any_lo || token + row >= w.u.len;
-              uint32_t c[4] = {x[n].x, x[n].y, x[n].z, x[n].w}, bits = 0;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if (out) c[j] = 0;
-                const uint32_t y = kv_nan_bytes<FMT>(c[j]);
-                c[j] &= ~((y >> 7) * 0xFFu);
-                bits |= ((y >> 7 & 1) | (y >> 14 & 2) | (y >> 21 & 4) | (y >> 28 & 8)) << (4 * j);
-              }
-              x[n] = make_uint4(c[0], c[1], c[2], c[3]);
-              reinterpret_cast<uint16_t*>(nan_notes)[((tiles_done & 3) * kKvManyTile + row) * CH + word] =
-                  static_cast<uint16_t>(bits);
-              any |= bits;
+            for (int j = 0; j < 4; ++j) {
+              if (out) c[j] = 0;
+              const uint32_t y = kv_nan_bytes<FMT>(c[j]);
+              c[j] &= ~((y >> 7) * 0xFFu);
+              bits |= ((y >> 7 & 1) | (y >> 14 & 2) | (y >> 21 & 4) | (y >> 28 & 8)) << (4 * j);
             }
-            if (any) sNan[tiles_done % kKvManyScales] = 1;
-            __threadfence_block();
+            *at = make_uint4(c[0], c[1], c[2], c[3]);
+            reinterpret_cast<uint16_t*>(nan_notes)[((item / 2 & 3) * kKvManyTile + row) * CH + word] = static_cast<uint16_t>(bits);
+            any |= bits;
           }
+          if (any) sNan[item / 2 % kKvManyScales] = 1;
+          __threadfence_block();
+        }
+#pragma unroll 1
+        for (int n0 = 0; n0 < CH; n0 += 4) {
+          uint4 x[4];
+          int row[4], word[4];
 #pragma unroll
-          for (int n = 0; n < N; ++n) {
-            const int row = 32 * wq + 8 * (n / (CH / 4)) + tl, word = (n % (CH / 4)) * 4 + (lane >> 3);
+          for (int n = 0; n < 4; ++n) x[n] = *raw_at(n0 + n, row[n], word[n]);
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
             const uint32_t c[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
             uint32_t f[8];
 #pragma unroll
@@ -499,40 +549,45 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
               f[2 * j] = kv_codes_to_f16x2<FMT>(c[j] & 0xFFFFu);
               f[2 * j + 1] = kv_codes_to_f16x2<FMT>(c[j] >> 16);
             }
-            uint8_t* to = dst + (word >> 2) * (kKvManyTile * 128) + row * 128;
-            const int ch = (word & 3) * 2;
-            *reinterpret_cast<uint4*>(to + ((ch ^ (row & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
-            *reinterpret_cast<uint4*>(to + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
+            uint8_t* to = dst + (word[n] >> 2) * (kKvManyTile * 128) + row[n] * 128;
+            const int ch = (word[n] & 3) * 2;
+            *reinterpret_cast<uint4*>(to + ((ch ^ (row[n] & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
+            *reinterpret_cast<uint4*>(to + (((ch + 1) ^ (row[n] & 7)) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&f_full[fs]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&raw_empty[slot]);
+          mbar_arrive(&f_full[fs]);
         }
       }
+      tiles_done += v.count;
     }
-  } else {
+  } else if (warp < 8) {
     // ------------------------------------------------------------------ softmax, a row a thread
-    kv_regs_more<184>();
     const int half = warp >> 2, row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + half * 128 + lanes, tO = tmem + 256 + half * 128 + lanes;
     uint8_t* sQ = smem + half * Cfg::WIDE;
     uint32_t tiles_done = 0, my_tiles = 0, segments = 0;
     bool ok = true;
-    while (ok && kv_many_next(a, most_q, group, w)) {
-      if (half && w.u.rows <= 128) {
-        tiles_done += w.count;
+    KvSegment v;
+    while (ok && next_segment(v)) {
+      if (half && v.rows <= 128) {
+        tiles_done += v.count;
         continue;
       }
       const int my_row = 128 * half + row;
-      const bool live = my_row < w.u.rows;
-      const int qi = (w.u.row0 + my_row) / group, hg = w.u.row0 + my_row - qi * group;
-      const int p = w.u.len - w.u.rows_q + qi;
-      const int lo = a.window ? p - a.window + 1 : 0, hi = a.causal ? min(w.u.len, p + 1) : w.u.len;
+      const bool live = my_row < v.rows;
+      const int qi = (v.row0 + my_row) / group, hg = v.row0 + my_row - qi * group;
+      const int p = v.len - v.rows_q + qi;
+      const int lo = a.window ? max(0, p - a.window + 1) : 0, hi = a.causal ? min(v.len, p + 1) : v.len;
+      const uint32_t width = static_cast<uint32_t>(max(hi - lo, 0));
       float row_mul;
       {
         uint4 x[D / 8];
-        const uint16_t* src = a.q + (w.u.q0 + qi) * a.stride_t + (w.h * group + hg) * a.stride_h;
+        const uint16_t* src = a.q + (v.q0 + qi) * a.stride_t + (v.head * group + hg) * a.stride_h;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) x[i] = live ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
         float amax = 0.f;
@@ -562,82 +617,103 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
               make_uint4(f[0], f[1], f[2], f[3]);
         }
         fence_proxy_async_smem();
-        mbar_arrive(&q_full[half]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[half]);
       }
       float m = -INFINITY, l = 0.f;
       uint32_t nan_d[D / 32];
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) nan_d[i] = 0;
-      for (int i = 0; i < w.count; ++i, ++tiles_done, ++my_tiles) {
-        const int token = (w.u.first_tile + w.tile + i) * kKvManyTile;
+#pragma unroll 1
+      for (int i = 0; i < v.count; ++i, ++tiles_done, ++my_tiles) {
+        const int token = v.token + i * kKvManyTile;
         const uint32_t st = tiles_done % kKvManyScales;
         ok = mbar_wait(&sc_full[st], (tiles_done / kKvManyScales) & 1, abort_flag, kSiteEpiTmemFull) &&
              mbar_wait(&s_full[half], my_tiles & 1, abort_flag, kSiteEpiTmemFull);
         if (!ok) break;
         tc_fence_after();
-        uint32_t s[4][32];
+        const float4* scales = sSC + st * 8;
+        const bool edge = token < v.all_lo || token + kKvManyTile > v.all_hi;
+        if (edge) {  // what the row does not see becomes -inf in place
+#pragma unroll 1
+          for (int g = 0; g < 8; ++g) {
+            uint32_t x[16];
+            tmem_ld_32x32b_x16(tS + 16 * g, x);
+            tmem_ld_wait();
+            tmem_regs_ready16(x);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) tmem_ld_32x32b_x32(tS + 32 * j, s[j]);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) tmem_regs_ready(s[j]);
-        const bool edge = token < w.u.all_lo || token + kKvManyTile > w.u.all_hi;
-        if (edge) {
-#pragma unroll
-          for (int j = 0; j < 128; ++j)
-            if (token + j < lo || token + j >= hi) s[j / 32][j % 32] = 0xFF800000u;
+            for (int j = 0; j < 16; ++j)
+              if (static_cast<uint32_t>(token + 16 * g + j - lo) >= width) x[j] = 0xFF800000u;
+            tmem_st_32x32b_x16(tS + 16 * g, x);
+          }
+          tmem_st_wait();
         }
+        // the row's largest z + log2 sV
         float most = -INFINITY;
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {
+          uint32_t x[32];
+          tmem_ld_32x32b_x32(tS + 32 * g, x);
+          tmem_ld_wait();
+          tmem_regs_ready(x);
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          float x = -INFINITY;
+          for (int k = 0; k < 2; ++k) {
+            float y0 = __uint_as_float(x[16 * k]), y1 = __uint_as_float(x[16 * k + 1]);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) x = fmaxf(x, __uint_as_float(s[g / 2][(g & 1) * 16 + j]));
-          const float4 sc = sSC[st * 8 + g];
-          most = fmaxf(most, fmaf(x, row_mul * sc.x, sc.y));
+            for (int j = 2; j < 16; j += 4) {
+              y0 = fmaxf(fmaxf(y0, __uint_as_float(x[16 * k + j])), __uint_as_float(x[16 * k + (j + 1) % 16]));
+              if (j + 2 < 16) y1 = fmaxf(fmaxf(y1, __uint_as_float(x[16 * k + j + 2])), __uint_as_float(x[16 * k + j + 3]));
+            }
+            const float4 sc = scales[2 * g + k];
+            most = fmaxf(most, fmaf(fmaxf(y0, y1), row_mul * sc.x, sc.y));
+          }
         }
         const bool past = most > m + 8.f;
         if (__any_sync(0xFFFFFFFFu, past)) {
-          const float to = past ? most : m;
-          const float keep = kv_exp2(m - (to == -INFINITY ? 0.f : to));
-          m = to;
+          const float keep = past && m > -INFINITY ? kv_exp2(m - most) : 1.f;  // (at m = -inf O and l are 0, or NaN)
           l *= keep;
+          m = past ? most : m;
           if (i > 0) {
-#pragma unroll
+#pragma unroll 1
             for (int j = 0; j < D / 16; ++j) {
               uint32_t o[16];
               tmem_ld_32x32b_x16(tO + 16 * j, o);
               tmem_ld_wait();
               tmem_regs_ready16(o);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * (past ? keep : 1.f));
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
               tmem_st_32x32b_x16(tO + 16 * j, o);
             }
           }
         }
         const float ref = m == -INFINITY ? 0.f : m;
+        // the weights, over the scores that were read before them
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {
+          uint32_t x[32], packed[16];
+          tmem_ld_32x32b_x32(tS + 32 * g, x);
+          tmem_ld_wait();
+          tmem_regs_ready(x);
 #pragma unroll
-        for (int g = 0; g < 8; g += 2) {
-          uint32_t packed[16];
-#pragma unroll
-          for (int gg = 0; gg < 2; ++gg) {
-            const float4 sc = sSC[st * 8 + g + gg];
+          for (int k = 0; k < 2; ++k) {
+            const float4 sc = scales[2 * g + k];
             const float mul = row_mul * sc.x, add = sc.y - ref;
             const uint64_t mul2 = pack_f32x2(mul, mul), add2 = pack_f32x2(add, add);
-            float sum0 = 0.f, sum1 = 0.f;
+            uint64_t sum2[2] = {0, 0};
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const uint32_t* x = &s[g / 2][gg * 16 + 2 * j];
+              const uint32_t* y = &x[16 * k + 2 * j];
               float z0, z1;
-              unpack_f32x2(kv_fma2(pack_f32x2(__uint_as_float(x[0]), __uint_as_float(x[1])), mul2, add2), z0, z1);
+              unpack_f32x2(kv_fma2(pack_f32x2(__uint_as_float(y[0]), __uint_as_float(y[1])), mul2, add2), z0, z1);
               const float p0 = kv_exp2(z0), p1 = kv_exp2(z1);
-              sum0 += p0;
-              sum1 += p1;
-              packed[gg * 8 + j] = kv_pack_f16(p0, p1);
+              sum2[j & 1] = kv_add2(sum2[j & 1], pack_f32x2(p0, p1));
+              packed[8 * k + j] = kv_pack_f16(p0, p1);
             }
+            float sum0, sum1;
+            unpack_f32x2(kv_add2(sum2[0], sum2[1]), sum0, sum1);
             l = fmaf(sum0 + sum1, sc.z, l);
           }
-          tmem_st_32x32b_x16(tS + g * 8, packed);
+          tmem_st_32x32b_x16(tS + 16 * g, packed);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -655,17 +731,17 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
             }
           }
         }
-        mbar_arrive(&p_full[half]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[half]);
       }
       if (!ok) break;
       ok = mbar_wait(&o_full[half], segments++ & 1, abort_flag, kSiteEpiTmemFull);
       if (!ok) break;
       tc_fence_after();
-      const bool whole = w.count == w.u.tiles;
+      const bool whole = v.part == 0;
       const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-      const int64_t at_row = static_cast<int64_t>(w.u.q0 + qi) * a.heads + w.h * group + hg;
-      float* part = reinterpret_cast<float*>(workspace + kv_many_slots_at(a.requests, D) +
-                                             (2 * blockIdx.x + (w.base < range_start ? 0 : 1)) * Cfg::SLOT);
+      const int64_t at_row = static_cast<int64_t>(v.q0 + qi) * a.heads + v.head * group + hg;
+      float* part = reinterpret_cast<float*>(workspace + kv_many_slots_at(a.requests, D) + (2 * blockIdx.x + v.part - 1) * Cfg::SLOT);
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
         uint32_t o[32];

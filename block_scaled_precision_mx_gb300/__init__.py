@@ -16,6 +16,7 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -481,33 +482,39 @@ def fp8_blockwise_gemm(qa, sa, qb, sb, M, N, K, out_dtype=OUT_BF16, out=None, st
 
 
 # ------------------------------------------------------------------ 8-bit key/value cache
+# (Calls of a few microseconds: each tensor is looked at once, on the way to its address.)
 _HALF = {torch.bfloat16: HALF_BF16, torch.float16: HALF_F16}
+_int32, _int64, _float32, _uint8 = torch.int32, torch.int64, torch.float32, torch.uint8
+
+
+def _at(t, dtype, name):
+    """Address of a contiguous CUDA tensor of that type."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    return t.data_ptr()
 
 
 def _rows_of_heads(x, name):
-    """(address, type, token stride, head stride) of x[tokens][heads][head_dim], strided but for the last axis."""
-    if x.dim() != 3 or x.dtype not in _HALF:
+    """(shape, address, type, token stride, head stride) of x[tokens][heads][head_dim], strided but for
+    the last axis."""
+    half = _HALF.get(x.dtype)
+    if half is None or x.dim() != 3:
         raise ValueError(f"{name} must be a 3-D bf16 or fp16 tensor")
-    if not x.is_cuda or x.stride(2) != 1:
+    st, sh, sd = x.stride()
+    if not x.is_cuda or sd != 1:
         raise ValueError(f"{name} must be a CUDA tensor whose last axis is contiguous")
-    return x.data_ptr(), _HALF[x.dtype], x.stride(0), x.stride(1)
+    return x.shape, x.data_ptr(), half, st, sh
 
 
 def _cache_shape(k_codes, v_codes, k_scale, v_scale):
-    if k_codes.dim() != 4 or k_codes.dtype != torch.uint8 or v_codes.dtype != torch.uint8:
-        raise ValueError("codes must be uint8 [num_blocks][kv_heads][block_tokens][head_dim]")
-    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
-        raise ValueError("scales must be float32 [num_blocks][kv_heads]")
     shape = k_codes.shape
-    if v_codes.shape != shape or k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
-        raise ValueError("codes and scales of one cache must agree in shape")
+    if len(shape) != 4 or v_codes.shape != shape:
+        raise ValueError("codes must be uint8 [num_blocks][kv_heads][block_tokens][head_dim]")
+    if k_scale.shape != shape[:2] or v_scale.shape != k_scale.shape:
+        raise ValueError("scales must be float32 [num_blocks][kv_heads]")
     return shape
-
-
-def _int32(**tensors):
-    for name, t in tensors.items():
-        if t.dtype != torch.int32:
-            raise ValueError(f"{name} must be int32")
 
 
 def kv_block_tables(block_tables: torch.Tensor, len_before: torch.Tensor, len_after: torch.Tensor,
@@ -517,28 +524,28 @@ def kv_block_tables(block_tables: torch.Tensor, len_before: torch.Tensor, len_af
     places (include/mx.h, kv_block_tables).  block_tables int32 [requests][max_blocks] and free_list
     int32 [capacity] are updated in place.  Returns (q_start int32 [requests + 1], slot_map int64
     [num_tokens], positions int32 [num_tokens], info int32 {free blocks left, blocks missing})."""
-    _int32(block_tables=block_tables, len_before=len_before, len_after=len_after, free_list=free_list,
-           free_count=free_count)
-    if block_tables.dim() != 2 or len_before.shape != block_tables.shape[:1] or len_after.shape != len_before.shape:
-        raise ValueError("block_tables is [requests][max_blocks], the lengths are [requests]")
-    requests, max_blocks = block_tables.shape
+    requests, max_blocks = block_tables.shape if block_tables.dim() == 2 else (0, 0)
+    if not requests or len_before.numel() != requests or len_after.numel() != requests or free_count.numel() < 1:
+        raise ValueError("block_tables is [requests][max_blocks], the lengths are [requests], free_count [1]")
+    at = (_at(block_tables, _int32, "block_tables"), _at(len_before, _int32, "len_before"),
+          _at(len_after, _int32, "len_after"), _at(free_list, _int32, "free_list"), _at(free_count, _int32, "free_count"))
     dev = block_tables.device
     if q_start is None:
-        q_start = torch.empty(requests + 1, dtype=torch.int32, device=dev)
+        q_start = torch.empty(requests + 1, dtype=_int32, device=dev)
     if slot_map is None:
-        slot_map = torch.empty(num_tokens, dtype=torch.int64, device=dev)
+        slot_map = torch.empty(num_tokens, dtype=_int64, device=dev)
     if positions is None:
-        positions = torch.empty(num_tokens, dtype=torch.int32, device=dev)
+        positions = torch.empty(num_tokens, dtype=_int32, device=dev)
     if info is None:
-        info = torch.empty(2, dtype=torch.int32, device=dev)
-    _int32(q_start=q_start, positions=positions, info=info)
-    if (slot_map.dtype != torch.int64 or slot_map.numel() < num_tokens or positions.numel() < num_tokens
-            or q_start.numel() < requests + 1 or info.numel() < 2):
-        raise ValueError("q_start [requests + 1], slot_map (int64) and positions [num_tokens], info [2]")
-    st = load().kv_block_tables(_ptr(block_tables), requests, max_blocks, _ptr(len_before), _ptr(len_after),
-                                _ptr(free_list), free_list.numel(), _ptr(free_count), block_tokens, num_tokens,
-                                _ptr(q_start), _ptr(slot_map), _ptr(positions), _ptr(info), _stream(stream))
-    _check(st, "kv_block_tables")
+        info = torch.empty(2, dtype=_int32, device=dev)
+    if (q_start.numel() <= requests or slot_map.numel() < num_tokens or positions.numel() < num_tokens
+            or info.numel() < 2):
+        raise ValueError("q_start has requests + 1 places, slot_map and positions num_tokens, info two")
+    st = load().kv_block_tables(at[0], requests, max_blocks, at[1], at[2], at[3], free_list.numel(), at[4], block_tokens,
+                                num_tokens, _at(q_start, _int32, "q_start"), _at(slot_map, _int64, "slot_map"),
+                                _at(positions, _int32, "positions"), _at(info, _int32, "info"), _stream(stream))
+    if st:
+        _check(st, "kv_block_tables")
     return q_start, slot_map, positions, info
 
 
@@ -546,19 +553,23 @@ def kv_cache_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_
                     v_codes: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor, elem: int = E4M3, stream=None):
     """Quantize keys and values k, v [tokens][kv_heads][head_dim] (bf16 or fp16, slices will do) into
     the cache at slot_map (int64), in place (include/mx.h, kv_cache_append)."""
-    k_at, half, k_st, k_sh = _rows_of_heads(k, "k")
-    v_at, v_half, v_st, v_sh = _rows_of_heads(v, "v")
+    shape, k_at, half, k_st, k_sh = _rows_of_heads(k, "k")
+    v_shape, v_at, v_half, v_st, v_sh = _rows_of_heads(v, "v")
     blocks, kv_heads, block_tokens, head_dim = _cache_shape(k_codes, v_codes, k_scale, v_scale)
-    if v_half != half or v.shape != k.shape or k.shape[1:] != (kv_heads, head_dim):
+    tokens = shape[0]
+    if v_half != half or v_shape != shape or shape[1] != kv_heads or shape[2] != head_dim:
         raise ValueError("k and v must be alike, [tokens][kv_heads][head_dim] of the cache")
-    if slot_map.dtype != torch.int64 or slot_map.numel() != k.shape[0]:
-        raise ValueError("slot_map must be int64 [tokens]")
-    st = load().kv_cache_append(k_at, v_at, half, k.shape[0], k_st, k_sh, v_st, v_sh, _ptr(slot_map), _ptr(k_codes),
-                                _ptr(v_codes), _ptr(k_scale), _ptr(v_scale), elem, blocks, kv_heads, block_tokens,
-                                head_dim, _stream(stream))
-    _check(st, "kv_cache_append")
+    if slot_map.numel() != tokens:
+        raise ValueError("slot_map must have a place for each token")
+    st = load().kv_cache_append(k_at, v_at, half, tokens, k_st, k_sh, v_st, v_sh, _at(slot_map, _int64, "slot_map"),
+                                _at(k_codes, _uint8, "k_codes"), _at(v_codes, _uint8, "v_codes"),
+                                _at(k_scale, _float32, "k_scale"), _at(v_scale, _float32, "v_scale"), elem, blocks,
+                                kv_heads, block_tokens, head_dim, _stream(stream))
+    if st:
+        _check(st, "kv_cache_append")
 
 
+@functools.lru_cache(maxsize=256)
 def kv_attention_workspace_bytes(num_tokens: int, requests: int, max_q_len: int, heads: int, kv_heads: int,
                                  head_dim: int) -> int:
     return int(load().kv_attention_workspace_bytes(num_tokens, requests, max_q_len, heads, kv_heads, head_dim))
@@ -572,32 +583,38 @@ def kv_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor, 
     lengths int32 [requests]: cached tokens, the queries' own among them; q_start int32 [requests + 1];
     softmax_scale defaults to head_dim ** -0.5.  Returns (out, like q but contiguous; lse float
     [tokens][heads])."""
-    q_at, half, q_st, q_sh = _rows_of_heads(q, "q")
+    shape, q_at, half, q_st, q_sh = _rows_of_heads(q, "q")
     blocks, kv_heads, block_tokens, head_dim = _cache_shape(k_codes, v_codes, k_scale, v_scale)
-    _int32(block_tables=block_tables, lengths=lengths, q_start=q_start)
-    tokens, heads, d = q.shape
+    tokens, heads, d = shape
     requests = lengths.numel()
-    if d != head_dim or block_tables.dim() != 2 or block_tables.shape[0] != requests or q_start.numel() != requests + 1:
+    table_rows, max_blocks = block_tables.shape if block_tables.dim() == 2 else (-1, 0)
+    if d != head_dim or table_rows != requests or q_start.numel() != requests + 1:
         raise ValueError("q [tokens][heads][head_dim], block_tables [requests][max_blocks], lengths [requests], "
                          "q_start [requests + 1]")
-    lib = load()
+    dev = q.device
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.empty(shape, dtype=q.dtype, device=dev)
+    elif out.shape != shape:
+        raise ValueError("out must be shaped like q")
     if lse is None:
-        lse = torch.empty((tokens, heads), dtype=torch.float32, device=q.device)
-    if out.shape != q.shape or out.dtype != q.dtype or lse.shape != q.shape[:2] or lse.dtype != torch.float32:
-        raise ValueError("out is shaped and typed like q, lse is float32 [tokens][heads]")
-    need = lib.kv_attention_workspace_bytes(tokens, requests, max_q_len, heads, kv_heads, head_dim)
+        lse = torch.empty((tokens, heads), dtype=_float32, device=dev)
+    elif lse.shape != shape[:2]:
+        raise ValueError("lse must be [tokens][heads]")
+    need = kv_attention_workspace_bytes(tokens, requests, max_q_len, heads, kv_heads, head_dim)
     if workspace is None:
-        workspace = _u8(max(16, need), q.device)
-    elif workspace.numel() * workspace.element_size() < need:
+        workspace = torch.empty(need, dtype=_uint8, device=dev)
+    elif workspace.numel() < need:
         raise ValueError(f"workspace must have {need} bytes")
-    st = lib.kv_attention(q_at, half, tokens, heads, q_st, q_sh, _ptr(k_codes), _ptr(v_codes), _ptr(k_scale),
-                          _ptr(v_scale), elem, blocks, kv_heads, block_tokens, head_dim, _ptr(block_tables),
-                          block_tables.shape[1], _ptr(lengths), _ptr(q_start), requests, max_q_len,
-                          head_dim ** -0.5 if softmax_scale is None else softmax_scale, int(bool(causal)), window,
-                          _ptr(out), _ptr(lse), _ptr(workspace), _stream(stream))
-    _check(st, "kv_attention")
+    st = load().kv_attention(q_at, half, tokens, heads, q_st, q_sh, _at(k_codes, _uint8, "k_codes"),
+                             _at(v_codes, _uint8, "v_codes"), _at(k_scale, _float32, "k_scale"),
+                             _at(v_scale, _float32, "v_scale"), elem, blocks, kv_heads, block_tokens, head_dim,
+                             _at(block_tables, _int32, "block_tables"), max_blocks, _at(lengths, _int32, "lengths"),
+                             _at(q_start, _int32, "q_start"), requests, max_q_len,
+                             head_dim ** -0.5 if softmax_scale is None else softmax_scale, causal, window,
+                             _at(out, q.dtype, "out"), _at(lse, _float32, "lse"), _at(workspace, _uint8, "workspace"),
+                             _stream(stream))
+    if st:
+        _check(st, "kv_attention")
     return out, lse
 
 

@@ -36,10 +36,10 @@ bool kv_codes_tmap(CUtensorMap* map, const void* codes, int64_t num_blocks, int6
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
-template <int FMT, bool F16, int D, int NT>
+template <int FMT, int D, int NT>
 mx_status kv_few_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_len, void* workspace, cudaStream_t st) {
   using Cfg = KvFewCfg<D, NT>;
-  auto kern = kv_attention_few_kernel<FMT, F16, D, NT>;
+  auto kern = kv_attention_few_kernel<FMT, D, NT>;
   static std::atomic<int> ctas[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MX_ERR_CUDA;
@@ -61,16 +61,16 @@ mx_status kv_few_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_len
   const int most_q = static_cast<int>(max_q_len);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   if (pdl_launch(kern, n, kKvFewThreads, Cfg::SMEM, st, tk, tv, a, most_q, ws) != cudaSuccess) return MX_ERR_CUDA;
-  if (n > 1 && pdl_launch(kv_join_kernel<F16, D, 8 * NT>, n - 1, 128, 0, st, a, static_cast<const uint8_t*>(ws),
+  if (n > 1 && pdl_launch(kv_join_kernel<D, 8 * NT>, n - 1, 128, 0, st, a, static_cast<const uint8_t*>(ws),
                           kKvSlotsAt) != cudaSuccess)
     return MX_ERR_CUDA;
   return launch_status();
 }
 
-template <int FMT, bool F16, int D>
+template <int FMT, int D>
 mx_status kv_many_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_len, void* workspace, cudaStream_t st) {
   using Cfg = KvManyCfg<D>;
-  auto kern = kv_attention_many_kernel<FMT, F16, D>;
+  auto kern = kv_attention_many_kernel<FMT, D>;
   static std::atomic<bool> attr_set[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MX_ERR_CUDA;
@@ -91,26 +91,33 @@ mx_status kv_many_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_le
   if (pdl_launch(kv_plan_kernel, 1, kKvPlanThreads, 0, st, a, most_q, n, ws) != cudaSuccess ||
       pdl_launch(kern, n, kKvManyThreads, Cfg::SMEM, st, tk, tv, a, most_q, ws) != cudaSuccess)
     return MX_ERR_CUDA;
-  if (n > 1 && pdl_launch(kv_join_kernel<F16, D, kKvManyRows>, dim3(n - 1, 8), 128, 0, st, a, static_cast<const uint8_t*>(ws),
+  if (n > 1 && pdl_launch(kv_join_kernel<D, kKvManyRows>, dim3(n - 1, 8), 128, 0, st, a, static_cast<const uint8_t*>(ws),
                           kv_many_slots_at(a.requests, D)) != cudaSuccess)
     return MX_ERR_CUDA;
   return launch_status();
 }
 
-template <int FMT, bool F16, int D>
+template <int FMT, int D>
 mx_status kv_attention_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_len, void* workspace, cudaStream_t st) {
   switch (kv_row_tiles(max_q_len, a.heads / a.kv_heads)) {
-    case 1: return kv_few_launch<FMT, F16, D, 1>(a, block_tokens, max_q_len, workspace, st);
-    case 2: return kv_few_launch<FMT, F16, D, 2>(a, block_tokens, max_q_len, workspace, st);
-    case 4: return kv_few_launch<FMT, F16, D, 4>(a, block_tokens, max_q_len, workspace, st);
+    case 1: return kv_few_launch<FMT, D, 1>(a, block_tokens, max_q_len, workspace, st);
+    case 2: return kv_few_launch<FMT, D, 2>(a, block_tokens, max_q_len, workspace, st);
+    case 4: return kv_few_launch<FMT, D, 4>(a, block_tokens, max_q_len, workspace, st);
   }
-  return kv_many_launch<FMT, F16, D>(a, block_tokens, max_q_len, workspace, st);
+  return kv_many_launch<FMT, D>(a, block_tokens, max_q_len, workspace, st);
 }
 
-template <int FMT, bool F16, int D>
-cudaError_t kv_append_launch(const KvAppendArgs& a, bool wide, dim3 grid, cudaStream_t st) {
-  return wide ? pdl_launch(kv_append_kernel<FMT, F16, D, 4>, grid, kKvAppendThreads, 0, st, a)
-              : pdl_launch(kv_append_kernel<FMT, F16, D, 1>, grid, kKvAppendThreads, 0, st, a);
+// A group of W warps holds a block's values of one head, 4 words of 8 a thread, or 8 where 8 warps would
+// not do otherwise.
+template <int FMT, bool F16>
+cudaError_t kv_append_launch(const KvAppendArgs& a, int head_dim, dim3 grid, cudaStream_t st) {
+#define KV_APPEND(D, W, PASSES) pdl_launch(kv_append_kernel<FMT, F16, D, W, PASSES>, grid, kKvAppendThreads, 0, st, a)
+  if (head_dim == 64)
+    return a.shift == 4 ? KV_APPEND(64, 1, 4) : a.shift == 5 ? KV_APPEND(64, 2, 4) : a.shift == 6 ? KV_APPEND(64, 4, 4)
+                                                                                                  : KV_APPEND(64, 8, 4);
+  return a.shift == 4 ? KV_APPEND(128, 2, 4) : a.shift == 5 ? KV_APPEND(128, 4, 4) : a.shift == 6 ? KV_APPEND(128, 8, 4)
+                                                                                                  : KV_APPEND(128, 8, 8);
+#undef KV_APPEND
 }
 
 }  // namespace
@@ -196,9 +203,8 @@ mx_status kv_cache_append(const void* k, const void* v, mx_half type, int64_t nu
   a.tokens = static_cast<int>(num_tokens);
   a.kv_heads = static_cast<int>(kv_heads);
   a.shift = kv_block_shift(block_tokens);
-  // A block's values of one head fit one warp's registers up to 4096 of them, else four warps'.
-  const bool wide = block_tokens * head_dim > 4096;
-  const int groups = wide ? 2 : 8;
+  const int64_t warps = static_cast<int64_t>(block_tokens) * head_dim / 1024;
+  const int groups = warps >= 8 ? 1 : static_cast<int>(8 / warps);
   const int64_t gy = (2 * kv_heads + groups - 1) / groups;
   // Tokens looked over by a CTA: a power of two that leaves about 2048 CTAs, at most a block's tokens.
   int chunk = 1;
@@ -206,14 +212,10 @@ mx_status kv_cache_append(const void* k, const void* v, mx_half type, int64_t nu
   a.chunk = chunk;
   const dim3 grid(static_cast<unsigned>((num_tokens + chunk - 1) / chunk), static_cast<unsigned>(gy));
   cudaStream_t st = as_stream(stream);
-  const bool f16 = type == MX_HALF_F16, d64 = head_dim == 64;
-  cudaError_t e;
-  if (elem == MX_E4M3)
-    e = f16 ? (d64 ? kv_append_launch<0, true, 64>(a, wide, grid, st) : kv_append_launch<0, true, 128>(a, wide, grid, st))
-            : (d64 ? kv_append_launch<0, false, 64>(a, wide, grid, st) : kv_append_launch<0, false, 128>(a, wide, grid, st));
-  else
-    e = f16 ? (d64 ? kv_append_launch<1, true, 64>(a, wide, grid, st) : kv_append_launch<1, true, 128>(a, wide, grid, st))
-            : (d64 ? kv_append_launch<1, false, 64>(a, wide, grid, st) : kv_append_launch<1, false, 128>(a, wide, grid, st));
+  const bool f16 = type == MX_HALF_F16;
+  const cudaError_t e = elem == MX_E4M3
+                            ? (f16 ? kv_append_launch<0, true>(a, head_dim, grid, st) : kv_append_launch<0, false>(a, head_dim, grid, st))
+                            : (f16 ? kv_append_launch<1, true>(a, head_dim, grid, st) : kv_append_launch<1, false>(a, head_dim, grid, st));
   if (e != cudaSuccess) return MX_ERR_CUDA;
   return launch_status();
 }
@@ -275,15 +277,14 @@ mx_status kv_attention(const void* q, mx_half type, int64_t num_tokens, int64_t 
   a.max_blocks = static_cast<int>(max_blocks);
   a.shift = kv_block_shift(block_tokens);
   a.causal = causal;
+  a.f16 = type == MX_HALF_F16;
   a.window = static_cast<int>(window < kKvMostTokens ? window : kKvMostTokens);
   cudaStream_t st = as_stream(stream);
-  const bool f16 = type == MX_HALF_F16, d64 = head_dim == 64, e5 = elem == MX_E5M2;
-#define KV_ATTN(FMT, H, D) kv_attention_launch<FMT, H, D>(a, block_tokens, max_q_len, workspace, st)
-  return e5 ? (f16 ? (d64 ? KV_ATTN(1, true, 64) : KV_ATTN(1, true, 128))
-                   : (d64 ? KV_ATTN(1, false, 64) : KV_ATTN(1, false, 128)))
-            : (f16 ? (d64 ? KV_ATTN(0, true, 64) : KV_ATTN(0, true, 128))
-                   : (d64 ? KV_ATTN(0, false, 64) : KV_ATTN(0, false, 128)));
-#undef KV_ATTN
+  if (elem == MX_E5M2)
+    return head_dim == 64 ? kv_attention_launch<1, 64>(a, block_tokens, max_q_len, workspace, st)
+                          : kv_attention_launch<1, 128>(a, block_tokens, max_q_len, workspace, st);
+  return head_dim == 64 ? kv_attention_launch<0, 64>(a, block_tokens, max_q_len, workspace, st)
+                        : kv_attention_launch<0, 128>(a, block_tokens, max_q_len, workspace, st);
 }
 
 }  // extern "C"

@@ -30,84 +30,10 @@ struct KvAttnArgs {
   int64_t num_blocks;
   int tokens, heads, kv_heads, requests, max_blocks, shift;
   int causal, window;
+  int f16;                 // q and out are FP16, else bf16
 };
 
 constexpr float kLn2 = 0.69314718055994531f;
-
-// One CTA per query row: keys in chunks of 128, one key a thread; then one or more output elements a
-// thread.  Right for every call and nothing more.
-template <int FMT, bool F16, int D>
-__global__ void __launch_bounds__(128) kv_attention_rows_kernel(const KvAttnArgs a) {
-  pdl_prologue();
-  const int t = blockIdx.x, head = blockIdx.y, h = head / (a.heads / a.kv_heads), tid = threadIdx.x;
-  __shared__ float qs[D], ps[128], red[4];
-  __shared__ int64_t where[128];
-  int lo = 0, hi = a.requests;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.q_start[mid] <= t) lo = mid;
-    else hi = mid;
-  }
-  const int r = lo, P = 1 << a.shift;
-  int len = a.lengths[r];
-  const int pos = len - (a.q_start[r + 1] - t);
-  if (t >= a.q_start[a.requests]) len = 0;
-  const int begin = a.window ? max(0, pos - a.window + 1) : 0;
-  const int end = a.causal ? min(len, pos + 1) : len;
-  if (tid < D) {
-    const uint16_t* src = a.q + t * a.stride_t + head * a.stride_h + tid;
-    qs[tid] = F16 ? __half2float(__ushort_as_half(*src)) : bf16_bits_to_float(*src);
-  }
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  __syncthreads();
-  for (int j0 = begin; j0 < end; j0 += 128) {
-    const int j = j0 + tid;
-    float z = -INFINITY, sv = 0.f;
-    if (j < end) {
-      const int block = a.tables[static_cast<int64_t>(r) * a.max_blocks + (j >> a.shift)];
-      const bool there = block >= 0 && block < a.num_blocks;
-      const int64_t bh = static_cast<int64_t>(there ? block : 0) * a.kv_heads + h;
-      const int64_t at = (bh * P + (j & (P - 1))) * D;
-      float acc = 0.f;
-      for (int d = 0; d < D; d += 4) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(a.k_codes + at + d);
-        const float2 x = kv_f16x2_to_float2(kv_codes_to_f16x2<FMT>(w & 0xFFFFu));
-        const float2 y = kv_f16x2_to_float2(kv_codes_to_f16x2<FMT>(w >> 16));
-        acc += qs[d] * x.x + qs[d + 1] * x.y + qs[d + 2] * y.x + qs[d + 3] * y.y;
-      }
-      z = acc * a.scale_log2 * a.k_scale[bh];
-      sv = a.v_scale[bh];
-      where[tid] = at;
-      if (!there) atomicOr(&g_mx_error_word, kSiteBadCache);
-    }
-    float zm = z;
-    for (int s = 16; s; s >>= 1) zm = fmaxf(zm, __shfl_xor_sync(0xFFFFFFFFu, zm, s));
-    if ((tid & 31) == 0) red[tid >> 5] = zm;
-    __syncthreads();
-    const float m_new = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float m_use = m_new == -INFINITY ? 0.f : m_new;
-    const float p = exp2f(z - m_use), keep = exp2f(m - m_use);
-    ps[tid] = p * sv;
-    float sum = p;
-    for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
-    __syncthreads();
-    if ((tid & 31) == 0) red[tid >> 5] = sum;
-    __syncthreads();
-    l = l * keep + (red[0] + red[1]) + (red[2] + red[3]);
-    m = m_new;
-    o *= keep;
-    if (tid < D)
-      for (int i = 0; i < min(128, end - j0); ++i)
-        o += ps[i] * kv_f16x2_to_float2(kv_codes_to_f16x2<FMT>(a.v_codes[where[i] + tid])).x;
-    __syncthreads();
-  }
-  if (tid < D) {
-    const float x = end > begin ? o / l : 0.f;
-    const int64_t at = (static_cast<int64_t>(t) * a.heads + head) * D + tid;
-    a.out[at] = F16 ? __half_as_ushort(__float2half_rn(x)) : __bfloat16_as_ushort(__float2bfloat16_rn(x));
-  }
-  if (tid == 0) a.lse[static_cast<int64_t>(t) * a.heads + head] = end > begin ? m * kLn2 + logf(l) : -INFINITY;
-}
 
 // ================================================================== few rows for each kv head
 // Queries of one request that share a kv head (query heads of the group x query tokens, at most 32 rows)
@@ -331,14 +257,16 @@ __device__ __forceinline__ void kv_clear_rest(const KvAttnArgs& a, int head_dim,
   for (int64_t i = first; i < rows; i += step) a.lse[static_cast<int64_t>(used) * a.heads + i] = -INFINITY;
 }
 
-template <bool F16>
-__device__ __forceinline__ uint32_t kv_pack_out(float lo, float hi) {
-  if (F16) return kv_pack_f16(lo, hi);
+__device__ __forceinline__ float2 kv_unpack2(uint32_t w, int f16) {
+  return f16 ? kv_unpack2<true>(w) : kv_unpack2<false>(w);
+}
+__device__ __forceinline__ uint32_t kv_pack_out(float lo, float hi, int f16) {
+  if (f16) return kv_pack_f16(lo, hi);
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <int FMT, bool F16, int D, int NT>
+template <int FMT, int D, int NT>
 __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
     kv_attention_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                             const KvAttnArgs a, int most_q, uint8_t* workspace) {
@@ -494,7 +422,7 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
         const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 y = kv_unpack2<F16>(u[j]);
+          const float2 y = kv_unpack2(u[j], a.f16);
           f[8 * i + 2 * j] = y.x;
           f[8 * i + 2 * j + 1] = y.y;
           amax = fmaxf(amax, fmaxf(fabsf(y.x), fabsf(y.y)));
@@ -740,7 +668,7 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
         const int64_t at_row = static_cast<int64_t>(req.q0 + qi) * a.heads + w.h * group + hg;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         *reinterpret_cast<uint2*>(a.out + at_row * D + d) =
-            sum == 0.f ? make_uint2(0, 0) : make_uint2(kv_pack_out<F16>(o.x * inv, o.y * inv), kv_pack_out<F16>(o.z * inv, o.w * inv));
+            sum == 0.f ? make_uint2(0, 0) : make_uint2(kv_pack_out(o.x * inv, o.y * inv, a.f16), kv_pack_out(o.z * inv, o.w * inv, a.f16));
         if (d == 0) a.lse[at_row] = sum == 0.f ? -INFINITY : (at + log2f(sum)) * kLn2;
       } else {
         *reinterpret_cast<float4*>(part + row * D + d) = o;
@@ -753,7 +681,7 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
 // Joins the segments of the units that range boundaries cut.  CTA c looks at the boundary where range c
 // begins; the first boundary inside a unit takes the unit.  Segments are added in order: the range that
 // the unit begins in left its one in slot 1, the others in slot 0.
-template <bool F16, int D, int ROWS>
+template <int D, int ROWS>
 __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, const uint8_t* workspace, size_t slots_at) {
   pdl_prologue();
   constexpr size_t kSlot = static_cast<size_t>(ROWS) * (D + 2) * 4;
@@ -809,7 +737,7 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, const 
     const int64_t at_row = static_cast<int64_t>(job.q0 + qi) * a.heads + job.head * group + hg;
     const float inv = 1.f / l;
     *reinterpret_cast<uint2*>(a.out + at_row * D + d) =
-        l == 0.f ? make_uint2(0, 0) : make_uint2(kv_pack_out<F16>(o.x * inv, o.y * inv), kv_pack_out<F16>(o.z * inv, o.w * inv));
+        l == 0.f ? make_uint2(0, 0) : make_uint2(kv_pack_out(o.x * inv, o.y * inv, a.f16), kv_pack_out(o.z * inv, o.w * inv, a.f16));
     if (d == 0) a.lse[at_row] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
   }
 }

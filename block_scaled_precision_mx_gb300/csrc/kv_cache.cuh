@@ -214,28 +214,34 @@ __device__ __forceinline__ float2 kv_unpack2(uint32_t w) {
 
 // A run is a stretch of new tokens with consecutive slots of one block.  A group of W warps takes one
 // (run, head, keys or values) at a time: the run's rows come into registers in one go (16 bytes a
-// thread and load, D / 8 lanes a row), the group finds the largest finite |x|, settles the block's
-// scale and writes the codes.  A run that starts a block sets its scale; one that goes on in a block
-// keeps the block's scale or grows it, and then the tokens in front are re-rounded to the new scale
-// (scales are powers of two, so that is exact but for codes that become subnormal).
-// One read of the input, one write of the codes; the block's old codes move only when its scale grows.
-template <int FMT, bool F16, int D, int W>
-__global__ void __launch_bounds__(kKvAppendThreads) kv_append_kernel(const KvAppendArgs a) {
+// thread and load, D / 8 lanes a row, PASSES loads a thread for a whole block), the group finds the
+// largest finite |x|, settles the block's scale and writes the codes.  A run that starts a block sets its
+// scale; one that goes on in a block keeps the block's scale or grows it, and then the tokens in front are
+// re-rounded to the new scale (scales are powers of two, so that is exact but for codes that become
+// subnormal).  One read of the input, one write of the codes; the block's old codes move only when its
+// scale grows.  The bound is memory; what keeps it busy is many small groups a SM (W and PASSES follow the
+// block's size so that a thread holds 4 or 8 words), hence few registers.
+template <int FMT, bool F16, int D, int W, int PASSES>
+__global__ void __launch_bounds__(kKvAppendThreads, 5) kv_append_kernel(const KvAppendArgs a) {
   pdl_prologue();
   constexpr int kLanesPerRow = D / 8, kGroupThreads = 32 * W, kRowsPerPass = kGroupThreads / kLanesPerRow;
-  constexpr int kPasses = 16, kGroups = kKvAppendThreads / kGroupThreads;
+  constexpr int kGroups = kKvAppendThreads / kGroupThreads;
+  __shared__ int64_t slot_of[2 * 128 + 1];  // slots of tokens t0 - 1 .. t0 + chunk + P - 1
   __shared__ int starts[128];
   __shared__ int num_starts;
   __shared__ uint32_t group_max[kGroups][W];
   const int tid = threadIdx.x, lane = tid & 31;
   const int P = 1 << a.shift, t0 = blockIdx.x * a.chunk;
   if (tid == 0) num_starts = 0;
+  for (int i = tid; i <= a.chunk + P; i += kKvAppendThreads) {
+    const int t = t0 - 1 + i;
+    slot_of[i] = t >= 0 && t < a.tokens ? a.slots[t] : -1;
+  }
   __syncthreads();
-  if (tid < a.chunk && t0 + tid < a.tokens) {
-    const int t = t0 + tid;
-    const int64_t slot = a.slots[t];
+  if (tid < a.chunk) {
+    const int64_t slot = slot_of[tid + 1];
     if (slot >= 0 && slot < a.num_slots) {
-      if (t == 0 || (slot & (P - 1)) == 0 || a.slots[t - 1] != slot - 1) starts[atomicAdd(&num_starts, 1)] = t;
+      if ((slot & (P - 1)) == 0 || slot_of[tid] != slot - 1) starts[atomicAdd(&num_starts, 1)] = tid;
     } else if (slot != -1) {
       atomicOr(&g_mx_error_word, kSiteBadCache);
     }
@@ -248,42 +254,39 @@ __global__ void __launch_bounds__(kKvAppendThreads) kv_append_kernel(const KvApp
   const int row0 = gt / kLanesPerRow, lr = gt % kLanesPerRow;
   const int64_t stride_t = a.stride_t[which];
   for (int s = 0; s < num_starts; ++s) {
-    const int t = starts[s];
-    const int64_t slot = a.slots[t];
+    const int at_t = starts[s];
+    const int64_t slot = slot_of[at_t + 1];
     const int off = static_cast<int>(slot & (P - 1));
     const int64_t block = slot >> a.shift;
+    float* scale_at = a.scale[which] + block * a.kv_heads + h;
+    const float old_scale = off ? *scale_at : 0.f;
     int n = 0;  // the run's length
     for (int i0 = 0; i0 < P; i0 += 32) {
       const int i = i0 + lane;
-      const bool same = off + i < P && t + i < a.tokens && a.slots[t + i] == slot + i;
-      const uint32_t m = __ballot_sync(0xFFFFFFFFu, same);
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, off + i < P && slot_of[at_t + 1 + i] == slot + i);
       n += m == 0xFFFFFFFFu ? 32 : __ffs(~m) - 1;
       if (m != 0xFFFFFFFFu) break;
     }
-    const uint16_t* src = a.x[which] + t * stride_t + h * a.stride_h[which] + lr * 8;
-    float* scale_at = a.scale[which] + block * a.kv_heads + h;
+    const uint16_t* src = a.x[which] + (t0 + at_t) * stride_t + h * a.stride_h[which] + lr * 8;
     uint8_t* dst = a.codes[which] + (block * a.kv_heads + h) * (static_cast<int64_t>(P) * D) + lr * 8;
-    const float old_scale = off ? *scale_at : 0.f;
-    uint4 v[kPasses];
+    uint4 v[PASSES];
 #pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
+    for (int p = 0; p < PASSES; ++p) {
       const int row = row0 + p * kRowsPerPass;
-      if (row < n) v[p] = *reinterpret_cast<const uint4*>(src + row * stride_t);
-      else v[p] = make_uint4(0, 0, 0, 0);
+      v[p] = row < n ? *reinterpret_cast<const uint4*>(src + row * stride_t) : make_uint4(0, 0, 0, 0);
     }
     // largest |x| as 16-bit patterns, two at a time: finite values order like their patterns
     uint32_t m2 = 0;
 #pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
+    for (int p = 0; p < PASSES; ++p)
       m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v[p].x & 0x7FFF7FFFu, v[p].y & 0x7FFF7FFFu),
                                  __vmaxu2(v[p].z & 0x7FFF7FFFu, v[p].w & 0x7FFF7FFFu)));
-    }
     constexpr uint32_t kInf = F16 ? 0x7C00u : 0x7F80u;
     uint32_t m1 = max(m2 & 0xFFFFu, m2 >> 16);
     if (m1 >= kInf) {  // an Inf or NaN among this thread's values: only the finite ones count
       m1 = 0;
 #pragma unroll
-      for (int p = 0; p < kPasses; ++p) {
+      for (int p = 0; p < PASSES; ++p) {
         const uint32_t w[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -323,7 +326,7 @@ __global__ void __launch_bounds__(kKvAppendThreads) kv_append_kernel(const KvApp
     }
     const float inv = 1.f / scale;
 #pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
+    for (int p = 0; p < PASSES; ++p) {
       const int row = row0 + p * kRowsPerPass;
       if (row < n) {
         const float2 x0 = kv_unpack2<F16>(v[p].x), x1 = kv_unpack2<F16>(v[p].y), x2 = kv_unpack2<F16>(v[p].z),

@@ -277,7 +277,7 @@ __device__ __forceinline__ uint64_t kv_add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-template <int FMT, bool F16, int D>
+template <int FMT, int D>
 __global__ void __launch_bounds__(kKvManyThreads, 1)
     kv_attention_many_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                              const KvAttnArgs a, int most_q, uint8_t* workspace) {
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
           const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 y = kv_unpack2<F16>(u[j]);
+            const float2 y = kv_unpack2(u[j], a.f16);
             amax = fmaxf(amax, fmaxf(fabsf(y.x), fabsf(y.y)));
           }
         }
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
           uint32_t f[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 y = kv_unpack2<F16>(u[j]);
+            const float2 y = kv_unpack2(u[j], a.f16);
             f[j] = kv_pack_f16(y.x * mul, y.y * mul);
           }
           *reinterpret_cast<uint4*>(sQ + (i >> 3) * (128 * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4)) =
@@ -760,8 +760,8 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             *reinterpret_cast<uint4*>(a.out + at_row * D + 32 * j + 8 * k) =
-                make_uint4(kv_pack_out<F16>(f[8 * k], f[8 * k + 1]), kv_pack_out<F16>(f[8 * k + 2], f[8 * k + 3]),
-                           kv_pack_out<F16>(f[8 * k + 4], f[8 * k + 5]), kv_pack_out<F16>(f[8 * k + 6], f[8 * k + 7]));
+                make_uint4(kv_pack_out(f[8 * k], f[8 * k + 1], a.f16), kv_pack_out(f[8 * k + 2], f[8 * k + 3], a.f16),
+                           kv_pack_out(f[8 * k + 4], f[8 * k + 5], a.f16), kv_pack_out(f[8 * k + 6], f[8 * k + 7], a.f16));
         } else if (live) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)

@@ -164,8 +164,10 @@ mx_status kv_block_tables(int32_t* block_tables, int64_t requests, int64_t max_b
   a.capacity = static_cast<int>(free_capacity);
   a.num_tokens = static_cast<int>(num_tokens);
   a.shift = shift;
-  const int64_t want = (num_tokens + kKvTablesThreads - 1) / kKvTablesThreads;
-  const unsigned grid = static_cast<unsigned>(want < 1 ? 1 : want > 128 ? 128 : want);
+  a.wide = aligned(slot_map, 16) && aligned(positions, 16);
+  // four tokens a thread, up to about two CTAs a SM; every CTA scans the requests for itself
+  const int64_t want = (num_tokens + 4 * kKvTablesThreads - 1) / (4 * kKvTablesThreads);
+  const unsigned grid = static_cast<unsigned>(want < 1 ? 1 : want > 304 ? 304 : want);
   if (pdl_launch(kv_block_tables_kernel, grid, kKvTablesThreads, 3 * 4 * (static_cast<size_t>(requests) + 1),
                  as_stream(stream), a) != cudaSuccess)
     return MX_ERR_CUDA;

@@ -70,22 +70,33 @@ struct KvJob {  // a range of the list, and the unit that it begins in
 
 constexpr size_t kKvSlotsAt = sizeof(KvJob) * kKvMaxCtas;  // in the workspace, behind the jobs
 
+// A segment as the loading warp tells the others of it, with its queries; count = 0: no more.
+struct alignas(16) KvFewSegment {
+  int count, token;            // tiles, and the first one's first token
+  int rows, q0, len, head;
+  int any_lo, all_lo, all_hi;  // tokens from any_lo on are seen by some row, [all_lo, all_hi) by all
+  int part;                    // 0: the whole unit; 1 + slot: a part of it
+};
+
 template <int D, int NT>
 struct KvFewCfg {
   static constexpr int ROWS = 8 * NT;
-  static constexpr int STAGES = 3;
+  static constexpr int STAGES = D == 128 ? 3 : 5;
   static constexpr int HALF = kKvTile * D;          // codes of K, or of V, in a tile
+  static constexpr int JOIN = NT < 2 ? NT : 2;      // 8-row tiles that are joined at a time
   static constexpr int O_STRIDE = D + 4;
-  static constexpr int OFF_O = STAGES * 2 * HALF;   // float [warps][ROWS][O_STRIDE]
-  static constexpr int OFF_ML = OFF_O + 4 * kKvWarps * ROWS * O_STRIDE;  // float2 [warps][ROWS]
-  static constexpr int OFF_Q = OFF_ML + 8 * kKvWarps * ROWS;            // uint2 [D / 16][NT][32]
-  static constexpr int OFF_QF = OFF_Q + (D / 16) * NT * 32 * 8;         // float [ROWS]
-  static constexpr int OFF_SEEN = OFF_QF + 4 * ROWS;                    // int2 [ROWS]
-  static constexpr int OFF_NAN = OFF_SEEN + 8 * ROWS;                   // u32 [ROWS][D / 32], bits of d
-  static constexpr int OFF_SC = OFF_NAN + 4 * ROWS * (D / 32);          // float4 [STAGES][4]
+  static constexpr int OFF_O = STAGES * 2 * HALF;   // float [warps][8 JOIN][O_STRIDE]
+  static constexpr int OFF_ML = OFF_O + 4 * kKvWarps * 8 * JOIN * O_STRIDE;  // float2 [warps][8 JOIN]
+  // two segments' queries
+  static constexpr int OFF_Q = OFF_ML + 8 * kKvWarps * 8 * JOIN;        // uint2 [2][D / 16][NT][32]
+  static constexpr int OFF_QF = OFF_Q + 2 * (D / 16) * NT * 32 * 8;     // float [2][ROWS]
+  static constexpr int OFF_SEEN = OFF_QF + 2 * 4 * ROWS;                // int2 [2][ROWS]
+  static constexpr int OFF_NAN = OFF_SEEN + 2 * 8 * ROWS;               // u32 [2][ROWS][D / 32], bits of d
+  static constexpr int OFF_SEG = OFF_NAN + 2 * 4 * ROWS * (D / 32);     // KvFewSegment [2]
+  static constexpr int OFF_SC = OFF_SEG + 2 * sizeof(KvFewSegment);     // float4 [STAGES][4]
   static constexpr int OFF_BAR = OFF_SC + 16 * 4 * STAGES;
-  static constexpr int SMEM = OFF_BAR + 8 * 2 * STAGES + 16 + 1024;
-  static constexpr int CTAS = NT == 1 ? 3 : 2;
+  static constexpr int SMEM = OFF_BAR + 8 * (2 * STAGES + 5) + 16 + 1024;
+  static constexpr int CTAS = NT == 1 ? (D == 64 ? 4 : 3) : 2;
   static constexpr size_t SLOT = static_cast<size_t>(ROWS) * (D + 2) * 4;  // (O, m, l) of a segment
 };
 
@@ -282,10 +293,14 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
   float* sQF = reinterpret_cast<float*>(smem + Cfg::OFF_QF);
   int2* sSeen = reinterpret_cast<int2*>(smem + Cfg::OFF_SEEN);
   uint32_t* sNan = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_NAN);
+  KvFewSegment* sSeg = reinterpret_cast<KvFewSegment*>(smem + Cfg::OFF_SEG);
   float4* sSC = reinterpret_cast<float4*>(smem + Cfg::OFF_SC);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);
   uint64_t* empty = full + Cfg::STAGES;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + Cfg::STAGES);
+  uint64_t* seg_full = empty + Cfg::STAGES;  // [2]
+  uint64_t* seg_empty = seg_full + 2;        // [2]
+  uint64_t* join_bar = seg_empty + 2;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(join_bar + 1);
   __shared__ KvPlanSmem plan;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int group = a.heads / a.kv_heads;
@@ -295,6 +310,11 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
       mbar_init(&full[i], 2);  // the boxes' bytes; the scales
       mbar_init(&empty[i], kKvWarps);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&seg_full[i], 1);
+      mbar_init(&seg_empty[i], kKvWarps);
+    }
+    mbar_init(join_bar, kKvWarps);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&tmK);
@@ -318,11 +338,79 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
     };
     const int P = 1 << a.shift, rows_box = min(P, kKvTile), boxes = kKvTile / rows_box;
     const int most_tiles = P > kKvTile ? 32 * P / kKvTile - 1 : 32 * P / kKvTile;  // (a segment may start inside a block)
+    const long long range_start = w.pos;
     int left = 0;
+    uint32_t seg = 0;
+    // tells the others of the next segment and brings its queries, as the fragments of Q^T
+    auto next_segment = [&]() {
+      const bool more = kv_next_segment(a, most_q, w);
+      const int buf = seg & 1;
+      if (!mbar_wait(&seg_empty[buf], ((seg >> 1) & 1) ^ 1, abort_flag, kSiteProducerEmpty)) return false;
+      ++seg;
+      const int rows = w.req.rows_q * group, pos0 = w.req.len - w.req.rows_q;  // (pos0: the first query's position)
+      if (lane == 0) {
+        KvFewSegment v;
+        v.count = more ? w.count : 0;
+        v.token = (w.req.first_tile + w.tile) * kKvTile;
+        v.rows = rows;
+        v.q0 = w.req.q0;
+        v.len = w.req.len;
+        v.head = w.h;
+        v.any_lo = a.window ? pos0 - a.window + 1 : 0;
+        v.all_lo = a.window ? w.req.len - a.window : 0;
+        v.all_hi = a.causal ? min(w.req.len, pos0 + 1) : w.req.len;
+        v.part = w.count == w.req.tiles ? 0 : w.base < range_start ? 1 : 2;
+        sSeg[buf] = v;
+      }
+      if (more) {
+        for (int i = lane; i < Cfg::ROWS * (D / 32); i += 32) sNan[buf * Cfg::ROWS * (D / 32) + i] = 0;
+        const int g = lane >> 2, c = lane & 3;
+#pragma unroll 1
+        for (int nt = 0; nt < NT; ++nt) {
+          const int row = nt * 8 + g;
+          uint4 x[LD / 8];
+          float amax = 0.f;
+          const int qi = row / group, hg = row - qi * group;
+          const uint16_t* src = a.q + (w.req.q0 + qi) * a.stride_t + (w.h * group + hg) * a.stride_h + c * LD;
+#pragma unroll
+          for (int i = 0; i < LD / 8; ++i) x[i] = row < rows ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
+          float f[LD];
+#pragma unroll
+          for (int i = 0; i < LD / 8; ++i) {
+            const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 y = kv_unpack2(u[j], a.f16);
+              f[8 * i + 2 * j] = y.x;
+              f[8 * i + 2 * j + 1] = y.y;
+              amax = fmaxf(amax, fmaxf(fabsf(y.x), fabsf(y.y)));
+            }
+          }
+          amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+          amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+          // 2^e with amax 2^e in [2^14, 2^15)
+          const int e = min(14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127), 120);
+          const float mul = amax > 0.f ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : 1.f;
+#pragma unroll
+          for (int i = 0; i < KS; ++i)
+            sQ[((buf * KS + i) * NT + nt) * 32 + lane] = make_uint2(kv_pack_f16(f[4 * i] * mul, f[4 * i + 1] * mul),
+                                                                    kv_pack_f16(f[4 * i + 2] * mul, f[4 * i + 3] * mul));
+          if (c == 0) {
+            sQF[buf * Cfg::ROWS + row] = a.scale_log2 / mul;
+            const int p = pos0 + (row < rows ? qi : 0);
+            sSeen[buf * Cfg::ROWS + row] =
+                make_int2(a.window ? p - a.window + 1 : 0, a.causal ? min(w.req.len, p + 1) : w.req.len);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_full[buf]);
+      return more;
+    };
     auto fetch = [&](Chunk& ch) {
       ch.tiles = 0;
       if (!left) {
-        if (!kv_next_segment(a, most_q, w)) return;
+        if (!next_segment()) return;
         left = w.count;
       }
       ch.tiles = min(left, most_tiles);
@@ -395,60 +483,25 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
   // -------------------------------------------------------------------- products and softmax
   const int g = lane >> 2, c = lane & 3;
   int stage = 0;
-  uint32_t phase = 0;
-  const long long range_start = w.pos;
-  while (kv_next_segment(a, most_q, w)) {
-    const KvRequest req = w.req;
-    const int count = w.count;
-    const int rows = req.rows_q * group;
-    const int pos0 = req.len - req.rows_q;  // the first query's position
-    // queries of n-tile `warp`, as the fragments of Q^T
-    for (int nt = warp; nt < NT; nt += kKvWarps) {
-      const int row = nt * 8 + g;
-      uint4 x[LD / 8];
-      float amax = 0.f;
-      float f[LD];
-      if (row < rows) {
-        const int qi = row / group, hg = row - qi * group;
-        const uint16_t* src = a.q + (req.q0 + qi) * a.stride_t + (w.h * group + hg) * a.stride_h + c * LD;
-#pragma unroll
-        for (int i = 0; i < LD / 8; ++i) x[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
-      } else {
-#pragma unroll
-        for (int i = 0; i < LD / 8; ++i) x[i] = make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int i = 0; i < LD / 8; ++i) {
-        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 y = kv_unpack2(u[j], a.f16);
-          f[8 * i + 2 * j] = y.x;
-          f[8 * i + 2 * j + 1] = y.y;
-          amax = fmaxf(amax, fmaxf(fabsf(y.x), fabsf(y.y)));
-        }
-      }
-      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-      // 2^e with amax 2^e in [2^14, 2^15)
-      const int e = min(14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127), 120);
-      const float mul = amax > 0.f ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : 1.f;
-#pragma unroll
-      for (int i = 0; i < KS; ++i)
-        sQ[(i * NT + nt) * 32 + lane] = make_uint2(kv_pack_f16(f[4 * i] * mul, f[4 * i + 1] * mul),
-                                                   kv_pack_f16(f[4 * i + 2] * mul, f[4 * i + 3] * mul));
-      if (c == 0) {
-        sQF[row] = a.scale_log2 / mul;
-        const int p = pos0 + (row < rows ? row / group : 0);
-        sSeen[row] = make_int2(a.window ? p - a.window + 1 : 0, a.causal ? min(req.len, p + 1) : req.len);
-      }
-    }
-    for (int i = tid; i < Cfg::ROWS * (D / 32); i += 32 * kKvWarps) sNan[i] = 0;
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * kKvWarps) : "memory");
+  uint32_t phase = 0, joins = 0;
+  auto warps_meet = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(join_bar);
+    return mbar_wait(join_bar, joins++ & 1, abort_flag, kSiteEpiTmemFull);
+  };
+  for (uint32_t seg = 0;; ++seg) {
+    const int buf = seg & 1;
+    if (!mbar_wait(&seg_full[buf], (seg >> 1) & 1, abort_flag, kSiteMmaFull)) break;
+    const KvFewSegment v = sSeg[buf];
+    if (v.count == 0) break;
+    const uint2* q_frag = sQ + buf * KS * NT * 32 + lane;
+    const float* q_mul = sQF + buf * Cfg::ROWS;
+    const int2* q_seen = sSeen + buf * Cfg::ROWS;
+    uint32_t* q_nan = sNan + buf * Cfg::ROWS * (D / 32);
     uint2 qf[NT == 1 ? KS : 1];
     if (NT == 1) {
 #pragma unroll
-      for (int i = 0; i < KS; ++i) qf[i] = sQ[i * 32 + lane];
+      for (int i = 0; i < KS; ++i) qf[i] = q_frag[i * 32];
     }
     float m[2 * NT], l[2 * NT];
 #pragma unroll
@@ -463,19 +516,18 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][n][j] = 0.f;
-    // what every row sees, and what any row sees
-    const int all_lo = a.window ? req.len - a.window : 0, all_hi = a.causal ? min(req.len, pos0 + 1) : req.len;
-    const int any_lo = a.window ? pos0 - a.window + 1 : 0;
 
-    for (int i = 0; i < count; ++i) {
-      const int token = (req.first_tile + w.tile + i) * kKvTile;
-      const bool ok = mbar_wait(&full[stage], phase, abort_flag, kSiteMmaFull);
+    bool ok = true;
+    for (int i = 0; i < v.count; ++i) {
+      const int token = v.token + i * kKvTile;
+      ok = mbar_wait(&full[stage], phase, abort_flag, kSiteMmaFull);
       const uint8_t* sK = smem + stage * 2 * Cfg::HALF + warp * 16 * D;
       const uint8_t* sV = sK + Cfg::HALF;
       const float4 sc = sSC[stage * 4 + warp];
-      const bool edge = token < all_lo || token + kKvTile > all_hi;
+      const bool edge = token < v.all_lo || token + kKvTile > v.all_hi;
       const int t0 = token + 16 * warp;
-      if (ok) {
+      if (!ok) break;
+      {
         // S^T
         float s[NT][4];
 #pragma unroll
@@ -496,7 +548,7 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
           const uint32_t a1 = kv_codes_to_f16x2<FMT>(wb & 0xFFFFu), a3 = kv_codes_to_f16x2<FMT>(wb >> 16);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const uint2 b = NT == 1 ? qf[NT == 1 ? k : 0] : sQ[(k * NT + n) * 32 + lane];
+            const uint2 b = NT == 1 ? qf[NT == 1 ? k : 0] : q_frag[(k * NT + n) * 32];
             kv_mma(s[n], a0, a1, a2, a3, b.x, b.y);
           }
         }
@@ -506,12 +558,12 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[n][j] = fmaf(s[n][j], sQF[n * 8 + 2 * c + (j & 1)] * sc.x, sc.y);
+          for (int j = 0; j < 4; ++j) s[n][j] = fmaf(s[n][j], q_mul[n * 8 + 2 * c + (j & 1)] * sc.x, sc.y);
           if (edge) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int t = t0 + g + 8 * (j >> 1);
-              const int2 seen = sSeen[n * 8 + 2 * c + (j & 1)];
+              const int2 seen = q_seen[n * 8 + 2 * c + (j & 1)];
               if (t < seen.x || t >= seen.y) s[n][j] = -INFINITY;
             }
           }
@@ -551,20 +603,20 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
           pb[n][1] = kv_transpose8x8(kv_pack_f16(p2, p3));
         }
         // V: tokens 2c, 2c + 1, 2c + 8, 2c + 9, this lane's D / 8 values of each
-        uint32_t v[4][VW];
+        uint32_t vw[4][VW];
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
           const int t = 2 * c + (tt & 1) + 8 * (tt >> 1);
           if (D == 128) {
             const uint4 x = *reinterpret_cast<const uint4*>(sV + t * 128 + ((g ^ (t & 7)) << 4));
-            v[tt][0] = x.x;
-            v[tt][1] = x.y;
-            v[tt][VW - 2] = x.z;
-            v[tt][VW - 1] = x.w;
+            vw[tt][0] = x.x;
+            vw[tt][1] = x.y;
+            vw[tt][VW - 2] = x.z;
+            vw[tt][VW - 1] = x.w;
           } else {
             const uint2 x = *reinterpret_cast<const uint2*>(sV + t * 64 + (((g >> 1) ^ ((t >> 1) & 3)) << 4) + (g & 1) * 8);
-            v[tt][0] = x.x;
-            v[tt][1] = x.y;
+            vw[tt][0] = x.x;
+            vw[tt][1] = x.y;
           }
         }
         if (edge) {
@@ -574,8 +626,8 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
             const int t = t0 + 2 * c + (tt & 1) + 8 * (tt >> 1);
 #pragma unroll
             for (int j = 0; j < VW; ++j) {
-              if (t < any_lo || t >= req.len) v[tt][j] = 0;
-              bad |= kv_nan_bytes<FMT>(v[tt][j]);
+              if (t < v.any_lo || t >= v.len) vw[tt][j] = 0;
+              bad |= kv_nan_bytes<FMT>(vw[tt][j]);
             }
           }
           if (bad) {  // (rare) for each NaN: note the rows that see it, clear the code
@@ -583,13 +635,13 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
             for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
               for (int j = 0; j < VW; ++j) {
-                const uint32_t x = kv_nan_bytes<FMT>(v[tt][j]);
-                v[tt][j] &= ~((x >> 7) * 0xFFu);
+                const uint32_t x = kv_nan_bytes<FMT>(vw[tt][j]);
+                vw[tt][j] &= ~((x >> 7) * 0xFFu);
                 const int t = t0 + 2 * c + (tt & 1) + 8 * (tt >> 1), d = (D / 8) * g + 4 * j;
                 if (x)
                   for (int row = 0; row < Cfg::ROWS; ++row)
-                    if (t >= sSeen[row].x && t < sSeen[row].y)
-                      atomicOr(&sNan[row * (D / 32) + (d >> 5)],
+                    if (t >= q_seen[row].x && t < q_seen[row].y)
+                      atomicOr(&q_nan[row * (D / 32) + (d >> 5)],
                                ((x >> 7 & 1) | (x >> 14 & 2) | (x >> 21 & 4) | (x >> 28 & 8)) << (d & 31));
               }
           }
@@ -597,8 +649,8 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
         // O^T
 #pragma unroll
         for (int j = 0; j < VW; ++j) {
-          const uint32_t x01 = __byte_perm(v[0][j], v[1][j], 0x5140), y01 = __byte_perm(v[0][j], v[1][j], 0x7362);
-          const uint32_t x23 = __byte_perm(v[2][j], v[3][j], 0x5140), y23 = __byte_perm(v[2][j], v[3][j], 0x7362);
+          const uint32_t x01 = __byte_perm(vw[0][j], vw[1][j], 0x5140), y01 = __byte_perm(vw[0][j], vw[1][j], 0x7362);
+          const uint32_t x23 = __byte_perm(vw[2][j], vw[3][j], 0x5140), y23 = __byte_perm(vw[2][j], vw[3][j], 0x7362);
           const uint32_t a0 = kv_codes_to_f16x2<FMT>(x01 & 0xFFFFu), a1 = kv_codes_to_f16x2<FMT>(x01 >> 16);
           const uint32_t a2 = kv_codes_to_f16x2<FMT>(x23 & 0xFFFFu), a3 = kv_codes_to_f16x2<FMT>(x23 >> 16);
           const uint32_t b0 = kv_codes_to_f16x2<FMT>(y01 & 0xFFFFu), b1 = kv_codes_to_f16x2<FMT>(y01 >> 16);
@@ -618,63 +670,74 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
       }
     }
 
+    if (!ok) break;
+
     // the four warps' (m, l, O) through shared memory
 #pragma unroll
-    for (int j = 0; j < 2 * NT; ++j) {
+    for (int j = 0; j < 2 * NT; ++j)
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) l[j] += __shfl_xor_sync(0xFFFFFFFFu, l[j], o);
-      const int row = (j >> 1) * 8 + 2 * c + (j & 1);
-      if (g == 0) sML[warp * Cfg::ROWS + row] = make_float2(m[j], l[j]);
+    float* part = reinterpret_cast<float*>(workspace + kKvSlotsAt + (2 * blockIdx.x + max(v.part - 1, 0)) * Cfg::SLOT);
 #pragma unroll
-      for (int k = 0; k < VW; ++k)
-        *reinterpret_cast<float4*>(&sO[(warp * Cfg::ROWS + row) * Cfg::O_STRIDE + (D / 8) * g + 4 * k]) =
-            make_float4(acc[2 * k][j >> 1][j & 1], acc[2 * k][j >> 1][2 + (j & 1)], acc[2 * k + 1][j >> 1][j & 1],
-                        acc[2 * k + 1][j >> 1][2 + (j & 1)]);
+    for (int n0 = 0; n0 < NT; n0 += Cfg::JOIN) {
+      if (!(ok = warps_meet())) break;  // what was joined before has been read
+#pragma unroll
+      for (int j = 2 * n0; j < 2 * (n0 + Cfg::JOIN); ++j) {
+        const int at = warp * 8 * Cfg::JOIN + ((j >> 1) - n0) * 8 + 2 * c + (j & 1);
+        if (g == 0) sML[at] = make_float2(m[j], l[j]);
+#pragma unroll
+        for (int k = 0; k < VW; ++k)
+          *reinterpret_cast<float4*>(&sO[at * Cfg::O_STRIDE + (D / 8) * g + 4 * k]) =
+              make_float4(acc[2 * k][j >> 1][j & 1], acc[2 * k][j >> 1][2 + (j & 1)], acc[2 * k + 1][j >> 1][j & 1],
+                          acc[2 * k + 1][j >> 1][2 + (j & 1)]);
+      }
+      if (!(ok = warps_meet())) break;
+      const int rows = min(v.rows - 8 * n0, 8 * Cfg::JOIN);
+      for (int i = tid; i < rows * (D / 4); i += 32 * kKvWarps) {
+        const int at = i / (D / 4), d = i % (D / 4) * 4, row = 8 * n0 + at;
+        float2 ml[kKvWarps];
+        float most = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kKvWarps; ++k) {
+          ml[k] = sML[k * 8 * Cfg::JOIN + at];
+          most = fmaxf(most, ml[k].x);
+        }
+        const float ref = most == -INFINITY ? 0.f : most;
+        float sum = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kKvWarps; ++k) {
+          const float f = kv_exp2(ml[k].x - ref);
+          const float4 x = *reinterpret_cast<const float4*>(&sO[(k * 8 * Cfg::JOIN + at) * Cfg::O_STRIDE + d]);
+          sum = fmaf(ml[k].y, f, sum);
+          o.x = fmaf(x.x, f, o.x);
+          o.y = fmaf(x.y, f, o.y);
+          o.z = fmaf(x.z, f, o.z);
+          o.w = fmaf(x.w, f, o.w);
+        }
+        if (const uint32_t nan = q_nan[row * (D / 32) + (d >> 5)] >> (d & 31) & 15) {
+          if (nan & 1) o.x = NAN;
+          if (nan & 2) o.y = NAN;
+          if (nan & 4) o.z = NAN;
+          if (nan & 8) o.w = NAN;
+        }
+        if (v.part == 0) {
+          const int qi = row / group, hg = row - qi * group;
+          const int64_t at_row = static_cast<int64_t>(v.q0 + qi) * a.heads + v.head * group + hg;
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          *reinterpret_cast<uint2*>(a.out + at_row * D + d) =
+              sum == 0.f ? make_uint2(0, 0)
+                         : make_uint2(kv_pack_out(o.x * inv, o.y * inv, a.f16), kv_pack_out(o.z * inv, o.w * inv, a.f16));
+          if (d == 0) a.lse[at_row] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+        } else {
+          *reinterpret_cast<float4*>(part + row * D + d) = o;
+          if (d == 0) *reinterpret_cast<float2*>(part + Cfg::ROWS * D + 2 * row) = make_float2(most, sum);
+        }
+      }
     }
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * kKvWarps) : "memory");
-    const bool whole = count == req.tiles;
-    const int slot = w.base < range_start ? 0 : 1;
-    float* part = reinterpret_cast<float*>(workspace + kKvSlotsAt + (2 * blockIdx.x + slot) * Cfg::SLOT);
-    for (int i = tid; i < rows * (D / 4); i += 32 * kKvWarps) {
-      const int row = i / (D / 4), d = i % (D / 4) * 4;
-      float2 ml[kKvWarps];
-      float most = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < kKvWarps; ++k) {
-        ml[k] = sML[k * Cfg::ROWS + row];
-        most = fmaxf(most, ml[k].x);
-      }
-      const float at = most == -INFINITY ? 0.f : most;
-      float sum = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < kKvWarps; ++k) {
-        const float f = kv_exp2(ml[k].x - at);
-        const float4 x = *reinterpret_cast<const float4*>(&sO[(k * Cfg::ROWS + row) * Cfg::O_STRIDE + d]);
-        sum = fmaf(ml[k].y, f, sum);
-        o.x = fmaf(x.x, f, o.x);
-        o.y = fmaf(x.y, f, o.y);
-        o.z = fmaf(x.z, f, o.z);
-        o.w = fmaf(x.w, f, o.w);
-      }
-      if (const uint32_t nan = sNan[row * (D / 32) + (d >> 5)] >> (d & 31) & 15) {
-        if (nan & 1) o.x = NAN;
-        if (nan & 2) o.y = NAN;
-        if (nan & 4) o.z = NAN;
-        if (nan & 8) o.w = NAN;
-      }
-      if (whole) {
-        const int qi = row / group, hg = row - qi * group;
-        const int64_t at_row = static_cast<int64_t>(req.q0 + qi) * a.heads + w.h * group + hg;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        *reinterpret_cast<uint2*>(a.out + at_row * D + d) =
-            sum == 0.f ? make_uint2(0, 0) : make_uint2(kv_pack_out(o.x * inv, o.y * inv, a.f16), kv_pack_out(o.z * inv, o.w * inv, a.f16));
-        if (d == 0) a.lse[at_row] = sum == 0.f ? -INFINITY : (at + log2f(sum)) * kLn2;
-      } else {
-        *reinterpret_cast<float4*>(part + row * D + d) = o;
-        if (d == 0) *reinterpret_cast<float2*>(part + Cfg::ROWS * D + 2 * row) = make_float2(most, sum);
-      }
-    }
+    if (!ok) break;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&seg_empty[buf]);
   }
 }
 

@@ -24,6 +24,7 @@ struct KvTablesArgs {
   int32_t* positions;      // [num_tokens]
   int32_t* info;           // {free blocks left, blocks missing}
   int requests, max_blocks, capacity, num_tokens, shift;  // P = 1 << shift
+  int wide;                // slots and positions are 16-byte aligned
 };
 
 constexpr int kKvTablesThreads = 512;
@@ -59,55 +60,60 @@ __global__ void __launch_bounds__(kKvTablesThreads) kv_block_tables_kernel(const
   int* gone_at = need_at + R + 1;     // [R + 1]
   __shared__ long long warp_sums[3][kKvTablesThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  long long carry[3] = {0, 0, 0};
   bool bad = false;
   const long long longest = static_cast<long long>(a.max_blocks) << a.shift;
-  for (int r0 = 0; r0 < R; r0 += kKvTablesThreads) {
-    const int r = r0 + tid;
-    long long v[3] = {0, 0, 0};
-    if (r < R) {
-      const int before = a.before[r], after = a.after[r];
-      if (before < 0 || after < 0 || before > longest || after > longest) {
-        bad = true;
-      } else {
-        const int held = (before + P - 1) >> a.shift, want = (after + P - 1) >> a.shift;
-        v[0] = max(after - before, 0);
-        v[1] = max(want - held, 0);
-        v[2] = max(held - want, 0);
-      }
+  // each thread takes a stretch of the requests; the stretches' sums are scanned
+  const int per = (R + kKvTablesThreads - 1) / kKvTablesThreads;
+  const int first_r = min(tid * per, R), end_r = min(first_r + per, R);
+  auto moves = [&](int r, int (&v)[3]) {
+    const int before = a.before[r], after = a.after[r];
+    v[0] = v[1] = v[2] = 0;
+    if (before < 0 || after < 0 || before > longest || after > longest) return false;
+    const int held = (before + P - 1) >> a.shift, want = (after + P - 1) >> a.shift;
+    v[0] = max(after - before, 0);
+    v[1] = max(want - held, 0);
+    v[2] = max(held - want, 0);
+    return true;
+  };
+  long long sum[3] = {0, 0, 0}, carry[3];
+  for (int r = first_r; r < end_r; ++r) {
+    int v[3];
+    if (!moves(r, v)) bad = true;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) sum[k] += v[k];
+  }
+  long long at[3];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    long long incl = sum[k];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += u;
     }
-    long long incl[3];
+    if (lane == 31) warp_sums[k][warp] = incl;
+    at[k] = incl - sum[k];
+  }
+  __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      incl[k] = v[k];
+  for (int k = 0; k < 3; ++k) {
+    long long s = lane < kKvTablesThreads / 32 ? warp_sums[k][lane] : 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xFFFFFFFFu, incl[k], o);
-        if (lane >= o) incl[k] += u;
-      }
-      if (lane == 31) warp_sums[k][warp] = incl[k];
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xFFFFFFFFu, s, o);
+      if (lane >= o) s += u;
     }
-    __syncthreads();
-    long long base[3], total[3];
+    carry[k] = __shfl_sync(0xFFFFFFFFu, s, 31);
+    at[k] += warp ? __shfl_sync(0xFFFFFFFFu, s, warp - 1) : 0;
+  }
+  for (int r = first_r; r < end_r; ++r) {  // (sums past 2^31 are only ever those of a call that is refused below)
+    int v[3];
+    moves(r, v);
+    new_at[r] = static_cast<int>(at[0]);
+    need_at[r] = static_cast<int>(at[1]);
+    gone_at[r] = static_cast<int>(at[2]);
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      long long s = lane < kKvTablesThreads / 32 ? warp_sums[k][lane] : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xFFFFFFFFu, s, o);
-        if (lane >= o) s += u;
-      }
-      total[k] = __shfl_sync(0xFFFFFFFFu, s, 31);
-      base[k] = warp ? __shfl_sync(0xFFFFFFFFu, s, warp - 1) : 0;
-    }
-    if (r < R) {  // (sums past 2^31 are only ever those of a call that is refused below)
-      new_at[r] = static_cast<int>(carry[0] + base[0] + incl[0] - v[0]);
-      need_at[r] = static_cast<int>(carry[1] + base[1] + incl[1] - v[1]);
-      gone_at[r] = static_cast<int>(carry[2] + base[2] + incl[2] - v[2]);
-    }
-#pragma unroll
-    for (int k = 0; k < 3; ++k) carry[k] += total[k];
-    __syncthreads();
+    for (int k = 0; k < 3; ++k) at[k] += v[k];
   }
   const long long count = *a.free_count, avail = count + carry[2], left = avail - carry[1];
   if (count < 0 || avail > a.capacity || carry[0] > a.num_tokens) bad = true;
@@ -146,20 +152,49 @@ __global__ void __launch_bounds__(kKvTablesThreads) kv_block_tables_kernel(const
     }
     for (int i = first; i < pushes; i += step) a.free_list[icount + i] = pushed(i);
   }
+  // four tokens a thread: one search, then along the prefix
   const int tokens = fits ? new_at[R] : 0;
-  for (int t = first; t < a.num_tokens; t += step) {
-    int64_t slot = -1;
-    int pos = -1;
-    if (t < tokens) {
-      const int r = kv_prefix_find(new_at, R, t);
-      const int before = a.before[r], held = (before + P - 1) >> a.shift;
-      pos = before + (t - new_at[r]);
-      const int b = pos >> a.shift;
-      const int block = b < held ? a.tables[static_cast<int64_t>(r) * a.max_blocks + b] : popped(need_at[r] + b - held);
-      slot = (static_cast<int64_t>(block) << a.shift) + (pos & (P - 1));
+  for (int64_t t0 = 4ll * first; t0 < a.num_tokens; t0 += 4ll * step) {
+    int64_t slot[4];
+    int pos[4];
+    int r = -1, next_at = 0, before = 0, held = 0, last_b = -1, block = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = static_cast<int>(t0) + i;
+      slot[i] = -1;
+      pos[i] = -1;
+      if (t < tokens) {
+        if (r < 0 || t >= next_at) {
+          if (r < 0) r = kv_prefix_find(new_at, R, t);
+          else
+            while (new_at[r + 1] <= t) ++r;
+          next_at = new_at[r + 1];
+          before = a.before[r];
+          held = (before + P - 1) >> a.shift;
+          last_b = -1;
+        }
+        pos[i] = before + (t - new_at[r]);
+        const int b = pos[i] >> a.shift;
+        if (b != last_b) {
+          block = b < held ? a.tables[static_cast<int64_t>(r) * a.max_blocks + b] : popped(need_at[r] + b - held);
+          last_b = b;
+        }
+        slot[i] = (static_cast<int64_t>(block) << a.shift) + (pos[i] & (P - 1));
+      }
     }
-    a.slots[t] = slot;
-    a.positions[t] = pos;
+    if (a.wide && t0 + 4 <= a.num_tokens) {
+      longlong2* s = reinterpret_cast<longlong2*>(a.slots + t0);
+      s[0] = make_longlong2(slot[0], slot[1]);
+      s[1] = make_longlong2(slot[2], slot[3]);
+      *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t0 + i < a.num_tokens) {
+          a.slots[t0 + i] = slot[i];
+          a.positions[t0 + i] = pos[i];
+        }
+    }
   }
 }
 
@@ -252,13 +287,17 @@ __global__ void __launch_bounds__(kKvAppendThreads, 5) kv_append_kernel(const Kv
   if (item >= 2 * a.kv_heads) return;  // (whole groups leave; the barriers below are a group's own)
   const int which = item / a.kv_heads, h = item - which * a.kv_heads;
   const int row0 = gt / kLanesPerRow, lr = gt % kLanesPerRow;
-  const int64_t stride_t = a.stride_t[which];
+  // (chosen, not indexed: an index would copy the arguments to local memory)
+  const uint16_t* x_at = which ? a.x[1] : a.x[0];
+  const int64_t stride_t = which ? a.stride_t[1] : a.stride_t[0], stride_h = which ? a.stride_h[1] : a.stride_h[0];
+  uint8_t* codes = which ? a.codes[1] : a.codes[0];
+  float* scales = which ? a.scale[1] : a.scale[0];
   for (int s = 0; s < num_starts; ++s) {
     const int at_t = starts[s];
     const int64_t slot = slot_of[at_t + 1];
     const int off = static_cast<int>(slot & (P - 1));
     const int64_t block = slot >> a.shift;
-    float* scale_at = a.scale[which] + block * a.kv_heads + h;
+    float* scale_at = scales + block * a.kv_heads + h;
     const float old_scale = off ? *scale_at : 0.f;
     int n = 0;  // the run's length
     for (int i0 = 0; i0 < P; i0 += 32) {
@@ -267,8 +306,8 @@ __global__ void __launch_bounds__(kKvAppendThreads, 5) kv_append_kernel(const Kv
       n += m == 0xFFFFFFFFu ? 32 : __ffs(~m) - 1;
       if (m != 0xFFFFFFFFu) break;
     }
-    const uint16_t* src = a.x[which] + (t0 + at_t) * stride_t + h * a.stride_h[which] + lr * 8;
-    uint8_t* dst = a.codes[which] + (block * a.kv_heads + h) * (static_cast<int64_t>(P) * D) + lr * 8;
+    const uint16_t* src = x_at + (t0 + at_t) * stride_t + h * stride_h + lr * 8;
+    uint8_t* dst = codes + (block * a.kv_heads + h) * (static_cast<int64_t>(P) * D) + lr * 8;
     uint4 v[PASSES];
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {

@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
-  pdl_prologue();
+  pdl_wait();  // (no early trigger: CTAs of the next kernel would take the places of this one's last CTAs)
   KvWalk w;
   kv_plan(a, most_q, plan, w);  // (its barriers also publish the mbarriers)
   if (tid == 0)
@@ -544,8 +544,9 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
           const uint4 x = ka[k / 4], y = kb[k / 4];
           const uint32_t wa = k % 4 == 0 ? x.x : k % 4 == 1 ? x.y : k % 4 == 2 ? x.z : x.w;
           const uint32_t wb = k % 4 == 0 ? y.x : k % 4 == 1 ? y.y : k % 4 == 2 ? y.z : y.w;
-          const uint32_t a0 = kv_codes_to_f16x2<FMT>(wa & 0xFFFFu), a2 = kv_codes_to_f16x2<FMT>(wa >> 16);
-          const uint32_t a1 = kv_codes_to_f16x2<FMT>(wb & 0xFFFFu), a3 = kv_codes_to_f16x2<FMT>(wb >> 16);
+          uint32_t a0, a1, a2, a3;
+          kv_codes4_to_f16<FMT>(wa, a0, a2);
+          kv_codes4_to_f16<FMT>(wb, a1, a3);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const uint2 b = NT == 1 ? qf[NT == 1 ? k : 0] : q_frag[(k * NT + n) * 32];
@@ -651,10 +652,11 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
         for (int j = 0; j < VW; ++j) {
           const uint32_t x01 = __byte_perm(vw[0][j], vw[1][j], 0x5140), y01 = __byte_perm(vw[0][j], vw[1][j], 0x7362);
           const uint32_t x23 = __byte_perm(vw[2][j], vw[3][j], 0x5140), y23 = __byte_perm(vw[2][j], vw[3][j], 0x7362);
-          const uint32_t a0 = kv_codes_to_f16x2<FMT>(x01 & 0xFFFFu), a1 = kv_codes_to_f16x2<FMT>(x01 >> 16);
-          const uint32_t a2 = kv_codes_to_f16x2<FMT>(x23 & 0xFFFFu), a3 = kv_codes_to_f16x2<FMT>(x23 >> 16);
-          const uint32_t b0 = kv_codes_to_f16x2<FMT>(y01 & 0xFFFFu), b1 = kv_codes_to_f16x2<FMT>(y01 >> 16);
-          const uint32_t b2 = kv_codes_to_f16x2<FMT>(y23 & 0xFFFFu), b3 = kv_codes_to_f16x2<FMT>(y23 >> 16);
+          uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+          kv_codes4_to_f16<FMT>(x01, a0, a1);
+          kv_codes4_to_f16<FMT>(x23, a2, a3);
+          kv_codes4_to_f16<FMT>(y01, b0, b1);
+          kv_codes4_to_f16<FMT>(y23, b2, b3);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             kv_mma(acc[2 * j][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);

@@ -209,6 +209,18 @@ __device__ __forceinline__ uint32_t kv_codes_to_f16x2(uint32_t two_codes) {
     asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e5m2x2 %0, lo;\n\t}" : "=r"(r) : "r"(two_codes));
   return r;
 }
+// four codes, low pair and high pair
+template <int FMT>
+__device__ __forceinline__ void kv_codes4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (FMT == 0)
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  else
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e5m2x2 %0, l;\n\tcvt.rn.f16x2.e5m2x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
 template <int FMT>
 __device__ __forceinline__ uint32_t kv_codes_from_floats(float lo, float hi) {
   return FMT == 0 ? cvt_e4m3x2(lo, hi) : cvt_e5m2x2(lo, hi);

@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
-  pdl_prologue();
+  pdl_wait();
   kv_clear_rest(a, D, blockIdx.x * kKvManyThreads + tid, gridDim.x * kKvManyThreads);
   uint8_t* nan_notes = workspace + kv_many_nan_at(a.requests) + blockIdx.x * Cfg::NAN_BYTES;
 
@@ -545,10 +545,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
             const uint32_t c[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
             uint32_t f[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              f[2 * j] = kv_codes_to_f16x2<FMT>(c[j] & 0xFFFFu);
-              f[2 * j + 1] = kv_codes_to_f16x2<FMT>(c[j] >> 16);
-            }
+            for (int j = 0; j < 4; ++j) kv_codes4_to_f16<FMT>(c[j], f[2 * j], f[2 * j + 1]);
             uint8_t* to = dst + (word[n] >> 2) * (kKvManyTile * 128) + row[n] * 128;
             const int ch = (word[n] & 3) * 2;
             *reinterpret_cast<uint4*>(to + ((ch ^ (row[n] & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);

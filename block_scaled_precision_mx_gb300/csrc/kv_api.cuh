@@ -19,11 +19,11 @@ bool kv_cache_shape_ok(int64_t num_blocks, int64_t kv_heads, int block_tokens, i
   return num_blocks <= 0x7FFFFFFFll / (kv_heads * block_tokens);
 }
 
-// 8-row tiles of the kernel for few rows: 1, 2 or 4; 0 where a kv head has more than 32 rows
+// 8-row tiles of the kernel for few rows: 1 or 2; 0 where a kv head has more than 16 rows
 int kv_row_tiles(int64_t max_q_len, int64_t group) {
-  if (max_q_len > 32 || group > 32) return max_q_len ? 0 : 1;
+  if (max_q_len > 16 || group > 16) return max_q_len ? 0 : 1;
   const int64_t rows = max_q_len * group;
-  return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 0;
+  return rows <= 8 ? 1 : rows <= 16 ? 2 : 0;
 }
 
 // codes as rows of head_dim bytes; a box is up to 64 tokens of one block and head
@@ -102,7 +102,6 @@ mx_status kv_attention_launch(const KvAttnArgs& a, int block_tokens, int64_t max
   switch (kv_row_tiles(max_q_len, a.heads / a.kv_heads)) {
     case 1: return kv_few_launch<FMT, D, 1>(a, block_tokens, max_q_len, workspace, st);
     case 2: return kv_few_launch<FMT, D, 2>(a, block_tokens, max_q_len, workspace, st);
-    case 4: return kv_few_launch<FMT, D, 4>(a, block_tokens, max_q_len, workspace, st);
   }
   return kv_many_launch<FMT, D>(a, block_tokens, max_q_len, workspace, st);
 }
@@ -248,13 +247,14 @@ mx_status kv_attention(const void* q, mx_half type, int64_t num_tokens, int64_t 
   if (!kv_cache_shape_ok(num_blocks, kv_heads, block_tokens, head_dim)) return MX_ERR_INVALID_ARG;
   if (heads < 1 || heads > 65535 || heads % kv_heads) return MX_ERR_INVALID_ARG;
   if (max_blocks < 1 || max_blocks > kKvMostTokens / block_tokens) return MX_ERR_INVALID_ARG;
+  if (num_tokens > kKvMostTokens / (heads / kv_heads)) return MX_ERR_INVALID_ARG;  // (rows of a kv head)
   if (max_q_len < 0 || max_q_len > num_tokens || window < 0 || window > 0x7FFFFFFF) return MX_ERR_INVALID_ARG;
   if (causal != 0 && causal != 1) return MX_ERR_INVALID_ARG;
   if (!(softmax_scale > 0.f) || softmax_scale > 1e30f) return MX_ERR_INVALID_ARG;
   if (q_stride_token % 8 || q_stride_head % 8) return MX_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_scale, 4) ||
       !aligned(v_scale, 4) || !aligned(block_tables, 4) || !aligned(lengths, 4) || !aligned(q_start, 4) ||
-      !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16))
+      !aligned(out, 32) || !aligned(lse, 4) || !aligned(workspace, 32))
     return MX_ERR_INVALID_ARG;
   if (num_tokens == 0) return MX_OK;
   KvAttnArgs a{};

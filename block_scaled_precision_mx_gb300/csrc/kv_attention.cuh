@@ -271,10 +271,12 @@ __device__ __forceinline__ void kv_clear_rest(const KvAttnArgs& a, int head_dim,
 __device__ __forceinline__ float2 kv_unpack2(uint32_t w, int f16) {
   return f16 ? kv_unpack2<true>(w) : kv_unpack2<false>(w);
 }
-__device__ __forceinline__ uint32_t kv_pack_out(float lo, float hi, int f16) {
-  if (f16) return kv_pack_f16(lo, hi);
+__device__ __forceinline__ uint32_t kv_pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t kv_pack_out(float lo, float hi, int f16) {
+  return f16 ? kv_pack_f16(lo, hi) : kv_pack_bf16(lo, hi);
 }
 
 template <int FMT, int D, int NT>

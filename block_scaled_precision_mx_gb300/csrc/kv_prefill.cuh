@@ -52,10 +52,11 @@ struct KvManyCfg {
   static constexpr int WIDE = 2 * RAW;             // the same in FP16; also 128 rows of Q
   static constexpr int OFF_F16 = 2 * WIDE;
   static constexpr int OFF_RAW = OFF_F16 + F16_SLOTS * WIDE;
-  static constexpr int OFF_SC = OFF_RAW + RAW_SLOTS * RAW;          // float4 [tiles][8 slices]
-  static constexpr int OFF_NAN = OFF_SC + kKvManyScales * 8 * 16;   // int [tiles]
+  static constexpr int OFF_SC = OFF_RAW + RAW_SLOTS * RAW;          // float2 [tiles][8 slices]: sK, log2 sV
+  static constexpr int OFF_MUL = OFF_SC + kKvManyScales * 8 * 8;    // float [128], for one row half
+  static constexpr int OFF_NAN = OFF_MUL + 4 * 128;                 // int [tiles]
   static constexpr int OFF_BAR = OFF_NAN + 4 * kKvManyScales;
-  static constexpr int BARS = 2 * RAW_SLOTS + 2 * F16_SLOTS + 4 * 2 + kKvManyScales + 2 * kKvManySegments + 1;
+  static constexpr int BARS = 2 * RAW_SLOTS + 2 * F16_SLOTS + 4 * 2 + kKvManyScales + 2 * kKvManySegments + 3;
   static constexpr int OFF_SEG = (OFF_BAR + 8 * BARS + 15) / 16 * 16;  // KvSegment [segments]
   static constexpr int SMEM = OFF_SEG + 64 * kKvManySegments + 16 + 1024;
   static constexpr size_t SLOT = static_cast<size_t>(kKvManyRows) * (D + 2) * 4;
@@ -64,7 +65,7 @@ struct KvManyCfg {
 
 // workspace: jobs, the requests' places (8 bytes each), NaN notes, segments
 __host__ __device__ constexpr size_t kv_many_nan_at(int64_t requests) {
-  return kKvSlotsAt + static_cast<size_t>((8 * (requests + 1) + 15) / 16 * 16);
+  return kKvSlotsAt + static_cast<size_t>((8 * (requests + 1) + 31) / 32 * 32);
 }
 __host__ __device__ constexpr size_t kv_many_slots_at(int64_t requests, int head_dim) {
   return kv_many_nan_at(requests) + static_cast<size_t>(kKvManyMaxCtas) * 4 * kKvManyTile * (head_dim / 8);
@@ -258,6 +259,13 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// 32 bytes a thread, a whole sector: a warp's threads write rows apart from each other
+__device__ __forceinline__ void kv_store32(void* to, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // one thread of a converged warp
 __device__ __forceinline__ bool kv_elect() {
   uint32_t p;
@@ -284,7 +292,8 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
   using Cfg = KvManyCfg<D>;
   extern __shared__ uint8_t kv_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(kv_smem_raw) + 1023) & ~uintptr_t(1023));
-  float4* sSC = reinterpret_cast<float4*>(smem + Cfg::OFF_SC);
+  float2* sSC = reinterpret_cast<float2*>(smem + Cfg::OFF_SC);
+  float* sMul = reinterpret_cast<float*>(smem + Cfg::OFF_MUL);
   volatile int* sNan = reinterpret_cast<volatile int*>(smem + Cfg::OFF_NAN);
   KvSegment* sSeg = reinterpret_cast<KvSegment*>(smem + Cfg::OFF_SEG);
   uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);
@@ -298,7 +307,9 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
   uint64_t* sc_full = o_full + 2;               // [kKvManyScales]
   uint64_t* seg_full = sc_full + kKvManyScales; // [kKvManySegments]
   uint64_t* seg_empty = seg_full + kKvManySegments;
-  uint64_t* drain_bar = seg_empty + kKvManySegments;
+  uint64_t* join_full = seg_empty + kKvManySegments;
+  uint64_t* join_empty = join_full + 1;
+  uint64_t* drain_bar = join_empty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_SEG + 64 * kKvManySegments);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
@@ -323,6 +334,8 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
       mbar_init(&seg_full[i], 1);
       mbar_init(&seg_empty[i], 13);  // warps 0-11 and 13
     }
+    mbar_init(join_full, 4);
+    mbar_init(join_empty, 4);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -413,7 +426,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
                           ((box_block * a.kv_heads + w.h) << a.shift) + (my & (P - 1)));
             if (half == 0) {
               const uint32_t st = tiles_done % kKvManyScales;
-              if (lane < 8) sSC[st * 8 + lane] = make_float4(slice_k, log2f(slice_v), 1.f / slice_v, 0.f);
+              if (lane < 8) sSC[st * 8 + lane] = make_float2(slice_k, log2f(slice_v));
               if (lane == 0) sNan[st] = 0;
               __syncwarp();
               if (lane == 0) mbar_arrive(&sc_full[st]);
@@ -436,45 +449,49 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
     bool ok = true;
     KvSegment v;
     while (ok && next_segment(v)) {
-      const int count = __shfl_sync(0xFFFFFFFFu, v.count, 0), halves = v.rows > 128 ? 2 : 1;
-      for (int i = 0; i <= count && ok; ++i) {  // V of tile i - 1, then K of tile i, each for both row halves
-        const uint32_t v_item = 2 * (tiles_done + i) - 1, k_item = v_item + 1;
-        const uint32_t v_slot = v_item % Cfg::F16_SLOTS, k_slot = k_item % Cfg::F16_SLOTS;
-        if (i > 0) ok = mbar_wait(&f_full[v_slot], (v_item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteMmaFull);
-        const uint32_t v_lo = __shfl_sync(0xFFFFFFFFu, (f_lo + v_slot * (Cfg::WIDE / 16)) | kLoN, 0);
-        const uint32_t k_lo = __shfl_sync(0xFFFFFFFFu, (f_lo + k_slot * (Cfg::WIDE / 16)) | kLoK, 0);
-        for (int h = 0; h < halves && ok; ++h) {
-          if (i > 0) {
-            ok = mbar_wait(&p_full[h], weights[h]++ & 1, abort_flag, kSiteMmaTmemEmpty);
-            if (!ok) break;
-            tc_fence_after();
-            if (kv_elect()) {
+      const int count = __shfl_sync(0xFFFFFFFFu, v.count, 0);
+      const bool single = v.rows <= 128;
+      const int steps = single ? count + 2 : 2 * (count + 1);
+      for (int step = 0; step < steps && ok; ++step) {
+        // half h: V of an earlier tile, then K of the next.  Two row halves: both take every tile; one: every second.
+        const int h = step & 1, pv = single ? step - 2 : (step >> 1) - 1, sc = single ? step : step >> 1;
+        const bool frees = single || h == 1;
+        if (pv >= 0) {
+          const uint32_t item = 2 * (tiles_done + pv) + 1, slot = item % Cfg::F16_SLOTS;
+          ok = mbar_wait(&f_full[slot], (item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteMmaFull) &&
+               mbar_wait(&p_full[h], weights[h]++ & 1, abort_flag, kSiteMmaTmemEmpty);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t v_lo = __shfl_sync(0xFFFFFFFFu, (f_lo + slot * (Cfg::WIDE / 16)) | kLoN, 0);
+          const bool first = single ? pv < 2 : pv == 0;
+          if (kv_elect()) {
 #pragma unroll
-              for (int k = 0; k < kKvManyTile / 16; ++k)  // O_h += P_h V, 16 tokens at a time
-                umma_f16_ts(tmem + 256 + h * 128, tmem + h * 128 + k * 8, desc_from_words(v_lo + k * (16 * 128 / 16), kHi), kIdO,
-                            i > 1 || k > 0);
-              if (i == count) umma_commit(&o_full[h]);
-              if (h == halves - 1) umma_commit(&f_empty[v_slot]);
-            }
-            __syncwarp();
+            for (int k = 0; k < kKvManyTile / 16; ++k)  // O_h += P_h V, 16 tokens at a time
+              umma_f16_ts(tmem + 256 + h * 128, tmem + h * 128 + k * 8, desc_from_words(v_lo + k * (16 * 128 / 16), kHi), kIdO,
+                          !first || k > 0);
+            if (pv >= count - (single ? 2 : 1)) umma_commit(&o_full[h]);
+            if (frees) umma_commit(&f_empty[slot]);
           }
-          if (i < count) {
-            if (h == 0) ok = mbar_wait(&f_full[k_slot], (k_item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteMmaFull);
-            if (i == 0 && ok) ok = mbar_wait(&q_full[h], segments[h]++ & 1, abort_flag, kSiteMmaFull);
-            if (!ok) break;
-            tc_fence_after();
-            if (kv_elect()) {
+          __syncwarp();
+        }
+        if (sc < count) {
+          const uint32_t item = 2 * (tiles_done + sc), slot = item % Cfg::F16_SLOTS;
+          ok = mbar_wait(&f_full[slot], (item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteMmaFull);
+          if (ok && sc == 0) ok = mbar_wait(&q_full[h], segments[h]++ & 1, abort_flag, kSiteMmaFull);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t k_lo = __shfl_sync(0xFFFFFFFFu, (f_lo + slot * (Cfg::WIDE / 16)) | kLoK, 0);
+          const uint32_t qh_lo = q_lo + (single ? 0 : h) * (Cfg::WIDE / 16);
+          if (kv_elect()) {
 #pragma unroll
-              for (int k = 0; k < D / 16; ++k) {  // S_h = Q_h K^T
-                const uint32_t at = (k / 4) * (kKvManyTile * 128 / 16) + (k % 4) * 2;
-                umma_f16_ss(tmem + h * 128, desc_from_words(q_lo + h * (Cfg::WIDE / 16) + at, kHi),
-                            desc_from_words(k_lo + at, kHi), kIdS, k > 0);
-              }
-              umma_commit(&s_full[h]);
-              if (h == halves - 1) umma_commit(&f_empty[k_slot]);
+            for (int k = 0; k < D / 16; ++k) {  // S_h = Q_h K^T
+              const uint32_t at = (k / 4) * (kKvManyTile * 128 / 16) + (k % 4) * 2;
+              umma_f16_ss(tmem + h * 128, desc_from_words(qh_lo + at, kHi), desc_from_words(k_lo + at, kHi), kIdS, k > 0);
             }
-            __syncwarp();
+            umma_commit(&s_full[h]);
+            if (frees) umma_commit(&f_empty[slot]);
           }
+          __syncwarp();
         }
       }
       tiles_done += count;
@@ -567,73 +584,105 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + half * 128 + lanes, tO = tmem + 256 + half * 128 + lanes;
     uint8_t* sQ = smem + half * Cfg::WIDE;
-    uint32_t tiles_done = 0, my_tiles = 0, segments = 0;
+    float2* join_ml = reinterpret_cast<float2*>(smem + Cfg::WIDE);          // one row half: half 1's (m, l) and NaN notes
+    uint32_t* join_nan = reinterpret_cast<uint32_t*>(smem + Cfg::WIDE + 1024);  // (where its queries would be)
+    uint32_t tiles_done = 0, my_tiles = 0, segments = 0, joins = 0;
+    uint32_t other_segments = 0;  // half 1's segments with tiles, as half 0 counts them
     bool ok = true;
-    KvSegment v;
-    while (ok && next_segment(v)) {
-      if (half && v.rows <= 128) {
-        tiles_done += v.count;
-        continue;
+    // A segment's queries as FP16; returns what this thread's row of scores is to be multiplied with.  The rows
+    // are copied to their places as they are, D / 8 lanes a row, and converted there, a row a thread.  (Short
+    // loops: code that runs once a segment is not in the instruction cache, and costs by its length.)
+    auto bring = [&](const KvSegment& v) {
+      constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;
+      const bool single = v.rows <= 128;
+      if (single && half == 1) {  // half 0 brings the rows of both
+        ok = mbar_wait(&q_full[0], (seg - 1) & 1, abort_flag, kSiteEpiTmemFull);
+        return sMul[row];
       }
-      const int my_row = 128 * half + row;
+      const int word = lane % LANES, sub = lane / LANES, row0 = 32 * (warp & 3);
+      int r = row0 + sub, qi = (v.row0 + half * 128 + r) / group, hg = v.row0 + half * 128 + r - qi * group;
+      const int qi_step = AT_ONCE / group, hg_step = AT_ONCE % group;
+      const uint32_t to = smem_u32(sQ) + (word >> 3) * (128 * 128);
+#pragma unroll 1
+      for (; r < row0 + 32; r += AT_ONCE) {
+        const uint16_t* src = a.q + (v.q0 + qi) * a.stride_t + (v.head * group + hg) * a.stride_h + 8 * word;
+        const uint32_t bytes = half * 128 + r < v.rows ? 16 : 0;  // (the rest of the 16 is zeros)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + r * 128 + (((word & 7) ^ (r & 7)) << 4)),
+                     "l"(bytes ? src : a.q), "r"(bytes)
+                     : "memory");
+        qi += qi_step;
+        hg += hg_step;
+        if (hg >= group) {
+          hg -= group;
+          ++qi;
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+      auto chunk = [&](int i) {
+        return reinterpret_cast<uint4*>(sQ + (i >> 3) * (128 * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4));
+      };
+      uint32_t most2 = 0;
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 x = *chunk(i);
+        most2 = __vmaxu2(most2, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+      }
+      const uint32_t most1 = max(most2 & 0xFFFFu, most2 >> 16);
+      const float amax = a.f16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(most1))) : __uint_as_float(most1 << 16);
+      // 2^e with amax 2^e in [2^14, 2^15)
+      const int e = min(14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127), 120);
+      const float mul = most1 ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : 1.f;
+#pragma unroll 2
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 x = *chunk(i);
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+        uint32_t f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 y = kv_unpack2(u[j], a.f16);
+          f[j] = kv_pack_f16(y.x * mul, y.y * mul);
+        }
+        *chunk(i) = make_uint4(f[0], f[1], f[2], f[3]);
+      }
+      const float row_mul = a.scale_log2 / mul;
+      if (single) sMul[row] = row_mul;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[half]);
+      return row_mul;
+    };
+    KvSegment v;
+    bool more = next_segment(v);
+    float row_mul = more ? bring(v) : 0.f;
+    while (ok && more) {
+      const bool single = v.rows <= 128;  // both halves work on the same rows, on every second tile
+      const int my_row = single ? row : 128 * half + row;
       const bool live = my_row < v.rows;
       const int qi = (v.row0 + my_row) / group, hg = v.row0 + my_row - qi * group;
       const int p = v.len - v.rows_q + qi;
       const int lo = a.window ? max(0, p - a.window + 1) : 0, hi = a.causal ? min(v.len, p + 1) : v.len;
       const uint32_t width = static_cast<uint32_t>(max(hi - lo, 0));
-      float row_mul;
-      {
-        uint4 x[D / 8];
-        const uint16_t* src = a.q + (v.q0 + qi) * a.stride_t + (v.head * group + hg) * a.stride_h;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) x[i] = live ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
-        float amax = 0.f;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 y = kv_unpack2(u[j], a.f16);
-            amax = fmaxf(amax, fmaxf(fabsf(y.x), fabsf(y.y)));
-          }
-        }
-        // 2^e with amax 2^e in [2^14, 2^15)
-        const int e = min(14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127), 120);
-        const float mul = amax > 0.f ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : 1.f;
-        row_mul = a.scale_log2 / mul;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-          uint32_t f[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 y = kv_unpack2(u[j], a.f16);
-            f[j] = kv_pack_f16(y.x * mul, y.y * mul);
-          }
-          *reinterpret_cast<uint4*>(sQ + (i >> 3) * (128 * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4)) =
-              make_uint4(f[0], f[1], f[2], f[3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[half]);
-      }
+      const int first = single ? half : 0;
       float m = -INFINITY, l = 0.f;
       uint32_t nan_d[D / 32];
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) nan_d[i] = 0;
 #pragma unroll 1
-      for (int i = 0; i < v.count; ++i, ++tiles_done, ++my_tiles) {
+      for (int i = first; i < v.count; i += single ? 2 : 1, ++my_tiles) {
         const int token = v.token + i * kKvManyTile;
-        const uint32_t st = tiles_done % kKvManyScales;
-        ok = mbar_wait(&sc_full[st], (tiles_done / kKvManyScales) & 1, abort_flag, kSiteEpiTmemFull) &&
+        const uint32_t tile = tiles_done + i, st = tile % kKvManyScales;
+        ok = mbar_wait(&sc_full[st], (tile / kKvManyScales) & 1, abort_flag, kSiteEpiTmemFull) &&
              mbar_wait(&s_full[half], my_tiles & 1, abort_flag, kSiteEpiTmemFull);
         if (!ok) break;
         tc_fence_after();
-        const float4* scales = sSC + st * 8;
+        const float2* scales = sSC + st * 8;
         const bool edge = token < v.all_lo || token + kKvManyTile > v.all_hi;
         if (edge) {  // what the row does not see becomes -inf in place
 #pragma unroll 1
           for (int g = 0; g < 8; ++g) {
+            const int t = token + 16 * g;
+            if (!__any_sync(0xFFFFFFFFu, t < lo || t + 16 > hi)) continue;
             uint32_t x[16];
             tmem_ld_32x32b_x16(tS + 16 * g, x);
             tmem_ld_wait();
@@ -661,7 +710,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
               y0 = fmaxf(fmaxf(y0, __uint_as_float(x[16 * k + j])), __uint_as_float(x[16 * k + (j + 1) % 16]));
               if (j + 2 < 16) y1 = fmaxf(fmaxf(y1, __uint_as_float(x[16 * k + j + 2])), __uint_as_float(x[16 * k + j + 3]));
             }
-            const float4 sc = scales[2 * g + k];
+            const float2 sc = scales[2 * g + k];
             most = fmaxf(most, fmaf(fmaxf(y0, y1), row_mul * sc.x, sc.y));
           }
         }
@@ -670,7 +719,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
           const float keep = past && m > -INFINITY ? kv_exp2(m - most) : 1.f;  // (at m = -inf O and l are 0, or NaN)
           l *= keep;
           m = past ? most : m;
-          if (i > 0) {
+          if (i > first) {
 #pragma unroll 1
             for (int j = 0; j < D / 16; ++j) {
               uint32_t o[16];
@@ -693,7 +742,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
           tmem_regs_ready(x);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float4 sc = scales[2 * g + k];
+            const float2 sc = scales[2 * g + k];
             const float mul = row_mul * sc.x, add = sc.y - ref;
             const uint64_t mul2 = pack_f32x2(mul, mul), add2 = pack_f32x2(add, add);
             uint64_t sum2[2] = {0, 0};
@@ -708,21 +757,21 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
             }
             float sum0, sum1;
             unpack_f32x2(kv_add2(sum2[0], sum2[1]), sum0, sum1);
-            l = fmaf(sum0 + sum1, sc.z, l);
+            l = fmaf(sum0 + sum1, kv_exp2(-sc.y), l);
           }
           tmem_st_32x32b_x16(tS + 16 * g, packed);
         }
         tmem_st_wait();
         tc_fence_before();
         if (edge) {  // NaN codes of V in tokens that this row sees
-          const uint32_t v_item = 2 * tiles_done + 1;
+          const uint32_t v_item = 2 * tile + 1;
           ok = mbar_wait(&f_full[v_item % Cfg::F16_SLOTS], (v_item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteEpiTmemFull);
           if (!ok) break;
           if (sNan[st]) {
             const int j0 = max(lo - token, 0), j1 = min(hi - token, kKvManyTile);
             for (int j = j0; j < j1; ++j) {
               const volatile uint32_t* note =
-                  reinterpret_cast<const volatile uint32_t*>(nan_notes + ((tiles_done & 3) * kKvManyTile + j) * (D / 8));
+                  reinterpret_cast<const volatile uint32_t*>(nan_notes + ((tile & 3) * kKvManyTile + j) * (D / 8));
 #pragma unroll
               for (int k = 0; k < D / 32; ++k) nan_d[k] |= note[k];
             }
@@ -732,43 +781,97 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[half]);
       }
       if (!ok) break;
-      ok = mbar_wait(&o_full[half], segments++ & 1, abort_flag, kSiteEpiTmemFull);
+      tiles_done += v.count;
+      if (!single) ++other_segments;
+      // The queries of the next segment, so that its first products run under this one's output.  (This half's
+      // products with the present ones have ended: its last scores have come.)
+      KvSegment next;
+      more = next_segment(next);
+      if (more && !single) row_mul = bring(next);
+      const bool any = first < v.count;  // whether this half had a tile
+      if (any) ok = mbar_wait(&o_full[half], segments++ & 1, abort_flag, kSiteEpiTmemFull);
       if (!ok) break;
       tc_fence_after();
-      const bool whole = v.part == 0;
-      const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-      const int64_t at_row = static_cast<int64_t>(v.q0 + qi) * a.heads + v.head * group + hg;
-      float* part = reinterpret_cast<float*>(workspace + kv_many_slots_at(a.requests, D) + (2 * blockIdx.x + v.part - 1) * Cfg::SLOT);
+      if (single && half == 1) {
+        join_ml[row] = make_float2(m, l);
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        uint32_t o[32];
-        tmem_ld_32x32b_x32(tO + 32 * j, o);
-        tmem_ld_wait();
-        tmem_regs_ready(o);
-        float f[32];
+        for (int j = 0; j < D / 32; ++j) join_nan[row * (D / 32) + j] = nan_d[j];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(join_full);
+        ok = mbar_wait(join_empty, joins++ & 1, abort_flag, kSiteEpiTmemFull);
+      } else {
+        float f0 = 1.f, f1 = 0.f;  // O = f0 O_half + f1 O_1
+        if (single) {
+          ok = mbar_wait(join_full, joins++ & 1, abort_flag, kSiteEpiTmemFull);
+          if (ok && v.count > 1) {
+            const float2 other = join_ml[row];
+            const float most = fmaxf(m, other.x), ref = most == -INFINITY ? 0.f : most;
+            f0 = kv_exp2(m - ref);
+            f1 = kv_exp2(other.x - ref);
+            l = l * f0 + other.y * f1;
+            m = most;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) f[k] = l == 0.f ? 0.f : __uint_as_float(o[k]) * inv;
-        if (nan_d[j]) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (nan_d[j] >> k & 1) f[k] = NAN;
+            for (int j = 0; j < D / 32; ++j) nan_d[j] |= join_nan[row * (D / 32) + j];
+          }
         }
-        if (live && whole) {
+        if (!ok) break;
+        const bool two = single && v.count > 1;
+        const bool whole = v.part == 0;
+        const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+        f0 *= inv;
+        f1 *= inv;
+        const int64_t at_row = static_cast<int64_t>(v.q0 + qi) * a.heads + v.head * group + hg;
+        float* part = reinterpret_cast<float*>(workspace + kv_many_slots_at(a.requests, D) + (2 * blockIdx.x + max(v.part - 1, 0)) * Cfg::SLOT);
+        if (two) {
+          ok = mbar_wait(&o_full[1], (other_segments++) & 1, abort_flag, kSiteEpiTmemFull);
+          if (!ok) break;
+          tc_fence_after();
+        }
+#pragma unroll 1
+        for (int j = 0; j < D / 16; ++j) {
+          uint32_t o[16];
+          float f[16];
+          tmem_ld_32x32b_x16(tO + 16 * j, o);
+          tmem_ld_wait();
+          tmem_regs_ready16(o);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4*>(a.out + at_row * D + 32 * j + 8 * k) =
-                make_uint4(kv_pack_out(f[8 * k], f[8 * k + 1], a.f16), kv_pack_out(f[8 * k + 2], f[8 * k + 3], a.f16),
-                           kv_pack_out(f[8 * k + 4], f[8 * k + 5], a.f16), kv_pack_out(f[8 * k + 6], f[8 * k + 7], a.f16));
-        } else if (live) {
+          for (int k = 0; k < 16; ++k) f[k] = __uint_as_float(o[k]) * f0;
+          if (two) {
+            tmem_ld_32x32b_x16(tO + 128 + 16 * j, o);
+            tmem_ld_wait();
+            tmem_regs_ready16(o);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<float4*>(part + my_row * D + 32 * j + 4 * k) =
-                make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
+            for (int k = 0; k < 16; ++k) f[k] = fmaf(__uint_as_float(o[k]), f1, f[k]);
+          }
+          const uint32_t nan = nan_d[0] & 0xFFFFu;  // (the notes move along)
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) nan_d[k] = (nan_d[k] >> 16) | (k + 1 < D / 32 ? nan_d[k + 1 < D / 32 ? k + 1 : k] << 16 : 0);
+          if (l == 0.f || nan) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) f[k] = nan >> k & 1 ? NAN : l == 0.f ? 0.f : f[k];
+          }
+          if (live && whole) {
+            uint32_t h[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) h[k] = kv_pack_out(f[2 * k], f[2 * k + 1], a.f16);
+            kv_store32(a.out + at_row * D + 16 * j, h);
+          } else if (live) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              kv_store32(part + my_row * D + 16 * j + 8 * k, reinterpret_cast<const uint32_t*>(&f[8 * k]));
+          }
+        }
+        if (live && whole) a.lse[at_row] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
+        else if (live) *reinterpret_cast<float2*>(part + kKvManyRows * D + 2 * my_row) = make_float2(m, l);
+        tc_fence_before();
+        if (single) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(join_empty);
         }
       }
-      if (live && whole) a.lse[at_row] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
-      else if (live) *reinterpret_cast<float2*>(part + kKvManyRows * D + 2 * my_row) = make_float2(m, l);
-      tc_fence_before();
+      if (!ok) break;
+      if (more && single) row_mul = bring(next);
+      v = next;
     }
   }
   tc_fence_before();

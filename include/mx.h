@@ -467,10 +467,10 @@ size_t kv_attention_workspace_bytes(int64_t num_tokens, int64_t requests, int64_
  * and up share kv head g.  Row i of n stands at position p = lengths[r] - n + i and sees the tokens
  * j < lengths[r] with j <= p if causal and j > p - window if window > 0.  No request has more than
  * max_q_len rows.
- *   out[num_tokens][heads][head_dim] (q's type) = softmax(softmax_scale * q k_j) v_j,
+ *   out[num_tokens][heads][head_dim] (q's type, 32-byte aligned) = softmax(softmax_scale * q k_j) v_j,
  *   lse[num_tokens][heads] (float) = log sum_j exp(softmax_scale * q k_j).
  * Rows that see no token, and rows from q_start[requests] on, give 0 and -inf.  NaN in tokens that a
- * row does not see does not reach it.  workspace: kv_attention_workspace_bytes bytes, 16-byte
+ * row does not see does not reach it.  workspace: kv_attention_workspace_bytes bytes, 32-byte
  * aligned, contents free; calls that may overlap need one each.
  * Sums and softmax statistics are FP32; the weights are rounded to FP16 for the second product.
  */

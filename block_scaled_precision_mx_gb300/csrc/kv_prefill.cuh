@@ -552,13 +552,13 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
           __threadfence_block();
         }
 #pragma unroll 1
-        for (int n0 = 0; n0 < CH; n0 += 4) {
-          uint4 x[4];
-          int row[4], word[4];
+        for (int n0 = 0; n0 < CH; n0 += 2) {
+          uint4 x[2];
+          int row[2], word[2];
 #pragma unroll
-          for (int n = 0; n < 4; ++n) x[n] = *raw_at(n0 + n, row[n], word[n]);
+          for (int n = 0; n < 2; ++n) x[n] = *raw_at(n0 + n, row[n], word[n]);
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
+          for (int n = 0; n < 2; ++n) {
             const uint32_t c[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
             uint32_t f[8];
 #pragma unroll
@@ -697,13 +697,17 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
         // the row's largest z + log2 sV
         float most = -INFINITY;
 #pragma unroll 1
-        for (int g = 0; g < 4; ++g) {
-          uint32_t x[32];
-          tmem_ld_32x32b_x32(tS + 32 * g, x);
+        for (int g2 = 0; g2 < 4; g2 += 2) {
+          uint32_t xx[2][32];
+          tmem_ld_32x32b_x32(tS + 32 * g2, xx[0]);
+          tmem_ld_32x32b_x32(tS + 32 * g2 + 32, xx[1]);
           tmem_ld_wait();
-          tmem_regs_ready(x);
+          tmem_regs_ready(xx[0]);
+          tmem_regs_ready(xx[1]);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
+          for (int kk = 0; kk < 4; ++kk) {
+            const int g = g2 + kk / 2, k = kk & 1;
+            uint32_t (&x)[32] = xx[kk / 2];
             float y0 = __uint_as_float(x[16 * k]), y1 = __uint_as_float(x[16 * k + 1]);
 #pragma unroll
             for (int j = 2; j < 16; j += 4) {

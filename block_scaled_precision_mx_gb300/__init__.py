@@ -575,13 +575,31 @@ def kv_attention_workspace_bytes(num_tokens: int, requests: int, max_q_len: int,
     return int(load().kv_attention_workspace_bytes(num_tokens, requests, max_q_len, heads, kv_heads, head_dim))
 
 
+_workspaces = {}        # (device, stream) -> the buffer that calls on that stream share
+_workspaces_old = []    # outgrown ones, kept: work in flight may use them
+
+
+def _kv_workspace(need, dev, stream):
+    """A workspace for a call that was given none: calls on one stream follow each other and share one;
+    a capture gets its own, since its graph may be replayed beside the stream."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(need, dtype=_uint8, device=dev)
+    ws = _workspaces.get((dev.index, stream))
+    if ws is None or ws.numel() < need:
+        with _lock:
+            _workspaces_old.append(ws)
+            ws = _workspaces[(dev.index, stream)] = torch.empty(need, dtype=_uint8, device=dev)
+    return ws
+
+
 def kv_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.Tensor,
                  v_scale: torch.Tensor, block_tables: torch.Tensor, lengths: torch.Tensor, q_start: torch.Tensor,
                  max_q_len: int, elem: int = E4M3, softmax_scale=None, causal: bool = True, window: int = 0, out=None,
                  lse=None, workspace=None, stream=None):
     """Attention of q [tokens][heads][head_dim] over the 8-bit cache (include/mx.h, kv_attention).
     lengths int32 [requests]: cached tokens, the queries' own among them; q_start int32 [requests + 1];
-    softmax_scale defaults to head_dim ** -0.5.  Returns (out, like q but contiguous; lse float
+    softmax_scale defaults to head_dim ** -0.5; calls without a workspace share one for each stream.
+    Returns (out, like q but contiguous; lse float
     [tokens][heads])."""
     shape, q_at, half, q_st, q_sh = _rows_of_heads(q, "q")
     blocks, kv_heads, block_tokens, head_dim = _cache_shape(k_codes, v_codes, k_scale, v_scale)
@@ -601,8 +619,9 @@ def kv_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor, 
     elif lse.shape != shape[:2]:
         raise ValueError("lse must be [tokens][heads]")
     need = kv_attention_workspace_bytes(tokens, requests, max_q_len, heads, kv_heads, head_dim)
+    at_stream = _stream(stream)
     if workspace is None:
-        workspace = torch.empty(need, dtype=_uint8, device=dev)
+        workspace = _kv_workspace(need, dev, at_stream)
     elif workspace.numel() < need:
         raise ValueError(f"workspace must have {need} bytes")
     st = load().kv_attention(q_at, half, tokens, heads, q_st, q_sh, _at(k_codes, _uint8, "k_codes"),
@@ -612,7 +631,7 @@ def kv_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor, 
                              _at(q_start, _int32, "q_start"), requests, max_q_len,
                              head_dim ** -0.5 if softmax_scale is None else softmax_scale, causal, window,
                              _at(out, q.dtype, "out"), _at(lse, _float32, "lse"), _at(workspace, _uint8, "workspace"),
-                             _stream(stream))
+                             at_stream)
     if st:
         _check(st, "kv_attention")
     return out, lse

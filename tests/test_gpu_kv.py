@@ -292,7 +292,7 @@ def test_prompt_head_groups(group):
     check_attention(attention_case(rng, [700, 64, 257], [150, 64, 200], 2 * group, 2, 128, 64, "bf16", 0), 0)
 
 
-@pytest.mark.parametrize("queries", [1, 4, 90])
+@pytest.mark.parametrize("queries", [1, 4, 20, 90])
 def test_one_long_context(queries):
     """Few rows over a long context: the work is split over it and joined."""
     rng = np.random.RandomState(queries)
@@ -300,7 +300,7 @@ def test_one_long_context(queries):
     check_attention(attention_case(rng, [9999, 30, 4000], [queries, min(30, queries), 2], 4, 4, 64, 16, "f16", 0), 0)
 
 
-@pytest.mark.parametrize("queries", [1, 6, 100])
+@pytest.mark.parametrize("queries", [1, 6, 30, 100])
 def test_scores_of_every_size(queries):
     """A large softmax scale (one weight near 1), a tiny one (all alike), and blocks of very unlike scales."""
     rng = np.random.RandomState(queries)
@@ -312,7 +312,7 @@ def test_scores_of_every_size(queries):
     check_attention(c, 0)
 
 
-@pytest.mark.parametrize("queries", [1, 5, 120])
+@pytest.mark.parametrize("queries", [1, 5, 30, 60, 120])
 def test_nan_reaches_only_rows_that_see_it(queries):
     rng = np.random.RandomState(3)
     c = attention_case(rng, [260, 130], [queries, queries], 4, 2, 128, 64, "bf16", 0)

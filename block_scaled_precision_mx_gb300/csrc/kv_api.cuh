@@ -90,8 +90,10 @@ mx_status kv_many_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_le
     return MX_ERR_CUDA;
   const int most_q = static_cast<int>(max_q_len);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  if (pdl_launch(kv_plan_kernel, 1, kKvPlanThreads, 0, st, a, most_q, n, ws) != cudaSuccess ||
-      pdl_launch(kern, n, kKvManyThreads, Cfg::SMEM, st, tk, tv, a, most_q, ws) != cudaSuccess)
+  // up to a request a thread, of up to 32 units, the kernel plans for itself
+  const int planned = a.requests > kKvManyThreads || max_q_len * (a.heads / a.kv_heads) > 32 * kKvManyRows;
+  if (planned && pdl_launch(kv_plan_kernel, 1, kKvPlanThreads, 0, st, a, most_q, n, ws) != cudaSuccess) return MX_ERR_CUDA;
+  if (pdl_launch(kern, n, kKvManyThreads, Cfg::SMEM, st, tk, tv, a, most_q, planned, ws) != cudaSuccess)
     return MX_ERR_CUDA;
   if (n > 1 && pdl_launch(kv_join_kernel<D, kKvManyRows>, dim3(n - 1, 16), 128, 0, st, a, static_cast<const uint8_t*>(ws),
                           kv_many_slots_at(a.requests, D)) != cudaSuccess)

@@ -108,6 +108,28 @@ __device__ __forceinline__ int kv_units_of(const KvRequest& req, int group) {
   return (req.rows_q * group + kKvManyRows - 1) / kKvManyRows;
 }
 
+// The unit of request r, whose units begin at place x, that job.begin falls into.
+__device__ __forceinline__ void kv_first_unit(const KvAttnArgs& a, const KvRequest& req, int r, int group, long long x,
+                                              KvJob& job) {
+#pragma unroll 1
+  for (int q_tile = 0;; ++q_tile) {
+    const KvUnit u = kv_unit(a, req, group, q_tile);
+    const long long all = static_cast<long long>(u.cost()) * a.kv_heads;
+    if (job.begin < x + all) {
+      job.head = static_cast<int>((job.begin - x) / u.cost());
+      job.unit = x + static_cast<long long>(job.head) * u.cost();
+      job.tiles = u.tiles;
+      job.q0 = u.q0;
+      job.row0 = u.row0;
+      job.rows = u.rows;
+      job.request = r;
+      job.q_tile = q_tile;
+      return;
+    }
+    x += all;
+  }
+}
+
 // Ranges of the list of all units (request by request, then 256 rows by 256 rows, then head by head): one
 // CTA sums the requests' costs, scans them and finds each range's first unit.  A request's units are summed
 // by a thread while they are few, by a warp otherwise.
@@ -171,24 +193,7 @@ __global__ void __launch_bounds__(kKvPlanThreads) kv_plan_kernel(const KvAttnArg
         if (place[mid] <= job.begin) lo = mid;
         else hi = mid;
       }
-      const KvRequest req = kv_request(a, lo, most_q, false);
-      long long x = place[lo];
-      for (int q_tile = 0;; ++q_tile) {
-        const KvUnit u = kv_unit(a, req, group, q_tile);
-        const long long all = static_cast<long long>(u.cost()) * a.kv_heads;
-        if (job.begin < x + all) {
-          job.head = static_cast<int>((job.begin - x) / u.cost());
-          job.unit = x + static_cast<long long>(job.head) * u.cost();
-          job.tiles = u.tiles;
-          job.q0 = u.q0;
-          job.row0 = u.row0;
-          job.rows = u.rows;
-          job.request = lo;
-          job.q_tile = q_tile;
-          break;
-        }
-        x += all;
-      }
+      kv_first_unit(a, kv_request(a, lo, most_q, false), lo, group, place[lo], job);
     }
     jobs[c] = job;
   }
@@ -213,7 +218,7 @@ __device__ __forceinline__ void kv_many_begin(const KvAttnArgs& a, int most_q, i
     w.u = kv_unit(a, w.req, group, w.q_tile);
   }
 }
-__device__ __forceinline__ bool kv_many_next(const KvAttnArgs& a, int most_q, int group, KvManyWalk& w) {
+__device__ __noinline__ bool kv_many_next(const KvAttnArgs& a, int most_q, int group, KvManyWalk& w) {
   while (w.pos < w.end) {
     const long long unit_end = w.base + w.u.cost();
     if (w.pos == unit_end) {
@@ -297,7 +302,7 @@ __device__ __forceinline__ uint64_t kv_add2(uint64_t a, uint64_t b) {
 template <int FMT, int D>
 __global__ void __launch_bounds__(kKvManyThreads, 1)
     kv_attention_many_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                             const KvAttnArgs a, int most_q, uint8_t* workspace) {
+                             const KvAttnArgs a, int most_q, int planned, uint8_t* workspace) {
   using Cfg = KvManyCfg<D>;
   extern __shared__ uint8_t kv_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(kv_smem_raw) + 1023) & ~uintptr_t(1023));
@@ -361,13 +366,51 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   pdl_wait();
   kv_clear_rest(a, D, blockIdx.x * kKvManyThreads + tid, gridDim.x * kKvManyThreads);
+  __shared__ KvJob job;
+  if (planned) {
+    if (tid == 0) job = reinterpret_cast<const KvJob*>(workspace)[blockIdx.x];
+  } else {
+    // Few requests of few units: every CTA finds its own range, a request a thread (a launch of kv_plan_kernel less).
+    __shared__ long long warp_sum[kKvManyThreads / 32];
+    KvRequest req{};
+    long long mine = 0;
+    if (tid < a.requests) {
+      req = kv_request(a, tid, most_q, blockIdx.x == 0);
+      const int units = kv_units_of(req, group);
+#pragma unroll 1
+      for (int i = 0; i < units; ++i) mine += kv_unit(a, req, group, i).cost();
+    }
+    mine *= a.kv_heads;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    long long before = incl - mine, total = 0;
+#pragma unroll 1
+    for (int i = 0; i < kKvManyThreads / 32; ++i) {
+      if (i < warp) before += warp_sum[i];
+      total += warp_sum[i];
+    }
+    KvJob mine_job{kv_cut(total, blockIdx.x, gridDim.x), kv_cut(total, blockIdx.x + 1, gridDim.x), 0, 0, 0, 0, 0, 0, 0, 0};
+    const bool here = mine_job.begin >= before && mine_job.begin < before + mine;
+    if (here) kv_first_unit(a, req, tid, group, before, mine_job);
+    if (here || (total == 0 && tid == 0)) {
+      job = mine_job;
+      reinterpret_cast<KvJob*>(workspace)[blockIdx.x] = mine_job;
+    }
+  }
+  __syncthreads();
   uint8_t* nan_notes = workspace + kv_many_nan_at(a.requests) + blockIdx.x * Cfg::NAN_BYTES;
 
   // the next segment, for every warp but the loading one; false at the end
   uint32_t seg = 0;
   auto next_segment = [&](KvSegment& v) {
     const uint32_t i = seg % kKvManySegments;
-    const bool ok = mbar_wait(&seg_full[i], (seg / kKvManySegments) & 1, abort_flag, kSiteMmaFull);
+    const bool ok = kv_wait(&seg_full[i], (seg / kKvManySegments) & 1, abort_flag, kSiteMmaFull);
     v = sSeg[i];
     __syncwarp();
     if (lane == 0) mbar_arrive(&seg_empty[i]);
@@ -378,7 +421,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
   if (warp == 12) {
     // ------------------------------------------------------------------ loads: item 2i = K, 2i + 1 = V of tile i
     KvManyWalk w;
-    kv_many_begin(a, most_q, group, reinterpret_cast<const KvJob*>(workspace)[blockIdx.x], w);
+    kv_many_begin(a, most_q, group, job, w);
     const long long range_start = w.pos;
     const int P = 1 << a.shift, rows_box = min(P, kKvTile), boxes = kKvManyTile / rows_box;
     const int most_tiles = 32 * P / kKvManyTile;
@@ -387,7 +430,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
     while (ok) {
       const bool more = kv_many_next(a, most_q, group, w);
       const uint32_t sl = seg % kKvManySegments;
-      if (!mbar_wait(&seg_empty[sl], ((seg / kKvManySegments) & 1) ^ 1, abort_flag, kSiteProducerEmpty)) break;
+      if (!kv_wait(&seg_empty[sl], ((seg / kKvManySegments) & 1) ^ 1, abort_flag, kSiteProducerEmpty)) break;
       if (lane == 0) {
         const int part = w.count == w.u.tiles ? 0 : w.base < range_start ? 1 : 2;
         KvSegment v{more ? w.count : 0, (w.u.first_tile + w.tile) * kKvManyTile, w.u.rows, w.u.row0, w.u.q0, w.u.rows_q,
@@ -424,7 +467,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
             const uint32_t item = 2 * tiles_done + half, slot = item % Cfg::RAW_SLOTS;
-            if (!mbar_wait(&raw_empty[slot], ((item / Cfg::RAW_SLOTS) & 1) ^ 1, abort_flag, kSiteProducerEmpty)) {
+            if (!kv_wait(&raw_empty[slot], ((item / Cfg::RAW_SLOTS) & 1) ^ 1, abort_flag, kSiteProducerEmpty)) {
               ok = false;
               break;
             }
@@ -467,8 +510,8 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
         const bool frees = single || h == 1;
         if (pv >= 0) {
           const uint32_t item = 2 * (tiles_done + pv) + 1, slot = item % Cfg::F16_SLOTS;
-          ok = mbar_wait(&f_full[slot], (item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteMmaFull) &&
-               mbar_wait(&p_full[h], weights[h]++ & 1, abort_flag, kSiteMmaTmemEmpty);
+          ok = kv_wait(&f_full[slot], (item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteMmaFull) &&
+               kv_wait(&p_full[h], weights[h]++ & 1, abort_flag, kSiteMmaTmemEmpty);
           if (!ok) break;
           tc_fence_after();
           const uint32_t v_lo = __shfl_sync(0xFFFFFFFFu, (f_lo + slot * (Cfg::WIDE / 16)) | kLoN, 0);
@@ -485,8 +528,8 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
         }
         if (sc < count) {
           const uint32_t item = 2 * (tiles_done + sc), slot = item % Cfg::F16_SLOTS;
-          ok = mbar_wait(&f_full[slot], (item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteMmaFull);
-          if (ok && sc == 0) ok = mbar_wait(&q_full[h], segments[h]++ & 1, abort_flag, kSiteMmaFull);
+          ok = kv_wait(&f_full[slot], (item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteMmaFull);
+          if (ok && sc == 0) ok = kv_wait(&q_full[h], segments[h]++ & 1, abort_flag, kSiteMmaFull);
           if (!ok) break;
           tc_fence_after();
           const uint32_t k_lo = __shfl_sync(0xFFFFFFFFu, (f_lo + slot * (Cfg::WIDE / 16)) | kLoK, 0);
@@ -523,8 +566,8 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
 #pragma unroll 1
       for (uint32_t item = 2 * tiles_done; item < items; ++item) {
         const uint32_t slot = item % Cfg::RAW_SLOTS, fs = item % Cfg::F16_SLOTS;
-        ok = mbar_wait(&raw_full[slot], (item / Cfg::RAW_SLOTS) & 1, abort_flag, kSiteMmaFull) &&
-             mbar_wait(&f_empty[fs], ((item / Cfg::F16_SLOTS) & 1) ^ 1, abort_flag, kSiteProducerEmpty);
+        ok = kv_wait(&raw_full[slot], (item / Cfg::RAW_SLOTS) & 1, abort_flag, kSiteMmaFull) &&
+             kv_wait(&f_empty[fs], ((item / Cfg::F16_SLOTS) & 1) ^ 1, abort_flag, kSiteProducerEmpty);
         if (!ok) break;
         uint8_t* src = smem + Cfg::OFF_RAW + slot * Cfg::RAW;
         uint8_t* dst = smem + Cfg::OFF_F16 + fs * Cfg::WIDE;
@@ -605,7 +648,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
       constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;
       const bool single = v.rows <= 128;
       if (single && half == 1) {  // half 0 brings the rows of both
-        ok = mbar_wait(&q_full[0], (seg - 1) & 1, abort_flag, kSiteEpiTmemFull);
+        ok = kv_wait(&q_full[0], (seg - 1) & 1, abort_flag, kSiteEpiTmemFull);
         return sMul[row];
       }
       const int word = lane % LANES, sub = lane / LANES, row0 = 32 * (warp & 3);
@@ -681,8 +724,8 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
       for (int i = first; i < v.count; i += single ? 2 : 1, ++my_tiles) {
         const int token = v.token + i * kKvManyTile;
         const uint32_t tile = tiles_done + i, st = tile % kKvManyScales;
-        ok = mbar_wait(&sc_full[st], (tile / kKvManyScales) & 1, abort_flag, kSiteEpiTmemFull) &&
-             mbar_wait(&s_full[half], my_tiles & 1, abort_flag, kSiteEpiTmemFull);
+        ok = kv_wait(&sc_full[st], (tile / kKvManyScales) & 1, abort_flag, kSiteEpiTmemFull) &&
+             kv_wait(&s_full[half], my_tiles & 1, abort_flag, kSiteEpiTmemFull);
         if (!ok) break;
         tc_fence_after();
         const float2* scales = sSC + st * 8;
@@ -778,7 +821,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
         tc_fence_before();
         if (edge) {  // NaN codes of V in tokens that this row sees
           const uint32_t v_item = 2 * tile + 1;
-          ok = mbar_wait(&f_full[v_item % Cfg::F16_SLOTS], (v_item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteEpiTmemFull);
+          ok = kv_wait(&f_full[v_item % Cfg::F16_SLOTS], (v_item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteEpiTmemFull);
           if (!ok) break;
           if (sNan[st]) {
             const int j0 = max(lo - token, 0), j1 = min(hi - token, kKvManyTile);
@@ -802,7 +845,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
       more = next_segment(next);
       if (more && !single) row_mul = bring(next);
       const bool any = first < v.count;  // whether this half had a tile
-      if (any) ok = mbar_wait(&o_full[half], segments++ & 1, abort_flag, kSiteEpiTmemFull);
+      if (any) ok = kv_wait(&o_full[half], segments++ & 1, abort_flag, kSiteEpiTmemFull);
       if (!ok) break;
       tc_fence_after();
       if (single && half == 1) {
@@ -811,11 +854,11 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
         for (int j = 0; j < D / 32; ++j) join_nan[row * (D / 32) + j] = nan_d[j];
         __syncwarp();
         if (lane == 0) mbar_arrive(join_full);
-        ok = mbar_wait(join_empty, joins++ & 1, abort_flag, kSiteEpiTmemFull);
+        ok = kv_wait(join_empty, joins++ & 1, abort_flag, kSiteEpiTmemFull);
       } else {
         float f0 = 1.f, f1 = 0.f;  // O = f0 O_half + f1 O_1
         if (single) {
-          ok = mbar_wait(join_full, joins++ & 1, abort_flag, kSiteEpiTmemFull);
+          ok = kv_wait(join_full, joins++ & 1, abort_flag, kSiteEpiTmemFull);
           if (ok && v.count > 1) {
             const float2 other = join_ml[row];
             const float most = fmaxf(m, other.x), ref = most == -INFINITY ? 0.f : most;
@@ -836,7 +879,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
         const int64_t at_row = static_cast<int64_t>(v.q0 + qi) * a.heads + v.head * group + hg;
         float* part = reinterpret_cast<float*>(workspace + kv_many_slots_at(a.requests, D) + (2 * blockIdx.x + max(v.part - 1, 0)) * Cfg::SLOT);
         if (two) {
-          ok = mbar_wait(&o_full[1], (other_segments++) & 1, abort_flag, kSiteEpiTmemFull);
+          ok = kv_wait(&o_full[1], (other_segments++) & 1, abort_flag, kSiteEpiTmemFull);
           if (!ok) break;
           tc_fence_after();
         }

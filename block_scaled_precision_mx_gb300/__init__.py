@@ -579,16 +579,21 @@ _workspaces = {}        # (device, stream) -> the buffer that calls on that stre
 _workspaces_old = []    # outgrown ones, kept: work in flight may use them
 
 
-def _kv_workspace(need, dev, stream):
+def _kv_workspace(need, dev, stream, given):
     """A workspace for a call that was given none: calls on one stream follow each other and share one;
     a capture gets its own, since its graph may be replayed beside the stream."""
     if torch.cuda.is_current_stream_capturing():
-        return torch.empty(need, dtype=_uint8, device=dev)
+        ws = torch.empty(need, dtype=_uint8, device=dev)
+        ws[:4096].zero_()  # (all that has to be clear)
+        return ws
     ws = _workspaces.get((dev.index, stream))
     if ws is None or ws.numel() < need:
         with _lock:
             _workspaces_old.append(ws)
-            ws = _workspaces[(dev.index, stream)] = torch.empty(need, dtype=_uint8, device=dev)
+            ws = torch.zeros(need, dtype=_uint8, device=dev)
+            if given is not None:  # cleared on torch's stream, used on another
+                torch.cuda.current_stream(dev).synchronize()
+            _workspaces[(dev.index, stream)] = ws
     return ws
 
 
@@ -598,7 +603,8 @@ def kv_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor, 
                  lse=None, workspace=None, stream=None):
     """Attention of q [tokens][heads][head_dim] over the 8-bit cache (include/mx.h, kv_attention).
     lengths int32 [requests]: cached tokens, the queries' own among them; q_start int32 [requests + 1];
-    softmax_scale defaults to head_dim ** -0.5; calls without a workspace share one for each stream.
+    softmax_scale defaults to head_dim ** -0.5; a workspace is zero before its first use, and calls
+    without one share one for each stream.
     Returns (out, like q but contiguous; lse float
     [tokens][heads])."""
     shape, q_at, half, q_st, q_sh = _rows_of_heads(q, "q")
@@ -621,7 +627,7 @@ def kv_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor, 
     need = kv_attention_workspace_bytes(tokens, requests, max_q_len, heads, kv_heads, head_dim)
     at_stream = _stream(stream)
     if workspace is None:
-        workspace = _kv_workspace(need, dev, at_stream)
+        workspace = _kv_workspace(need, dev, at_stream, stream)
     elif workspace.numel() < need:
         raise ValueError(f"workspace must have {need} bytes")
     st = load().kv_attention(q_at, half, tokens, heads, q_st, q_sh, _at(k_codes, _uint8, "k_codes"),
@@ -639,7 +645,10 @@ def kv_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor, 
 
 def mx_check(stream=None) -> int:
     """Synchronize the stream and return the library's device status (MX_OK / MX_ERR_TIMEOUT / ...)."""
-    return int(load().mx_check(_stream(stream)))
+    status = int(load().mx_check(_stream(stream)))
+    if status == MX_ERR_TIMEOUT:  # a kernel that gave up may have left its workspace as it was
+        _workspaces.clear()
+    return status
 
 
 def num_sms() -> int:

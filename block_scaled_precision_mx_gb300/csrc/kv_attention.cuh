@@ -51,7 +51,7 @@ __device__ __forceinline__ bool kv_wait(uint64_t* bar, uint32_t parity, volatile
 //  * The work is the list of (request, kv head) units, each a row of 64-token tiles; all tiles of all
 //    units, in order, are cut into gridDim.x equal ranges, one for each resident CTA, whatever the
 //    lengths are.  A range is a few segments of units; a unit that one CTA has whole is finished
-//    there, else each segment leaves (O, m, l) in the workspace and kv_join_kernel joins them in order.
+//    there, else each segment leaves (O, m, l) in the workspace and the CTA that finishes last joins them, in order.
 //  * One warp keeps a ring of tiles in flight: TMA boxes of a block's rows of codes (128 or 64 bytes,
 //    swizzled), so a tile's codes cross the SM once, and the scales of its four 16-token slices.  It walks
 //    the units, tells the other warps of the next segment and brings its queries while the present one runs.
@@ -74,8 +74,8 @@ __device__ __forceinline__ bool kv_wait(uint64_t* bar, uint32_t parity, volatile
 //    NaN codes of V (0 * NaN) are taken out and put into the rows that see them at the end.
 //
 // Measured (D = 128, E4M3): 8 requests of up to 65536 tokens, 8 kv heads, 8 rows each: 129 us, 6.07 TB/s, 0.90
-// of the measured copy rate.  64 of up to 4096, 4 rows: 61 us, 5.5 TB/s; about 10 us of that is what a call of any
-// size takes (1 request, 777 tokens: 11.5 us), the join among it.  What bounds it: memory latency where a CTA's ring
+// of the measured copy rate.  64 of up to 4096, 4 rows: 62 us, 5.4 TB/s; about 10 us of that is what a call of any
+// size takes (1 request, 777 tokens: 11 us), the join among it.  What bounds it: memory latency where a CTA's ring
 // runs dry at a segment's first tiles.  Three CTAs of three 16 KB stages a SM: two CTAs 63 us, four of two
 // stages 72 us (64 x 4096); at D = 64 four CTAs of five 8 KB stages: 36 us, two 39, five of three stages 45.
 constexpr int kKvTile = 64;
@@ -88,7 +88,10 @@ struct KvJob {  // a range of the list, and the unit that it begins in
   int tiles, head, q0, row0, rows, request, q_tile;  // rows row0 .. row0 + rows - 1 of the request's head group
 };
 
-constexpr size_t kKvSlotsAt = sizeof(KvJob) * kKvMaxCtas;  // in the workspace, behind the jobs
+// Workspace: counters of the cut units (zero between calls), the jobs (many rows), then parts.
+constexpr size_t kKvJobsAt = 4096;
+static_assert(4 * kKvMaxCtas <= kKvJobsAt, "a counter for each range");
+constexpr size_t kKvSlotsAt = kKvJobsAt + sizeof(KvJob) * kKvMaxCtas;
 
 // A segment as the loading warp tells the others of it, with its queries; count = 0: no more.
 struct alignas(16) KvFewSegment {
@@ -96,6 +99,8 @@ struct alignas(16) KvFewSegment {
   int rows, q0, len, head;
   int any_lo, all_lo, all_hi;  // tokens from any_lo on are seen by some row, [all_lo, all_hi) by all
   int part;                    // 0: the whole unit; 1 + slot: a part of it
+  int parts, first, first_slot;  // a cut unit: how many ranges have tiles of it, the first of them and its slot
+  long long place;             // and where its tiles begin in the list
 };
 
 template <int D, int NT>
@@ -178,6 +183,11 @@ constexpr int kKvUnitCost = 3;
 
 __device__ __forceinline__ int KvRequest::cost() const { return tiles ? tiles + kKvUnitCost : 0; }
 
+// the range, of n, that place p of a list of `total` places is in
+__device__ __forceinline__ int kv_range_of(long long total, long long p, int n) {
+  if (total < (1 << 21)) return static_cast<int>((static_cast<unsigned>(p + 1) * static_cast<unsigned>(n) - 1) / static_cast<unsigned>(total));
+  return static_cast<int>(((p + 1) * n - 1) / total);
+}
 // place i n-ths into a list of `total` places
 __device__ __forceinline__ long long kv_cut(long long total, int i, int n) {
   if (total < (1 << 21)) return static_cast<unsigned>(total) * static_cast<unsigned>(i) / static_cast<unsigned>(n);
@@ -300,6 +310,29 @@ __device__ __forceinline__ uint32_t kv_pack_out(float lo, float hi, int f16) {
   return f16 ? kv_pack_f16(lo, hi) : kv_pack_bf16(lo, hi);
 }
 
+// (m, l, O) and a further part's, joined
+__device__ __forceinline__ void kv_join(float& m, float& l, float4& o, float2 ml, float4 x) {
+  const float most = fmaxf(m, ml.x), ref = most == -INFINITY ? 0.f : most;
+  const float f0 = kv_exp2(m - ref), f1 = kv_exp2(ml.x - ref);
+  l = l * f0 + ml.y * f1;
+  o.x = o.x * f0 + x.x * f1;
+  o.y = o.y * f0 + x.y * f1;
+  o.z = o.z * f0 + x.z * f1;
+  o.w = o.w * f0 + x.w * f1;
+  m = most;
+}
+// Four elements of a row's output from d on, and the row's lse.  row: of the head group, from token q0 on.
+template <int D>
+__device__ __forceinline__ void kv_finish(const KvAttnArgs& a, int q0, int row, int group, int head, int d, float m, float l,
+                                          float4 o) {
+  const int qi = row / group, hg = row - qi * group;
+  const int64_t at_row = static_cast<int64_t>(q0 + qi) * a.heads + head * group + hg;
+  const float inv = 1.f / l;
+  *reinterpret_cast<uint2*>(a.out + at_row * D + d) =
+      l == 0.f ? make_uint2(0, 0) : make_uint2(kv_pack_out(o.x * inv, o.y * inv, a.f16), kv_pack_out(o.z * inv, o.w * inv, a.f16));
+  if (d == 0) a.lse[at_row] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
+}
+
 template <int FMT, int D, int NT>
 __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
     kv_attention_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -324,6 +357,7 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
   uint64_t* seg_empty = seg_full + 2;        // [2]
   uint64_t* join_bar = seg_empty + 2;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(join_bar + 1);
+  volatile int* last_part = abort_flag + 1;
   __shared__ KvPlanSmem plan;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int group = a.heads / a.kv_heads;
@@ -346,9 +380,6 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
   pdl_wait();  // (no early trigger: CTAs of the next kernel would take the places of this one's last CTAs)
   KvWalk w;
   kv_plan(a, most_q, plan, w);  // (its barriers also publish the mbarriers)
-  if (tid == 0)
-    reinterpret_cast<KvJob*>(workspace)[blockIdx.x] =
-        KvJob{w.pos, w.end, w.base, w.req.tiles, w.h, w.req.q0, 0, w.req.rows_q * group, w.r, 0};
   kv_clear_rest(a, D, blockIdx.x * kKvFewThreads + tid, gridDim.x * kKvFewThreads);
 
   if (warp == kKvWarps) {
@@ -383,6 +414,15 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
         v.all_lo = a.window ? w.req.len - a.window : 0;
         v.all_hi = a.causal ? min(w.req.len, pos0 + 1) : w.req.len;
         v.part = w.count == w.req.tiles ? 0 : w.base < range_start ? 1 : 2;
+        if (v.part) {
+          const long long total = plan.total;
+          const int n = gridDim.x;
+          v.place = w.base + kKvUnitCost;
+          v.first = kv_range_of(total, v.place, n);
+          // (fewer places than ranges: a range has one or none)
+          v.parts = total < n ? w.req.tiles : kv_range_of(total, v.place + w.req.tiles - 1, n) - v.first + 1;
+          v.first_slot = w.base < kv_cut(total, v.first, n) ? 0 : 1;
+        }
         sSeg[buf] = v;
       }
       if (more) {
@@ -747,13 +787,7 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
           if (nan & 8) o.w = NAN;
         }
         if (v.part == 0) {
-          const int qi = row / group, hg = row - qi * group;
-          const int64_t at_row = static_cast<int64_t>(v.q0 + qi) * a.heads + v.head * group + hg;
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          *reinterpret_cast<uint2*>(a.out + at_row * D + d) =
-              sum == 0.f ? make_uint2(0, 0)
-                         : make_uint2(kv_pack_out(o.x * inv, o.y * inv, a.f16), kv_pack_out(o.z * inv, o.w * inv, a.f16));
-          if (d == 0) a.lse[at_row] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+          kv_finish<D>(a, v.q0, row, group, v.head, d, most, sum, o);
         } else {
           *reinterpret_cast<float4*>(part + row * D + d) = o;
           if (d == 0) *reinterpret_cast<float2*>(part + Cfg::ROWS * D + 2 * row) = make_float2(most, sum);
@@ -761,6 +795,35 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
       }
     }
     if (!ok) break;
+    if (v.part) {
+      // A part of a unit that range boundaries cut: the CTA that writes the last part joins them, in order.
+      __threadfence();
+      if (!warps_meet()) break;
+      unsigned int* counter = reinterpret_cast<unsigned int*>(workspace) + v.first;
+      if (tid == 0) {
+        *last_part = atomicAdd(counter, 1u) == static_cast<unsigned>(v.parts) - 1;
+        __threadfence();
+      }
+      if (!warps_meet()) break;
+      if (*last_part) {
+        const long long total = plan.total;
+        for (int i = tid; i < v.rows * (D / 4); i += 32 * kKvWarps) {
+          const int row = i / (D / 4), d = i % (D / 4) * 4;
+          float most = -INFINITY, sum = 0.f;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+          for (int k = 0; k < v.parts; ++k) {
+            const int range = total < gridDim.x ? kv_range_of(total, v.place + k, gridDim.x) : v.first + k;
+            const float* from = reinterpret_cast<const float*>(workspace + kKvSlotsAt + (2 * range + (k ? 0 : v.first_slot)) * Cfg::SLOT);
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + Cfg::ROWS * D + 2 * row));
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(from + row * D + d));
+            kv_join(most, sum, o, ml, x);
+          }
+          kv_finish<D>(a, v.q0, row, group, v.head, d, most, sum, o);
+        }
+        if (tid == 0) *counter = 0;
+      }
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(&seg_empty[buf]);
   }
@@ -775,7 +838,7 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, const 
   constexpr size_t kSlot = static_cast<size_t>(ROWS) * (D + 2) * 4;
   __shared__ int list[kKvMaxCtas];
   __shared__ int listed;
-  const KvJob* jobs = reinterpret_cast<const KvJob*>(workspace);
+  const KvJob* jobs = reinterpret_cast<const KvJob*>(workspace + kKvJobsAt);
   const int c = blockIdx.x + 1, ranges = gridDim.x + 1;
   const KvJob job = jobs[c];
   const long long before = jobs[c - 1].begin, total = jobs[ranges - 1].end;
@@ -812,21 +875,9 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, const 
       const float* part = reinterpret_cast<const float*>(workspace + slots_at + list[k] * kSlot);
       const float2 ml = *reinterpret_cast<const float2*>(part + ROWS * D + 2 * row);
       const float4 x = *reinterpret_cast<const float4*>(part + row * D + d);
-      const float most = fmaxf(m, ml.x), ref = most == -INFINITY ? 0.f : most;
-      const float f0 = kv_exp2(m - ref), f1 = kv_exp2(ml.x - ref);
-      l = l * f0 + ml.y * f1;
-      o.x = o.x * f0 + x.x * f1;
-      o.y = o.y * f0 + x.y * f1;
-      o.z = o.z * f0 + x.z * f1;
-      o.w = o.w * f0 + x.w * f1;
-      m = most;
+      kv_join(m, l, o, ml, x);
     }
-    const int qi = (job.row0 + row) / group, hg = job.row0 + row - qi * group;
-    const int64_t at_row = static_cast<int64_t>(job.q0 + qi) * a.heads + job.head * group + hg;
-    const float inv = 1.f / l;
-    *reinterpret_cast<uint2*>(a.out + at_row * D + d) =
-        l == 0.f ? make_uint2(0, 0) : make_uint2(kv_pack_out(o.x * inv, o.y * inv, a.f16), kv_pack_out(o.z * inv, o.w * inv, a.f16));
-    if (d == 0) a.lse[at_row] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
+    kv_finish<D>(a, job.q0, job.row0 + row, group, job.head, d, m, l, o);
   }
 }
 

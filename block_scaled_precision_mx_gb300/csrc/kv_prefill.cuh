@@ -3,8 +3,8 @@
 //
 // A unit is 256 rows (query tokens x query heads of the group) of one request and kv head against the
 // tokens that any of them sees, in tiles of 128.  One CTA a SM, persistent over an equal range of all
-// units' tiles (kv_plan_kernel); a unit cut by a range boundary leaves (O, m, l) and kv_join_kernel
-// joins the pieces, as for few rows.  Roles:
+// units' tiles (found by the kernel itself for few requests, else by kv_plan_kernel); a unit cut by a range
+// boundary leaves (O, m, l) in parts, which kv_join_kernel joins in order.  Roles:
 //
 //   warps 0-3, 4-7   softmax of rows 0-127 and 128-255, a row a thread.  They bring their queries into
 //                    shared memory as FP16 (a power of two for each row, exact to 2^-29 of its largest),
@@ -20,8 +20,8 @@
 // folded into the exponent, and the reference m is renewed only when a score passes it by 8; the row's O in
 // tensor memory is then rescaled by its own thread, between two products.
 //
-// Measured (D = 128, 32 query and 8 kv heads, E4M3): 4096 queries over 32768 tokens 1.61 ms, 1.28 PFLOP/s, 0.68 of the
-// measured bf16 rate; 6 prompts of 711 to 1500 tokens 197 us (872 units of 11 tiles; 78 us of products).  What bounds it: a tile's products are 2048 cycles, but a half's chain of softmax (~2300 cycles:
+// Measured (D = 128, 32 query and 8 kv heads, E4M3): 4096 queries over 32768 tokens 1.60 ms, 1.29 PFLOP/s, 0.68 of the
+// measured bf16 rate; 6 prompts of 711 to 1500 tokens 193 us (872 units of 11 tiles; 78 us of products).  What bounds it: a tile's products are 2048 cycles, but a half's chain of softmax (~2300 cycles:
 // maximum 560, weights 1260, waits), its P V and its next S is ~3700, because S and P share tensor memory (O and
 // S of two halves fill it) and S(i + 1) has to follow P(i) V; and shared memory carries 320 KB a tile (2560
 // cycles: Q 64, K and V 64 each, the codes in, out and back as FP16 128).  Tried and slower: one pass over the
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kKvPlanThreads) kv_plan_kernel(const KvAttnArg
   }
   if (tid == 0) place[a.requests] = total;
   __syncthreads();
-  KvJob* jobs = reinterpret_cast<KvJob*>(workspace);
+  KvJob* jobs = reinterpret_cast<KvJob*>(workspace + kKvJobsAt);
   for (int c = tid; c < ranges; c += kKvPlanThreads) {
     KvJob job{kv_cut(total, c, ranges), kv_cut(total, c + 1, ranges), 0, 0, 0, 0, 0, 0, 0, 0};
     if (job.begin < total) {
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
   kv_clear_rest(a, D, blockIdx.x * kKvManyThreads + tid, gridDim.x * kKvManyThreads);
   __shared__ KvJob job;
   if (planned) {
-    if (tid == 0) job = reinterpret_cast<const KvJob*>(workspace)[blockIdx.x];
+    if (tid == 0) job = reinterpret_cast<const KvJob*>(workspace + kKvJobsAt)[blockIdx.x];
   } else {
     // Few requests of few units: every CTA finds its own range, a request a thread (a launch of kv_plan_kernel less).
     __shared__ long long warp_sum[kKvManyThreads / 32];
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
     if (here) kv_first_unit(a, req, tid, group, before, mine_job);
     if (here || (total == 0 && tid == 0)) {
       job = mine_job;
-      reinterpret_cast<KvJob*>(workspace)[blockIdx.x] = mine_job;
+      reinterpret_cast<KvJob*>(workspace + kKvJobsAt)[blockIdx.x] = mine_job;
     }
   }
   __syncthreads();

@@ -376,7 +376,7 @@ def test_side_stream_own_buffers_and_graph(queries):
     t, heads, d = c["q"].shape
     q = c["q"].clone()
     out, lse = torch.empty(t, heads, d, dtype=q.dtype, device="cuda"), torch.empty(t, heads, device="cuda")
-    ws = torch.empty(max(16, mx.kv_attention_workspace_bytes(t, 2, queries, heads, 2, d)), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(mx.kv_attention_workspace_bytes(t, 2, queries, heads, 2, d), dtype=torch.uint8, device="cuda")
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
 
@@ -395,6 +395,22 @@ def test_side_stream_own_buffers_and_graph(queries):
     torch.cuda.synchronize()
     want = mx.kv_attention(q, *tensors, max_q_len=queries)
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert mx.mx_check() == mx.MX_OK
+
+
+def test_a_workspace_serves_call_after_call():
+    """One workspace, cleared once, for calls of unlike sizes in turn: its counters are zero after each, and what
+    else earlier calls left in it does not matter."""
+    rng = np.random.RandomState(21)
+    ws = torch.full((mx.kv_attention_workspace_bytes(1, 4, 1000, 8, 2, 128),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws[:4096] = 0
+    for lens, queries in (([5000, 70], [1, 1]), ([3], [1]), ([900, 40, 2000], [100, 40, 3]), ([20000], [2]), ([5000, 70], [1, 1])):
+        c = attention_case(rng, lens, queries, 8, 2, 128, 64, "bf16", 0)
+        for _ in range(2):
+            out, lse = run_attention(c, 0, workspace=ws)
+            want = run_attention(c, 0)
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+            assert not ws[:4096].any()
     assert mx.mx_check() == mx.MX_OK
 
 

@@ -357,6 +357,38 @@ def test_cache_past_32_bits():
     assert mx.mx_check() == mx.MX_OK
 
 
+@pytest.mark.parametrize("requests,queries,tokens", [(1100, 1, 16384), (2100, 20, 16384), (3000, 3, 200), (16384, 1, 64)])
+def test_many_requests(requests, queries, tokens):
+    """More tiles in all than the ranges' 32-bit arithmetic takes, and as many requests as there may be: every
+    request's table names one block over and over, so it sees that block's tokens, weighted alike."""
+    rng = np.random.RandomState(requests)
+    p, d, h, heads = 64, 64, 8, 16
+    c = attention_case(rng, [p], [queries], heads, h, d, p, "bf16", 0)
+    c["q"] = c["q"].repeat(requests, 1, 1)
+    c["tables"] = np.full((requests, -(-tokens // p)), c["tables"][0, 0], np.int32)
+    c["lens"] = np.full(requests, tokens, np.int32)
+    c["q_start"] = np.arange(requests + 1, dtype=np.int32) * queries
+    out, lse = run_attention(c, 0, causal=False)
+    assert mx.mx_check() == mx.MX_OK
+    assert (out.view(requests, -1) == out.view(requests, -1)[:1]).float().mean() > 0.9  # (splits differ: last bits may)
+    small = dict(c, q=c["q"][:queries], tables=c["tables"][:1], lens=np.array([p]), q_start=np.array([0, queries]))
+    full, rest = divmod(tokens, p)
+    want, want_lse, tol, lse_tol = ref.attention(
+        small["q"].double().cpu().numpy(), c["kc"], c["vc"], c["ks"], c["vs"], small["tables"], small["lens"],
+        small["q_start"], 0, d ** -0.5, False, 0)
+    if rest:  # the last block is seen in part: the reference over all of the tokens
+        want, want_lse, tol, lse_tol = ref.attention(
+            small["q"].double().cpu().numpy(), c["kc"], c["vc"], c["ks"], c["vs"], small["tables"], np.array([tokens]),
+            small["q_start"], 0, d ** -0.5, False, 0)
+    else:
+        want_lse, lse_tol = want_lse + np.log(full), lse_tol + tokens * 2.0 ** -23
+        tol = tol * 2 + tokens * 2.0 ** -23 * np.abs(want).max()
+    out = out.double().cpu().numpy().reshape(requests, queries, heads, d)
+    lse = lse.double().cpu().numpy().reshape(requests, queries, heads)
+    assert (np.abs(out - want) <= tol + 2.0 ** -8 * (np.abs(want) + tol) + 2.0 ** -25).all()
+    assert (np.abs(lse - want_lse) <= lse_tol).all()
+
+
 @pytest.mark.parametrize("queries", [1, 70])
 def test_blocks_out_of_range_are_not_read_and_reported(queries):
     rng = np.random.RandomState(1)

@@ -618,17 +618,17 @@ def kv_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor, 
     dev = q.device
     if out is None:
         out = torch.empty(shape, dtype=q.dtype, device=dev)
-    elif out.shape != shape:
+    elif out.shape != shape or _at(out, q.dtype, "out") is None:
         raise ValueError("out must be shaped like q")
     if lse is None:
         lse = torch.empty((tokens, heads), dtype=_float32, device=dev)
-    elif lse.shape != shape[:2]:
+    elif lse.shape != shape[:2] or _at(lse, _float32, "lse") is None:
         raise ValueError("lse must be [tokens][heads]")
     need = kv_attention_workspace_bytes(tokens, requests, max_q_len, heads, kv_heads, head_dim)
     at_stream = _stream(stream)
     if workspace is None:
         workspace = _kv_workspace(need, dev, at_stream, stream)
-    elif workspace.numel() < need:
+    elif workspace.numel() < need or _at(workspace, _uint8, "workspace") is None:
         raise ValueError(f"workspace must have {need} bytes")
     st = load().kv_attention(q_at, half, tokens, heads, q_st, q_sh, _at(k_codes, _uint8, "k_codes"),
                              _at(v_codes, _uint8, "v_codes"), _at(k_scale, _float32, "k_scale"),
@@ -636,8 +636,7 @@ def kv_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor, 
                              _at(block_tables, _int32, "block_tables"), max_blocks, _at(lengths, _int32, "lengths"),
                              _at(q_start, _int32, "q_start"), requests, max_q_len,
                              head_dim ** -0.5 if softmax_scale is None else softmax_scale, causal, window,
-                             _at(out, q.dtype, "out"), _at(lse, _float32, "lse"), _at(workspace, _uint8, "workspace"),
-                             at_stream)
+                             out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), at_stream)
     if st:
         _check(st, "kv_attention")
     return out, lse

@@ -646,7 +646,9 @@ def mx_check(stream=None) -> int:
     """Synchronize the stream and return the library's device status (MX_OK / MX_ERR_TIMEOUT / ...)."""
     status = int(load().mx_check(_stream(stream)))
     if status == MX_ERR_TIMEOUT:  # a kernel that gave up may have left its workspace as it was
-        _workspaces.clear()
+        with _lock:
+            _workspaces_old.extend(_workspaces.values())
+            _workspaces.clear()
     return status
 
 

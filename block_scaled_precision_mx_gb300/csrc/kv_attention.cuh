@@ -161,14 +161,14 @@ struct KvRequest {
 __device__ __forceinline__ KvRequest kv_request(const KvAttnArgs& a, int r, int most_q, bool tell) {
   KvRequest v;
   v.q0 = a.q_start[r];
-  v.rows_q = a.q_start[r + 1] - v.q0;
+  const int end = a.q_start[r + 1];
   v.len = a.lengths[r];
-  const int most = a.max_blocks << a.shift;
-  if (v.rows_q < 0 || v.rows_q > most_q || v.len < 0 || v.len > most || v.q0 < 0 || v.q0 + max(v.rows_q, 0) > a.tokens) {
-    if (tell) atomicOr(&g_mx_error_word, kSiteBadCache);
-    v.rows_q = 0;
-    v.len = 0;
-  }
+  // (compared before they are subtracted: differences of any two 32-bit numbers do not fit)
+  const bool ok = v.q0 >= 0 && v.q0 <= end && end <= a.tokens && end - v.q0 <= most_q && v.len >= 0 &&
+                  v.len <= a.max_blocks << a.shift;
+  if (!ok && tell) atomicOr(&g_mx_error_word, kSiteBadCache);
+  v.rows_q = ok ? end - v.q0 : 0;
+  v.len = ok ? v.len : 0;
   const int lo = a.window ? max(0, v.len - v.rows_q - a.window + 1) : 0;
   v.first_tile = lo / kKvTile;
   v.tiles = v.rows_q ? max(1, (v.len + kKvTile - 1) / kKvTile - v.first_tile) : 0;
@@ -292,7 +292,7 @@ __device__ __forceinline__ bool kv_next_segment(const KvAttnArgs& a, int most_q,
 
 // Rows that no request has: 0 and -inf.
 __device__ __forceinline__ void kv_clear_rest(const KvAttnArgs& a, int head_dim, int first, int step) {
-  const int used = min(max(a.q_start[a.requests], 0), a.tokens);
+  const int end = a.q_start[a.requests], used = end >= 0 && end <= a.tokens ? end : a.tokens;
   const int64_t rows = static_cast<int64_t>(a.tokens - used) * a.heads, words = rows * head_dim / 8;
   uint4* out = reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(used) * a.heads * head_dim);
   for (int64_t i = first; i < words; i += step) out[i] = make_uint4(0, 0, 0, 0);

@@ -1,0 +1,61 @@
+"""What the key/value cache's operators do with device inputs that break their contract, on the GPU: nothing is
+read or written out of range, mx_check reports it, and what does not depend on the broken input is right; and
+inputs that look broken but are not."""
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_precision_mx_gb300 as mx
+from tests import kv_reference as ref
+from tests.test_gpu_kv import attention_case, built, gpu  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+MOST, LEAST = 2 ** 31 - 1, -2 ** 31
+
+
+def reported():
+    assert mx.mx_check() == mx.MX_ERR_INVALID_ARG
+    assert mx.mx_check() == mx.MX_OK
+
+
+# ------------------------------------------------------------------ attention
+BROKEN = [{"q_start": {1: -1}}, {"q_start": {1: LEAST}}, {"q_start": {1: MOST}}, {"q_start": {1: MOST, 2: LEAST}},
+          {"q_start": {1: LEAST, 2: MOST}}, {"q_start": {1: MOST, 2: LEAST + 3}}, {"q_start": {1: "past"}},
+          {"q_start": {1: "fewer"}}, {"q_start": {3: MOST}}, {"q_start": {3: LEAST}}, {"q_start": {0: -5}},
+          {"lens": {1: -1}}, {"lens": {1: "past"}}, {"lens": {0: MOST, 2: LEAST}}]
+
+
+@pytest.mark.parametrize("broken", BROKEN, ids=str)
+@pytest.mark.parametrize("queries,more", [(4, 0), (40, 0), (40, 600)])
+def test_broken_lengths_and_query_starts(queries, more, broken):
+    """A request whose rows or length are out of range is left out; the others' rows are right, and no other row
+    of the output is touched.  (`more` empty requests: the ranges are planned by a kernel of their own.)"""
+    rng = np.random.RandomState(queries)
+    c = attention_case(rng, [100, 90, 80] + [0] * more, [queries] * 3 + [0] * more, 4, 2, 128, 16, "bf16", 0, q_pad=3)
+    tokens, most = len(c["q"]), c["tables"].shape[1] * 16
+    for name, places in broken.items():
+        for i, v in places.items():
+            v = {"past": tokens + 1 if name == "q_start" else most + 1, "fewer": queries - 1}.get(v, v)
+            c[name][i] = v
+    starts = c["q_start"].astype(np.int64)
+    out = torch.full(c["q"].shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full(c["q"].shape[:2], 7.0, device="cuda")
+    args = [gpu(c[n]) for n in ("kc", "vc", "ks", "vs", "tables", "lens", "q_start")]
+    mx.kv_attention(c["q"], *args, max_q_len=queries, out=out, lse=lse)
+    reported()
+    got, got_lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    touched = np.zeros(tokens, bool)
+    if 0 <= starts[-1] <= tokens:                                  # rows that no request has
+        touched[starts[-1]:] = True
+        assert (got[starts[-1]:] == 0).all() and (got_lse[starts[-1]:] == -np.inf).all()
+    for r in range(3):
+        a, b, n = starts[r], starts[r + 1], int(c["lens"][r])
+        if not (0 <= a < b <= tokens and b - a <= queries and 0 <= n <= most):
+            continue
+        touched[a:b] = True
+        want, want_lse, tol, lse_tol = ref.attention(
+            c["q"][a:b].double().cpu().numpy(), c["kc"], c["vc"], c["ks"], c["vs"], c["tables"][r:r + 1], [n],
+            [0, b - a], 0, 128 ** -0.5, True, 0)
+        assert (np.abs(got[a:b] - want) <= tol + 2.0 ** -8 * (np.abs(want) + tol) + 2.0 ** -25).all()
+        assert (np.abs(got_lse[a:b] - want_lse) <= lse_tol).all()
+    assert (got[~touched] == 7).all() and (got_lse[~touched] == 7).all()

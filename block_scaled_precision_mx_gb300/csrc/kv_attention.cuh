@@ -11,6 +11,7 @@
 #include <cmath>
 
 #include "kv_cache.cuh"
+#include "kv_ring.cuh"
 
 namespace mxgb {
 
@@ -499,7 +500,7 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
     };
     int stage = 0;
     uint32_t phase = 0;
-    long issued = 0;
+    uint32_t issued = 0;
     bool ok = true;
     Chunk cur, next;
     fetch(cur);
@@ -536,10 +537,8 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
       cur = next;
     }
     // every copy has landed before the CTA's shared memory goes
-    for (int i = 0; i < Cfg::STAGES; ++i)
-      if (issued > i)
-        mbar_drain(&full[i], static_cast<uint32_t>(((i + (issued - 1 - i) / Cfg::STAGES * Cfg::STAGES) / Cfg::STAGES) & 1),
-                   kWaitBudgetNs);
+    for (uint32_t i = 0; i < Cfg::STAGES; ++i)
+      if (issued > i) mbar_drain(&full[i], kv_ring_last_parity(issued, i, Cfg::STAGES), kWaitBudgetNs);
     return;
   }
 

@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
     const long long range_start = w.pos;
     const int P = 1 << a.shift, rows_box = min(P, kKvTile), boxes = kKvManyTile / rows_box;
     const int most_tiles = 32 * P / kKvManyTile;
-    uint32_t tiles_done = 0;
+    uint32_t tiles_done = 0, issued = 0;  // issued: items, for the end (a wait that gives up may leave a tile's second out)
     bool ok = true;
     while (ok) {
       const bool more = kv_many_next(a, most_q, group, w);
@@ -471,6 +471,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
               ok = false;
               break;
             }
+            ++issued;
             if (lane == 0) mbar_arrive_expect_tx(&raw_full[slot], bytes);
             __syncwarp();
             if (load)
@@ -488,9 +489,8 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
       }
     }
     // every copy has landed before the CTA's shared memory goes
-    const uint32_t items = 2 * tiles_done;
     for (uint32_t i = 0; i < Cfg::RAW_SLOTS; ++i)
-      if (items > i) mbar_drain(&raw_full[i], ((items - 1 - i) / Cfg::RAW_SLOTS) & 1, kWaitBudgetNs);
+      if (issued > i) mbar_drain(&raw_full[i], kv_ring_last_parity(issued, i, Cfg::RAW_SLOTS), kWaitBudgetNs);
   } else if (warp == 13) {
     // ------------------------------------------------------------------ products (the whole warp keeps step, one thread issues)
     constexpr uint32_t kHi = smem_desc_hi(1024, kSwizzle128B);

@@ -36,12 +36,14 @@ struct KvAttnArgs {
 
 constexpr float kLn2 = 0.69314718055994531f;
 
-// mbar_wait with its waiting loop out of line: the roles' loops stay short, which prompts gain 1% and drafts 3% by.
+// mbar_wait by a whole warp, whose lanes all get the same answer: one that went on while another gave up would wait
+// for it for ever at the next operation of the whole warp.  The waiting loop is out of line: the roles' loops stay
+// short, which prompts gain 1% and drafts 3% by.
 __device__ __noinline__ bool kv_wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned int site) {
-  return mbar_wait(bar, parity, abort_flag, site);
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, site));
 }
 __device__ __forceinline__ bool kv_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned int site) {
-  return mbar_try_wait(bar, parity) || kv_wait_on(bar, parity, abort_flag, site);
+  return __all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)) || kv_wait_on(bar, parity, abort_flag, site);
 }
 
 // ================================================================== few rows for each kv head
@@ -400,7 +402,7 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
     auto next_segment = [&]() {
       const bool more = kv_next_segment(a, most_q, w);
       const int buf = seg & 1;
-      if (!mbar_wait(&seg_empty[buf], ((seg >> 1) & 1) ^ 1, abort_flag, kSiteProducerEmpty)) return false;
+      if (!kv_wait(&seg_empty[buf], ((seg >> 1) & 1) ^ 1, abort_flag, kSiteProducerEmpty)) return false;
       ++seg;
       const int rows = w.req.rows_q * group, pos0 = w.req.len - w.req.rows_q;  // (pos0: the first query's position)
       if (lane == 0) {
@@ -507,7 +509,7 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
     while (cur.tiles && ok) {
       for (int i = 0; i < cur.tiles; ++i) {
         const int token = cur.token + i * kKvTile, first = (token >> a.shift) - (cur.token >> a.shift);
-        if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, kSiteProducerEmpty)) {
+        if (!kv_wait(&empty[stage], phase ^ 1, abort_flag, kSiteProducerEmpty)) {
           ok = false;
           break;
         }
@@ -549,11 +551,11 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
   auto warps_meet = [&]() {
     __syncwarp();
     if (lane == 0) mbar_arrive(join_bar);
-    return mbar_wait(join_bar, joins++ & 1, abort_flag, kSiteEpiTmemFull);
+    return kv_wait(join_bar, joins++ & 1, abort_flag, kSiteEpiTmemFull);
   };
   for (uint32_t seg = 0;; ++seg) {
     const int buf = seg & 1;
-    if (!mbar_wait(&seg_full[buf], (seg >> 1) & 1, abort_flag, kSiteMmaFull)) break;
+    if (!kv_wait(&seg_full[buf], (seg >> 1) & 1, abort_flag, kSiteMmaFull)) break;
     const KvFewSegment v = sSeg[buf];
     if (v.count == 0) break;
     const uint2* q_frag = sQ + buf * KS * NT * 32 + lane;
@@ -582,7 +584,7 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
     bool ok = true;
     for (int i = 0; i < v.count; ++i) {
       const int token = v.token + i * kKvTile;
-      ok = mbar_wait(&full[stage], phase, abort_flag, kSiteMmaFull);
+      ok = kv_wait(&full[stage], phase, abort_flag, kSiteMmaFull);
       const uint8_t* sK = smem + stage * 2 * Cfg::HALF + warp * 16 * D;
       const uint8_t* sV = sK + Cfg::HALF;
       const float4 sc = sSC[stage * 4 + warp];

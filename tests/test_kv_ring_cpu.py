@@ -43,3 +43,12 @@ def test_the_loaders_count_what_they_issue():
     text = open(os.path.join(CSRC, "kv_prefill.cuh")).read()
     gave_up, counted = text.index("!kv_wait(&raw_empty[slot]"), text.index("++issued;")
     assert gave_up < counted < text.index("mbar_arrive_expect_tx(&raw_full[slot], bytes)")
+
+
+def test_whole_warps_wait_by_one_vote():
+    """The kernels' roles wait through kv_wait, whose lanes agree; a wait of single lanes would let some of a warp
+    give up in front of the next operation of the whole warp."""
+    for name in ("kv_attention.cuh", "kv_prefill.cuh"):
+        text = re.sub(r"//.*", "", open(os.path.join(CSRC, name)).read())
+        for m in re.finditer(r"\bmbar_(?:try_)?wait\(", text):
+            assert "__all_sync(0xFFFFFFFFu, " in text[m.start() - 40:m.start()], text[m.start() - 60:m.end()]

@@ -283,6 +283,10 @@ mx_status kv_attention(const void* q, mx_half type, int64_t num_tokens, int64_t 
   a.f16 = type == MX_HALF_F16;
   a.window = static_cast<int>(window < kKvMostTokens ? window : kKvMostTokens);
   cudaStream_t st = as_stream(stream);
+  // A call's launches speak to each other through the workspace.  Host threads that share a stream, and with it a
+  // workspace, take turns, so that no other call's launch comes between them.
+  static std::mutex turn;
+  const std::lock_guard<std::mutex> hold(turn);
   if (elem == MX_E5M2)
     return head_dim == 64 ? kv_attention_launch<1, 64>(a, block_tokens, max_q_len, workspace, st)
                           : kv_attention_launch<1, 128>(a, block_tokens, max_q_len, workspace, st);

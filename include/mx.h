@@ -473,7 +473,7 @@ size_t kv_attention_workspace_bytes(int64_t num_tokens, int64_t requests, int64_
  * row does not see does not reach it.  workspace: kv_attention_workspace_bytes bytes, 32-byte
  * aligned; its first 4096 bytes are zero before its first use and are left zero, so that the next call can use it,
  * for whatever sizes it is large enough (after MX_ERR_TIMEOUT they are to be cleared again); calls that may
- * overlap need one each.
+ * overlap need one each.  Calls from several host threads on one stream do not overlap, and may share one.
  * Sums and softmax statistics are FP32; the weights are rounded to FP16 for the second product.
  */
 mx_status kv_attention(const void* q, mx_half type, int64_t num_tokens, int64_t heads, int64_t q_stride_token,

@@ -588,12 +588,15 @@ def _kv_workspace(need, dev, stream, given):
         return ws
     ws = _workspaces.get((dev.index, stream))
     if ws is None or ws.numel() < need:
-        with _lock:
-            _workspaces_old.append(ws)
-            ws = torch.zeros(need, dtype=_uint8, device=dev)
-            if given is not None:  # cleared on torch's stream, used on another
-                torch.cuda.current_stream(dev).synchronize()
-            _workspaces[(dev.index, stream)] = ws
+        with _lock:  # (and looked at again: another thread may have made it)
+            ws = _workspaces.get((dev.index, stream))
+            if ws is None or ws.numel() < need:
+                if ws is not None:
+                    _workspaces_old.append(ws)
+                ws = torch.zeros(need, dtype=_uint8, device=dev)
+                if given is not None:  # cleared on torch's stream, used on another
+                    torch.cuda.current_stream(dev).synchronize()
+                _workspaces[(dev.index, stream)] = ws
     return ws
 
 

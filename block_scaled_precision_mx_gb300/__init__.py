@@ -580,8 +580,12 @@ _workspaces_old = []    # outgrown ones, kept: work in flight may use them
 
 
 def _kv_workspace(need, dev, stream, given):
-    """A workspace for a call that was given none: calls on one stream follow each other and share one;
-    a capture gets its own, since its graph may be replayed beside the stream."""
+    """A workspace for a call that was given none, made and cleared on the stream that the call goes to: calls
+    on one stream follow each other and share one; a capture gets its own, since its graph may be replayed
+    beside the stream."""
+    if given is not None and stream != _stream(None):
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)):
+            return _kv_workspace(need, dev, stream, None)
     if torch.cuda.is_current_stream_capturing():
         ws = torch.empty(need, dtype=_uint8, device=dev)
         ws[:4096].zero_()  # (all that has to be clear)
@@ -593,10 +597,7 @@ def _kv_workspace(need, dev, stream, given):
             if ws is None or ws.numel() < need:
                 if ws is not None:
                     _workspaces_old.append(ws)
-                ws = torch.zeros(need, dtype=_uint8, device=dev)
-                if given is not None:  # cleared on torch's stream, used on another
-                    torch.cuda.current_stream(dev).synchronize()
-                _workspaces[(dev.index, stream)] = ws
+                ws = _workspaces[(dev.index, stream)] = torch.zeros(need, dtype=_uint8, device=dev)
     return ws
 
 

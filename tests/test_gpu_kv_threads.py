@@ -48,3 +48,54 @@ def test_threads_on_one_stream():
     assert not errors, errors
     assert not wrong, wrong[:10]
     assert mx.mx_check() == mx.MX_OK
+
+
+@pytest.mark.parametrize("lens,queries", [([3000, 75], [1, 1]), ([900, 400], [100, 400])])
+@pytest.mark.parametrize("given", [False, True])
+def test_graphs_and_calls_side_by_side(lens, queries, given):
+    """A graph captured without a workspace, on torch's stream or forked to a stream that is passed in, replayed
+    beside calls on both streams."""
+    args, most = case(5, lens, queries)
+    other, other_most = case(6, [700, 2000], [200, 1])
+    want, other_want = mx.kv_attention(*args, most), mx.kv_attention(*other, other_most)
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    main, side, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=main):
+        if given:
+            side.wait_stream(main)
+        mx.kv_attention(*args, most, out=out, lse=lse, stream=side if given else None)
+        if given:
+            main.wait_stream(side)
+    for _ in range(20):
+        out.fill_(7)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(main):
+            graph.replay()
+        with torch.cuda.stream(side):
+            got = [mx.kv_attention(*other, other_most) for _ in range(2)]
+        got += [mx.kv_attention(*other, other_most, stream=side)]
+        got += [mx.kv_attention(*other, other_most)]
+        torch.cuda.synchronize()
+        assert same((out, lse), want)
+        assert all(same(g, other_want) for g in got)
+    assert mx.mx_check() == mx.MX_OK
+
+
+def test_capture_of_a_stream_that_is_passed_in():
+    """The captured stream is not torch's current one."""
+    args, most = case(7, [900, 400], [100, 400])
+    want = mx.kv_attention(*args, most)
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    side, graph, current = torch.cuda.Stream(), torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        with torch.cuda.stream(current):
+            mx.kv_attention(*args, most, out=out, lse=lse, stream=side)
+    for _ in range(3):
+        out.fill_(7)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same((out, lse), want)
+    assert mx.mx_check() == mx.MX_OK

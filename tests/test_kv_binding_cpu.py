@@ -44,3 +44,53 @@ def test_only_outgrown_buffers_are_put_aside():
     assert mx._workspaces_old == []
     b = mx._kv_workspace(6000, CPU, 7, None)
     assert len(mx._workspaces_old) == 1 and mx._workspaces_old[0] is a and mx._workspaces[(None, 7)] is b
+
+
+class Streams:
+    """torch's current stream, as the binding asks for it and changes it; `capturing` names the streams that are captured."""
+
+    def __init__(self, monkeypatch, current, capturing=()):
+        self.current, self.cleared_on, zeros, zero_ = current, [], torch.zeros, torch.Tensor.zero_
+        monkeypatch.setattr(mx, "_stream", lambda s: self.current if s is None else int(s))
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: self.current in capturing)
+        monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: handle)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: pytest.fail("waits for a stream"))
+
+        class Within:
+            def __init__(inner, handle):
+                inner.handle = handle
+
+            def __enter__(inner):
+                inner.before, self.current = self.current, inner.handle
+
+            def __exit__(inner, *exc):
+                self.current = inner.before
+        monkeypatch.setattr(torch.cuda, "stream", Within)
+
+        def noted(fn):
+            def call(*a, **k):
+                self.cleared_on.append(self.current)
+                return fn(*a, **k)
+            return call
+        monkeypatch.setattr(torch, "zeros", noted(zeros))
+        monkeypatch.setattr(torch.Tensor, "zero_", noted(zero_))
+
+
+def test_a_given_streams_buffer_is_made_on_it(monkeypatch):
+    s = Streams(monkeypatch, current=3)
+    a = mx._kv_workspace(5000, CPU, 9, 9)
+    assert s.cleared_on == [9] and s.current == 3
+    assert mx._kv_workspace(5000, CPU, 9, 9) is a and mx._kv_workspace(5000, CPU, 3, None) is not a
+    assert s.cleared_on == [9, 3]
+
+
+def test_a_given_stream_under_capture_gets_its_own(monkeypatch):
+    s = Streams(monkeypatch, current=3, capturing=(9,))
+    a, b = (mx._kv_workspace(5000, CPU, 9, 9) for _ in range(2))
+    assert a is not b and not mx._workspaces and s.cleared_on == [9, 9]
+
+
+def test_a_capture_elsewhere_does_not_clear_a_given_streams_buffer(monkeypatch):
+    s = Streams(monkeypatch, current=3, capturing=(3,))
+    a = mx._kv_workspace(5000, CPU, 9, 9)
+    assert s.cleared_on == [9] and mx._workspaces[(None, 9)] is a

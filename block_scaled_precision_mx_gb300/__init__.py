@@ -575,6 +575,7 @@ def kv_attention_workspace_bytes(num_tokens: int, requests: int, max_q_len: int,
     return int(load().kv_attention_workspace_bytes(num_tokens, requests, max_q_len, heads, kv_heads, head_dim))
 
 
+_LEGACY, _PER_THREAD = 1, 2  # handles of CUDA's default streams; 0 is the first of them
 _workspaces = {}        # (device, stream) -> the buffer that calls on that stream share
 _workspaces_old = []    # outgrown ones, kept: work in flight may use them
 
@@ -584,6 +585,8 @@ def _kv_workspace(need, dev, stream, given):
     on one stream follow each other and share one; a capture gets its own, since its graph may be replayed
     beside the stream."""
     if given is not None and stream != _stream(None):
+        if stream == _LEGACY:
+            stream = 0
         with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)):
             return _kv_workspace(need, dev, stream, None)
     if torch.cuda.is_current_stream_capturing():
@@ -608,9 +611,8 @@ def kv_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor, 
     """Attention of q [tokens][heads][head_dim] over the 8-bit cache (include/mx.h, kv_attention).
     lengths int32 [requests]: cached tokens, the queries' own among them; q_start int32 [requests + 1];
     softmax_scale defaults to head_dim ** -0.5; a workspace is zero before its first use, and calls
-    without one share one for each stream.
-    Returns (out, like q but contiguous; lse float
-    [tokens][heads])."""
+    without one share one for each stream (on the per-thread default stream the caller gives one).
+    Returns (out, like q but contiguous; lse float [tokens][heads])."""
     shape, q_at, half, q_st, q_sh = _rows_of_heads(q, "q")
     blocks, kv_heads, block_tokens, head_dim = _cache_shape(k_codes, v_codes, k_scale, v_scale)
     tokens, heads, d = shape
@@ -631,6 +633,8 @@ def kv_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor, 
     need = kv_attention_workspace_bytes(tokens, requests, max_q_len, heads, kv_heads, head_dim)
     at_stream = _stream(stream)
     if workspace is None:
+        if at_stream == _PER_THREAD:  # (another stream in every thread under one handle: nothing can be kept for it)
+            raise ValueError("a call on the per-thread default stream needs a workspace of the caller's")
         workspace = _kv_workspace(need, dev, at_stream, stream)
     elif workspace.numel() < need or _at(workspace, _uint8, "workspace") is None:
         raise ValueError(f"workspace must have {need} bytes")

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import block_scaled_precision_mx_gb300 as mx
+from block_scaled_precision_mx_gb300 import build as mxbuild
 
 CPU = torch.device("cpu")
 
@@ -94,3 +95,43 @@ def test_a_capture_elsewhere_does_not_clear_a_given_streams_buffer(monkeypatch):
     s = Streams(monkeypatch, current=3, capturing=(3,))
     a = mx._kv_workspace(5000, CPU, 9, 9)
     assert s.cleared_on == [9] and mx._workspaces[(None, 9)] is a
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """kv_attention on CPU tensors up to the library's entry, which only notes (workspace, its bytes, stream)."""
+    mxbuild.build()
+    real, noted = mx.load(), []
+
+    class Library:
+        kv_attention_workspace_bytes = staticmethod(lambda *a: real.kv_attention_workspace_bytes(*a))
+
+        @staticmethod
+        def kv_attention(*a):
+            noted.append((a[-2], a[-1]))
+            return mx.MX_OK
+    monkeypatch.setattr(mx, "load", lambda: Library)
+    monkeypatch.setattr(mx, "_at", lambda t, dtype, name: t.data_ptr())
+    monkeypatch.setattr(mx, "_rows_of_heads", lambda x, name: (x.shape, x.data_ptr(), 0, *x.stride()[:2]))
+    mx.kv_attention_workspace_bytes.cache_clear()
+
+    def call(requests, queries, heads=8, kv_heads=2, d=128, **kw):
+        q = torch.zeros(requests * queries, heads, d, dtype=torch.bfloat16)
+        codes, scale = torch.zeros(1, kv_heads, 16, d, dtype=torch.uint8), torch.ones(1, kv_heads)
+        ints = torch.zeros(requests + 1, dtype=torch.int32)
+        mx.kv_attention(q, codes, codes, scale, scale, ints[:requests, None], ints[:requests], ints, queries, **kw)
+        return noted[-1]
+    yield call
+    mx.kv_attention_workspace_bytes.cache_clear()
+
+
+def test_handles_of_default_streams(monkeypatch, calls):
+    """2 is another stream in every thread: nothing is kept for it, and a call on it brings its workspace.  1 is 0."""
+    Streams(monkeypatch, current=0)
+    with pytest.raises(ValueError, match="per-thread"):
+        calls(2, 1, stream=2)
+    assert not mx._workspaces
+    ws = torch.zeros(1 << 24, dtype=torch.uint8)
+    assert calls(2, 1, stream=2, workspace=ws) == (ws.data_ptr(), 2)
+    shared, _ = calls(2, 1)
+    assert calls(2, 1, stream=1) == (shared, 1) and len(mx._workspaces) == 1

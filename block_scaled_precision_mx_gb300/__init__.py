@@ -577,7 +577,8 @@ def kv_attention_workspace_bytes(num_tokens: int, requests: int, max_q_len: int,
 
 _LEGACY, _PER_THREAD = 1, 2  # handles of CUDA's default streams; 0 is the first of them
 _workspaces = {}        # (device, stream) -> the buffer that calls on that stream share
-_workspaces_old = []    # outgrown ones, kept: work in flight may use them
+_workspaces_old = []    # outgrown ones, kept: work in flight may use them (each is larger than the last, and sizes are few)
+_MOST_REQUESTS = 16384
 
 
 def _kv_workspace(need, dev, stream, given):
@@ -630,14 +631,17 @@ def kv_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor, 
         lse = torch.empty((tokens, heads), dtype=_float32, device=dev)
     elif lse.shape != shape[:2] or _at(lse, _float32, "lse") is None:
         raise ValueError("lse must be [tokens][heads]")
-    need = kv_attention_workspace_bytes(tokens, requests, max_q_len, heads, kv_heads, head_dim)
     at_stream = _stream(stream)
     if workspace is None:
         if at_stream == _PER_THREAD:  # (another stream in every thread under one handle: nothing can be kept for it)
             raise ValueError("a call on the per-thread default stream needs a workspace of the caller's")
+        # (for the most requests, 0.1 MB more: a size follows from the kernel and head_dim alone)
+        need = kv_attention_workspace_bytes(1, _MOST_REQUESTS, max_q_len, heads, kv_heads, head_dim)
         workspace = _kv_workspace(need, dev, at_stream, stream)
-    elif workspace.numel() < need or _at(workspace, _uint8, "workspace") is None:
-        raise ValueError(f"workspace must have {need} bytes")
+    else:
+        need = kv_attention_workspace_bytes(tokens, requests, max_q_len, heads, kv_heads, head_dim)
+        if workspace.numel() < need or _at(workspace, _uint8, "workspace") is None:
+            raise ValueError(f"workspace must have {need} bytes")
     st = load().kv_attention(q_at, half, tokens, heads, q_st, q_sh, _at(k_codes, _uint8, "k_codes"),
                              _at(v_codes, _uint8, "v_codes"), _at(k_scale, _float32, "k_scale"),
                              _at(v_scale, _float32, "v_scale"), elem, blocks, kv_heads, block_tokens, head_dim,

@@ -111,6 +111,7 @@ def calls(monkeypatch):
             noted.append((a[-2], a[-1]))
             return mx.MX_OK
     monkeypatch.setattr(mx, "load", lambda: Library)
+    monkeypatch.setattr(mx, "_stream", lambda s: 0 if s is None else int(s))
     monkeypatch.setattr(mx, "_at", lambda t, dtype, name: t.data_ptr())
     monkeypatch.setattr(mx, "_rows_of_heads", lambda x, name: (x.shape, x.data_ptr(), 0, *x.stride()[:2]))
     mx.kv_attention_workspace_bytes.cache_clear()
@@ -135,3 +136,21 @@ def test_handles_of_default_streams(monkeypatch, calls):
     assert calls(2, 1, stream=2, workspace=ws) == (ws.data_ptr(), 2)
     shared, _ = calls(2, 1)
     assert calls(2, 1, stream=1) == (shared, 1) and len(mx._workspaces) == 1
+
+
+def test_buffers_are_few_whatever_the_requests(calls):
+    """One buffer a kernel and head size, however many requests calls have: prompts of 1 to 256 requests, and as
+    many as there may be, then every kernel at both head sizes."""
+    prompts = {calls(n, 17)[0] for n in (*range(1, 257, 5), 16384)}
+    assert len(prompts) == 1 and not mx._workspaces_old
+    for d in (64, 128):
+        for queries in (1, 2, 4, 17, 40):
+            for n in (1, 3, 300):
+                calls(n, queries, heads=8, kv_heads=2, d=d)
+    assert not mx._workspaces_old                                 # (the largest came first)
+    mx._workspaces.clear()
+    for n in (1, 300):
+        for queries, d in ((1, 64), (1, 128), (4, 64), (4, 128), (40, 64), (40, 128)):
+            calls(n, queries, d=d)
+    kept = sum(w.numel() for w in (*mx._workspaces.values(), *mx._workspaces_old))
+    assert len(mx._workspaces_old) <= 5 and kept <= 100e6          # (44 MB the largest, smaller ones together as much)

@@ -484,11 +484,11 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
       ch.len = w.req.len;
       ch.h = w.h;
       left -= ch.tiles;
-      const int page = (ch.token >> a.shift) + lane;
+      const int page = (ch.token >> a.shift) + lane, any_lo = a.window ? ch.len - w.req.rows_q - a.window + 1 : 0;
       ch.block = -1;
       ch.sk = 0.f;
       ch.sv = 1.f;
-      if (page << a.shift < ch.len) {
+      if (page << a.shift < ch.len && (page + 1) << a.shift > any_lo) {  // (what is in front of every row's window is not read)
         ch.block = a.tables[static_cast<int64_t>(w.r) * a.max_blocks + page];
         if (ch.block < 0 || ch.block >= a.num_blocks) {
           atomicOr(&g_mx_error_word, kSiteBadCache);

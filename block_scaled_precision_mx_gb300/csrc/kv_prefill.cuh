@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
         const int page = (token0 >> a.shift) + lane;
         int block = -1;
         float sk = 1.f, sv = 1.f;
-        if (page << a.shift < w.u.len) {
+        if (page << a.shift < w.u.len && (page + 1) << a.shift > w.u.any_lo) {  // (what is in front of every row's window is not read)
           block = a.tables[static_cast<int64_t>(w.r) * a.max_blocks + page];
           if (block < 0 || block >= a.num_blocks) {
             atomicOr(&g_mx_error_word, kSiteBadCache);

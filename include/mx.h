@@ -406,7 +406,8 @@ size_t mx_scale_bytes(int64_t rows, int64_t cols, int block, int block_rows, mx_
  *   k_scale, v_scale  float [num_blocks][kv_heads]; a token's value is code * scale.
  * head_dim is 64 or 128, kv_heads at most 1024, and num_blocks * kv_heads * P at most 2^31 - 1.
  * A request's tokens are in the blocks that its row of block_tables[requests][max_blocks] (int32)
- * names, P by P; entries past its length are not read.  requests is at most 16384, max_blocks * P and
+ * names, P by P; entries past its length are not read, nor by kv_attention those that lie in front of every
+ * row's window (a caller may have given such blocks back).  requests is at most 16384, max_blocks * P and
  * the tokens of a call at most 2^30.  Lengths, block
  * numbers and slots are on the device and the host cannot see them: where they break their
  * contract nothing is read or written out of range, and mx_check returns MX_ERR_INVALID_ARG.

@@ -7,7 +7,7 @@ import torch
 
 import block_scaled_precision_mx_gb300 as mx
 from tests import kv_reference as ref
-from tests.test_gpu_kv import attention_case, built, gpu  # noqa: F401
+from tests.test_gpu_kv import attention_case, built, check_attention, gpu  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 MOST, LEAST = 2 ** 31 - 1, -2 ** 31
@@ -59,3 +59,17 @@ def test_broken_lengths_and_query_starts(queries, more, broken):
         assert (np.abs(got[a:b] - want) <= tol + 2.0 ** -8 * (np.abs(want) + tol) + 2.0 ** -25).all()
         assert (np.abs(got_lse[a:b] - want_lse) <= lse_tol).all()
     assert (got[~touched] == 7).all() and (got_lse[~touched] == 7).all()
+
+
+@pytest.mark.parametrize("queries", [1, 4, 40, 100])
+@pytest.mark.parametrize("p", [16, 64])
+def test_table_entries_in_front_of_the_window_are_not_read(p, queries):
+    """A caller with a sliding window gives back the blocks that it has left behind."""
+    rng = np.random.RandomState(queries + p)
+    lens = [400, 257, 20]
+    for window in (1, 30, 100):
+        c = attention_case(rng, lens, [min(n, queries) for n in lens], 4, 2, 128, p, "bf16", 0)
+        for r, n in enumerate(lens):
+            first = max(0, n - min(n, queries) - window + 1)
+            c["tables"][r, :first // p] = rng.choice([-1, -5], first // p)
+        check_attention(c, 0, window=window)

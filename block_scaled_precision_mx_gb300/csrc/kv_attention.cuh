@@ -121,7 +121,7 @@ struct KvFewCfg {
   static constexpr int OFF_SEEN = OFF_QF + 2 * 4 * ROWS;                // int2 [2][ROWS]
   static constexpr int OFF_NAN = OFF_SEEN + 2 * 8 * ROWS;               // u32 [2][ROWS][D / 32], bits of d
   static constexpr int OFF_SEG = OFF_NAN + 2 * 4 * ROWS * (D / 32);     // KvFewSegment [2]
-  static constexpr int OFF_SC = OFF_SEG + 2 * sizeof(KvFewSegment);     // float4 [STAGES][4]
+  static constexpr int OFF_SC = OFF_SEG + 2 * sizeof(KvFewSegment);     // float4 [STAGES][4]: sK, log2 sV, 1 / sV, how codes are taken
   static constexpr int OFF_BAR = OFF_SC + 16 * 4 * STAGES;
   static constexpr int SMEM = OFF_BAR + 8 * (2 * STAGES + 5) + 16 + 1024;
   static constexpr int CTAS = NT == 1 ? (D == 64 ? 4 : 3) : 2;
@@ -153,6 +153,51 @@ __device__ __forceinline__ uint32_t kv_pack_f16(float lo, float hi) {
 template <int FMT>
 __device__ __forceinline__ uint32_t kv_nan_bytes(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + (FMT == 0 ? 0x01010101u : 0x04040404u)) & 0x80808080u;
+}
+
+// Scales are 0 or in [2^-48, 2^48]: within it 2^(z + log2 sV - m) and its quotient by sV stay numbers of FP32 that
+// count (two blocks' are at most 2^96 apart).  The codes of a block of scale 0 are taken as zeros; those of one of any
+// other scale as NaN, which reaches the rows that see it as a NaN in the cache does.
+constexpr float kKvLeastScale = 1.f / (1ull << kKvMaxExp), kKvMostScale = static_cast<float>(1ull << kKvMaxExp);
+constexpr int kKvTakeZero = 1, kKvTakeNan = 0x80;  // 1 + the byte that each code is taken as; 0: as it is
+
+// What a scale says of its block's codes; the scale itself becomes one in range.
+__device__ __forceinline__ int kv_check_scale(float& s, float for_zero) {
+  if (s >= kKvLeastScale && s <= kKvMostScale) return 0;
+  const bool zero = s == 0.f;
+  s = zero ? for_zero : 1.f;
+  return zero ? kKvTakeZero : kKvTakeNan;
+}
+// Both scales of a block; of K, and of V << 8.  tell: some row sees the block.
+__device__ __forceinline__ int kv_check_scales(float& sk, float& sv, bool tell) {
+  const int take = kv_check_scale(sk, 1.f) | kv_check_scale(sv, kKvLeastScale) << 8;
+  if (tell && take & (kKvTakeNan | kKvTakeNan << 8)) atomicOr(&g_mx_error_word, kSiteBadCache);
+  return take;
+}
+__device__ __forceinline__ uint32_t kv_four_taken(int take) { return static_cast<uint32_t>(take - 1) * 0x01010101u; }
+// A warp's slice of 16 tokens whose codes are not taken as they are: K, and V `half` behind it.  (Rare.)
+template <int D>
+__device__ __noinline__ void kv_take_slice(uint8_t* at, int half, int take) {
+  for (int i = 16 * (threadIdx.x & 31); i < 16 * D; i += 512) {
+    const uint32_t k = kv_four_taken(take & 0xFF), v = kv_four_taken(take >> 8);
+    if (take & 0xFF) *reinterpret_cast<uint4*>(at + i) = make_uint4(k, k, k, k);
+    if (take >> 8) *reinterpret_cast<uint4*>(at + half + i) = make_uint4(v, v, v, v);
+  }
+  fence_proxy_async_smem();  // (copies come to the same place next)
+  __syncwarp();
+}
+// Block and scales of a table entry.  tell: some row sees it.
+__device__ __forceinline__ void kv_look_up(const KvAttnArgs& a, int request, int page, int head, bool tell, int& block,
+                                           float& sk, float& sv) {
+  block = a.tables[static_cast<int64_t>(request) * a.max_blocks + page];
+  if (block < 0 || block >= a.num_blocks) {
+    if (tell) atomicOr(&g_mx_error_word, kSiteBadCache);
+    block = -1;
+  } else {
+    const int64_t at = static_cast<int64_t>(block) * a.kv_heads + head;
+    sk = a.k_scale[at];
+    sv = a.v_scale[at];
+  }
 }
 
 // A request as the kernels go through it.
@@ -390,7 +435,7 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
     // A chunk is up to 32 blocks of a segment: lane i holds block i and its scales, read while the chunk
     // before it is loaded.
     struct Chunk {
-      int token, len, h, tiles, block;
+      int token, tiles, h, block, take;
       float sk, sv;
     };
     const int P = 1 << a.shift, rows_box = min(P, kKvTile), boxes = kKvTile / rows_box;
@@ -481,24 +526,14 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
       }
       ch.tiles = min(left, most_tiles);
       ch.token = (w.req.first_tile + w.tile + w.count - left) * kKvTile;
-      ch.len = w.req.len;
       ch.h = w.h;
       left -= ch.tiles;
-      const int page = (ch.token >> a.shift) + lane, any_lo = a.window ? ch.len - w.req.rows_q - a.window + 1 : 0;
+      const int page = (ch.token >> a.shift) + lane, any_lo = a.window ? w.req.len - w.req.rows_q - a.window + 1 : 0;
       ch.block = -1;
-      ch.sk = 0.f;
+      ch.sk = 1.f;
       ch.sv = 1.f;
-      if (page << a.shift < ch.len && (page + 1) << a.shift > any_lo) {  // (what is in front of every row's window is not read)
-        ch.block = a.tables[static_cast<int64_t>(w.r) * a.max_blocks + page];
-        if (ch.block < 0 || ch.block >= a.num_blocks) {
-          atomicOr(&g_mx_error_word, kSiteBadCache);
-          ch.block = -1;
-        } else {
-          const int64_t at = static_cast<int64_t>(ch.block) * a.kv_heads + ch.h;
-          ch.sk = a.k_scale[at];
-          ch.sv = a.v_scale[at];
-        }
-      }
+      if (page << a.shift < w.req.len && (page + 1) << a.shift > any_lo)  // (what is in front of every row's window is not read)
+        kv_look_up(a, w.r, page, ch.h, true, ch.block, ch.sk, ch.sv);
     };
     int stage = 0;
     uint32_t phase = 0;
@@ -525,8 +560,10 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
           tma_load_2d(dst + Cfg::HALF, &tmV, &full[stage], 0, row);
         }
         const int from = ((token + 16 * (lane & 3)) >> a.shift) - (cur.token >> a.shift);  // lanes 0..3: the slices' scales
+        if (i == 0) cur.take = kv_check_scales(cur.sk, cur.sv, true);  // (here, where the first boxes are on their way)
         const float slice_k = __shfl_sync(0xFFFFFFFFu, cur.sk, from), slice_v = __shfl_sync(0xFFFFFFFFu, cur.sv, from);
-        if (lane < 4) sSC[stage * 4 + lane] = make_float4(slice_k, log2f(slice_v), 1.f / slice_v, 0.f);
+        const int take = __shfl_sync(0xFFFFFFFFu, cur.take, from);
+        if (lane < 4) sSC[stage * 4 + lane] = make_float4(slice_k, log2f(slice_v), 1.f / slice_v, __int_as_float(take));
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[stage]);
         ++issued;
@@ -591,6 +628,7 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
       const bool edge = token < v.all_lo || token + kKvTile > v.all_hi;
       const int t0 = token + 16 * warp;
       if (!ok) break;
+      if (const int take = __float_as_int(sc.w)) kv_take_slice<D>(smem + stage * 2 * Cfg::HALF + warp * 16 * D, Cfg::HALF, take);
       {
         // S^T
         float s[NT][4];

@@ -84,7 +84,7 @@ struct KvUnit {
   int q0, rows_q, len;                // the request
   int row0, rows;                     // this unit's rows of its head group
   int first_tile, tiles;
-  int any_lo, all_lo, all_hi;         // tokens from any_lo on are seen by some row; [all_lo, all_hi) by all
+  int any_lo, any_hi, all_lo, all_hi; // tokens [any_lo, any_hi) are seen by some row; [all_lo, all_hi) by all
   __device__ __forceinline__ int cost() const { return tiles + kKvUnitCost; }
 };
 
@@ -99,9 +99,9 @@ __device__ __forceinline__ KvUnit kv_unit(const KvAttnArgs& a, const KvRequest& 
   u.any_lo = a.window ? max(0, p0 - a.window + 1) : 0;
   u.all_lo = a.window ? max(0, p1 - a.window + 1) : 0;
   u.all_hi = a.causal ? min(req.len, p0 + 1) : req.len;
-  const int hi = a.causal ? min(req.len, p1 + 1) : req.len;
+  u.any_hi = a.causal ? min(req.len, p1 + 1) : req.len;
   u.first_tile = u.any_lo / kKvManyTile;
-  u.tiles = max(1, (max(hi, 0) + kKvManyTile - 1) / kKvManyTile - u.first_tile);
+  u.tiles = max(1, (max(u.any_hi, 0) + kKvManyTile - 1) / kKvManyTile - u.first_tile);
   return u;
 }
 __device__ __forceinline__ int kv_units_of(const KvRequest& req, int group) {
@@ -299,6 +299,12 @@ __device__ __forceinline__ uint64_t kv_add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// One lane's box of codes in place of a load.  (Rare.)
+__device__ __noinline__ void kv_fill_box(uint8_t* to, int bytes, uint32_t four) {
+  for (int i = 0; i < bytes; i += 16) *reinterpret_cast<uint4*>(to + i) = make_uint4(four, four, four, four);
+  fence_proxy_async_smem();  // (a copy may come to the same place next)
+}
+
 template <int FMT, int D>
 __global__ void __launch_bounds__(kKvManyThreads, 1)
     kv_attention_many_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -445,23 +451,16 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
         const int page = (token0 >> a.shift) + lane;
         int block = -1;
         float sk = 1.f, sv = 1.f;
-        if (page << a.shift < w.u.len && (page + 1) << a.shift > w.u.any_lo) {  // (what is in front of every row's window is not read)
-          block = a.tables[static_cast<int64_t>(w.r) * a.max_blocks + page];
-          if (block < 0 || block >= a.num_blocks) {
-            atomicOr(&g_mx_error_word, kSiteBadCache);
-            block = -1;
-          } else {
-            const int64_t at = static_cast<int64_t>(block) * a.kv_heads + w.h;
-            sk = a.k_scale[at];
-            sv = a.v_scale[at];
-          }
-        }
+        const bool told = page << a.shift < w.u.any_hi;  // (behind any_hi another unit's rows may see it)
+        if (page << a.shift < w.u.len && (page + 1) << a.shift > w.u.any_lo)  // (in front of any_lo no row sees it)
+          kv_look_up(a, w.r, page, w.h, told, block, sk, sv);
+        const int take = kv_check_scales(sk, sv, told);
+        const bool odd = __any_sync(0xFFFFFFFFu, take != 0);  // some block's codes are not taken as they are
         for (int i = 0; i < n && ok; ++i, ++tiles_done) {
           const int token = token0 + i * kKvManyTile, from = (token - token0) >> a.shift;
           const int my = token + lane * rows_box;
-          const int box_block = __shfl_sync(0xFFFFFFFFu, block, min((my - token0) >> a.shift, 31));
-          const bool load = lane < boxes && box_block >= 0;
-          const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, load)) * rows_box * D;
+          const int box_at = min((my - token0) >> a.shift, 31), box_block = __shfl_sync(0xFFFFFFFFu, block, box_at);
+          const int box_take = odd ? __shfl_sync(0xFFFFFFFFu, take, box_at) : 0;
           const int slice = ((lane & 7) * 16) >> a.shift;
           const float slice_k = __shfl_sync(0xFFFFFFFFu, sk, from + slice), slice_v = __shfl_sync(0xFFFFFFFFu, sv, from + slice);
 #pragma unroll 1
@@ -471,11 +470,19 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
               ok = false;
               break;
             }
+            uint8_t* dst = smem + Cfg::OFF_RAW + slot * Cfg::RAW + lane * rows_box * D;
+            const int taken = half ? box_take >> 8 : box_take & 0xFF;
+            const bool load = lane < boxes && box_block >= 0 && !taken;
+            const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, load)) * rows_box * D;
+            if (odd) {
+              if (lane < boxes && taken) kv_fill_box(dst, rows_box * D, kv_four_taken(taken));
+              __syncwarp();
+            }
             ++issued;
             if (lane == 0) mbar_arrive_expect_tx(&raw_full[slot], bytes);
             __syncwarp();
             if (load)
-              tma_load_2d(smem + Cfg::OFF_RAW + slot * Cfg::RAW + lane * rows_box * D, half ? &tmV : &tmK, &raw_full[slot], 0,
+              tma_load_2d(dst, half ? &tmV : &tmK, &raw_full[slot], 0,
                           ((box_block * a.kv_heads + w.h) << a.shift) + (my & (P - 1)));
             if (half == 0) {
               const uint32_t st = tiles_done % kKvManyScales;

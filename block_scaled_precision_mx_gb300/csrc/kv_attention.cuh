@@ -186,13 +186,13 @@ __device__ __noinline__ void kv_take_slice(uint8_t* at, int half, int take) {
   fence_proxy_async_smem();  // (copies come to the same place next)
   __syncwarp();
 }
-// Block and scales of a table entry.  tell: some row sees it.
-__device__ __forceinline__ void kv_look_up(const KvAttnArgs& a, int request, int page, int head, bool tell, int& block,
-                                           float& sk, float& sv) {
+// Block and scales of a table entry.  A number out of range has no block, and scales that are none.
+__device__ __forceinline__ void kv_look_up(const KvAttnArgs& a, int request, int page, int head, int& block, float& sk,
+                                           float& sv) {
   block = a.tables[static_cast<int64_t>(request) * a.max_blocks + page];
   if (block < 0 || block >= a.num_blocks) {
-    if (tell) atomicOr(&g_mx_error_word, kSiteBadCache);
     block = -1;
+    sk = sv = NAN;
   } else {
     const int64_t at = static_cast<int64_t>(block) * a.kv_heads + head;
     sk = a.k_scale[at];
@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
       ch.sk = 1.f;
       ch.sv = 1.f;
       if (page << a.shift < w.req.len && (page + 1) << a.shift > any_lo)  // (what is in front of every row's window is not read)
-        kv_look_up(a, w.r, page, ch.h, true, ch.block, ch.sk, ch.sv);
+        kv_look_up(a, w.r, page, ch.h, ch.block, ch.sk, ch.sv);
     };
     int stage = 0;
     uint32_t phase = 0;

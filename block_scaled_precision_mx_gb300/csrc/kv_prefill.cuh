@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
         float sk = 1.f, sv = 1.f;
         const bool told = page << a.shift < w.u.any_hi;  // (behind any_hi another unit's rows may see it)
         if (page << a.shift < w.u.len && (page + 1) << a.shift > w.u.any_lo)  // (in front of any_lo no row sees it)
-          kv_look_up(a, w.r, page, w.h, told, block, sk, sv);
+          kv_look_up(a, w.r, page, w.h, block, sk, sv);
         const int take = kv_check_scales(sk, sv, told);
         const bool odd = __any_sync(0xFFFFFFFFu, take != 0);  // some block's codes are not taken as they are
         for (int i = 0; i < n && ok; ++i, ++tiles_done) {

@@ -405,8 +405,8 @@ size_t mx_scale_bytes(int64_t rows, int64_t cols, int block, int block_rows, mx_
  *   k_codes, v_codes  u8 [num_blocks][kv_heads][P][head_dim], E4M3 or E5M2, 16-byte aligned;
  *   k_scale, v_scale  float [num_blocks][kv_heads]; a token's value is code * scale.
  * Scales are 0 or between 2^-48 and 2^48 (kv_cache_append writes powers of two of that range); a block of
- * scale 0 holds zeros, whatever its codes.  Any other scale breaks the contract (below): attention gives NaN
- * in the rows that see the block, and only there.
+ * scale 0 holds zeros, whatever its codes.  Any other scale breaks the contract (below), and so does a block
+ * number out of range: attention gives NaN in the rows that see the block, and only there.
  * head_dim is 64 or 128, kv_heads at most 1024, and num_blocks * kv_heads * P at most 2^31 - 1.
  * A request's tokens are in the blocks that its row of block_tables[requests][max_blocks] (int32)
  * names, P by P; entries past its length are not read, nor by kv_attention those that lie in front of every

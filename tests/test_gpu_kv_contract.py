@@ -7,7 +7,7 @@ import torch
 
 import block_scaled_precision_mx_gb300 as mx
 from tests import kv_reference as ref
-from tests.test_gpu_kv import attention_case, built, check_attention, gpu  # noqa: F401
+from tests.test_gpu_kv import attention_case, built, check_attention, gpu, run_attention  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 MOST, LEAST = 2 ** 31 - 1, -2 ** 31
@@ -73,3 +73,16 @@ def test_table_entries_in_front_of_the_window_are_not_read(p, queries):
             first = max(0, n - min(n, queries) - window + 1)
             c["tables"][r, :first // p] = rng.choice([-1, -5], first // p)
         check_attention(c, 0, window=window)
+
+
+@pytest.mark.parametrize("bad", [-1, "past"])
+@pytest.mark.parametrize("queries", [1, 4, 40, 100])
+def test_a_block_out_of_range_gives_nan_where_it_is_seen(queries, bad):
+    rng = np.random.RandomState(queries)
+    c = attention_case(rng, [200, 130], [queries, queries], 4, 2, 128, 64, "bf16", 0)
+    want = run_attention(c, 0)
+    c["tables"][0, 0] = len(c["ks"]) if bad == "past" else bad
+    out, lse = run_attention(c, 0)
+    reported()
+    assert torch.isnan(out[:queries]).all() and torch.isnan(lse[:queries]).all()
+    assert torch.equal(out[queries:], want[0][queries:]) and torch.equal(lse[queries:], want[1][queries:])

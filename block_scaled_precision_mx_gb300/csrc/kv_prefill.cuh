@@ -704,7 +704,9 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
         }
         *chunk(i) = make_uint4(f[0], f[1], f[2], f[3]);
       }
-      const float row_mul = a.scale_log2 / mul;
+      // Times a block's scale (2^-48 at least) it is not to become 0: masked scores are -inf before that product, and
+      // -inf * 0 is no mask.  At 2^-101 and below, every score (below 2^38 before it, times 2^48 at most) is 0 to 2^-15.
+      const float row_mul = fmaxf(a.scale_log2 / mul, 1.f / (1ull << 50) / (1ull << 51));
       if (single) sMul[row] = row_mul;
       fence_proxy_async_smem();
       __syncwarp();

@@ -1,6 +1,6 @@
 """The scales of a key/value cache that kv_cache_append did not write, on the GPU: blocks of scale 0, blocks that
-a row does not see with any scale at all, the ends of the range.
-Few rows (1, 4) and prompts (40, 100 queries), against the 64-bit reference and its tolerances."""
+a row does not see with any scale at all, the ends of the range, and products of a row's and a block's scale
+that leave FP32.  Few rows (1, 4) and prompts (40, 100 queries), against the 64-bit reference and its tolerances."""
 import numpy as np
 import pytest
 import torch
@@ -73,3 +73,17 @@ def test_the_ends_of_the_scales_range(queries):
         c[n][c["tables"][r, :2]] = 2.0 ** -48
     c["vs"][c["tables"][0, 2:4]] = 2.0 ** 48
     check_attention(c, 0, scale=1e-3)
+
+
+@pytest.mark.parametrize("queries", QUERIES)
+def test_products_of_scales_below_the_smallest_number(queries):
+    """A tiny softmax scale, tiny queries and key blocks of 2^-48: every visible token weighs the same, and
+    masked ones nothing."""
+    rng = np.random.RandomState(queries + 3)
+    c = attention_case(rng, [200, 120], [queries, queries], 4, 2, 128, 64, "bf16", 0)
+    c["ks"][c["tables"][0, 1]] = 2.0 ** -48
+    check_attention(c, 0, scale=1e-37)
+    check_attention(c, 0, scale=1e-37, window=20)
+    c["q"] = (c["q"].double() * 2.0 ** -110).to(torch.bfloat16)
+    check_attention(c, 0)
+    check_attention(c, 0, scale=1e-30, window=20)

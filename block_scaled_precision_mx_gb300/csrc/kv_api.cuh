@@ -66,10 +66,10 @@ mx_status kv_few_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_len
   return launch_status();
 }
 
-template <int FMT, int D>
+template <int FMT, int D, bool F16>
 mx_status kv_many_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_len, void* workspace, cudaStream_t st) {
   using Cfg = KvManyCfg<D>;
-  auto kern = kv_attention_many_kernel<FMT, D>;
+  auto kern = kv_attention_many_kernel<FMT, D, F16>;
   static std::atomic<bool> attr_set[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MX_ERR_CUDA;
@@ -104,7 +104,8 @@ mx_status kv_attention_launch(const KvAttnArgs& a, int block_tokens, int64_t max
     case 1: return kv_few_launch<FMT, D, 1>(a, block_tokens, max_q_len, workspace, st);
     case 2: return kv_few_launch<FMT, D, 2>(a, block_tokens, max_q_len, workspace, st);
   }
-  return kv_many_launch<FMT, D>(a, block_tokens, max_q_len, workspace, st);
+  return a.f16 ? kv_many_launch<FMT, D, true>(a, block_tokens, max_q_len, workspace, st)
+               : kv_many_launch<FMT, D, false>(a, block_tokens, max_q_len, workspace, st);
 }
 
 // A group of W warps holds a block's values of one head, 4 words of 8 a thread, or 8 where 8 warps would

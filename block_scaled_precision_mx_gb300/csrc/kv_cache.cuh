@@ -143,14 +143,21 @@ __global__ void __launch_bounds__(kKvTablesThreads) kv_block_tables_kernel(const
     const int at = iavail - 1 - j;
     return at < icount ? a.free_list[at] : pushed(at - icount);
   };
+  bool negative = false;  // a block number below 0 among the held, the free or the given-back ones
   if (fits) {
     const int pops = need_at[R], pushes = max(gone_at[R] - pops, 0);
     for (int j = first; j < pops; j += step) {
       const int r = kv_prefix_find(need_at, R, j);
       const int held = (a.before[r] + P - 1) >> a.shift;
-      a.tables[static_cast<int64_t>(r) * a.max_blocks + held + (j - need_at[r])] = popped(j);
+      const int block = popped(j);
+      negative = negative || block < 0;
+      a.tables[static_cast<int64_t>(r) * a.max_blocks + held + (j - need_at[r])] = block;
     }
-    for (int i = first; i < pushes; i += step) a.free_list[icount + i] = pushed(i);
+    for (int i = first; i < pushes; i += step) {
+      const int block = pushed(i);
+      negative = negative || block < 0;
+      a.free_list[icount + i] = block;
+    }
   }
   // four tokens a thread: one search, then along the prefix
   const int tokens = fits ? new_at[R] : 0;
@@ -179,7 +186,8 @@ __global__ void __launch_bounds__(kKvTablesThreads) kv_block_tables_kernel(const
           block = b < held ? a.tables[static_cast<int64_t>(r) * a.max_blocks + b] : popped(need_at[r] + b - held);
           last_b = b;
         }
-        slot[i] = (static_cast<int64_t>(block) << a.shift) + (pos[i] & (P - 1));
+        negative = negative || block < 0;  // (such a token has no slot: -1, not one that may happen to be -1)
+        slot[i] = block < 0 ? -1 : (static_cast<int64_t>(block) << a.shift) + (pos[i] & (P - 1));
       }
     }
     if (a.wide && t0 + 4 <= a.num_tokens) {
@@ -196,6 +204,7 @@ __global__ void __launch_bounds__(kKvTablesThreads) kv_block_tables_kernel(const
         }
     }
   }
+  if (negative) atomicOr(&g_mx_error_word, kSiteBadCache);
 }
 
 // ================================================================== 8-bit codes

@@ -431,7 +431,9 @@ size_t mx_scale_bytes(int64_t rows, int64_t cols, int block, int block_rows, mx_
  * If the stack has too few blocks nothing is moved, info[1] is how many are missing (0 otherwise),
  * info[0] is free_count, and all slots and positions are -1.
  * Contract: 0 <= lengths <= max_blocks * P; the stack stays within its capacity; new tokens at most
- * num_tokens; no block is held twice.  Where it is broken nothing is moved and q_start is 0.
+ * num_tokens; no block is held twice.  Where lengths or counts break it nothing is moved and q_start is 0.
+ * Block numbers are moved as they are; one below 0 that is moved or that a new token's place needs is reported,
+ * and the token's slot is -1.
  * One launch; the same inputs give the same outputs, and the same call again changes nothing.
  */
 mx_status kv_block_tables(int32_t* block_tables, int64_t requests, int64_t max_blocks, const int32_t* len_before,

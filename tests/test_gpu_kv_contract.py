@@ -86,3 +86,27 @@ def test_a_block_out_of_range_gives_nan_where_it_is_seen(queries, bad):
     reported()
     assert torch.isnan(out[:queries]).all() and torch.isnan(lse[:queries]).all()
     assert torch.equal(out[queries:], want[0][queries:]) and torch.equal(lse[queries:], want[1][queries:])
+
+
+# ------------------------------------------------------------------ block tables
+def test_tables_negative_blocks_are_reported():
+    """A table's entry or a free block below 0 gives its tokens no place, not even the last of its block."""
+    p = 16
+    tables = gpu(np.array([[-1, -1], [3, -1], [-1, -1]], np.int32))
+    free = gpu(np.array([5, -2, 6, 0], np.int32))
+    count = torch.tensor([3], dtype=torch.int32, device="cuda")
+    # request 0 goes on in an entry that was never assigned; 1 goes on in its own; 2 takes 6, then the bad one
+    before, after = np.array([10, 10, 0], np.int32), np.array([16, 16, 20], np.int32)
+    q_start, slots, positions, info = mx.kv_block_tables(tables, gpu(before), gpu(after), free, count, 32, p)
+    reported()
+    want = [-1] * 6 + list(range(3 * p + 10, 3 * p + 16)) + list(range(6 * p, 7 * p)) + [-1] * 4
+    assert slots.cpu().tolist() == want
+    assert q_start.cpu().tolist() == [0, 6, 12, 32] and info.cpu().tolist() == [1, 0]
+
+
+def test_tables_negative_blocks_given_back_are_reported():
+    tables = gpu(np.array([[2, -3]], np.int32))
+    free = gpu(np.array([0, 1, -9, -9], np.int32))
+    count = torch.tensor([2], dtype=torch.int32, device="cuda")
+    mx.kv_block_tables(tables, gpu(np.array([20], np.int32)), gpu(np.array([0], np.int32)), free, count, 0, 16)
+    reported()

@@ -158,7 +158,6 @@ __device__ __forceinline__ uint32_t kv_nan_bytes(uint32_t w) {
 // Scales are 0 or in [2^-48, 2^48]: within it 2^(z + log2 sV - m) and its quotient by sV stay numbers of FP32 that
 // count (two blocks' are at most 2^96 apart).  The codes of a block of scale 0 are taken as zeros; those of one of any
 // other scale as NaN, which reaches the rows that see it as a NaN in the cache does.
-constexpr float kKvLeastScale = 1.f / (1ull << kKvMaxExp), kKvMostScale = static_cast<float>(1ull << kKvMaxExp);
 constexpr int kKvTakeZero = 1, kKvTakeNan = 0x80;  // 1 + the byte that each code is taken as; 0: as it is
 
 // What a scale says of its block's codes; the scale itself becomes one in range.

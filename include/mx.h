@@ -452,7 +452,8 @@ mx_status kv_block_tables(int32_t* block_tables, int64_t requests, int64_t max_b
  * values (MAX 448 or 57344; 1 if amax = 0), q = RNE-satfinite(x / scale), NaN -> 0x7F.  A run that
  * starts at offset 0 sets its block's scale from its own values.  One that starts later keeps the
  * block's scale or, where its values need a larger one, raises it, and the codes at the offsets in
- * front of it are rounded again to the new scale.
+ * front of it are rounded again to the new scale; a scale of 0 becomes the run's own (the tokens in front are zeros),
+ * and where the block's scale is out of range the run is left out.
  */
 mx_status kv_cache_append(const void* k, const void* v, mx_half type, int64_t num_tokens, int64_t k_stride_token,
                           int64_t k_stride_head, int64_t v_stride_token, int64_t v_stride_head,

@@ -7,7 +7,7 @@ import torch
 
 import block_scaled_precision_mx_gb300 as mx
 from tests import kv_reference as ref
-from tests.test_gpu_kv import attention_case, built, check_attention, gpu, run_attention  # noqa: F401
+from tests.test_gpu_kv import attention_case, built, check_attention, gpu, run_attention, values  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 MOST, LEAST = 2 ** 31 - 1, -2 ** 31
@@ -110,3 +110,51 @@ def test_tables_negative_blocks_given_back_are_reported():
     count = torch.tensor([2], dtype=torch.int32, device="cuda")
     mx.kv_block_tables(tables, gpu(np.array([20], np.int32)), gpu(np.array([0], np.int32)), free, count, 0, 16)
     reported()
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("elem", [mx.E4M3, mx.E5M2])
+def test_append_to_a_block_of_scale_zero(elem):
+    """Its tokens are zeros, whatever their codes; zeros that follow leave it a block of zeros."""
+    p, d, h = 16, 64, 2
+    rng = np.random.RandomState(elem)
+    codes = rng.randint(0, 100, (2, h, p, d)).astype(np.uint8)
+    codes[:, :, :, 7] = 0x7F                                        # (NaN codes are zeros too)
+    scale = np.zeros((2, h), np.float32)
+    x = values(rng, (2, h, d), torch.bfloat16)
+    x[0, 0] = 0                                                    # block 0, head 0: a token of zeros
+    slots = np.array([5, p + 3], np.int64)
+    kc, vc, ks, vs = gpu(codes), gpu(codes), gpu(scale), gpu(scale)
+    mx.kv_cache_append(x.cuda(), x.cuda(), gpu(slots), kc, vc, ks, vs, elem=elem)
+    assert mx.mx_check() == mx.MX_OK
+    table = ref.decode_table(elem)
+    for c, s in ((kc, ks), (vc, vs)):
+        c, s = c.cpu().numpy(), s.cpu().numpy()
+        for t, (block, off) in enumerate(((0, 5), (1, 3))):
+            for head in range(h):
+                want = ref.scale_for(x[t, head].double().numpy(), elem)
+                assert s[block, head] == want
+                got = table[c[block, head]] * s[block, head]
+                assert (got[:off] == 0).all()
+                assert np.array_equal(got[off], table[ref.encode(x[t, head].double().numpy() / want, elem)] * want)
+                assert np.array_equal(c[block, head, off + 1:], codes[block, head, off + 1:])
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -1.0, 2.0 ** -60, 2.0 ** 60])
+def test_append_to_a_block_of_an_unusable_scale_is_left_out_and_reported(scale):
+    p, d, h = 16, 64, 2
+    rng = np.random.RandomState(7)
+    codes = rng.randint(0, 100, (2, h, p, d)).astype(np.uint8)
+    scales = np.ones((2, h), np.float32)
+    scales[0, 1] = scale
+    x = values(rng, (2, h, d), torch.bfloat16).cuda()
+    slots = np.array([5, p + 3], np.int64)
+    want = ref.append(x.double().cpu().numpy(), slots[1:], codes, np.ones((2, h), np.float32), 0)
+    kc, vc, ks, vs = gpu(codes), gpu(codes), gpu(scales), gpu(np.ones((2, h), np.float32))
+    mx.kv_cache_append(x, x, gpu(slots), kc, vc, ks, vs)
+    reported()
+    kc, ks = kc.cpu().numpy(), ks.cpu().numpy()
+    assert np.array_equal(kc[0, 1], codes[0, 1]) and np.array_equal(ks[0, 1], scales[0, 1], equal_nan=True)
+    both = ref.append(x.double().cpu().numpy(), slots, codes, np.ones((2, h), np.float32), 0)
+    assert np.array_equal(vc.cpu().numpy(), both[0]) and np.array_equal(vs.cpu().numpy(), both[1])
+    assert np.array_equal(kc[0, 0], both[0][0, 0]) and np.array_equal(kc[1], both[0][1]) and ks[0, 0] == both[1][0, 0]

@@ -59,10 +59,13 @@ class Layer:
 
     def step(self, x, after, most_new):
         """Hidden states x of the new tokens, the requests' lengths with them (int32, on the device), and the
-        most new tokens of a request.  Returns (queries, attention's result, its lse, the layer's result)."""
+        most new tokens of a request.  Returns (queries, attention's result, its lse, the layer's result);
+        raises, with everything as it was, if the cache has too few blocks."""
         q_start, slots, positions, info = mx.kv_block_tables(
             self.tables, self.lengths, after, self.free, self.free_count, x.shape[0], self.block_tokens)
         qkv = self.project(x, self.qkv, (self.heads + 2 * self.kv_heads) * self.head_dim)
+        if int(info[1]):  # (read here, while the projection runs)
+            raise RuntimeError(f"{int(info[1])} cache blocks are missing: nothing was moved, the step cannot go on")
         q, k, v = qkv.view(x.shape[0], -1, self.head_dim).split([self.heads, self.kv_heads, self.kv_heads], dim=1)
         mx.kv_cache_append(k, v, slots, *self.codes, *self.scale)
         out, lse = mx.kv_attention(q, *self.codes, *self.scale, self.tables, after, q_start, most_new)

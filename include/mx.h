@@ -430,6 +430,8 @@ size_t mx_scale_bytes(int64_t rows, int64_t cols, int block, int block_rows, mx_
  * block * P + position % P.  num_tokens may exceed their number: the rest is -1.
  * If the stack has too few blocks nothing is moved, info[1] is how many are missing (0 otherwise),
  * info[0] is free_count, and all slots and positions are -1.
+ * The step has to stop there (q_start numbers the tokens all the same, and the tables have no blocks for them):
+ * look at info[1] on the host before kv_attention.
  * Contract: 0 <= lengths <= max_blocks * P; the stack stays within its capacity; new tokens at most
  * num_tokens; no block is held twice.  Where lengths or counts break it nothing is moved and q_start is 0.
  * Block numbers are moved as they are; one below 0 that is moved or that a new token's place needs is reported,

@@ -92,7 +92,7 @@ mx_status kv_many_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_le
   if (planned && pdl_launch(kv_plan_kernel, 1, kKvPlanThreads, 0, st, a, most_q, n, ws) != cudaSuccess) return MX_ERR_CUDA;
   if (pdl_launch(kern, n, kKvManyThreads, Cfg::SMEM, st, tk, tv, a, most_q, planned, ws) != cudaSuccess)
     return MX_ERR_CUDA;
-  if (n > 1 && pdl_launch(kv_join_kernel<D, kKvManyRows>, dim3(n - 1, 16), 128, 0, st, a, static_cast<const uint8_t*>(ws),
+  if (n > 1 && pdl_launch(kv_join_kernel<D>, dim3(n - 1, 16), 128, 0, st, a, static_cast<const uint8_t*>(ws),
                           kv_many_slots_at(a.requests, D)) != cudaSuccess)
     return MX_ERR_CUDA;
   return launch_status();

@@ -111,12 +111,11 @@ struct KvFewCfg {
   static constexpr int ROWS = 8 * NT;
   static constexpr int STAGES = D == 128 ? 3 : 5;
   static constexpr int HALF = kKvTile * D;          // codes of K, or of V, in a tile
-  static constexpr int JOIN = NT < 2 ? NT : 2;      // 8-row tiles that are joined at a time
   static constexpr int O_STRIDE = D + 4;
-  static constexpr int OFF_O = STAGES * 2 * HALF;   // float [warps][8 JOIN][O_STRIDE]
-  static constexpr int OFF_ML = OFF_O + 4 * kKvWarps * 8 * JOIN * O_STRIDE;  // float2 [warps][8 JOIN]
+  static constexpr int OFF_O = STAGES * 2 * HALF;   // float [warps][ROWS][O_STRIDE]
+  static constexpr int OFF_ML = OFF_O + 4 * kKvWarps * ROWS * O_STRIDE;  // float2 [warps][ROWS]
   // two segments' queries
-  static constexpr int OFF_Q = OFF_ML + 8 * kKvWarps * 8 * JOIN;        // uint2 [2][D / 16][NT][32]
+  static constexpr int OFF_Q = OFF_ML + 8 * kKvWarps * ROWS;        // uint2 [2][D / 16][NT][32]
   static constexpr int OFF_QF = OFF_Q + 2 * (D / 16) * NT * 32 * 8;     // float [2][ROWS]
   static constexpr int OFF_SEEN = OFF_QF + 2 * 4 * ROWS;                // int2 [2][ROWS]
   static constexpr int OFF_NAN = OFF_SEEN + 2 * 8 * ROWS;               // u32 [2][ROWS][D / 32], bits of d
@@ -781,58 +780,53 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) l[j] += __shfl_xor_sync(0xFFFFFFFFu, l[j], o);
     float* part = reinterpret_cast<float*>(workspace + kKvSlotsAt + (2 * blockIdx.x + max(v.part - 1, 0)) * Cfg::SLOT);
+    if (!warps_meet()) break;  // what was joined before has been read
 #pragma unroll
-    for (int n0 = 0; n0 < NT; n0 += Cfg::JOIN) {
-      if (!(ok = warps_meet())) break;  // what was joined before has been read
+    for (int j = 0; j < 2 * NT; ++j) {
+      const int at = warp * Cfg::ROWS + (j >> 1) * 8 + 2 * c + (j & 1);
+      if (g == 0) sML[at] = make_float2(m[j], l[j]);
 #pragma unroll
-      for (int j = 2 * n0; j < 2 * (n0 + Cfg::JOIN); ++j) {
-        const int at = warp * 8 * Cfg::JOIN + ((j >> 1) - n0) * 8 + 2 * c + (j & 1);
-        if (g == 0) sML[at] = make_float2(m[j], l[j]);
+      for (int k = 0; k < VW; ++k)
+        *reinterpret_cast<float4*>(&sO[at * Cfg::O_STRIDE + (D / 8) * g + 4 * k]) =
+            make_float4(acc[2 * k][j >> 1][j & 1], acc[2 * k][j >> 1][2 + (j & 1)], acc[2 * k + 1][j >> 1][j & 1],
+                        acc[2 * k + 1][j >> 1][2 + (j & 1)]);
+    }
+    if (!warps_meet()) break;
+    for (int i = tid; i < v.rows * (D / 4); i += 32 * kKvWarps) {
+      const int row = i / (D / 4), d = i % (D / 4) * 4;
+      float2 ml[kKvWarps];
+      float most = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < VW; ++k)
-          *reinterpret_cast<float4*>(&sO[at * Cfg::O_STRIDE + (D / 8) * g + 4 * k]) =
-              make_float4(acc[2 * k][j >> 1][j & 1], acc[2 * k][j >> 1][2 + (j & 1)], acc[2 * k + 1][j >> 1][j & 1],
-                          acc[2 * k + 1][j >> 1][2 + (j & 1)]);
+      for (int k = 0; k < kKvWarps; ++k) {
+        ml[k] = sML[k * Cfg::ROWS + row];
+        most = fmaxf(most, ml[k].x);
       }
-      if (!(ok = warps_meet())) break;
-      const int rows = min(v.rows - 8 * n0, 8 * Cfg::JOIN);
-      for (int i = tid; i < rows * (D / 4); i += 32 * kKvWarps) {
-        const int at = i / (D / 4), d = i % (D / 4) * 4, row = 8 * n0 + at;
-        float2 ml[kKvWarps];
-        float most = -INFINITY;
+      const float ref = most == -INFINITY ? 0.f : most;
+      float sum = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < kKvWarps; ++k) {
-          ml[k] = sML[k * 8 * Cfg::JOIN + at];
-          most = fmaxf(most, ml[k].x);
-        }
-        const float ref = most == -INFINITY ? 0.f : most;
-        float sum = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < kKvWarps; ++k) {
-          const float f = kv_exp2(ml[k].x - ref);
-          const float4 x = *reinterpret_cast<const float4*>(&sO[(k * 8 * Cfg::JOIN + at) * Cfg::O_STRIDE + d]);
-          sum = fmaf(ml[k].y, f, sum);
-          o.x = fmaf(x.x, f, o.x);
-          o.y = fmaf(x.y, f, o.y);
-          o.z = fmaf(x.z, f, o.z);
-          o.w = fmaf(x.w, f, o.w);
-        }
-        if (const uint32_t nan = q_nan[row * (D / 32) + (d >> 5)] >> (d & 31) & 15) {
-          if (nan & 1) o.x = NAN;
-          if (nan & 2) o.y = NAN;
-          if (nan & 4) o.z = NAN;
-          if (nan & 8) o.w = NAN;
-        }
-        if (v.part == 0) {
-          kv_finish<D>(a, v.q0, row, group, v.head, d, most, sum, o);
-        } else {
-          *reinterpret_cast<float4*>(part + row * D + d) = o;
-          if (d == 0) *reinterpret_cast<float2*>(part + Cfg::ROWS * D + 2 * row) = make_float2(most, sum);
-        }
+      for (int k = 0; k < kKvWarps; ++k) {
+        const float f = kv_exp2(ml[k].x - ref);
+        const float4 x = *reinterpret_cast<const float4*>(&sO[(k * Cfg::ROWS + row) * Cfg::O_STRIDE + d]);
+        sum = fmaf(ml[k].y, f, sum);
+        o.x = fmaf(x.x, f, o.x);
+        o.y = fmaf(x.y, f, o.y);
+        o.z = fmaf(x.z, f, o.z);
+        o.w = fmaf(x.w, f, o.w);
+      }
+      if (const uint32_t nan = q_nan[row * (D / 32) + (d >> 5)] >> (d & 31) & 15) {
+        if (nan & 1) o.x = NAN;
+        if (nan & 2) o.y = NAN;
+        if (nan & 4) o.z = NAN;
+        if (nan & 8) o.w = NAN;
+      }
+      if (v.part == 0) {
+        kv_finish<D>(a, v.q0, row, group, v.head, d, most, sum, o);
+      } else {
+        *reinterpret_cast<float4*>(part + row * D + d) = o;
+        if (d == 0) *reinterpret_cast<float2*>(part + Cfg::ROWS * D + 2 * row) = make_float2(most, sum);
       }
     }
-    if (!ok) break;
     if (v.part) {
       // A part of a unit that range boundaries cut: the CTA that writes the last part joins them, in order.
       __threadfence();
@@ -864,58 +858,6 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&seg_empty[buf]);
-  }
-}
-
-// Joins the segments of the units that range boundaries cut.  CTA c looks at the boundary where range c
-// begins; the first boundary inside a unit takes the unit.  Segments are added in order: the range that
-// the unit begins in left its one in slot 1, the others in slot 0.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, const uint8_t* workspace, size_t slots_at) {
-  pdl_prologue();
-  constexpr size_t kSlot = static_cast<size_t>(ROWS) * (D + 2) * 4;
-  __shared__ int list[kKvMaxCtas];
-  __shared__ int listed;
-  const KvJob* jobs = reinterpret_cast<const KvJob*>(workspace + kKvJobsAt);
-  const int c = blockIdx.x + 1, ranges = gridDim.x + 1;
-  const KvJob job = jobs[c];
-  const long long before = jobs[c - 1].begin, total = jobs[ranges - 1].end;
-  if (job.begin >= total || job.unit == job.begin || before > job.unit) return;
-  const long long unit_end = job.unit + job.tiles + kKvUnitCost;
-  if (threadIdx.x < 32) {
-    int n = 0;
-    for (int k0 = c - 1; k0 < ranges; k0 += 32) {
-      const int k = k0 + threadIdx.x;
-      bool has = false, over = true;
-      if (k < ranges) {
-        const long long b = jobs[k].begin, e = jobs[k].end;
-        over = b >= unit_end;
-        const int from = kv_tiles_before(b - job.unit, job.tiles), to = kv_tiles_before(e - job.unit, job.tiles);
-        has = !over && to > from && to - from < job.tiles;  // (a range that has all of it has finished it)
-      }
-      const uint32_t m = __ballot_sync(0xFFFFFFFFu, has);
-      if (has) list[n + __popc(m & ((1u << threadIdx.x) - 1))] = 2 * k + (k == c - 1 ? 1 : 0);
-      n += __popc(m);
-      if (__any_sync(0xFFFFFFFFu, over)) break;
-    }
-    if (threadIdx.x == 0) listed = n;
-  }
-  __syncthreads();
-  const int n = listed;
-  if (n == 0) return;
-  const int group = a.heads / a.kv_heads;
-  for (int i = blockIdx.y * 128 + threadIdx.x; i < job.rows * (D / 4); i += 128 * gridDim.y) {
-    const int row = i / (D / 4), d = i % (D / 4) * 4;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float* part = reinterpret_cast<const float*>(workspace + slots_at + list[k] * kSlot);
-      const float2 ml = *reinterpret_cast<const float2*>(part + ROWS * D + 2 * row);
-      const float4 x = *reinterpret_cast<const float4*>(part + row * D + d);
-      kv_join(m, l, o, ml, x);
-    }
-    kv_finish<D>(a, job.q0, job.row0 + row, group, job.head, d, m, l, o);
   }
 }
 

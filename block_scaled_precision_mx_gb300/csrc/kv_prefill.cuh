@@ -949,4 +949,56 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
   if (warp == 13) tmem_dealloc(tmem, 512);
 }
 
+// Joins the segments of the units that range boundaries cut.  CTA c looks at the boundary where range c
+// begins; the first boundary inside a unit takes the unit.  Segments are added in order: the range that
+// the unit begins in left its one in slot 1, the others in slot 0.
+template <int D>
+__global__ void __launch_bounds__(128) kv_join_kernel(const KvAttnArgs a, const uint8_t* workspace, size_t slots_at) {
+  pdl_prologue();
+  constexpr size_t kSlot = static_cast<size_t>(kKvManyRows) * (D + 2) * 4;
+  __shared__ int list[kKvMaxCtas];
+  __shared__ int listed;
+  const KvJob* jobs = reinterpret_cast<const KvJob*>(workspace + kKvJobsAt);
+  const int c = blockIdx.x + 1, ranges = gridDim.x + 1;
+  const KvJob job = jobs[c];
+  const long long before = jobs[c - 1].begin, total = jobs[ranges - 1].end;
+  if (job.begin >= total || job.unit == job.begin || before > job.unit) return;
+  const long long unit_end = job.unit + job.tiles + kKvUnitCost;
+  if (threadIdx.x < 32) {
+    int n = 0;
+    for (int k0 = c - 1; k0 < ranges; k0 += 32) {
+      const int k = k0 + threadIdx.x;
+      bool has = false, over = true;
+      if (k < ranges) {
+        const long long b = jobs[k].begin, e = jobs[k].end;
+        over = b >= unit_end;
+        const int from = kv_tiles_before(b - job.unit, job.tiles), to = kv_tiles_before(e - job.unit, job.tiles);
+        has = !over && to > from && to - from < job.tiles;  // (a range that has all of it has finished it)
+      }
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, has);
+      if (has) list[n + __popc(m & ((1u << threadIdx.x) - 1))] = 2 * k + (k == c - 1 ? 1 : 0);
+      n += __popc(m);
+      if (__any_sync(0xFFFFFFFFu, over)) break;
+    }
+    if (threadIdx.x == 0) listed = n;
+  }
+  __syncthreads();
+  const int n = listed;
+  if (n == 0) return;
+  const int group = a.heads / a.kv_heads;
+  for (int i = blockIdx.y * 128 + threadIdx.x; i < job.rows * (D / 4); i += 128 * gridDim.y) {
+    const int row = i / (D / 4), d = i % (D / 4) * 4;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float* part = reinterpret_cast<const float*>(workspace + slots_at + list[k] * kSlot);
+      const float2 ml = *reinterpret_cast<const float2*>(part + kKvManyRows * D + 2 * row);
+      const float4 x = *reinterpret_cast<const float4*>(part + row * D + d);
+      kv_join(m, l, o, ml, x);
+    }
+    kv_finish<D>(a, job.q0, job.row0 + row, group, job.head, d, m, l, o);
+  }
+}
+
 }  // namespace mxgb

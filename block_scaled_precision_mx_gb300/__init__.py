@@ -498,14 +498,15 @@ def _at(t, dtype, name):
 
 def _rows_of_heads(x, name):
     """(shape, address, type, token stride, head stride) of x[tokens][heads][head_dim], strided but for
-    the last axis."""
+    the last axis.  (An axis of one has no stride to speak of: torch may give it any.)"""
     half = _HALF.get(x.dtype)
     if half is None or x.dim() != 3:
         raise ValueError(f"{name} must be a 3-D bf16 or fp16 tensor")
     st, sh, sd = x.stride()
     if not x.is_cuda or sd != 1:
         raise ValueError(f"{name} must be a CUDA tensor whose last axis is contiguous")
-    return x.shape, x.data_ptr(), half, st, sh
+    shape = x.shape
+    return shape, x.data_ptr(), half, st if shape[0] > 1 else 0, sh if shape[1] > 1 else 0
 
 
 def _cache_shape(k_codes, v_codes, k_scale, v_scale):

@@ -158,3 +158,26 @@ def test_append_to_a_block_of_an_unusable_scale_is_left_out_and_reported(scale):
     both = ref.append(x.double().cpu().numpy(), slots, codes, np.ones((2, h), np.float32), 0)
     assert np.array_equal(vc.cpu().numpy(), both[0]) and np.array_equal(vs.cpu().numpy(), both[1])
     assert np.array_equal(kc[0, 0], both[0][0, 0]) and np.array_equal(kc[1], both[0][1]) and ks[0, 0] == both[1][0, 0]
+
+
+# ------------------------------------------------------------------ strides
+@pytest.mark.parametrize("tokens,heads", [(1, 1), (3, 1), (1, 4)])
+def test_axes_of_one_with_odd_strides(tokens, heads):
+    """A tensor's axis of one may have any stride, one that is no multiple of 8 among them."""
+    rng = np.random.RandomState(tokens + heads)
+    c = attention_case(rng, [70], [tokens], heads, 1, 64, 16, "bf16", 0)
+    c["q"] = c["q"].clone()
+    check_attention(c, 0)
+    st = 3 if tokens == 1 else heads * 64, 5 if heads == 1 else 64
+    want = run_attention(c, 0)
+    got = run_attention(dict(c, q=c["q"].as_strided(c["q"].shape, (*st, 1))), 0)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    k = c["q"][:, :1].clone()
+    slots = gpu(np.arange(tokens, dtype=np.int64))
+    caches = []
+    for x in (k, k.as_strided(k.shape, (3 if tokens == 1 else 64, 5, 1))):
+        cache = [torch.zeros(1, 1, 16, 64, dtype=torch.uint8, device="cuda") for _ in range(2)] + [torch.ones(1, 1, device="cuda") for _ in range(2)]
+        mx.kv_cache_append(x, x, slots, *cache)
+        caches.append(cache)
+    assert mx.mx_check() == mx.MX_OK
+    assert all(torch.equal(a, b) for a, b in zip(*caches))

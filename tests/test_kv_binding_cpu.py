@@ -154,3 +154,19 @@ def test_buffers_are_few_whatever_the_requests(calls):
             calls(n, queries, d=d)
     kept = sum(w.numel() for w in (*mx._workspaces.values(), *mx._workspaces_old))
     assert len(mx._workspaces_old) <= 5 and kept <= 100e6          # (44 MB the largest, smaller ones together as much)
+
+
+def test_strides_of_axes_of_one_do_not_matter():
+    """Strides go to the library, which takes multiples of 8; torch gives an axis of one any stride."""
+    class Cuda:
+        is_cuda, dtype = True, torch.bfloat16
+
+        def __init__(self, x):
+            self.shape, self.dim, self.stride, self.data_ptr = x.shape, x.dim, x.stride, x.data_ptr
+    x = torch.zeros(5, 64, 1, dtype=torch.bfloat16).transpose(1, 2)            # one head, stride 1
+    assert x.shape == (5, 1, 64) and x.stride() == (64, 1, 1)
+    assert mx._rows_of_heads(Cuda(x), "k")[3:] == (64, 0)
+    x = torch.zeros(3, 3, 100, dtype=torch.bfloat16)[1:2, :1, :64]             # one token of one head
+    assert mx._rows_of_heads(Cuda(x), "k")[3:] == (0, 0)
+    x = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    assert mx._rows_of_heads(Cuda(x), "k")[3:] == (128, 64)

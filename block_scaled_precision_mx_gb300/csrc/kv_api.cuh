@@ -20,7 +20,7 @@ bool kv_cache_shape_ok(int64_t num_blocks, int64_t kv_heads, int block_tokens, i
 }
 
 // 8-row tiles of the kernel for few rows: 1 or 2; 0 where a kv head has more than 16 rows and the kernel for
-// many takes them.  (24 requests, 2048-token windows: 8 rows 28 us, 16 rows 35 us here; 24 to 64 rows 54 to 56 us
+// many takes them.  (24 requests, 2048-token windows: 8 rows 30 us, 16 rows 38 us here; 24 to 64 rows 54 to 56 us
 // there.  Four row tiles here would hold 32 rows of O in 128 registers a thread: 63 us at best.)
 int kv_row_tiles(int64_t max_q_len, int64_t group) {
   if (max_q_len > 16 || group > 16) return max_q_len ? 0 : 1;

@@ -76,9 +76,9 @@ __device__ __forceinline__ bool kv_wait(uint64_t* bar, uint32_t parity, volatile
 //  * Tiles that some row does not see whole are masked; codes there that no row sees are cleared, and
 //    NaN codes of V (0 * NaN) are taken out and put into the rows that see them at the end.
 //
-// Measured (D = 128, E4M3): 8 requests of up to 65536 tokens, 8 kv heads, 8 rows each: 129 us, 6.07 TB/s, 0.90
+// Measured (D = 128, E4M3): 8 requests of up to 65536 tokens, 8 kv heads, 8 rows each: 130 us, 6.0 TB/s, 0.90
 // of the measured copy rate.  64 of up to 4096, 4 rows: 62 us, 5.4 TB/s; about 10 us of that is what a call of any
-// size takes (1 request, 777 tokens: 11 us), the join among it.  What bounds it: memory latency where a CTA's ring
+// size takes (1 request, 777 tokens: 13 us), the join among it.  What bounds it: memory latency where a CTA's ring
 // runs dry at a segment's first tiles.  Three CTAs of three 16 KB stages a SM: two CTAs 63 us, four of two
 // stages 72 us (64 x 4096); at D = 64 four CTAs of five 8 KB stages: 36 us, two 39, five of three stages 45.
 constexpr int kKvTile = 64;

@@ -20,10 +20,10 @@
 // folded into the exponent, and the reference m is renewed only when a score passes it by 8; the row's O in
 // tensor memory is then rescaled by its own thread, between two products.
 //
-// Measured (D = 128, 32 query and 8 kv heads, E4M3): 4096 queries over 32768 tokens 1.60 ms, 1.29 PFLOP/s, 0.68 of the
-// measured bf16 rate; 6 prompts of 711 to 1500 tokens 193 us (872 units of 11 tiles; 78 us of products).  What bounds it: a tile's products are 2048 cycles, but a half's chain of softmax (~2300 cycles:
-// maximum 560, weights 1260, waits), its P V and its next S is ~3700, because S and P share tensor memory (O and
-// S of two halves fill it) and S(i + 1) has to follow P(i) V; and shared memory carries 320 KB a tile (2560
+// Measured (D = 128, 32 query and 8 kv heads, E4M3): 4096 queries over 32768 tokens 1.59 ms, 1.29 PFLOP/s, 0.66 of the
+// measured bf16 rate; 6 prompts of 711 to 1500 tokens 193 us (872 units of 11 tiles; 75 us of products).
+// What bounds it: a tile's products are 2048 cycles, but a half's chain of softmax (~2300 cycles: maximum 560,
+// weights 1260, waits), its P V and its next S is ~3700, because S and P share tensor memory (O and S of two halves fill it) and S(i + 1) has to follow P(i) V; and shared memory carries 320 KB a tile (2560
 // cycles: Q 64, K and V 64 each, the codes in, out and back as FP16 128).  Tried and slower: one pass over the
 // scores with the weights held in registers until their maximum is known (2.2 ms), P V started at half of the
 // weights (1.68 ms), 16 scores a step (1.82 ms), one row half's tiles split in columns (1.69 ms).

@@ -409,11 +409,11 @@ size_t mx_scale_bytes(int64_t rows, int64_t cols, int block, int block_rows, mx_
  * number out of range: attention gives NaN in the rows that see the block, and only there.
  * head_dim is 64 or 128, kv_heads at most 1024, and num_blocks * kv_heads * P at most 2^31 - 1.
  * A request's tokens are in the blocks that its row of block_tables[requests][max_blocks] (int32)
- * names, P by P; entries past its length are not read, nor by kv_attention those that lie in front of every
- * row's window (a caller may have given such blocks back).  requests is at most 16384, max_blocks * P and
- * the tokens of a call at most 2^30.  Lengths, block
- * numbers and slots are on the device and the host cannot see them: where they break their
- * contract nothing is read or written out of range, and mx_check returns MX_ERR_INVALID_ARG.
+ * names, P by P; entries past its length are not read, nor by kv_attention those that lie in front of
+ * every row's window (a caller may have given such blocks back).  requests is at most 16384,
+ * max_blocks * P and the tokens of a call at most 2^30.  Lengths, block numbers and slots are on the
+ * device and the host cannot see them: where they break their contract nothing is read or written out
+ * of range, and mx_check returns MX_ERR_INVALID_ARG.
  */
 
 /*
@@ -475,15 +475,19 @@ size_t kv_attention_workspace_bytes(int64_t num_tokens, int64_t requests, int64_
  * cached tokens (so append first).  heads is a multiple of kv_heads; query heads g * heads / kv_heads
  * and up share kv head g.  Row i of n stands at position p = lengths[r] - n + i and sees the tokens
  * j < lengths[r] with j <= p if causal and j > p - window if window > 0.  No request has more than
- * max_q_len rows.
+ * max_q_len rows (itself at most num_tokens).  softmax_scale is positive and at most 1e30.
  *   out[num_tokens][heads][head_dim] (q's type, 32-byte aligned) = softmax(softmax_scale * q k_j) v_j,
  *   lse[num_tokens][heads] (float) = log sum_j exp(softmax_scale * q k_j).
- * Rows that see no token, and rows from q_start[requests] on, give 0 and -inf.  NaN in tokens that a
- * row does not see does not reach it.  workspace: kv_attention_workspace_bytes bytes, 32-byte
- * aligned; its first 4096 bytes are zero before its first use and are left zero, so that the next call can use it,
- * for whatever sizes it is large enough (after MX_ERR_TIMEOUT they are to be cleared again); calls that may
- * overlap need one each.  Calls from several host threads on one stream do not overlap, and may share one.
- * Sums and softmax statistics are FP32; the weights are rounded to FP16 for the second product.
+ * Rows that see no token, and rows from q_start[requests] on, give 0 and -inf.  Rows of a request whose
+ * length or rows break their contract, and rows in front of q_start[0], are not written.  NaN in tokens
+ * that a row does not see does not reach it, nor does the scale of a block that it does not see.
+ * Infinities in the cache (E5M2; append writes none) may come out as NaN.  workspace:
+ * kv_attention_workspace_bytes bytes, 32-byte aligned; its first 4096 bytes are zero before its first
+ * use and are left zero, so that the next call can use it, for whatever sizes it is large enough (after
+ * MX_ERR_TIMEOUT they are to be cleared again); calls that may overlap need one each.  Calls from
+ * several host threads on one stream do not overlap, and may share one.
+ * Sums and softmax statistics are FP32.  For the second product each token's weight, times its block's V scale, is
+ * rounded to FP16 beside the row's largest: below 2^-14 of it bits are lost, from 2^-25 on it is 0.
  */
 mx_status kv_attention(const void* q, mx_half type, int64_t num_tokens, int64_t heads, int64_t q_stride_token,
                        int64_t q_stride_head, const void* k_codes, const void* v_codes, const float* k_scale,
@@ -495,9 +499,9 @@ mx_status kv_attention(const void* q, mx_half type, int64_t num_tokens, int64_t 
 /*
  * mx_check -- synchronizes `stream`, then reads and clears the library's device error word.
  * Returns MX_ERR_TIMEOUT if a kernel's bounded wait ran out since the last check,
- * MX_ERR_INVALID_ARG if the only events were device inputs that broke their contract (a grouped
- * GEMM's offsets, a key/value cache's lengths, blocks or slots), MX_ERR_CUDA on a pending CUDA error, MX_OK otherwise.  This is the only call that
- * synchronizes.
+ * MX_ERR_INVALID_ARG if the only events were device inputs that broke their contract (a grouped GEMM's
+ * offsets, a key/value cache's lengths, query starts, blocks, slots or scales), MX_ERR_CUDA on a pending CUDA error, MX_OK
+ * otherwise.  This is the only call that synchronizes.
  */
 mx_status mx_check(void* stream);
 

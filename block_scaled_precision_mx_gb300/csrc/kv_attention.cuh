@@ -157,6 +157,9 @@ __device__ __forceinline__ uint32_t kv_nan_bytes(uint32_t w) {
 // Scales are 0 or in [2^-48, 2^48]: within it 2^(z + log2 sV - m) and its quotient by sV stay numbers of FP32 that
 // count (two blocks' are at most 2^96 apart).  The codes of a block of scale 0 are taken as zeros; those of one of any
 // other scale as NaN, which reaches the rows that see it as a NaN in the cache does.
+// What a V scale of 0 counts as, beside codes that are zeros: below other blocks' scales, which then keep the bits of
+// their weights, but no further from 1 than lse bears (log2 sV is in its reference: 2^-48 cost it a bit).
+constexpr float kKvZeroAs = 1.f / (1 << 24);
 constexpr int kKvTakeZero = 1, kKvTakeNan = 0x80;  // 1 + the byte that each code is taken as; 0: as it is
 
 // What a scale says of its block's codes; the scale itself becomes one in range.
@@ -168,7 +171,7 @@ __device__ __forceinline__ int kv_check_scale(float& s, float for_zero) {
 }
 // Both scales of a block; of K, and of V << 8.  tell: some row sees the block.
 __device__ __forceinline__ int kv_check_scales(float& sk, float& sv, bool tell) {
-  const int take = kv_check_scale(sk, 1.f) | kv_check_scale(sv, kKvLeastScale) << 8;
+  const int take = kv_check_scale(sk, 1.f) | kv_check_scale(sv, kKvZeroAs) << 8;
   if (tell && take & (kKvTakeNan | kKvTakeNan << 8)) atomicOr(&g_mx_error_word, kSiteBadCache);
   return take;
 }

@@ -87,3 +87,16 @@ def test_products_of_scales_below_the_smallest_number(queries):
     c["q"] = (c["q"].double() * 2.0 ** -110).to(torch.bfloat16)
     check_attention(c, 0)
     check_attention(c, 0, scale=1e-30, window=20)
+
+
+@pytest.mark.parametrize("queries", [1, 4, 17])
+@pytest.mark.parametrize("elem", [0, 1])
+def test_lse_beside_value_scales_of_zero(elem, queries):
+    """Short requests, whose lse is small, over value blocks of scale 0, alone and beside others."""
+    for seed in range(6):
+        rng = np.random.RandomState(100 * queries + seed)
+        lens = [*range(1, 40), 70, 100]
+        c = attention_case(rng, lens, [min(queries, n) for n in lens], 6, 2, 64, 32, "f16", elem)
+        c["vs"][c["tables"][:, 0]] = 0
+        check_attention(c, elem)
+        check_attention(c, elem, window=1)

@@ -11,7 +11,8 @@ Entry points (same names as the C ABI):
   mx_quantize, mx_quantize_dual, mx_gemm, nvfp4_quantize, nvfp4_gemm, fp8_blockwise_gemm,
   mx_gemm_grouped, mx_gemm_mxout, mx_scales_from_fp32_blocks, nvfp4_quantize_ex, nvfp4_quantize_2d,
   nvfp4_quantize_grouped, nvfp4_gemm_grouped, nvfp4_gemm_grouped_ex, fp8_blockwise_gemm_grouped, mx_scale_bytes,
-  nvfp4_workspace_bytes, mx_check, kv_block_tables, kv_cache_append, kv_attention.
+  nvfp4_workspace_bytes, mx_check, kv_block_tables, kv_cache_append, kv_attention, qk_norm_rope,
+  qk_norm_rope_backward, kv_draft_trees, kv_verify_drafts, kv_cache_compact.
 """
 from __future__ import annotations
 
@@ -39,7 +40,8 @@ EXPORTS = (
     "nvfp4_quantize_2d", "mx_gemm_grouped", "mx_gemm_mxout", "mx_unswizzle_scales", "mx_swizzle_scales",
     "mx_selftest_wait_timeout", "mx_gemm_mxout_ex", "nvfp4_gemm_grouped", "nvfp4_quantize_grouped",
     "nvfp4_gemm_grouped_ex", "fp8_blockwise_gemm_grouped", "kv_block_tables", "kv_cache_append",
-    "kv_attention_workspace_bytes", "kv_attention",
+    "kv_attention_workspace_bytes", "kv_attention", "qk_norm_rope", "qk_norm_rope_workspace_bytes",
+    "qk_norm_rope_backward", "kv_draft_trees", "kv_verify_drafts", "kv_cache_compact",
 )
 
 
@@ -104,6 +106,14 @@ def load():
             "kv_attention_workspace_bytes": (ctypes.c_size_t, [i64, i64, i64, i64, i64, i32]),
             "kv_attention": (i32, [vp, i32, i64, i64, i64, i64, vp, vp, vp, vp, i32, i64, i64, i32, i32, vp, i64, vp, vp,
                                    i64, i64, ctypes.c_float, i32, i64, vp, vp, vp, vp]),
+            "qk_norm_rope": (i32, [vp, vp, i32, i64, i64, i64, i32, i64, i64, i64, i64, vp, vp, i32, vp, i64, i32, vp,
+                                   ctypes.c_float, i32, vp, vp, i64, i64, i64, i64, vp]),
+            "qk_norm_rope_workspace_bytes": (ctypes.c_size_t, [i32]),
+            "qk_norm_rope_backward": (i32, [vp, vp, vp, vp, i32, i64, i64, i64, i32, *[i64] * 8, vp, vp, i32, vp, i64, i32, vp,
+                                            ctypes.c_float, i32, vp, vp, i64, i64, i64, i64, vp, vp, vp, vp]),
+            "kv_draft_trees": (i32, [vp, i64, vp, vp, i64, i64, i64, vp, i64, vp, vp]),
+            "kv_verify_drafts": (i32, [vp, i64, vp, i64, i64, vp, vp, i64, vp, i64, i64, vp, vp, vp, vp, vp, vp]),
+            "kv_cache_compact": (i32, [vp, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, vp, i32, i64, i64, i32, i32, vp, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -653,6 +663,210 @@ def kv_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor, 
     if st:
         _check(st, "kv_attention")
     return out, lse
+
+
+# ------------------------------------------------------------------ norm and rotation; drafted tokens
+def _qk_out(out, like, name):
+    """(tensor, address, token stride, head stride) of an output shaped like a [tokens][heads][head_dim] tensor."""
+    if out is None:
+        out = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    shape, at, _, st, sh = _rows_of_heads(out, name)
+    if shape != like.shape or out.dtype is not like.dtype:
+        raise ValueError(f"{name} must be shaped and typed like its input")
+    return out, at, st, sh
+
+
+def _qk_rest(q, q_weight, k_weight, cos_sin, positions, kv_heads):
+    """(q_weight's address, k_weight's, whether they are FP32, table's address, its positions, rot_dim, positions' address)"""
+    tokens, _, head_dim = q.shape
+    wide = q_weight.dtype is _float32
+    kind = _float32 if wide else q.dtype
+    if q_weight.numel() != head_dim or (kv_heads and (k_weight is None or k_weight.numel() != head_dim)):
+        raise ValueError("weights must have head_dim values")
+    if positions is None:
+        if cos_sin is not None:
+            raise ValueError("a rotation needs positions")
+    elif positions.numel() != tokens:
+        raise ValueError("positions must have a place for each token")
+    if cos_sin is not None and cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be float32 [positions][rot_dim]")
+    return (_at(q_weight, kind, "q_weight"), _at(k_weight, kind, "k_weight") if kv_heads else None, wide,
+            None if cos_sin is None else _at(cos_sin, _float32, "cos_sin"), 0 if cos_sin is None else cos_sin.shape[0],
+            0 if cos_sin is None else cos_sin.shape[1], None if positions is None else _at(positions, _int32, "positions"))
+
+
+def qk_norm_rope(q: torch.Tensor, k, q_weight: torch.Tensor, k_weight, cos_sin, positions, eps: float = 1e-6,
+                 interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """RMS norm of each head of q [tokens][heads][head_dim] and k [tokens][kv_heads][head_dim] (or None) and rotation
+    to positions (int32; -1 leaves a token out) by cos_sin float32 [positions][rot_dim] (or None)
+    (include/mx.h, qk_norm_rope).  Slices will do; outputs may be q and k themselves.  Returns (q_out, k_out)."""
+    shape, q_at, half, q_st, q_sh = _rows_of_heads(q, "q")
+    k_at, k_st, k_sh, kv_heads = None, 0, 0, 0
+    if k is not None:
+        k_shape, k_at, k_half, k_st, k_sh = _rows_of_heads(k, "k")
+        if k_half != half or k_shape[0] != shape[0] or k_shape[2] != shape[2]:
+            raise ValueError("q and k must be alike but for their heads")
+        kv_heads = k_shape[1]
+    qw, kw, wide, table, places, rot, pos = _qk_rest(q, q_weight, k_weight, cos_sin, positions, kv_heads)
+    q_out, qo_at, qo_st, qo_sh = _qk_out(q_out, q, "q_out")
+    ko_at, ko_st, ko_sh = None, 0, 0
+    if k is not None:
+        k_out, ko_at, ko_st, ko_sh = _qk_out(k_out, k, "k_out")
+    st = load().qk_norm_rope(q_at, k_at, half, shape[0], shape[1], kv_heads, shape[2], q_st, q_sh, k_st, k_sh, qw, kw, wide,
+                             table, places, rot, pos, eps, interleaved, qo_at, ko_at, qo_st, qo_sh, ko_st, ko_sh,
+                             _stream(stream))
+    if st:
+        _check(st, "qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out, q: torch.Tensor, k, q_weight: torch.Tensor, k_weight, cos_sin,
+                          positions, eps: float = 1e-6, interleaved: bool = False, dq=None, dk=None, dq_weight=None,
+                          dk_weight=None, workspace=None, stream=None):
+    """Gradients of qk_norm_rope(q, k, ...) from those of its results (include/mx.h, qk_norm_rope_backward).
+    Returns (dq, dk, dq_weight float32 [head_dim], dk_weight)."""
+    shape, q_at, half, q_st, q_sh = _rows_of_heads(q, "q")
+    g_shape, g_at, g_half, g_st, g_sh = _rows_of_heads(dq_out, "dq_out")
+    if g_shape != shape or g_half != half or (k is None) != (dk_out is None):
+        raise ValueError("gradients must be shaped and typed like q and k")
+    k_at, k_st, k_sh, kv_heads, gk_at, gk_st, gk_sh = None, 0, 0, 0, None, 0, 0
+    if k is not None:
+        k_shape, k_at, k_half, k_st, k_sh = _rows_of_heads(k, "k")
+        gk_shape, gk_at, gk_half, gk_st, gk_sh = _rows_of_heads(dk_out, "dk_out")
+        if k_half != half or k_shape[0] != shape[0] or k_shape[2] != shape[2]:
+            raise ValueError("q and k must be alike but for their heads")
+        if gk_shape != k_shape or gk_half != half:
+            raise ValueError("gradients must be shaped and typed like q and k")
+        kv_heads = k_shape[1]
+    qw, kw, wide, table, places, rot, pos = _qk_rest(q, q_weight, k_weight, cos_sin, positions, kv_heads)
+    dq, dq_at, dq_st, dq_sh = _qk_out(dq, q, "dq")
+    dk_at, dk_st, dk_sh = None, 0, 0
+    if k is not None:
+        dk, dk_at, dk_st, dk_sh = _qk_out(dk, k, "dk")
+    dev, head_dim = q.device, shape[2]
+    if dq_weight is None:
+        dq_weight = torch.empty(head_dim, dtype=_float32, device=dev)
+    if dk_weight is None:
+        dk_weight = torch.empty(head_dim, dtype=_float32, device=dev)
+    if dq_weight.numel() != head_dim or dk_weight.numel() != head_dim:
+        raise ValueError("the weights' gradients must have head_dim values")
+    at_stream = _stream(stream)
+    need = int(load().qk_norm_rope_workspace_bytes(head_dim))
+    if workspace is None:
+        workspace = _call_workspace(need, dev, at_stream)
+    elif workspace.numel() < need:
+        raise ValueError(f"workspace must have {need} bytes")
+    st = load().qk_norm_rope_backward(g_at, gk_at, q_at, k_at, half, shape[0], shape[1], kv_heads, head_dim, g_st, g_sh, gk_st,
+                                      gk_sh, q_st, q_sh, k_st, k_sh, qw, kw, wide, table, places, rot, pos, eps, interleaved,
+                                      dq_at, dk_at, dq_st, dq_sh, dk_st, dk_sh, _at(dq_weight, _float32, "dq_weight"),
+                                      _at(dk_weight, _float32, "dk_weight"), _at(workspace, _uint8, "workspace"), at_stream)
+    if st:
+        _check(st, "qk_norm_rope_backward")
+    return dq, dk, dq_weight, dk_weight
+
+
+def _call_workspace(need, dev, stream):
+    """A workspace that need not be clear, for one call: torch's allocator has it back when the call's work on the
+    stream is in order in front of the next owner's, so it is made as one of that stream's."""
+    if stream == _stream(None):
+        return torch.empty(need, dtype=_uint8, device=dev)
+    if stream == _PER_THREAD:
+        raise ValueError("a call on the per-thread default stream needs a workspace of the caller's")
+    with torch.cuda.stream(torch.cuda.ExternalStream(0 if stream == _LEGACY else stream, device=dev)):
+        return torch.empty(need, dtype=_uint8, device=dev)
+
+
+def kv_draft_trees(parents: torch.Tensor, lengths: torch.Tensor, q_start: torch.Tensor, max_q_len: int, window: int = 0,
+                   tree_mask=None, positions=None, stream=None):
+    """Visibility and positions of trees of drafted tokens from their parents (int32 [tokens], numbers within a request;
+    -1: none) (include/mx.h, kv_draft_trees).  Returns (tree_mask int64 [tokens][ceil(max_q_len / 64)], positions int32
+    [tokens])."""
+    tokens, requests, dev = parents.numel(), lengths.numel(), parents.device
+    if q_start.numel() != requests + 1:
+        raise ValueError("q_start must be [requests + 1]")
+    if tree_mask is None:
+        tree_mask = torch.empty((tokens, max(1, (max_q_len + 63) // 64)), dtype=_int64, device=dev)
+    if positions is None:
+        positions = torch.empty(tokens, dtype=_int32, device=dev)
+    if tree_mask.dim() != 2 or tree_mask.shape[0] != tokens or positions.numel() != tokens:
+        raise ValueError("tree_mask must be [tokens][words] and positions [tokens]")
+    st = load().kv_draft_trees(_at(parents, _int32, "parents"), tokens, _at(lengths, _int32, "lengths"),
+                               _at(q_start, _int32, "q_start"), requests, max_q_len, window,
+                               _at(tree_mask, _int64, "tree_mask"), tree_mask.shape[1], _at(positions, _int32, "positions"),
+                               _stream(stream))
+    if st:
+        _check(st, "kv_draft_trees")
+    return tree_mask, positions
+
+
+def _probs(x, tokens, name):
+    """(address, row stride, vocabulary) of probabilities [tokens][vocab], rows apart but contiguous."""
+    if x.dtype is not _float32 or x.dim() != 2 or not x.is_cuda or x.shape[0] != tokens:
+        raise ValueError(f"{name} must be a float32 CUDA tensor [tokens][vocab]")
+    st, sv = x.stride()
+    vocab = x.shape[1]
+    if sv != 1 and vocab > 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return x.data_ptr(), st if tokens > 1 else vocab, vocab
+
+
+def kv_verify_drafts(target_probs: torch.Tensor, drafts: torch.Tensor, parents: torch.Tensor, q_start: torch.Tensor,
+                     accept_random: torch.Tensor, sample_random: torch.Tensor, draft_probs=None, max_q_len=None, path=None,
+                     tokens=None, counts=None, stream=None):
+    """Which drafted tokens the target's probabilities [tokens][vocab] keep, by given random numbers, and the token
+    behind them (include/mx.h, kv_verify_drafts).  drafts, parents int32 [tokens]; q_start int32 [requests + 1];
+    accept_random float32 [tokens], sample_random float32 [requests]; draft_probs: what the drafts were drawn from, or
+    None where they are certain.  Returns (path int32 [tokens], tokens int32 [tokens], counts int32 [requests])."""
+    n, requests, dev = drafts.numel(), sample_random.numel(), drafts.device
+    t_at, t_st, vocab = _probs(target_probs, n, "target_probs")
+    d_at, d_st = None, 0
+    if draft_probs is not None:
+        d_at, d_st, d_vocab = _probs(draft_probs, n, "draft_probs")
+        if d_vocab != vocab:
+            raise ValueError("draft_probs must be shaped like target_probs")
+    if parents.numel() != n or accept_random.numel() != n or q_start.numel() != requests + 1:
+        raise ValueError("parents and accept_random are [tokens], q_start is [requests + 1]")
+    if path is None:
+        path = torch.empty(n, dtype=_int32, device=dev)
+    if tokens is None:
+        tokens = torch.empty(n, dtype=_int32, device=dev)
+    if counts is None:
+        counts = torch.empty(requests, dtype=_int32, device=dev)
+    if path.numel() != n or tokens.numel() != n or counts.numel() != requests:
+        raise ValueError("path and tokens are [tokens], counts is [requests]")
+    st = load().kv_verify_drafts(t_at, t_st, d_at, d_st, vocab, _at(drafts, _int32, "drafts"), _at(parents, _int32, "parents"),
+                                 n, _at(q_start, _int32, "q_start"), requests, min(n, 1024) if max_q_len is None else max_q_len,
+                                 _at(accept_random, _float32, "accept_random"), _at(sample_random, _float32, "sample_random"),
+                                 _at(path, _int32, "path"), _at(tokens, _int32, "tokens"), _at(counts, _int32, "counts"),
+                                 _stream(stream))
+    if st:
+        _check(st, "kv_verify_drafts")
+    return path, tokens, counts
+
+
+def kv_cache_compact(path: torch.Tensor, counts: torch.Tensor, lengths: torch.Tensor, q_start: torch.Tensor,
+                     block_tables: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.Tensor,
+                     v_scale: torch.Tensor, elem: int = E4M3, kept_lengths=None, stream=None):
+    """Moves the accepted nodes' keys and values together in the cache, in place (include/mx.h, kv_cache_compact).
+    path and counts as kv_verify_drafts gives them.  Returns kept_lengths int32 [requests]."""
+    blocks, kv_heads, block_tokens, head_dim = _cache_shape(k_codes, v_codes, k_scale, v_scale)
+    requests = lengths.numel()
+    table_rows, max_blocks = block_tables.shape if block_tables.dim() == 2 else (-1, 0)
+    if table_rows != requests or counts.numel() != requests or q_start.numel() != requests + 1:
+        raise ValueError("block_tables is [requests][max_blocks], lengths and counts are [requests], q_start [requests + 1]")
+    if kept_lengths is None:
+        kept_lengths = torch.empty(requests, dtype=_int32, device=lengths.device)
+    elif kept_lengths.numel() != requests:
+        raise ValueError("kept_lengths must be [requests]")
+    st = load().kv_cache_compact(_at(path, _int32, "path"), _at(counts, _int32, "counts"), path.numel(),
+                                 _at(lengths, _int32, "lengths"), _at(q_start, _int32, "q_start"), requests,
+                                 _at(block_tables, _int32, "block_tables"), max_blocks, _at(k_codes, _uint8, "k_codes"),
+                                 _at(v_codes, _uint8, "v_codes"), _at(k_scale, _float32, "k_scale"),
+                                 _at(v_scale, _float32, "v_scale"), elem, blocks, kv_heads, block_tokens, head_dim,
+                                 _at(kept_lengths, _int32, "kept_lengths"), _stream(stream))
+    if st:
+        _check(st, "kv_cache_compact")
+    return kept_lengths
 
 
 def mx_check(stream=None) -> int:

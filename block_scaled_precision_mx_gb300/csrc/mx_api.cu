@@ -17,7 +17,9 @@
 #include "mx_quantize.cuh"
 #include "kv_attention.cuh"
 #include "kv_cache.cuh"
+#include "kv_drafts.cuh"
 #include "kv_prefill.cuh"
+#include "qk_norm.cuh"
 
 using namespace mxgb;
 
@@ -987,3 +989,4 @@ extern "C" mx_status nvfp4_quantize_noalloc(const void* x, int64_t rows, int64_t
 }
 
 #include "kv_api.cuh"
+#include "kv_drafts_api.cuh"

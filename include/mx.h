@@ -497,6 +497,120 @@ mx_status kv_attention(const void* q, mx_half type, int64_t num_tokens, int64_t 
                        int64_t window, void* out, float* lse, void* workspace, void* stream);
 
 /*
+ * Norm and rotation of queries and keys.
+ *
+ * qk_norm_rope -- RMS norm of each head with weights and rotation to its token's position, in one pass:
+ *   y = R(p) (x r * w),  r = (mean_i x_i^2 + eps)^(-1/2)  over the head's head_dim values, in FP32, rounded once.
+ * q, k: num_tokens tokens of heads (kv_heads) heads of head_dim values, bf16 or fp16, 16-byte aligned, values
+ * contiguous, token and head strides (in elements) multiples of 8: slices of a fused projection will do.  kv_heads may
+ * be 0 (k, k_weight and k_out NULL then).  head_dim is a multiple of 8, at most 256.  Outputs have strides of their own
+ * and may be the inputs themselves (same address and strides); they may not overlap them otherwise.
+ * q_weight, k_weight [head_dim]: x's type, or FP32 with weight_f32 = 1.
+ * cos_sin float [max_positions][rot_dim], 16-byte aligned: rot_dim / 2 cosines of a position's angles, then their sines.
+ * R turns the first rot_dim values of a head (a multiple of 16; 0: none, and cos_sin may be NULL), as pairs
+ * (i, rot_dim / 2 + i), or (2i, 2i + 1) with interleaved = 1: (a, b) -> (a cos - b sin, b cos + a sin).
+ * positions int32 [num_tokens] (may be NULL with rot_dim 0); -1 leaves a token out: its rows are not written.  Any
+ * other position out of range is left out and reported by mx_check.  0 <= eps <= 1.
+ */
+mx_status qk_norm_rope(const void* q, const void* k, mx_half type, int64_t num_tokens, int64_t heads, int64_t kv_heads,
+                       int head_dim, int64_t q_stride_token, int64_t q_stride_head, int64_t k_stride_token,
+                       int64_t k_stride_head, const void* q_weight, const void* k_weight, int weight_f32,
+                       const float* cos_sin, int64_t max_positions, int rot_dim, const int32_t* positions, float eps,
+                       int interleaved, void* q_out, void* k_out, int64_t q_out_stride_token, int64_t q_out_stride_head,
+                       int64_t k_out_stride_token, int64_t k_out_stride_head, void* stream);
+
+/* Bytes of workspace qk_norm_rope_backward needs (0 if head_dim is not supported). */
+size_t qk_norm_rope_workspace_bytes(int head_dim);
+
+/*
+ * qk_norm_rope_backward -- gradients of qk_norm_rope with respect to q, k and the weights.  With g = R(p)^T dy, xh = x r:
+ *   dx = r (w g - xh mean(w g xh)),   dw = sum over tokens and heads of g xh.
+ * dq_out, dk_out: the results' gradients; q, k: the forward pass's inputs (not its results); all as there, with their own
+ * strides.  dq, dk may be dq_out, dk_out themselves, or q, k.  A token that the forward pass left out gets zeros in dq
+ * and dk and adds nothing to the weights' gradients, dq_weight and dk_weight, float [head_dim], which are written, not
+ * added to, in an order of sums that depends on the sizes alone.  workspace: qk_norm_rope_workspace_bytes bytes, 16-byte
+ * aligned, contents need not be initialised; calls that may overlap need one each.
+ */
+mx_status qk_norm_rope_backward(const void* dq_out, const void* dk_out, const void* q, const void* k, mx_half type,
+                                int64_t num_tokens, int64_t heads, int64_t kv_heads, int head_dim,
+                                int64_t dq_out_stride_token, int64_t dq_out_stride_head, int64_t dk_out_stride_token,
+                                int64_t dk_out_stride_head, int64_t q_stride_token, int64_t q_stride_head,
+                                int64_t k_stride_token, int64_t k_stride_head, const void* q_weight, const void* k_weight,
+                                int weight_f32, const float* cos_sin, int64_t max_positions, int rot_dim,
+                                const int32_t* positions, float eps, int interleaved, void* dq, void* dk,
+                                int64_t dq_stride_token, int64_t dq_stride_head, int64_t dk_stride_token,
+                                int64_t dk_stride_head, float* dq_weight, float* dk_weight, void* workspace, void* stream);
+
+/*
+ * Trees of drafted tokens.
+ *
+ * A step may run a tree of tokens for each request: row q_start[r] + i is node i of request r's tree, of at most
+ * max_q_len <= 1024 nodes.  Node 0 is the root: the last token that the request has for certain.  A node's parent has
+ * a smaller number; parents[] are numbers within the request, -1 has none.  Nodes are cached in order, node i at place
+ * lengths[r] - n + i of the request (n its nodes; lengths[r] counts them), which kv_block_tables gives slots for; the
+ * position that a node stands for is lengths[r] - n + its depth.  q_start and lengths break their contract as for
+ * kv_attention: such a request is left out and reported by mx_check.
+ */
+
+/*
+ * kv_draft_trees -- what each node sees, and where it stands.
+ *   tree_mask[num_tokens][mask_words]: bit j % 64 of word j / 64 is set for the node itself and its ancestors j, with a
+ *   window > 0 only for those at a depth greater than its own less the window;
+ *   positions[num_tokens] = lengths[r] - n + depth (a node without parent has depth 0).
+ * 64 mask_words >= max_q_len, mask_words <= 16.  A request with a parent out of range gets masks of 0 and positions -1,
+ * and is reported.  Rows from q_start[requests] on get the same; rows of requests that are left out are not written.
+ */
+mx_status kv_draft_trees(const int32_t* parents, int64_t num_tokens, const int32_t* lengths, const int32_t* q_start,
+                         int64_t requests, int64_t max_q_len, int64_t window, int64_t* tree_mask, int64_t mask_words,
+                         int32_t* positions, void* stream);
+
+/*
+ * kv_verify_drafts -- which drafts stay, and the token behind them.
+ *
+ * target_probs[num_tokens] are rows of vocab probabilities (FP32, rows target_stride apart): row q_start[r] + i is the
+ * target model's distribution of the token that follows node i.  drafts[num_tokens] are the nodes' tokens (the root's is
+ * not read).  With draft_probs (rows draft_stride apart) the children of node i were drawn from row i of it, one after
+ * the other and independently; without (NULL) they are certain: some tokens, each different from its siblings.
+ * From the root on, the children of the last accepted node u are tried in order.  With P = target(u), Z = 1, W = 0,
+ * child x (accept_random its number) is accepted if accept_random q(x) Z < P(x), where q = draft(u), and then its
+ * children are tried; else W += Z, P = max(target(u) - W q, 0), Z = sum P.  Certain drafts have q(x) = 1: accepted if
+ * accept_random Z < P(x), else P(x) = 0 and Z -= P(x).  Behind the last accepted node the next token is the first whose
+ * running sum of P is above sample_random[r] sum P; where nothing is left of P, target(u) is drawn from instead.
+ * For each request, at its rows from q_start[r] on:
+ *   counts[r] = accepted nodes, the root among them (0 for a request without rows);
+ *   path[..] = the accepted nodes, the root first, then -1;
+ *   tokens[..] = the accepted drafts and then the next token, counts[r] of them, then -1.
+ * Rows from q_start[requests] on get -1.  Sums are of whole multiples of 2^-60 (where W > 1, of 2^-52): no order changes
+ * them.  Random numbers are in [0, 1).  A probability or random number that is negative, NaN or 2 and above counts as 0
+ * and is reported.  A request with a token or parent out of range gets counts 0 and -1, and is reported; one whose P and
+ * target are all 0 gets -1 as its next token, and is reported.  Requests with broken starts get counts 0.
+ * vocab is at most 2^20, probabilities need 4-byte alignment.
+ */
+mx_status kv_verify_drafts(const float* target_probs, int64_t target_stride, const float* draft_probs, int64_t draft_stride,
+                           int64_t vocab, const int32_t* drafts, const int32_t* parents, int64_t num_tokens,
+                           const int32_t* q_start, int64_t requests, int64_t max_q_len, const float* accept_random,
+                           const float* sample_random, int32_t* path, int32_t* tokens, int32_t* counts, void* stream);
+
+/*
+ * kv_cache_compact -- moves the accepted nodes' keys and values together, in place.
+ *
+ * Node path[q_start[r] + i] of request r, i < counts[r], moves to place lengths[r] - n + i; kept_lengths[r] becomes
+ * lengths[r] - n + counts[r], the request's length from then on (give it to kv_block_tables, which takes the blocks
+ * behind it back).  path rises and counts[r] <= n <= 1024 (as kv_verify_drafts gives them).  What moves into one block is
+ * a run: the block keeps its scale or, where a value would not fit (|value| > MAX scale), raises it to the smallest
+ * 2^k that does, and the codes in front of the run are rounded again, as kv_cache_append does; codes whose block has the
+ * same scale move as they are.  A block of scale 0 takes the run's own.  Codes from kept_lengths[r] on are left as
+ * they were.  A request whose path, counts, blocks, length or starts break their contract is left as it is, keeps
+ * lengths[r] and is reported.  Tokens of a block whose scale is out of range become NaN; a run into such a block is left
+ * out; both are reported.  No two requests have a block that is written to in common.  kept_lengths may not
+ * overlap lengths or counts.
+ */
+mx_status kv_cache_compact(const int32_t* path, const int32_t* counts, int64_t num_tokens, const int32_t* lengths,
+                           const int32_t* q_start, int64_t requests, const int32_t* block_tables, int64_t max_blocks,
+                           void* k_codes, void* v_codes, float* k_scale, float* v_scale, mx_elem elem, int64_t num_blocks,
+                           int64_t kv_heads, int block_tokens, int head_dim, int32_t* kept_lengths, void* stream);
+
+/*
  * mx_check -- synchronizes `stream`, then reads and clears the library's device error word.
  * Returns MX_ERR_TIMEOUT if a kernel's bounded wait ran out since the last check,
  * MX_ERR_INVALID_ARG if the only events were device inputs that broke their contract (a grouped GEMM's

@@ -320,6 +320,18 @@ def _own_verify(s, case):
 
 def _own_compact(s, case):
     import block_scaled_precision_mx_gb300 as mx
+    # The operator works in place, and the same path on a cache that it has been through once is another task: the blocks
+    # that a pass writes to are put back in front of the next one.
+    names = ("k_codes", "v_codes", "k_scale", "v_scale")
+    if "before" not in s:
+        p, length = case["block_tokens"], s["lengths"].long()
+        first = (length - s["q_start"].long().diff()) // p
+        page = first[:, None] + torch.arange(_blocks(s["most_path"], p) + 1, device="cuda")[None]
+        s["blocks"] = s["tables"].long().gather(1, torch.minimum(page, (length - 1)[:, None] // p)).reshape(-1)
+        s["before"] = [s[name][s["blocks"]] for name in names]
+    else:
+        for name, was in zip(names, s["before"]):
+            s[name].index_copy_(0, s["blocks"], was)
     kept = mx.kv_cache_compact(s["path"], s["counts"], s["lengths"], s["q_start"], s["tables"], s["k_codes"], s["v_codes"],
                                s["k_scale"], s["v_scale"], elem={"e4m3": mx.E4M3, "e5m2": mx.E5M2}[case["codes"]])
     kind = CODES[case["codes"]]

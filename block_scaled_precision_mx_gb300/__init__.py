@@ -12,7 +12,7 @@ Entry points (same names as the C ABI):
   mx_gemm_grouped, mx_gemm_mxout, mx_scales_from_fp32_blocks, nvfp4_quantize_ex, nvfp4_quantize_2d,
   nvfp4_quantize_grouped, nvfp4_gemm_grouped, nvfp4_gemm_grouped_ex, fp8_blockwise_gemm_grouped, mx_scale_bytes,
   nvfp4_workspace_bytes, mx_check, kv_block_tables, kv_cache_append, kv_attention, qk_norm_rope,
-  qk_norm_rope_backward, kv_draft_trees, kv_verify_drafts, kv_cache_compact.
+  qk_norm_rope_backward, kv_draft_trees, kv_tree_attention, kv_verify_drafts, kv_cache_compact.
 """
 from __future__ import annotations
 
@@ -41,7 +41,7 @@ EXPORTS = (
     "mx_selftest_wait_timeout", "mx_gemm_mxout_ex", "nvfp4_gemm_grouped", "nvfp4_quantize_grouped",
     "nvfp4_gemm_grouped_ex", "fp8_blockwise_gemm_grouped", "kv_block_tables", "kv_cache_append",
     "kv_attention_workspace_bytes", "kv_attention", "qk_norm_rope", "qk_norm_rope_workspace_bytes",
-    "qk_norm_rope_backward", "kv_draft_trees", "kv_verify_drafts", "kv_cache_compact",
+    "qk_norm_rope_backward", "kv_draft_trees", "kv_tree_attention", "kv_verify_drafts", "kv_cache_compact",
 )
 
 
@@ -112,6 +112,8 @@ def load():
             "qk_norm_rope_backward": (i32, [vp, vp, vp, vp, i32, i64, i64, i64, i32, *[i64] * 8, vp, vp, i32, vp, i64, i32, vp,
                                             ctypes.c_float, i32, vp, vp, i64, i64, i64, i64, vp, vp, vp, vp]),
             "kv_draft_trees": (i32, [vp, i64, vp, vp, i64, i64, i64, vp, i64, vp, vp]),
+            "kv_tree_attention": (i32, [vp, i32, i64, i64, i64, i64, vp, vp, vp, vp, i32, i64, i64, i32, i32, vp, i64, vp, vp,
+                                        i64, i64, vp, i64, vp, ctypes.c_float, i64, vp, vp, vp, vp]),
             "kv_verify_drafts": (i32, [vp, i64, vp, i64, i64, vp, vp, i64, vp, i64, i64, vp, vp, vp, vp, vp, vp]),
             "kv_cache_compact": (i32, [vp, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, vp, i32, i64, i64, i32, i32, vp, vp]),
         }
@@ -625,6 +627,30 @@ def kv_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor, 
     softmax_scale defaults to head_dim ** -0.5; a workspace is zero before its first use, and calls
     without one share one for each stream (on the per-thread default stream the caller gives one).
     Returns (out, like q but contiguous; lse float [tokens][heads])."""
+    return _kv_attention("kv_attention", (), (causal,), q, k_codes, v_codes, k_scale, v_scale, block_tables, lengths, q_start,
+                         max_q_len, elem, softmax_scale, window, out, lse, workspace, stream)
+
+
+def kv_tree_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.Tensor,
+                      v_scale: torch.Tensor, block_tables: torch.Tensor, lengths: torch.Tensor, q_start: torch.Tensor,
+                      max_q_len: int, tree_mask: torch.Tensor, positions=None, elem: int = E4M3, softmax_scale=None,
+                      window: int = 0, out=None, lse=None, workspace=None, stream=None):
+    """kv_attention of a tree's queries: of their request's newest tokens, the tree's nodes, they see those whose bits
+    tree_mask int64 [tokens][words] has (include/mx.h, kv_tree_attention).  positions int32 [tokens] with a window;
+    kv_draft_trees gives both.  All else as kv_attention."""
+    tokens = q.shape[0]
+    if tree_mask.dim() != 2 or tree_mask.shape[0] != tokens or (positions is not None and positions.numel() != tokens):
+        raise ValueError("tree_mask must be [tokens][words], positions [tokens]")
+    if window and positions is None:
+        raise ValueError("a window needs positions")
+    tree = (_at(tree_mask, _int64, "tree_mask"), tree_mask.shape[1],
+            None if positions is None else _at(positions, _int32, "positions"))
+    return _kv_attention("kv_tree_attention", tree, (), q, k_codes, v_codes, k_scale, v_scale, block_tables, lengths, q_start,
+                         max_q_len, elem, softmax_scale, window, out, lse, workspace, stream)
+
+
+def _kv_attention(entry, tree, causal, q, k_codes, v_codes, k_scale, v_scale, block_tables, lengths, q_start, max_q_len, elem,
+                  softmax_scale, window, out, lse, workspace, stream):
     shape, q_at, half, q_st, q_sh = _rows_of_heads(q, "q")
     blocks, kv_heads, block_tokens, head_dim = _cache_shape(k_codes, v_codes, k_scale, v_scale)
     tokens, heads, d = shape
@@ -653,15 +679,15 @@ def kv_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor, 
         need = kv_attention_workspace_bytes(tokens, requests, max_q_len, heads, kv_heads, head_dim)
         if workspace.numel() < need or _at(workspace, _uint8, "workspace") is None:
             raise ValueError(f"workspace must have {need} bytes")
-    st = load().kv_attention(q_at, half, tokens, heads, q_st, q_sh, _at(k_codes, _uint8, "k_codes"),
+    st = getattr(load(), entry)(q_at, half, tokens, heads, q_st, q_sh, _at(k_codes, _uint8, "k_codes"),
                              _at(v_codes, _uint8, "v_codes"), _at(k_scale, _float32, "k_scale"),
                              _at(v_scale, _float32, "v_scale"), elem, blocks, kv_heads, block_tokens, head_dim,
                              _at(block_tables, _int32, "block_tables"), max_blocks, _at(lengths, _int32, "lengths"),
-                             _at(q_start, _int32, "q_start"), requests, max_q_len,
-                             head_dim ** -0.5 if softmax_scale is None else softmax_scale, causal, window,
+                             _at(q_start, _int32, "q_start"), requests, max_q_len, *tree,
+                             head_dim ** -0.5 if softmax_scale is None else softmax_scale, *causal, window,
                              out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), at_stream)
     if st:
-        _check(st, "kv_attention")
+        _check(st, entry)
     return out, lse
 
 

@@ -38,10 +38,10 @@ bool kv_codes_tmap(CUtensorMap* map, const void* codes, int64_t num_blocks, int6
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
-template <int FMT, int D, int NT>
+template <int FMT, int D, int NT, bool TREE>
 mx_status kv_few_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_len, void* workspace, cudaStream_t st) {
   using Cfg = KvFewCfg<D, NT>;
-  auto kern = kv_attention_few_kernel<FMT, D, NT>;
+  auto kern = kv_attention_few_kernel<FMT, D, NT, TREE>;
   static std::atomic<int> ctas[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MX_ERR_CUDA;
@@ -66,10 +66,10 @@ mx_status kv_few_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_len
   return launch_status();
 }
 
-template <int FMT, int D, bool F16>
+template <int FMT, int D, bool F16, bool TREE>
 mx_status kv_many_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_len, void* workspace, cudaStream_t st) {
   using Cfg = KvManyCfg<D>;
-  auto kern = kv_attention_many_kernel<FMT, D, F16>;
+  auto kern = kv_attention_many_kernel<FMT, D, F16, TREE>;
   static std::atomic<bool> attr_set[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MX_ERR_CUDA;
@@ -89,7 +89,7 @@ mx_status kv_many_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_le
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   // up to a request a thread, of up to 32 units, the kernel plans for itself
   const int planned = a.requests > kKvManyThreads || max_q_len * (a.heads / a.kv_heads) > 32 * kKvManyRows;
-  if (planned && pdl_launch(kv_plan_kernel, 1, kKvPlanThreads, 0, st, a, most_q, n, ws) != cudaSuccess) return MX_ERR_CUDA;
+  if (planned && pdl_launch(kv_plan_kernel<TREE>, 1, kKvPlanThreads, 0, st, a, most_q, n, ws) != cudaSuccess) return MX_ERR_CUDA;
   if (pdl_launch(kern, n, kKvManyThreads, Cfg::SMEM, st, tk, tv, a, most_q, planned, ws) != cudaSuccess)
     return MX_ERR_CUDA;
   if (n > 1 && pdl_launch(kv_join_kernel<D>, dim3(n - 1, 16), 128, 0, st, a, static_cast<const uint8_t*>(ws),
@@ -98,14 +98,14 @@ mx_status kv_many_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_le
   return launch_status();
 }
 
-template <int FMT, int D>
+template <int FMT, int D, bool TREE>
 mx_status kv_attention_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_len, void* workspace, cudaStream_t st) {
   switch (kv_row_tiles(max_q_len, a.heads / a.kv_heads)) {
-    case 1: return kv_few_launch<FMT, D, 1>(a, block_tokens, max_q_len, workspace, st);
-    case 2: return kv_few_launch<FMT, D, 2>(a, block_tokens, max_q_len, workspace, st);
+    case 1: return kv_few_launch<FMT, D, 1, TREE>(a, block_tokens, max_q_len, workspace, st);
+    case 2: return kv_few_launch<FMT, D, 2, TREE>(a, block_tokens, max_q_len, workspace, st);
   }
-  return a.f16 ? kv_many_launch<FMT, D, true>(a, block_tokens, max_q_len, workspace, st)
-               : kv_many_launch<FMT, D, false>(a, block_tokens, max_q_len, workspace, st);
+  return a.f16 ? kv_many_launch<FMT, D, true, TREE>(a, block_tokens, max_q_len, workspace, st)
+               : kv_many_launch<FMT, D, false, TREE>(a, block_tokens, max_q_len, workspace, st);
 }
 
 // A group of W warps holds a block's values of one head, 4 words of 8 a thread, or 8 where 8 warps would
@@ -119,6 +119,80 @@ cudaError_t kv_append_launch(const KvAppendArgs& a, int head_dim, dim3 grid, cud
   return a.shift == 4 ? KV_APPEND(128, 2, 4) : a.shift == 5 ? KV_APPEND(128, 4, 4) : a.shift == 6 ? KV_APPEND(128, 8, 4)
                                                                                                   : KV_APPEND(128, 8, 8);
 #undef KV_APPEND
+}
+
+std::mutex kv_turn;
+
+// kv_attention and, with a mask, kv_tree_attention
+template <bool TREE>
+mx_status kv_attention_call(const void* q, mx_half type, int64_t num_tokens, int64_t heads, int64_t q_stride_token,
+                       int64_t q_stride_head, const void* k_codes, const void* v_codes, const float* k_scale,
+                       const float* v_scale, mx_elem elem, int64_t num_blocks, int64_t kv_heads, int block_tokens,
+                       int head_dim, const int32_t* block_tables, int64_t max_blocks, const int32_t* lengths,
+                       const int32_t* q_start, int64_t requests, int64_t max_q_len, const int64_t* tree_mask,
+                       int64_t mask_words, const int32_t* positions, float softmax_scale, int causal, int64_t window,
+                       void* out, float* lse, void* workspace, void* stream) {
+  if (num_tokens < 0 || num_tokens > kKvMostTokens || requests < 1 || requests > kKvMaxRequests)
+    return MX_ERR_INVALID_ARG;
+  if (!k_codes || !v_codes || !k_scale || !v_scale || !block_tables || !lengths || !q_start || !workspace ||
+      (num_tokens && (!q || !out || !lse)))
+    return MX_ERR_INVALID_ARG;
+  if (type != MX_HALF_BF16 && type != MX_HALF_F16) return MX_ERR_INVALID_ARG;
+  if (elem != MX_E4M3 && elem != MX_E5M2) return elem == MX_E2M1 ? MX_ERR_UNSUPPORTED : MX_ERR_INVALID_ARG;
+  if (!kv_cache_shape_ok(num_blocks, kv_heads, block_tokens, head_dim)) return MX_ERR_INVALID_ARG;
+  if (heads < 1 || heads > 65535 || heads % kv_heads) return MX_ERR_INVALID_ARG;
+  if (max_blocks < 1 || max_blocks > kKvMostTokens / block_tokens) return MX_ERR_INVALID_ARG;
+  if (num_tokens > kKvMostTokens / (heads / kv_heads)) return MX_ERR_INVALID_ARG;  // (rows of a kv head)
+  if (max_q_len < 0 || max_q_len > num_tokens || window < 0 || window > 0x7FFFFFFF) return MX_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return MX_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.f) || softmax_scale > 1e30f) return MX_ERR_INVALID_ARG;
+  if (q_stride_token % 8 || q_stride_head % 8) return MX_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_scale, 4) ||
+      !aligned(v_scale, 4) || !aligned(block_tables, 4) || !aligned(lengths, 4) || !aligned(q_start, 4) ||
+      !aligned(out, 32) || !aligned(lse, 4) || !aligned(workspace, 32))
+    return MX_ERR_INVALID_ARG;
+  if (TREE) {
+    if (max_q_len > kKvMostNodes || mask_words < 1 || mask_words > kKvMostNodes / 64 || mask_words * 64 < max_q_len ||
+        !aligned(tree_mask, 8) || !aligned(positions, 4) || (num_tokens && (!tree_mask || (window && !positions))))
+      return MX_ERR_INVALID_ARG;
+  }
+  if (num_tokens == 0) return MX_OK;
+  KvAttnArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.stride_t = q_stride_token;
+  a.stride_h = q_stride_head;
+  a.k_codes = static_cast<const uint8_t*>(k_codes);
+  a.v_codes = static_cast<const uint8_t*>(v_codes);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.tables = block_tables;
+  a.lengths = lengths;
+  a.q_start = q_start;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
+  a.num_blocks = num_blocks;
+  a.tokens = static_cast<int>(num_tokens);
+  a.heads = static_cast<int>(heads);
+  a.kv_heads = static_cast<int>(kv_heads);
+  a.requests = static_cast<int>(requests);
+  a.max_blocks = static_cast<int>(max_blocks);
+  a.shift = kv_block_shift(block_tokens);
+  a.causal = causal;
+  a.f16 = type == MX_HALF_F16;
+  a.window = static_cast<int>(window < kKvMostTokens ? window : kKvMostTokens);
+  a.tree_mask = reinterpret_cast<const uint64_t*>(tree_mask);
+  a.positions = positions;
+  a.tree_words = static_cast<int>(mask_words);
+  cudaStream_t st = as_stream(stream);
+  // A call's launches speak to each other through the workspace.  Host threads that share a stream, and with it a
+  // workspace, take turns, so that no other call's launch comes between them.
+  const std::lock_guard<std::mutex> hold(kv_turn);
+  if (elem == MX_E5M2)
+    return head_dim == 64 ? kv_attention_launch<1, 64, TREE>(a, block_tokens, max_q_len, workspace, st)
+                          : kv_attention_launch<1, 128, TREE>(a, block_tokens, max_q_len, workspace, st);
+  return head_dim == 64 ? kv_attention_launch<0, 64, TREE>(a, block_tokens, max_q_len, workspace, st)
+                        : kv_attention_launch<0, 128, TREE>(a, block_tokens, max_q_len, workspace, st);
 }
 
 }  // namespace
@@ -239,60 +313,23 @@ mx_status kv_attention(const void* q, mx_half type, int64_t num_tokens, int64_t 
                        int head_dim, const int32_t* block_tables, int64_t max_blocks, const int32_t* lengths,
                        const int32_t* q_start, int64_t requests, int64_t max_q_len, float softmax_scale, int causal,
                        int64_t window, void* out, float* lse, void* workspace, void* stream) {
-  if (num_tokens < 0 || num_tokens > kKvMostTokens || requests < 1 || requests > kKvMaxRequests)
-    return MX_ERR_INVALID_ARG;
-  if (!k_codes || !v_codes || !k_scale || !v_scale || !block_tables || !lengths || !q_start || !workspace ||
-      (num_tokens && (!q || !out || !lse)))
-    return MX_ERR_INVALID_ARG;
-  if (type != MX_HALF_BF16 && type != MX_HALF_F16) return MX_ERR_INVALID_ARG;
-  if (elem != MX_E4M3 && elem != MX_E5M2) return elem == MX_E2M1 ? MX_ERR_UNSUPPORTED : MX_ERR_INVALID_ARG;
-  if (!kv_cache_shape_ok(num_blocks, kv_heads, block_tokens, head_dim)) return MX_ERR_INVALID_ARG;
-  if (heads < 1 || heads > 65535 || heads % kv_heads) return MX_ERR_INVALID_ARG;
-  if (max_blocks < 1 || max_blocks > kKvMostTokens / block_tokens) return MX_ERR_INVALID_ARG;
-  if (num_tokens > kKvMostTokens / (heads / kv_heads)) return MX_ERR_INVALID_ARG;  // (rows of a kv head)
-  if (max_q_len < 0 || max_q_len > num_tokens || window < 0 || window > 0x7FFFFFFF) return MX_ERR_INVALID_ARG;
-  if (causal != 0 && causal != 1) return MX_ERR_INVALID_ARG;
-  if (!(softmax_scale > 0.f) || softmax_scale > 1e30f) return MX_ERR_INVALID_ARG;
-  if (q_stride_token % 8 || q_stride_head % 8) return MX_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_scale, 4) ||
-      !aligned(v_scale, 4) || !aligned(block_tables, 4) || !aligned(lengths, 4) || !aligned(q_start, 4) ||
-      !aligned(out, 32) || !aligned(lse, 4) || !aligned(workspace, 32))
-    return MX_ERR_INVALID_ARG;
-  if (num_tokens == 0) return MX_OK;
-  KvAttnArgs a{};
-  a.q = static_cast<const uint16_t*>(q);
-  a.stride_t = q_stride_token;
-  a.stride_h = q_stride_head;
-  a.k_codes = static_cast<const uint8_t*>(k_codes);
-  a.v_codes = static_cast<const uint8_t*>(v_codes);
-  a.k_scale = k_scale;
-  a.v_scale = v_scale;
-  a.tables = block_tables;
-  a.lengths = lengths;
-  a.q_start = q_start;
-  a.out = static_cast<uint16_t*>(out);
-  a.lse = lse;
-  a.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
-  a.num_blocks = num_blocks;
-  a.tokens = static_cast<int>(num_tokens);
-  a.heads = static_cast<int>(heads);
-  a.kv_heads = static_cast<int>(kv_heads);
-  a.requests = static_cast<int>(requests);
-  a.max_blocks = static_cast<int>(max_blocks);
-  a.shift = kv_block_shift(block_tokens);
-  a.causal = causal;
-  a.f16 = type == MX_HALF_F16;
-  a.window = static_cast<int>(window < kKvMostTokens ? window : kKvMostTokens);
-  cudaStream_t st = as_stream(stream);
-  // A call's launches speak to each other through the workspace.  Host threads that share a stream, and with it a
-  // workspace, take turns, so that no other call's launch comes between them.
-  static std::mutex turn;
-  const std::lock_guard<std::mutex> hold(turn);
-  if (elem == MX_E5M2)
-    return head_dim == 64 ? kv_attention_launch<1, 64>(a, block_tokens, max_q_len, workspace, st)
-                          : kv_attention_launch<1, 128>(a, block_tokens, max_q_len, workspace, st);
-  return head_dim == 64 ? kv_attention_launch<0, 64>(a, block_tokens, max_q_len, workspace, st)
-                        : kv_attention_launch<0, 128>(a, block_tokens, max_q_len, workspace, st);
+  return kv_attention_call<false>(q, type, num_tokens, heads, q_stride_token, q_stride_head, k_codes, v_codes, k_scale, v_scale,
+                                  elem, num_blocks, kv_heads, block_tokens, head_dim, block_tables, max_blocks, lengths, q_start,
+                                  requests, max_q_len, nullptr, 0, nullptr, softmax_scale, causal, window, out, lse, workspace,
+                                  stream);
+}
+
+mx_status kv_tree_attention(const void* q, mx_half type, int64_t num_tokens, int64_t heads, int64_t q_stride_token,
+                            int64_t q_stride_head, const void* k_codes, const void* v_codes, const float* k_scale,
+                            const float* v_scale, mx_elem elem, int64_t num_blocks, int64_t kv_heads, int block_tokens,
+                            int head_dim, const int32_t* block_tables, int64_t max_blocks, const int32_t* lengths,
+                            const int32_t* q_start, int64_t requests, int64_t max_q_len, const int64_t* tree_mask,
+                            int64_t mask_words, const int32_t* positions, float softmax_scale, int64_t window, void* out,
+                            float* lse, void* workspace, void* stream) {
+  return kv_attention_call<true>(q, type, num_tokens, heads, q_stride_token, q_stride_head, k_codes, v_codes, k_scale, v_scale,
+                                 elem, num_blocks, kv_heads, block_tokens, head_dim, block_tables, max_blocks, lengths, q_start,
+                                 requests, max_q_len, tree_mask, mask_words, positions, softmax_scale, 0, window, out, lse,
+                                 workspace, stream);
 }
 
 }  // extern "C"

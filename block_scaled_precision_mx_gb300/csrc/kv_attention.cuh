@@ -6,6 +6,9 @@
 // Query i of a request with L cached tokens and Q queries stands at position p = L - Q + i and sees
 // j < L, with j <= p (causal) and j > p - window (a window).  A row that sees nothing gives 0 and
 // lse = -inf.
+//
+// With a tree of drafted tokens (the kernels' TREE) the Q newest tokens are a tree's nodes: a query sees, of the
+// C = L - Q tokens in front of them, j > position - window, and of the nodes those whose bits its row of the mask has.
 #pragma once
 
 #include <cmath>
@@ -32,6 +35,9 @@ struct KvAttnArgs {
   int tokens, heads, kv_heads, requests, max_blocks, shift;
   int causal, window;
   int f16;                 // q and out are FP16, else bf16
+  const uint64_t* tree_mask;    // TREE: [tokens][tree_words]
+  const int32_t* positions;     // TREE, with a window: [tokens]
+  int tree_words;
 };
 
 constexpr float kLn2 = 0.69314718055994531f;
@@ -207,6 +213,7 @@ struct KvRequest {
   __device__ int cost() const;
 };
 
+template <bool TREE>
 __device__ __forceinline__ KvRequest kv_request(const KvAttnArgs& a, int r, int most_q, bool tell) {
   KvRequest v;
   v.q0 = a.q_start[r];
@@ -214,7 +221,7 @@ __device__ __forceinline__ KvRequest kv_request(const KvAttnArgs& a, int r, int 
   v.len = a.lengths[r];
   // (compared before they are subtracted: differences of any two 32-bit numbers do not fit)
   const bool ok = v.q0 >= 0 && v.q0 <= end && end <= a.tokens && end - v.q0 <= most_q && v.len >= 0 &&
-                  v.len <= a.max_blocks << a.shift;
+                  v.len <= a.max_blocks << a.shift && (!TREE || v.len >= end - v.q0);
   if (!ok && tell) atomicOr(&g_mx_error_word, kSiteBadCache);
   v.rows_q = ok ? end - v.q0 : 0;
   v.len = ok ? v.len : 0;
@@ -222,6 +229,15 @@ __device__ __forceinline__ KvRequest kv_request(const KvAttnArgs& a, int r, int 
   v.first_tile = lo / kKvTile;
   v.tiles = v.rows_q ? max(1, (v.len + kKvTile - 1) / kKvTile - v.first_tile) : 0;
   return v;
+}
+
+// Of a tree, row i of a request with n of them: the first token in front of the nodes that it sees, of `context`.  Its
+// position is a node's of this request, or is told and taken as the nearest.
+__device__ __forceinline__ int kv_tree_first(const KvAttnArgs& a, int token, int context, int n) {
+  if (!a.window) return 0;
+  const int p = a.positions[token], near = min(max(p, context), context + n - 1);
+  if (p != near) atomicOr(&g_mx_error_word, kSiteBadCache);
+  return min(max(near - a.window + 1, 0), context);
 }
 
 // The list of all units' work, in 64-token tiles, is cut into equal ranges.  A unit costs its tiles and
@@ -258,12 +274,13 @@ struct KvPlanSmem {
   long long pos, end, base, total;
   int r, h;
 };
+template <bool TREE>
 __device__ __forceinline__ void kv_plan(const KvAttnArgs& a, int most_q, KvPlanSmem& sm, KvWalk& w) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.requests + kKvFewThreads - 1) / kKvFewThreads;
   const int r0 = min(tid * per, a.requests), r1 = min(r0 + per, a.requests);
   long long mine = 0;
-  for (int r = r0; r < r1; ++r) mine += kv_request(a, r, most_q, blockIdx.x == 0).cost();
+  for (int r = r0; r < r1; ++r) mine += kv_request<TREE>(a, r, most_q, blockIdx.x == 0).cost();
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -285,7 +302,7 @@ __device__ __forceinline__ void kv_plan(const KvAttnArgs& a, int most_q, KvPlanS
   if (pos >= before && pos < before + mine) {
     long long at = before;
     for (int r = r0; r < r1; ++r) {
-      const int cost = kv_request(a, r, most_q, false).cost();
+      const int cost = kv_request<TREE>(a, r, most_q, false).cost();
       const long long all = static_cast<long long>(cost) * a.kv_heads;
       if (pos < at + all) {
         sm.r = r;
@@ -308,13 +325,14 @@ __device__ __forceinline__ void kv_plan(const KvAttnArgs& a, int most_q, KvPlanS
   w.base = sm.base;
   w.r = sm.r;
   w.h = sm.h;
-  if (w.pos < sm.total) w.req = kv_request(a, w.r, most_q, false);
+  if (w.pos < sm.total) w.req = kv_request<TREE>(a, w.r, most_q, false);
 }
 // tiles of a unit in front of place x of its cost
 __device__ __forceinline__ int kv_tiles_before(long long x, int tiles) {
   return static_cast<int>(min(max(x - kKvUnitCost, 0ll), static_cast<long long>(tiles)));
 }
 // The next segment that has tiles, from w.pos on; false at the range's end.
+template <bool TREE>
 __device__ __forceinline__ bool kv_next_segment(const KvAttnArgs& a, int most_q, KvWalk& w) {
   while (w.pos < w.end) {
     const long long unit_end = w.base + w.req.cost();
@@ -323,7 +341,7 @@ __device__ __forceinline__ bool kv_next_segment(const KvAttnArgs& a, int most_q,
       if (++w.h == a.kv_heads) {
         w.h = 0;
         while (++w.r < a.requests) {
-          w.req = kv_request(a, w.r, most_q, false);
+          w.req = kv_request<TREE>(a, w.r, most_q, false);
           if (w.req.tiles) break;
         }
         if (w.r >= a.requests) return false;
@@ -382,7 +400,7 @@ __device__ __forceinline__ void kv_finish(const KvAttnArgs& a, int q0, int row, 
   if (d == 0) a.lse[at_row] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
 }
 
-template <int FMT, int D, int NT>
+template <int FMT, int D, int NT, bool TREE>
 __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
     kv_attention_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                             const KvAttnArgs a, int most_q, uint8_t* workspace) {
@@ -408,8 +426,14 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(join_bar + 1);
   volatile int* last_part = abort_flag + 1;
   __shared__ KvPlanSmem plan;
+  __shared__ uint32_t sNodes[2][TREE ? Cfg::ROWS : 1];  // the nodes that a row sees
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int group = a.heads / a.kv_heads;
+  // whether a row that sees [seen.x, seen.y), and of a tree its nodes behind that, sees token t
+  auto sees = [&](int buf, int row, int2 seen, int t) {
+    if (TREE && t >= seen.y) return t - seen.y < 32 && (sNodes[buf][TREE ? row : 0] >> ((t - seen.y) & 31) & 1);
+    return t >= seen.x && t < seen.y;
+  };
 
   if (tid == 0) {
     for (int i = 0; i < Cfg::STAGES; ++i) {
@@ -428,7 +452,7 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
   }
   pdl_wait();  // (no early trigger: CTAs of the next kernel would take the places of this one's last CTAs)
   KvWalk w;
-  kv_plan(a, most_q, plan, w);  // (its barriers also publish the mbarriers)
+  kv_plan<TREE>(a, most_q, plan, w);  // (its barriers also publish the mbarriers)
   kv_clear_rest(a, D, blockIdx.x * kKvFewThreads + tid, gridDim.x * kKvFewThreads);
 
   if (warp == kKvWarps) {
@@ -446,7 +470,7 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
     uint32_t seg = 0;
     // tells the others of the next segment and brings its queries, as the fragments of Q^T
     auto next_segment = [&]() {
-      const bool more = kv_next_segment(a, most_q, w);
+      const bool more = kv_next_segment<TREE>(a, most_q, w);
       const int buf = seg & 1;
       if (!kv_wait(&seg_empty[buf], ((seg >> 1) & 1) ^ 1, abort_flag, kSiteProducerEmpty)) return false;
       ++seg;
@@ -461,7 +485,7 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
         v.head = w.h;
         v.any_lo = a.window ? pos0 - a.window + 1 : 0;
         v.all_lo = a.window ? w.req.len - a.window : 0;
-        v.all_hi = a.causal ? min(w.req.len, pos0 + 1) : w.req.len;
+        v.all_hi = TREE ? pos0 : a.causal ? min(w.req.len, pos0 + 1) : w.req.len;
         v.part = w.count == w.req.tiles ? 0 : w.base < range_start ? 1 : 2;
         if (v.part) {
           const long long total = plan.total;
@@ -509,9 +533,17 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
                                                                     kv_pack_f16(f[4 * i + 2] * mul, f[4 * i + 3] * mul));
           if (c == 0) {
             sQF[buf * Cfg::ROWS + row] = a.scale_log2 / mul;
-            const int p = pos0 + (row < rows ? qi : 0);
-            sSeen[buf * Cfg::ROWS + row] =
-                make_int2(a.window ? p - a.window + 1 : 0, a.causal ? min(w.req.len, p + 1) : w.req.len);
+            if (TREE) {  // (its rows are at most 16)
+              const int token = w.req.q0 + qi;
+              sSeen[buf * Cfg::ROWS + row] = make_int2(row < rows ? kv_tree_first(a, token, pos0, w.req.rows_q) : 0, pos0);
+              sNodes[buf][row] = row < rows ? static_cast<uint32_t>(a.tree_mask[static_cast<int64_t>(token) * a.tree_words]) &
+                                                  ((1u << w.req.rows_q) - 1)
+                                            : 0;
+            } else {
+              const int p = pos0 + (row < rows ? qi : 0);
+              sSeen[buf * Cfg::ROWS + row] =
+                  make_int2(a.window ? p - a.window + 1 : 0, a.causal ? min(w.req.len, p + 1) : w.req.len);
+            }
           }
         }
       }
@@ -667,8 +699,8 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int t = t0 + g + 8 * (j >> 1);
-              const int2 seen = q_seen[n * 8 + 2 * c + (j & 1)];
-              if (t < seen.x || t >= seen.y) s[n][j] = -INFINITY;
+              const int row = n * 8 + 2 * c + (j & 1);
+              if (!sees(buf, row, q_seen[row], t)) s[n][j] = -INFINITY;
             }
           }
 #pragma unroll
@@ -744,7 +776,7 @@ __global__ void __launch_bounds__(kKvFewThreads, KvFewCfg<D, NT>::CTAS)
                 const int t = t0 + 2 * c + (tt & 1) + 8 * (tt >> 1), d = (D / 8) * g + 4 * j;
                 if (x)
                   for (int row = 0; row < Cfg::ROWS; ++row)
-                    if (t >= q_seen[row].x && t < q_seen[row].y)
+                    if (sees(buf, row, q_seen[row], t))
                       atomicOr(&q_nan[row * (D / 32) + (d >> 5)],
                                ((x >> 7 & 1) | (x >> 14 & 2) | (x >> 21 & 4) | (x >> 28 & 8)) << (d & 31));
               }

@@ -88,6 +88,7 @@ struct KvUnit {
   __device__ __forceinline__ int cost() const { return tiles + kKvUnitCost; }
 };
 
+template <bool TREE>
 __device__ __forceinline__ KvUnit kv_unit(const KvAttnArgs& a, const KvRequest& req, int group, int q_tile) {
   KvUnit u;
   u.q0 = req.q0;
@@ -95,10 +96,12 @@ __device__ __forceinline__ KvUnit kv_unit(const KvAttnArgs& a, const KvRequest& 
   u.len = req.len;
   u.row0 = q_tile * kKvManyRows;
   u.rows = min(kKvManyRows, req.rows_q * group - u.row0);
-  const int p0 = req.len - req.rows_q + u.row0 / group, p1 = req.len - req.rows_q + (u.row0 + u.rows - 1) / group;
+  // (a tree's rows may stand at any of its positions)
+  const int p0 = req.len - req.rows_q + (TREE ? 0 : u.row0 / group);
+  const int p1 = TREE ? req.len - 1 : req.len - req.rows_q + (u.row0 + u.rows - 1) / group;
   u.any_lo = a.window ? max(0, p0 - a.window + 1) : 0;
   u.all_lo = a.window ? max(0, p1 - a.window + 1) : 0;
-  u.all_hi = a.causal ? min(req.len, p0 + 1) : req.len;
+  u.all_hi = TREE ? p0 : a.causal ? min(req.len, p0 + 1) : req.len;
   u.any_hi = a.causal ? min(req.len, p1 + 1) : req.len;
   u.first_tile = u.any_lo / kKvManyTile;
   u.tiles = max(1, (max(u.any_hi, 0) + kKvManyTile - 1) / kKvManyTile - u.first_tile);
@@ -109,11 +112,12 @@ __device__ __forceinline__ int kv_units_of(const KvRequest& req, int group) {
 }
 
 // The unit of request r, whose units begin at place x, that job.begin falls into.
+template <bool TREE>
 __device__ __forceinline__ void kv_first_unit(const KvAttnArgs& a, const KvRequest& req, int r, int group, long long x,
                                               KvJob& job) {
 #pragma unroll 1
   for (int q_tile = 0;; ++q_tile) {
-    const KvUnit u = kv_unit(a, req, group, q_tile);
+    const KvUnit u = kv_unit<TREE>(a, req, group, q_tile);
     const long long all = static_cast<long long>(u.cost()) * a.kv_heads;
     if (job.begin < x + all) {
       job.head = static_cast<int>((job.begin - x) / u.cost());
@@ -133,6 +137,7 @@ __device__ __forceinline__ void kv_first_unit(const KvAttnArgs& a, const KvReque
 // Ranges of the list of all units (request by request, then 256 rows by 256 rows, then head by head): one
 // CTA sums the requests' costs, scans them and finds each range's first unit.  A request's units are summed
 // by a thread while they are few, by a warp otherwise.
+template <bool TREE>
 __global__ void __launch_bounds__(kKvPlanThreads) kv_plan_kernel(const KvAttnArgs a, int most_q, int ranges,
                                                                  uint8_t* workspace) {
   pdl_prologue();
@@ -141,18 +146,18 @@ __global__ void __launch_bounds__(kKvPlanThreads) kv_plan_kernel(const KvAttnArg
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = a.heads / a.kv_heads;
   if (static_cast<long long>(most_q) * group <= 8 * kKvManyRows) {
     for (int r = tid; r < a.requests; r += kKvPlanThreads) {
-      const KvRequest req = kv_request(a, r, most_q, true);
+      const KvRequest req = kv_request<TREE>(a, r, most_q, true);
       const int units = kv_units_of(req, group);
       long long sum = 0;
-      for (int i = 0; i < units; ++i) sum += kv_unit(a, req, group, i).cost();
+      for (int i = 0; i < units; ++i) sum += kv_unit<TREE>(a, req, group, i).cost();
       place[r] = sum * a.kv_heads;
     }
   } else {
     for (int r = warp; r < a.requests; r += kKvPlanThreads / 32) {
-      const KvRequest req = kv_request(a, r, most_q, lane == 0);
+      const KvRequest req = kv_request<TREE>(a, r, most_q, lane == 0);
       const int units = kv_units_of(req, group);
       long long sum = 0;
-      for (int i = lane; i < units; i += 32) sum += kv_unit(a, req, group, i).cost();
+      for (int i = lane; i < units; i += 32) sum += kv_unit<TREE>(a, req, group, i).cost();
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
       if (lane == 0) place[r] = sum * a.kv_heads;
@@ -193,7 +198,7 @@ __global__ void __launch_bounds__(kKvPlanThreads) kv_plan_kernel(const KvAttnArg
         if (place[mid] <= job.begin) lo = mid;
         else hi = mid;
       }
-      kv_first_unit(a, kv_request(a, lo, most_q, false), lo, group, place[lo], job);
+      kv_first_unit<TREE>(a, kv_request<TREE>(a, lo, most_q, false), lo, group, place[lo], job);
     }
     jobs[c] = job;
   }
@@ -206,6 +211,7 @@ struct KvManyWalk {
   KvUnit u;
   int tile, count;  // the current segment
 };
+template <bool TREE>
 __device__ __forceinline__ void kv_many_begin(const KvAttnArgs& a, int most_q, int group, const KvJob& job, KvManyWalk& w) {
   w.pos = job.begin;
   w.end = job.end;
@@ -214,10 +220,11 @@ __device__ __forceinline__ void kv_many_begin(const KvAttnArgs& a, int most_q, i
   w.h = job.head;
   w.q_tile = job.q_tile;
   if (w.pos < w.end) {
-    w.req = kv_request(a, w.r, most_q, false);
-    w.u = kv_unit(a, w.req, group, w.q_tile);
+    w.req = kv_request<TREE>(a, w.r, most_q, false);
+    w.u = kv_unit<TREE>(a, w.req, group, w.q_tile);
   }
 }
+template <bool TREE>
 __device__ __noinline__ bool kv_many_next(const KvAttnArgs& a, int most_q, int group, KvManyWalk& w) {
   while (w.pos < w.end) {
     const long long unit_end = w.base + w.u.cost();
@@ -229,10 +236,10 @@ __device__ __noinline__ bool kv_many_next(const KvAttnArgs& a, int most_q, int g
           w.q_tile = 0;
           do {
             if (++w.r >= a.requests) return false;
-            w.req = kv_request(a, w.r, most_q, false);
+            w.req = kv_request<TREE>(a, w.r, most_q, false);
           } while (w.req.rows_q == 0);
         }
-        w.u = kv_unit(a, w.req, group, w.q_tile);
+        w.u = kv_unit<TREE>(a, w.req, group, w.q_tile);
       }
       continue;
     }
@@ -307,7 +314,23 @@ __device__ __noinline__ void kv_fill_box(uint8_t* to, int bytes, uint32_t four) 
   fence_proxy_async_smem();  // (a copy may come to the same place next)
 }
 
-template <int FMT, int D, bool F16>
+// Which of the 16 tokens from t on a row of a tree sees, as bits: `nodes` is its row of the mask (null: none of the nodes),
+// first the first token that it sees of those in front of the nodes, n how many nodes there are.
+__device__ __forceinline__ uint32_t kv_tree_sees16(const uint64_t* nodes, int words, int n, int context, int first, int t) {
+  const int o = t - context;
+  uint32_t b = 0xFFFFu;
+  if (o > -16) {
+    const int w = o >> 6, sh = o & 63;  // (w = -1: what is in front of the nodes)
+    const uint64_t at = w < 0 ? ~0ull : nodes && w < words ? nodes[w] : 0;
+    const uint64_t behind = sh > 48 && nodes && w + 1 < words ? nodes[w + 1] : 0;
+    b &= static_cast<uint32_t>(at >> sh) | (sh > 48 ? static_cast<uint32_t>(behind << (64 - sh)) : 0);
+    if (n - o < 16) b &= (1u << max(n - o, 0)) - 1;
+  }
+  if (first > t) b &= ~0u << min(first - t, 16);
+  return b;
+}
+
+template <int FMT, int D, bool F16, bool TREE>
 __global__ void __launch_bounds__(kKvManyThreads, 1)
     kv_attention_many_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                              const KvAttnArgs a, int most_q, int planned, uint8_t* workspace) {
@@ -383,10 +406,10 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
     KvRequest req{};
     long long mine = 0;
     if (tid < a.requests) {
-      req = kv_request(a, tid, most_q, blockIdx.x == 0);
+      req = kv_request<TREE>(a, tid, most_q, blockIdx.x == 0);
       const int units = kv_units_of(req, group);
 #pragma unroll 1
-      for (int i = 0; i < units; ++i) mine += kv_unit(a, req, group, i).cost();
+      for (int i = 0; i < units; ++i) mine += kv_unit<TREE>(a, req, group, i).cost();
     }
     mine *= a.kv_heads;
     long long incl = mine;
@@ -405,7 +428,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
     }
     KvJob mine_job{kv_cut(total, blockIdx.x, gridDim.x), kv_cut(total, blockIdx.x + 1, gridDim.x), 0, 0, 0, 0, 0, 0, 0, 0};
     const bool here = mine_job.begin >= before && mine_job.begin < before + mine;
-    if (here) kv_first_unit(a, req, tid, group, before, mine_job);
+    if (here) kv_first_unit<TREE>(a, req, tid, group, before, mine_job);
     if (here || (total == 0 && tid == 0)) {
       job = mine_job;
       reinterpret_cast<KvJob*>(workspace + kKvJobsAt)[blockIdx.x] = mine_job;
@@ -429,14 +452,14 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
   if (warp == 12) {
     // ------------------------------------------------------------------ loads: item 2i = K, 2i + 1 = V of tile i
     KvManyWalk w;
-    kv_many_begin(a, most_q, group, job, w);
+    kv_many_begin<TREE>(a, most_q, group, job, w);
     const long long range_start = w.pos;
     const int P = 1 << a.shift, rows_box = min(P, kKvTile), boxes = kKvManyTile / rows_box;
     const int most_tiles = 32 * P / kKvManyTile;
     uint32_t tiles_done = 0, issued = 0;  // issued: items, for the end (a wait that gives up may leave a tile's second out)
     bool ok = true;
     while (ok) {
-      const bool more = kv_many_next(a, most_q, group, w);
+      const bool more = kv_many_next<TREE>(a, most_q, group, w);
       const uint32_t sl = seg % kKvManySegments;
       if (!kv_wait(&seg_empty[sl], ((seg / kKvManySegments) & 1) ^ 1, abort_flag, kSiteProducerEmpty)) break;
       if (lane == 0) {
@@ -723,8 +746,10 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
       const int my_row = single ? row : 128 * half + row;
       const bool live = my_row < v.rows;
       const int qi = (v.row0 + my_row) / group, hg = v.row0 + my_row - qi * group;
-      const int p = v.len - v.rows_q + qi;
-      const int lo = a.window ? max(0, p - a.window + 1) : 0, hi = a.causal ? min(v.len, p + 1) : v.len;
+      const int context = v.len - v.rows_q, p = context + qi;
+      const uint64_t* nodes = TREE && live ? a.tree_mask + static_cast<int64_t>(v.q0 + qi) * a.tree_words : nullptr;
+      const int lo = TREE ? (live ? kv_tree_first(a, v.q0 + qi, context, v.rows_q) : 0) : a.window ? max(0, p - a.window + 1) : 0;
+      const int hi = TREE ? context : a.causal ? min(v.len, p + 1) : v.len;
       const uint32_t width = static_cast<uint32_t>(max(hi - lo, 0));
       const int first = single ? half : 0;
       float m = -INFINITY, l = 0.f;
@@ -750,9 +775,16 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
             tmem_ld_32x32b_x16(tS + 16 * g, x);
             tmem_ld_wait();
             tmem_regs_ready16(x);
+            if (TREE) {
+              const uint32_t seen = kv_tree_sees16(nodes, a.tree_words, v.rows_q, context, lo, t);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (static_cast<uint32_t>(token + 16 * g + j - lo) >= width) x[j] = 0xFF800000u;
+              for (int j = 0; j < 16; ++j)
+                if (!(seen >> j & 1)) x[j] = 0xFF800000u;
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (static_cast<uint32_t>(token + 16 * g + j - lo) >= width) x[j] = 0xFF800000u;
+            }
             tmem_st_32x32b_x16(tS + 16 * g, x);
           }
           tmem_st_wait();
@@ -835,8 +867,9 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
           ok = kv_wait(&f_full[v_item % Cfg::F16_SLOTS], (v_item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteEpiTmemFull);
           if (!ok) break;
           if (sNan[st]) {
-            const int j0 = max(lo - token, 0), j1 = min(hi - token, kKvManyTile);
+            const int j0 = max(lo - token, 0), j1 = min((TREE ? v.len : hi) - token, kKvManyTile);
             for (int j = j0; j < j1; ++j) {
+              if (TREE && !(kv_tree_sees16(nodes, a.tree_words, v.rows_q, context, lo, token + j) & 1)) continue;
               const volatile uint32_t* note =
                   reinterpret_cast<const volatile uint32_t*>(nan_notes + ((tile & 3) * kKvManyTile + j) * (D / 8));
 #pragma unroll

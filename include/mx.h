@@ -565,6 +565,25 @@ mx_status kv_draft_trees(const int32_t* parents, int64_t num_tokens, const int32
                          int32_t* positions, void* stream);
 
 /*
+ * kv_tree_attention -- kv_attention of a tree's queries over the cache and over the nodes that they see.
+ *
+ * As kv_attention, but that of a request's n newest tokens, its nodes, row i sees those whose bits tree_mask has in row
+ * q_start[r] + i (kv_draft_trees gives one; any other does, and bits from n on are not looked at), and of the
+ * lengths[r] - n tokens in front of them all, or those j > positions[q_start[r] + i] - window with a window > 0.  The
+ * nodes follow the mask alone.  positions is read only with a window (NULL will do without) and lies in
+ * [lengths[r] - n, lengths[r]); one that does not is reported, and taken as the nearest that does.  A request whose
+ * length is less than n breaks its contract.  max_q_len <= 1024, 64 mask_words >= max_q_len, mask_words <= 16.
+ * workspace: as for kv_attention, and the same one will do.
+ */
+mx_status kv_tree_attention(const void* q, mx_half type, int64_t num_tokens, int64_t heads, int64_t q_stride_token,
+                            int64_t q_stride_head, const void* k_codes, const void* v_codes, const float* k_scale,
+                            const float* v_scale, mx_elem elem, int64_t num_blocks, int64_t kv_heads, int block_tokens,
+                            int head_dim, const int32_t* block_tables, int64_t max_blocks, const int32_t* lengths,
+                            const int32_t* q_start, int64_t requests, int64_t max_q_len, const int64_t* tree_mask,
+                            int64_t mask_words, const int32_t* positions, float softmax_scale, int64_t window, void* out,
+                            float* lse, void* workspace, void* stream);
+
+/*
  * kv_verify_drafts -- which drafts stay, and the token behind them.
  *
  * target_probs[num_tokens] are rows of vocab probabilities (FP32, rows target_stride apart): row q_start[r] + i is the

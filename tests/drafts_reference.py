@@ -158,3 +158,59 @@ def norm_backward(dy, x, w, table, positions, eps, interleaved, half_step, small
     bound = r * (np.abs(w) * most + np.abs(xh) * (np.abs(w) * most * np.abs(xh)).mean(2, keepdims=True))
     return (dx, dw, np.abs(dx) * half_step + bound * (2 * d + 32) * 2.0 ** -24 * (1 + half_step) + smallest,
             (most * np.abs(xh)).sum((0, 1)) * (t * h + d + 16) * 2.0 ** -24)
+
+
+# ------------------------------------------------------------------ attention of a tree's queries
+def sees(mask, positions, lengths, q_start, window):
+    """For each request, bool [rows][length]: which tokens each of its rows sees."""
+    out = []
+    for r, length in enumerate(lengths):
+        a, b = int(q_start[r]), int(q_start[r + 1])
+        context = int(length) - (b - a)
+        s = np.zeros((b - a, int(length)), bool)
+        for i in range(b - a):
+            first = max(0, int(positions[a + i]) - window + 1) if window else 0
+            s[i, first:context] = True
+            for j in range(b - a):
+                s[i, context + j] = int(mask[a + i, j // 64]) >> (j % 64) & 1
+        out.append(s)
+    return out
+
+
+def tree_attention(q, k_codes, v_codes, k_scale, v_scale, tables, lengths, q_start, seen, elem, softmax_scale):
+    """(out, lse, out's tolerance but for its own rounding, lse's): the formula and the tolerances of
+    kv_reference.attention, for rows that see what `seen` says."""
+    table, p = kv.decode_table(elem), k_codes.shape[2]
+    t, heads, d = q.shape
+    group = heads // k_codes.shape[1]
+    out, lse = np.zeros((t, heads, d)), np.full((t, heads), -np.inf)
+    tol, lse_tol = np.zeros((t, heads, d)), np.zeros((t, heads))
+    q = q.astype(np.float64)
+    for r, length in enumerate(lengths):
+        a, b = int(q_start[r]), int(q_start[r + 1])
+        if a == b:
+            continue
+        blocks = tables[r, :-(-int(length) // p)]
+        for h in range(k_codes.shape[1]):
+            k = (table[k_codes[blocks, h]] * k_scale[blocks, h].astype(np.float64)[:, None, None]).reshape(-1, d)[:length]
+            c = table[v_codes[blocks, h]].reshape(-1, d)[:length]
+            sv = np.repeat(v_scale[blocks, h].astype(np.float64), p)[:length]
+            for i in range(a, b):
+                at = np.flatnonzero(seen[r][i - a])
+                if not len(at):
+                    continue
+                mine = slice(h * group, (h + 1) * group)
+                with np.errstate(invalid="ignore"):
+                    z = softmax_scale * q[i, mine] @ k[at].T
+                    zabs = softmax_scale * np.abs(q[i, mine]) @ np.abs(k[at]).T
+                    m = z.max(1, keepdims=True)
+                    e = np.exp(z - m)
+                    l = e.sum(1, keepdims=True)
+                    w, v, n = e / l, c[at] * sv[at, None], len(at)
+                    dz = (d + 8) * 2.0 ** -24 * zabs.max(1, keepdims=True)
+                    out[i, mine] = w @ v
+                    lse[i, mine] = (m + np.log(l))[:, 0]
+                    tol[i, mine] = (w @ np.abs(v) * (2.0 ** -11 + 2 * dz + n * 2.0 ** -23 + 2.0 ** -20)
+                                    + 2.0 ** -25 * np.abs(c[at]).sum(0) * sv[at].max())
+                    lse_tol[i, mine] = (dz + n * 2.0 ** -23 + 2.0 ** -20 + 2.0 ** -22 * np.abs(m + np.log(l)))[:, 0]
+    return out, lse, tol, lse_tol

@@ -63,6 +63,24 @@ def test_trees_refuse_bad_arguments(lib):
     assert call(**dict(ok, tokens=0, most=0, parents=None, mask=None, pos=None)) == mx.MX_OK
 
 
+def test_tree_attention_refuses_bad_arguments(lib):
+    ok = dict(q=FAKE, type=0, tokens=40, heads=32, qst=4096, qsh=128, kc=FAKE, vc=FAKE, ks=FAKE, vs=FAKE, elem=0,
+              blocks=16, kv_heads=8, p=64, d=128, tables=FAKE, max_blocks=4, lengths=FAKE, q_start=FAKE, requests=4,
+              max_q=16, mask=FAKE, words=1, pos=FAKE, scale=0.1, window=5, out=FAKE, lse=FAKE, ws=FAKE)
+
+    def call(**a):
+        return lib.kv_tree_attention(a["q"], a["type"], a["tokens"], a["heads"], a["qst"], a["qsh"], a["kc"], a["vc"], a["ks"],
+                                     a["vs"], a["elem"], a["blocks"], a["kv_heads"], a["p"], a["d"], a["tables"],
+                                     a["max_blocks"], a["lengths"], a["q_start"], a["requests"], a["max_q"], a["mask"],
+                                     a["words"], a["pos"], a["scale"], a["window"], a["out"], a["lse"], a["ws"], None)
+    refuses(call, ok, [{k: None} for k in ("q", "kc", "vc", "ks", "vs", "tables", "lengths", "q_start", "mask", "pos", "out",
+                                           "lse", "ws")]
+            + [{"mask": FAKE + 4}, {"pos": FAKE + 2}, {"words": 0}, {"words": 17}, {"tokens": 400, "max_q": 65},
+               {"tokens": 4000, "max_q": 1025, "words": 16}, {"max_q": 41}, {"heads": 30}, {"window": -1}, {"scale": 0.0},
+               {"type": 5}, {"ws": FAKE + 8}], [{"elem": 2}])
+    assert call(**dict(ok, tokens=0, max_q=0, q=None, out=None, lse=None, mask=None, pos=None)) == mx.MX_OK
+
+
 def test_verify_refuses_bad_arguments(lib):
     ok = dict(target=FAKE, tst=1000, draft=FAKE, dst=1000, vocab=1000, drafts=FAKE, parents=FAKE, tokens=40, q_start=FAKE,
               requests=4, most=16, accept=FAKE, sample=FAKE, path=FAKE, out=FAKE, counts=FAKE)

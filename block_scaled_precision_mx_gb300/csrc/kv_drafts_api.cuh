@@ -27,7 +27,7 @@ bool qk_norm_ok(mx_half type, int64_t num_tokens, int64_t heads, int64_t kv_head
     return false;
   if (head_dim < 8 || head_dim > 256 || head_dim % 8) return false;
   if (!q_weight || (kv_heads && !k_weight) || (weight_f32 != 0 && weight_f32 != 1)) return false;
-  if (!aligned(q_weight, weight_f32 ? 4 : 2) || !aligned(k_weight, weight_f32 ? 4 : 2)) return false;
+  if (!aligned(q_weight, 16) || !aligned(k_weight, 16)) return false;
   if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 16 || (interleaved != 0 && interleaved != 1)) return false;
   if (rot_dim && (!cos_sin || !aligned(cos_sin, 16) || !positions || max_positions < 1 || max_positions > kKvMostTokens))
     return false;
@@ -37,7 +37,7 @@ bool qk_norm_ok(mx_half type, int64_t num_tokens, int64_t heads, int64_t kv_head
 bool qk_rows_ok(const void* x, int64_t tokens, int64_t heads, int64_t st, int64_t sh) {
   return tokens == 0 || heads == 0 || (x && aligned(x, 16) && st % 8 == 0 && sh % 8 == 0);
 }
-template <bool BACK, int LANES, bool F16, int HEADS>
+template <bool BACK, int LANES, bool F16, bool INTER, int HEADS>
 mx_status qk_norm_launch_as(const QkNormArgs& a, cudaStream_t st, int64_t* ctas) {
   constexpr int kAtOnce = 32 / LANES * HEADS;
   const int64_t parts = (a.heads[0] + kAtOnce - 1) / kAtOnce + (a.heads[1] + kAtOnce - 1) / kAtOnce;
@@ -45,15 +45,20 @@ mx_status qk_norm_launch_as(const QkNormArgs& a, cudaStream_t st, int64_t* ctas)
   if (BACK) grid = grid < kQkMaxCtas ? grid : kQkMaxCtas;
   else if (grid > 0x7FFFFFFF) return MX_ERR_INVALID_ARG;
   if (ctas) *ctas = grid;
-  const auto kern = BACK ? qk_norm_rope_backward_kernel<LANES, F16, HEADS> : qk_norm_rope_kernel<LANES, F16, HEADS>;
+  const auto kern = BACK ? qk_norm_rope_backward_kernel<LANES, F16, INTER, HEADS> : qk_norm_rope_kernel<LANES, F16, INTER, HEADS>;
   return pdl_launch(kern, static_cast<unsigned>(grid), kQkThreads, 0, st, a) == cudaSuccess ? launch_status() : MX_ERR_CUDA;
+}
+template <bool BACK, bool F16, bool INTER>
+mx_status qk_norm_launch_with(const QkNormArgs& a, cudaStream_t st, int64_t* ctas) {
+  constexpr int kHeads = BACK ? 2 : 4;
+  return a.dim <= 64    ? qk_norm_launch_as<BACK, 8, F16, INTER, kHeads>(a, st, ctas)
+         : a.dim <= 128 ? qk_norm_launch_as<BACK, 16, F16, INTER, kHeads>(a, st, ctas)
+                        : qk_norm_launch_as<BACK, 32, F16, INTER, kHeads>(a, st, ctas);
 }
 template <bool BACK>
 mx_status qk_norm_launch(const QkNormArgs& a, bool f16, cudaStream_t st, int64_t* ctas) {
-  constexpr int kHeads = BACK ? 2 : 4;
-#define QK_NORM(LANES) (f16 ? qk_norm_launch_as<BACK, LANES, true, kHeads>(a, st, ctas) : qk_norm_launch_as<BACK, LANES, false, kHeads>(a, st, ctas))
-  return a.dim <= 64 ? QK_NORM(8) : a.dim <= 128 ? QK_NORM(16) : QK_NORM(32);
-#undef QK_NORM
+  if (f16) return a.interleaved ? qk_norm_launch_with<BACK, true, true>(a, st, ctas) : qk_norm_launch_with<BACK, true, false>(a, st, ctas);
+  return a.interleaved ? qk_norm_launch_with<BACK, false, true>(a, st, ctas) : qk_norm_launch_with<BACK, false, false>(a, st, ctas);
 }
 
 }  // namespace

@@ -12,6 +12,16 @@
 
 namespace mxgb {
 
+template <bool F16>
+__device__ __forceinline__ uint32_t kv_pack2(float lo, float hi) {
+  if (F16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 struct QkNormArgs {
   const uint16_t* x[2];     // queries, keys: [tokens][heads][D], bf16 or fp16
   int64_t xst[2], xsh[2];
@@ -29,103 +39,89 @@ struct QkNormArgs {
 
 constexpr int kQkThreads = 256;
 
-// eight values of a head's row, as FP32
-template <bool F16>
-__device__ __forceinline__ void qk_load8(float (&f)[8], const uint16_t* at, bool on) {
-  const uint4 v = on ? *reinterpret_cast<const uint4*>(at) : make_uint4(0, 0, 0, 0);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// A lane has eight values of a head's row, four at `at[0]` and four at `at[1]`, so chosen that what a rotation turns
+// together is in one lane: with pairs (i, rot / 2 + i) four from each half, else eight in a row.  (Eight in a row for both,
+// with a shuffle for each value: 16384 tokens of 40 heads 120 us.)
+template <int LANES, bool INTER>
+struct QkLane {
+  int at[2];
+  float c[4], s[4];  // cosines and sines: of (i, 4 + i) of its values, or of (2i, 2i + 1)
+  int turn_at;
+  bool on, turns;
+
+  __device__ __forceinline__ QkLane(const QkNormArgs& a) {
+    const int l = threadIdx.x % LANES;
+    on = 8 * l < a.dim;
+    turns = 8 * l < a.rot;
+    turn_at = 4 * l;
+    at[0] = !INTER && turns ? 4 * l : 8 * l;
+    at[1] = !INTER && turns ? a.rot / 2 + 4 * l : 8 * l + 4;
+  }
+  __device__ __forceinline__ void load(uint2 (&v)[2], const uint16_t* row, bool live) const {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 t = kv_unpack2<F16>(w[i]);
-    f[2 * i] = t.x;
-    f[2 * i + 1] = t.y;
+    for (int i = 0; i < 2; ++i) v[i] = on && live ? *reinterpret_cast<const uint2*>(row + at[i]) : make_uint2(0, 0);
   }
-}
-template <bool F16>
-__device__ __forceinline__ uint32_t qk_pack2(float lo, float hi) {
-  if (F16) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
+  template <bool F16>
+  __device__ __forceinline__ void store(uint16_t* row, const float (&f)[8], bool live) const {
+    if (!on || !live) return;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<uint2*>(row + at[i]) =
+          make_uint2(kv_pack2<F16>(f[4 * i], f[4 * i + 1]), kv_pack2<F16>(f[4 * i + 2], f[4 * i + 3]));
   }
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
+  template <bool F16>
+  __device__ __forceinline__ void weights(float (&w)[8], const QkNormArgs& a, int which) const {
+    const void* from = which ? a.weight[1] : a.weight[0];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (on && a.weight_f32) {
+        v = *reinterpret_cast<const float4*>(static_cast<const float*>(from) + at[i]);
+      } else if (on) {
+        const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(from) + at[i]);
+        const float2 lo = kv_unpack2<F16>(u.x), hi = kv_unpack2<F16>(u.y);
+        v = make_float4(lo.x, lo.y, hi.x, hi.y);
+      }
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+  }
+  __device__ __forceinline__ void angles(const QkNormArgs& a, int p) {
+    float4 cc = make_float4(1.f, 1.f, 1.f, 1.f), ss = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (turns) {
+      const float* row = a.table + static_cast<int64_t>(p) * a.rot + turn_at;
+      cc = *reinterpret_cast<const float4*>(row);
+      ss = *reinterpret_cast<const float4*>(row + a.rot / 2);
+    }
+    c[0] = cc.x, c[1] = cc.y, c[2] = cc.z, c[3] = cc.w;
+    s[0] = ss.x, s[1] = ss.y, s[2] = ss.z, s[3] = ss.w;
+  }
+  // f turned (BACK: turned back)
+  template <bool BACK>
+  __device__ __forceinline__ void turn(float (&f)[8]) const {
+    if (!turns) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float& x = f[INTER ? 2 * i : i];
+      float& y = f[INTER ? 2 * i + 1 : 4 + i];
+      const float sn = BACK ? -s[i] : s[i], u = x;
+      x = fmaf(-sn, y, u * c[i]);
+      y = fmaf(sn, u, y * c[i]);
+    }
+  }
+};
 template <bool F16>
-__device__ __forceinline__ void qk_store8(uint16_t* at, const float (&f)[8]) {
-  *reinterpret_cast<uint4*>(at) = make_uint4(qk_pack2<F16>(f[0], f[1]), qk_pack2<F16>(f[2], f[3]),
-                                             qk_pack2<F16>(f[4], f[5]), qk_pack2<F16>(f[6], f[7]));
+__device__ __forceinline__ void qk_unpack8(float (&f)[8], const uint2 (&v)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 lo = kv_unpack2<F16>(v[i].x), hi = kv_unpack2<F16>(v[i].y);
+    f[4 * i] = lo.x, f[4 * i + 1] = lo.y, f[4 * i + 2] = hi.x, f[4 * i + 3] = hi.y;
+  }
 }
 template <int LANES>
 __device__ __forceinline__ float qk_sum(float x) {
 #pragma unroll
   for (int o = LANES / 2; o; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
   return x;
-}
-
-// A lane's part of a token's cosines and sines, and of a weight: eight values each.  `turns` and `partner` say where
-// the lane's values lie in the rotation.
-template <int LANES>
-struct QkLane {
-  float c[8], s[8];
-  int col, partner;  // the first of its values; the lane (of the warp) that has what they are turned with
-  bool on, turns;
-
-  __device__ __forceinline__ QkLane(const QkNormArgs& a) {
-    const int lane = threadIdx.x & 31, l = lane % LANES, half = a.rot / 16;
-    col = 8 * l;
-    on = col < a.dim;
-    turns = col < a.rot;
-    partner = a.interleaved || !turns ? lane : l < half ? lane + half : lane - half;
-  }
-  // the angles of a position.  Interleaved: a pair's values have the same; else the two halves have.
-  __device__ __forceinline__ void angles(const QkNormArgs& a, int p) {
-    if (!turns) return;
-    const float* row = a.table + static_cast<int64_t>(p) * a.rot;
-    const int half = a.rot / 2;
-    if (a.interleaved) {
-      const float4 cc = *reinterpret_cast<const float4*>(row + col / 2), ss = *reinterpret_cast<const float4*>(row + half + col / 2);
-      c[0] = c[1] = cc.x, c[2] = c[3] = cc.y, c[4] = c[5] = cc.z, c[6] = c[7] = cc.w;
-      s[1] = ss.x, s[3] = ss.y, s[5] = ss.z, s[7] = ss.w;
-      s[0] = -ss.x, s[2] = -ss.y, s[4] = -ss.z, s[6] = -ss.w;
-    } else {
-      const int at = col < half ? col : col - half;
-      const float sign = col < half ? -1.f : 1.f;
-#pragma unroll
-      for (int i = 0; i < 8; i += 4) {
-        const float4 cc = *reinterpret_cast<const float4*>(row + at + i), ss = *reinterpret_cast<const float4*>(row + half + at + i);
-        c[i] = cc.x, c[i + 1] = cc.y, c[i + 2] = cc.z, c[i + 3] = cc.w;
-        s[i] = sign * ss.x, s[i + 1] = sign * ss.y, s[i + 2] = sign * ss.z, s[i + 3] = sign * ss.w;
-      }
-    }
-  }
-  // f turned (BACK: turned back).  By all lanes of a warp.
-  template <bool BACK>
-  __device__ __forceinline__ void turn(const QkNormArgs& a, float (&f)[8]) const {
-    if (a.rot == 0) return;
-    float o[8];
-    if (a.interleaved) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = f[i ^ 1];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xFFFFFFFFu, f[i], partner);
-    }
-    if (!turns) return;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = fmaf(BACK ? -s[i] : s[i], o[i], f[i] * c[i]);
-  }
-};
-
-__device__ __forceinline__ void qk_weights(float (&w)[8], const QkNormArgs& a, int which, int col, bool on, bool f16) {
-  const void* from = which ? a.weight[1] : a.weight[0];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    w[i] = 0.f;
-    if (!on) continue;
-    if (a.weight_f32) w[i] = static_cast<const float*>(from)[col + i];
-    else if (f16) w[i] = __half2float(static_cast<const __half*>(from)[col + i]);
-    else w[i] = __bfloat162float(static_cast<const __nv_bfloat16*>(from)[col + i]);
-  }
 }
 
 // The token's position; -1: it is left out.  Others out of range are told.
@@ -137,9 +133,9 @@ __device__ __forceinline__ int qk_position(const QkNormArgs& a, int token) {
   return -1;
 }
 
-// LANES lanes have a head's row, eight values each; a warp takes HEADS * 32 / LANES heads of a token's queries or of
-// its keys at a time, all loads first.  Memory is the bound.
-template <int LANES, bool F16, int HEADS>
+// LANES lanes have a head's row; a warp takes HEADS * 32 / LANES heads of a token's queries or of its keys, all loads
+// first.  Memory is the bound.
+template <int LANES, bool F16, bool INTER, int HEADS>
 __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkNormArgs a) {
   pdl_prologue();
   constexpr int ROWS = 32 / LANES, AT_ONCE = ROWS * HEADS;
@@ -150,93 +146,96 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkNormAr
   const int token = static_cast<int>(item / parts), part = static_cast<int>(item - static_cast<int64_t>(token) * parts);
   const int which = part >= parts0, h0 = (which ? part - parts0 : part) * AT_ONCE + sub;
   const int heads = which ? a.heads[1] : a.heads[0];
-  QkLane<LANES> lane(a);
+  QkLane<LANES, INTER> lane(a);
+  const uint16_t* x = (which ? a.x[1] : a.x[0]) + token * (which ? a.xst[1] : a.xst[0]);
+  uint16_t* y = (which ? a.out[1] : a.out[0]) + token * (which ? a.ost[1] : a.ost[0]);
+  const int64_t xsh = which ? a.xsh[1] : a.xsh[0], osh = which ? a.osh[1] : a.osh[0];
+  uint2 v[HEADS][2];
+#pragma unroll
+  for (int i = 0; i < HEADS; ++i) lane.load(v[i], x + (h0 + i * ROWS) * xsh, h0 + i * ROWS < heads);
+  float w[8];
+  lane.template weights<F16>(w, a, which);
   const int p = qk_position(a, token);
   if (p < 0) return;
-  const uint16_t* x = (which ? a.x[1] : a.x[0]) + token * (which ? a.xst[1] : a.xst[0]) + lane.col;
-  uint16_t* y = (which ? a.out[1] : a.out[0]) + token * (which ? a.ost[1] : a.ost[0]) + lane.col;
-  const int64_t xsh = which ? a.xsh[1] : a.xsh[0], osh = which ? a.osh[1] : a.osh[0];
-  float f[HEADS][8], w[8];
-#pragma unroll
-  for (int i = 0; i < HEADS; ++i) qk_load8<F16>(f[i], x + (h0 + i * ROWS) * xsh, lane.on && h0 + i * ROWS < heads);
-  qk_weights(w, a, which, lane.col, lane.on, F16);
   lane.angles(a, p);
   const float inv_dim = 1.f / a.dim;
 #pragma unroll
   for (int i = 0; i < HEADS; ++i) {
-    float sum = 0.f;
+    float f[8], sum = 0.f;
+    qk_unpack8<F16>(f, v[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum = fmaf(f[i][j], f[i][j], sum);
+    for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
     const float r = rsqrtf(fmaf(qk_sum<LANES>(sum), inv_dim, a.eps));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[i][j] *= r * w[j];
-    lane.template turn<false>(a, f[i]);
-    if (lane.on && h0 + i * ROWS < heads) qk_store8<F16>(y + (h0 + i * ROWS) * osh, f[i]);
+    for (int j = 0; j < 8; ++j) f[j] *= r * w[j];
+    lane.template turn<false>(f);
+    lane.template store<F16>(y + (h0 + i * ROWS) * osh, f, h0 + i * ROWS < heads);
   }
 }
 
-// The same items, warp after warp of a grid of a fixed size; the weights' gradients are summed by each lane over all its
-// items, then over the CTA's warps, and the CTAs' sums by the next kernel, in the same order each time.
-template <int LANES, bool F16, int HEADS>
+// The queries' items, then the keys', warp after warp of a grid of a fixed size; the weights' gradients are summed by
+// each lane over its items, then over the CTA's warps, and the CTAs' sums by the next kernel, in the same order each time.
+template <int LANES, bool F16, bool INTER, int HEADS>
 __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_backward_kernel(const QkNormArgs a) {
   pdl_prologue();
   constexpr int ROWS = 32 / LANES, AT_ONCE = ROWS * HEADS, WARPS = kQkThreads / 32;
-  const int warp = threadIdx.x >> 5, sub = (threadIdx.x & 31) / LANES;
-  const int parts0 = (a.heads[0] + AT_ONCE - 1) / AT_ONCE, parts = parts0 + (a.heads[1] + AT_ONCE - 1) / AT_ONCE;
-  const int64_t items = static_cast<int64_t>(a.tokens) * parts;
-  QkLane<LANES> lane(a);
-  const float inv_dim = 1.f / a.dim;
-  float dw[2][8] = {};
-  for (int64_t item = static_cast<int64_t>(blockIdx.x) * WARPS + warp; item < items; item += static_cast<int64_t>(gridDim.x) * WARPS) {
-    const int token = static_cast<int>(item / parts), part = static_cast<int>(item - static_cast<int64_t>(token) * parts);
-    const int which = part >= parts0, h0 = (which ? part - parts0 : part) * AT_ONCE + sub;
-    const int heads = which ? a.heads[1] : a.heads[0];
-    const int p = qk_position(a, token);
-    const uint16_t* x = (which ? a.x[1] : a.x[0]) + token * (which ? a.xst[1] : a.xst[0]) + lane.col;
-    const uint16_t* dy = (which ? a.dy[1] : a.dy[0]) + token * (which ? a.dst[1] : a.dst[0]) + lane.col;
-    uint16_t* dx = (which ? a.out[1] : a.out[0]) + token * (which ? a.ost[1] : a.ost[0]) + lane.col;
-    const int64_t xsh = which ? a.xsh[1] : a.xsh[0], dsh = which ? a.dsh[1] : a.dsh[0], osh = which ? a.osh[1] : a.osh[0];
-    float f[HEADS][8], g[HEADS][8], w[8];
-#pragma unroll
-    for (int i = 0; i < HEADS; ++i) {
-      const bool on = p >= 0 && lane.on && h0 + i * ROWS < heads;
-      qk_load8<F16>(f[i], x + (h0 + i * ROWS) * xsh, on);
-      qk_load8<F16>(g[i], dy + (h0 + i * ROWS) * dsh, on);
-    }
-    qk_weights(w, a, which, lane.col, lane.on, F16);
-    lane.angles(a, max(p, 0));
-#pragma unroll
-    for (int i = 0; i < HEADS; ++i) {
-      lane.template turn<true>(a, g[i]);
-      float sum = 0.f, dot = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        sum = fmaf(f[i][j], f[i][j], sum);
-        dot = fmaf(g[i][j] * w[j], f[i][j], dot);
-      }
-      const float r = rsqrtf(fmaf(qk_sum<LANES>(sum), inv_dim, a.eps));
-      const float mean = qk_sum<LANES>(dot) * r * inv_dim;
-      float o[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float xh = f[i][j] * r, gx = g[i][j] * xh;
-        o[j] = r * fmaf(g[i][j], w[j], -xh * mean);
-        dw[0][j] += which ? 0.f : gx;
-        dw[1][j] += which ? gx : 0.f;
-      }
-      if (lane.on && h0 + i * ROWS < heads) qk_store8<F16>(dx + (h0 + i * ROWS) * osh, o);
-    }
-  }
-  // the warp's rows, then the CTA's warps
   __shared__ float sums[WARPS][2][8 * LANES];
+  const int warp = threadIdx.x >> 5, sub = (threadIdx.x & 31) / LANES;
+  QkLane<LANES, INTER> lane(a);
+  const float inv_dim = 1.f / a.dim;
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const int heads = which ? a.heads[1] : a.heads[0], parts = (heads + AT_ONCE - 1) / AT_ONCE;
+    const int64_t items = static_cast<int64_t>(a.tokens) * parts;
+    const int64_t xst = which ? a.xst[1] : a.xst[0], dst = which ? a.dst[1] : a.dst[0], ost = which ? a.ost[1] : a.ost[0];
+    const int64_t xsh = which ? a.xsh[1] : a.xsh[0], dsh = which ? a.dsh[1] : a.dsh[0], osh = which ? a.osh[1] : a.osh[0];
+    const uint16_t* x = which ? a.x[1] : a.x[0];
+    const uint16_t* dy = which ? a.dy[1] : a.dy[0];
+    uint16_t* dx = which ? a.out[1] : a.out[0];
+    float w[8], dw[8] = {};
+    if (items) lane.template weights<F16>(w, a, which);
+    for (int64_t item = static_cast<int64_t>(blockIdx.x) * WARPS + warp; item < items; item += static_cast<int64_t>(gridDim.x) * WARPS) {
+      const int token = static_cast<int>(item / parts), h0 = static_cast<int>(item - static_cast<int64_t>(token) * parts) * AT_ONCE + sub;
+      const int p = qk_position(a, token);
+      uint2 v[HEADS][2], u[HEADS][2];
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
+      for (int i = 0; i < HEADS; ++i) {
+        const int h = h0 + i * ROWS;
+        lane.load(v[i], x + token * xst + h * xsh, h < heads);
+        lane.load(u[i], dy + token * dst + h * dsh, h < heads);
+      }
+      lane.angles(a, max(p, 0));
+#pragma unroll
+      for (int i = 0; i < HEADS; ++i) {
+        const int h = h0 + i * ROWS;
+        float f[8], g[8], sum = 0.f, dot = 0.f;
+        qk_unpack8<F16>(f, v[i]);
+        qk_unpack8<F16>(g, u[i]);
+        lane.template turn<true>(g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          sum = fmaf(f[j], f[j], sum);
+          dot = fmaf(g[j] * w[j], f[j], dot);
+        }
+        const float r = rsqrtf(fmaf(qk_sum<LANES>(sum), inv_dim, a.eps));
+        const float mean = qk_sum<LANES>(dot) * r * inv_dim;
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float xh = f[j] * r;
+          o[j] = p < 0 ? 0.f : r * fmaf(g[j], w[j], -xh * mean);
+          if (p >= 0 && h < heads) dw[j] = fmaf(g[j], xh, dw[j]);
+        }
+        lane.template store<F16>(dx + token * ost + h * osh, o, h < heads);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
 #pragma unroll
-      for (int o = LANES; o < 32; o <<= 1) dw[k][j] += __shfl_xor_sync(0xFFFFFFFFu, dw[k][j], o);
-      if (sub == 0) sums[warp][k][lane.col + j] = dw[k][j];
+      for (int o = LANES; o < 32; o <<= 1) dw[j] += __shfl_xor_sync(0xFFFFFFFFu, dw[j], o);
+      if (sub == 0 && lane.on) sums[warp][which][lane.at[j / 4] + j % 4] = dw[j];
     }
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * a.dim; i += kQkThreads) {
     const int k = i >= a.dim, d = k ? i - a.dim : i;

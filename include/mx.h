@@ -505,7 +505,7 @@ mx_status kv_attention(const void* q, mx_half type, int64_t num_tokens, int64_t 
  * contiguous, token and head strides (in elements) multiples of 8: slices of a fused projection will do.  kv_heads may
  * be 0 (k, k_weight and k_out NULL then).  head_dim is a multiple of 8, at most 256.  Outputs have strides of their own
  * and may be the inputs themselves (same address and strides); they may not overlap them otherwise.
- * q_weight, k_weight [head_dim]: x's type, or FP32 with weight_f32 = 1.
+ * q_weight, k_weight [head_dim], 16-byte aligned: x's type, or FP32 with weight_f32 = 1.
  * cos_sin float [max_positions][rot_dim], 16-byte aligned: rot_dim / 2 cosines of a position's angles, then their sines.
  * R turns the first rot_dim values of a head (a multiple of 16; 0: none, and cos_sin may be NULL), as pairs
  * (i, rot_dim / 2 + i), or (2i, 2i + 1) with interleaved = 1: (a, b) -> (a cos - b sin, b cos + a sin).

@@ -67,14 +67,19 @@ mx_status kv_few_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_len
 }
 
 template <int FMT, int D, bool F16, bool TREE>
+constexpr auto kv_many_kernel() {
+  if constexpr (TREE) return kv_tree_many_kernel<FMT, D, F16>;
+  else return kv_attention_many_kernel<FMT, D, F16>;
+}
+template <int FMT, int D, bool F16, bool TREE>
 mx_status kv_many_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_len, void* workspace, cudaStream_t st) {
-  using Cfg = KvManyCfg<D>;
-  auto kern = kv_attention_many_kernel<FMT, D, F16, TREE>;
+  constexpr int kSmem = TREE ? KvTreeCfg<D>::SMEM : KvManyCfg<D>::SMEM;
+  auto kern = kv_many_kernel<FMT, D, F16, TREE>();
   static std::atomic<bool> attr_set[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MX_ERR_CUDA;
   if (!attr_set[dev].load(std::memory_order_relaxed)) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM) != cudaSuccess)
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
       return MX_ERR_CUDA;
     attr_set[dev].store(true, std::memory_order_relaxed);
   }
@@ -90,7 +95,7 @@ mx_status kv_many_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_le
   // up to a request a thread, of up to 32 units, the kernel plans for itself
   const int planned = a.requests > kKvManyThreads || max_q_len * (a.heads / a.kv_heads) > 32 * kKvManyRows;
   if (planned && pdl_launch(kv_plan_kernel<TREE>, 1, kKvPlanThreads, 0, st, a, most_q, n, ws) != cudaSuccess) return MX_ERR_CUDA;
-  if (pdl_launch(kern, n, kKvManyThreads, Cfg::SMEM, st, tk, tv, a, most_q, planned, ws) != cudaSuccess)
+  if (pdl_launch(kern, n, kKvManyThreads, kSmem, st, tk, tv, a, most_q, planned, ws) != cudaSuccess)
     return MX_ERR_CUDA;
   if (n > 1 && pdl_launch(kv_join_kernel<D>, dim3(n - 1, 16), 128, 0, st, a, static_cast<const uint8_t*>(ws),
                           kv_many_slots_at(a.requests, D)) != cudaSuccess)

@@ -314,23 +314,7 @@ __device__ __noinline__ void kv_fill_box(uint8_t* to, int bytes, uint32_t four) 
   fence_proxy_async_smem();  // (a copy may come to the same place next)
 }
 
-// Which of the 16 tokens from t on a row of a tree sees, as bits: `nodes` is its row of the mask (null: none of the nodes),
-// first the first token that it sees of those in front of the nodes, n how many nodes there are.
-__device__ __forceinline__ uint32_t kv_tree_sees16(const uint64_t* nodes, int words, int n, int context, int first, int t) {
-  const int o = t - context;
-  uint32_t b = 0xFFFFu;
-  if (o > -16) {
-    const int w = o >> 6, sh = o & 63;  // (w = -1: what is in front of the nodes)
-    const uint64_t at = w < 0 ? ~0ull : nodes && w < words ? nodes[w] : 0;
-    const uint64_t behind = sh > 48 && nodes && w + 1 < words ? nodes[w + 1] : 0;
-    b &= static_cast<uint32_t>(at >> sh) | (sh > 48 ? static_cast<uint32_t>(behind << (64 - sh)) : 0);
-    if (n - o < 16) b &= (1u << max(n - o, 0)) - 1;
-  }
-  if (first > t) b &= ~0u << min(first - t, 16);
-  return b;
-}
-
-template <int FMT, int D, bool F16, bool TREE>
+template <int FMT, int D, bool F16>
 __global__ void __launch_bounds__(kKvManyThreads, 1)
     kv_attention_many_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                              const KvAttnArgs a, int most_q, int planned, uint8_t* workspace) {
@@ -406,10 +390,10 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
     KvRequest req{};
     long long mine = 0;
     if (tid < a.requests) {
-      req = kv_request<TREE>(a, tid, most_q, blockIdx.x == 0);
+      req = kv_request<false>(a, tid, most_q, blockIdx.x == 0);
       const int units = kv_units_of(req, group);
 #pragma unroll 1
-      for (int i = 0; i < units; ++i) mine += kv_unit<TREE>(a, req, group, i).cost();
+      for (int i = 0; i < units; ++i) mine += kv_unit<false>(a, req, group, i).cost();
     }
     mine *= a.kv_heads;
     long long incl = mine;
@@ -428,7 +412,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
     }
     KvJob mine_job{kv_cut(total, blockIdx.x, gridDim.x), kv_cut(total, blockIdx.x + 1, gridDim.x), 0, 0, 0, 0, 0, 0, 0, 0};
     const bool here = mine_job.begin >= before && mine_job.begin < before + mine;
-    if (here) kv_first_unit<TREE>(a, req, tid, group, before, mine_job);
+    if (here) kv_first_unit<false>(a, req, tid, group, before, mine_job);
     if (here || (total == 0 && tid == 0)) {
       job = mine_job;
       reinterpret_cast<KvJob*>(workspace + kKvJobsAt)[blockIdx.x] = mine_job;
@@ -452,14 +436,14 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
   if (warp == 12) {
     // ------------------------------------------------------------------ loads: item 2i = K, 2i + 1 = V of tile i
     KvManyWalk w;
-    kv_many_begin<TREE>(a, most_q, group, job, w);
+    kv_many_begin<false>(a, most_q, group, job, w);
     const long long range_start = w.pos;
     const int P = 1 << a.shift, rows_box = min(P, kKvTile), boxes = kKvManyTile / rows_box;
     const int most_tiles = 32 * P / kKvManyTile;
     uint32_t tiles_done = 0, issued = 0;  // issued: items, for the end (a wait that gives up may leave a tile's second out)
     bool ok = true;
     while (ok) {
-      const bool more = kv_many_next<TREE>(a, most_q, group, w);
+      const bool more = kv_many_next<false>(a, most_q, group, w);
       const uint32_t sl = seg % kKvManySegments;
       if (!kv_wait(&seg_empty[sl], ((seg / kKvManySegments) & 1) ^ 1, abort_flag, kSiteProducerEmpty)) break;
       if (lane == 0) {
@@ -746,10 +730,8 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
       const int my_row = single ? row : 128 * half + row;
       const bool live = my_row < v.rows;
       const int qi = (v.row0 + my_row) / group, hg = v.row0 + my_row - qi * group;
-      const int context = v.len - v.rows_q, p = context + qi;
-      const uint64_t* nodes = TREE && live ? a.tree_mask + static_cast<int64_t>(v.q0 + qi) * a.tree_words : nullptr;
-      const int lo = TREE ? (live ? kv_tree_first(a, v.q0 + qi, context, v.rows_q) : 0) : a.window ? max(0, p - a.window + 1) : 0;
-      const int hi = TREE ? context : a.causal ? min(v.len, p + 1) : v.len;
+      const int p = v.len - v.rows_q + qi;
+      const int lo = a.window ? max(0, p - a.window + 1) : 0, hi = a.causal ? min(v.len, p + 1) : v.len;
       const uint32_t width = static_cast<uint32_t>(max(hi - lo, 0));
       const int first = single ? half : 0;
       float m = -INFINITY, l = 0.f;
@@ -775,16 +757,9 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
             tmem_ld_32x32b_x16(tS + 16 * g, x);
             tmem_ld_wait();
             tmem_regs_ready16(x);
-            if (TREE) {
-              const uint32_t seen = kv_tree_sees16(nodes, a.tree_words, v.rows_q, context, lo, t);
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (!(seen >> j & 1)) x[j] = 0xFF800000u;
-            } else {
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (static_cast<uint32_t>(token + 16 * g + j - lo) >= width) x[j] = 0xFF800000u;
-            }
+            for (int j = 0; j < 16; ++j)
+              if (static_cast<uint32_t>(token + 16 * g + j - lo) >= width) x[j] = 0xFF800000u;
             tmem_st_32x32b_x16(tS + 16 * g, x);
           }
           tmem_st_wait();
@@ -867,9 +842,8 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
           ok = kv_wait(&f_full[v_item % Cfg::F16_SLOTS], (v_item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteEpiTmemFull);
           if (!ok) break;
           if (sNan[st]) {
-            const int j0 = max(lo - token, 0), j1 = min((TREE ? v.len : hi) - token, kKvManyTile);
+            const int j0 = max(lo - token, 0), j1 = min(hi - token, kKvManyTile);
             for (int j = j0; j < j1; ++j) {
-              if (TREE && !(kv_tree_sees16(nodes, a.tree_words, v.rows_q, context, lo, token + j) & 1)) continue;
               const volatile uint32_t* note =
                   reinterpret_cast<const volatile uint32_t*>(nan_notes + ((tile & 3) * kKvManyTile + j) * (D / 8));
 #pragma unroll

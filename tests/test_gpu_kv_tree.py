@@ -143,13 +143,17 @@ def test_nan_reaches_the_rows_that_see_it(nodes, elem):
 @pytest.mark.parametrize("nodes", [[3, 4, 2, 1], [40, 17, 64, 5], [130, 1, 0, 200]])
 @pytest.mark.parametrize("window", [0, 70])
 def test_a_chain_is_a_draft(nodes, window):
-    """Bit by bit what kv_attention gives for the same tokens in a row."""
+    """What kv_attention gives for the same tokens in a row: bit by bit where the same kernel does both (up to 16 rows a
+    kv head), else both within the formula's tolerance."""
     a = inputs([50, 64, 0, 300], nodes, 64, 2, 4, 128, mx.E4M3, reach=1, window=window, pad=2)
     got = call(a)
     want = mx.kv_attention(a["q"].cuda(), *(gpu(c) for c in a["codes"]), *(gpu(s) for s in a["scales"]), gpu(a["tables"]),
                            gpu(a["lengths"]), gpu(a["q_start"]), a["most"], window=window)
     ok()
-    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    if max(nodes) <= 4:
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    check(a, got)
+    check(a, want)
 
 
 @pytest.mark.parametrize("nodes", [[3, 4, 2], [40, 17, 64]])

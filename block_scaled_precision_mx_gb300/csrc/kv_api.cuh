@@ -66,20 +66,15 @@ mx_status kv_few_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_len
   return launch_status();
 }
 
-template <int FMT, int D, bool F16, bool TREE>
-constexpr auto kv_many_kernel() {
-  if constexpr (TREE) return kv_tree_many_kernel<FMT, D, F16>;
-  else return kv_attention_many_kernel<FMT, D, F16>;
-}
-template <int FMT, int D, bool F16, bool TREE>
+template <int FMT, int D, bool F16, bool TREE, bool ONE>
 mx_status kv_many_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_len, void* workspace, cudaStream_t st) {
-  constexpr int kSmem = TREE ? KvTreeCfg<D>::SMEM : KvManyCfg<D>::SMEM;
-  auto kern = kv_many_kernel<FMT, D, F16, TREE>();
+  using Cfg = KvManyCfg<D, TREE, ONE>;
+  auto kern = kv_attention_many_kernel<FMT, D, F16, TREE, ONE>;
   static std::atomic<bool> attr_set[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MX_ERR_CUDA;
   if (!attr_set[dev].load(std::memory_order_relaxed)) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM) != cudaSuccess)
       return MX_ERR_CUDA;
     attr_set[dev].store(true, std::memory_order_relaxed);
   }
@@ -95,7 +90,7 @@ mx_status kv_many_launch(const KvAttnArgs& a, int block_tokens, int64_t max_q_le
   // up to a request a thread, of up to 32 units, the kernel plans for itself
   const int planned = a.requests > kKvManyThreads || max_q_len * (a.heads / a.kv_heads) > 32 * kKvManyRows;
   if (planned && pdl_launch(kv_plan_kernel<TREE>, 1, kKvPlanThreads, 0, st, a, most_q, n, ws) != cudaSuccess) return MX_ERR_CUDA;
-  if (pdl_launch(kern, n, kKvManyThreads, kSmem, st, tk, tv, a, most_q, planned, ws) != cudaSuccess)
+  if (pdl_launch(kern, n, kKvManyThreads, Cfg::SMEM, st, tk, tv, a, most_q, planned, ws) != cudaSuccess)
     return MX_ERR_CUDA;
   if (n > 1 && pdl_launch(kv_join_kernel<D>, dim3(n - 1, 16), 128, 0, st, a, static_cast<const uint8_t*>(ws),
                           kv_many_slots_at(a.requests, D)) != cudaSuccess)
@@ -109,8 +104,12 @@ mx_status kv_attention_launch(const KvAttnArgs& a, int block_tokens, int64_t max
     case 1: return kv_few_launch<FMT, D, 1, TREE>(a, block_tokens, max_q_len, workspace, st);
     case 2: return kv_few_launch<FMT, D, 2, TREE>(a, block_tokens, max_q_len, workspace, st);
   }
-  return a.f16 ? kv_many_launch<FMT, D, true, TREE>(a, block_tokens, max_q_len, workspace, st)
-               : kv_many_launch<FMT, D, false, TREE>(a, block_tokens, max_q_len, workspace, st);
+  if constexpr (TREE && D == 128)  // (D = 64 has room for its buffers in either case)
+    if (max_q_len * (a.heads / a.kv_heads) <= 128)
+      return a.f16 ? kv_many_launch<FMT, D, true, TREE, true>(a, block_tokens, max_q_len, workspace, st)
+                   : kv_many_launch<FMT, D, false, TREE, true>(a, block_tokens, max_q_len, workspace, st);
+  return a.f16 ? kv_many_launch<FMT, D, true, TREE, false>(a, block_tokens, max_q_len, workspace, st)
+               : kv_many_launch<FMT, D, false, TREE, false>(a, block_tokens, max_q_len, workspace, st);
 }
 
 // A group of W warps holds a block's values of one head, 4 words of 8 a thread, or 8 where 8 warps would

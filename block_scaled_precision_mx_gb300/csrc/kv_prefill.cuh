@@ -39,7 +39,6 @@ namespace mxgb {
 constexpr int kKvManyThreads = 512;
 constexpr int kKvManyTile = 128;
 constexpr int kKvManyRows = 256;
-constexpr int kKvManyScales = 8;  // tiles whose scales are kept
 constexpr int kKvPlanThreads = 512;
 constexpr int kKvManyMaxCtas = 160;
 
@@ -54,21 +53,30 @@ struct alignas(16) KvSegment {
 static_assert(sizeof(KvSegment) <= 64, "a segment's place in shared memory");
 constexpr int kKvManySegments = 4;
 
-template <int D>
+// TREE: a tree's rows, few for many tokens, so that a tile's way through the CTA counts: three groups of warps convert items
+// in turn, D = 64 has twice the buffers, and of one row half K and V come in the order of the products (32 trees of 16 to
+// 32 nodes, 4 query heads, up to 4096 tokens: 87 us without all that, 76 with it).  ONE: no unit has more than 128 rows, so that the place of the other half's queries is free.
+template <int D, bool TREE, bool ONE>
 struct KvManyCfg {
-  static constexpr int RAW_SLOTS = 4, F16_SLOTS = 3;
+  static constexpr int RAW_SLOTS = !TREE ? 4 : D == 64 ? 8 : ONE ? 6 : 4, F16_SLOTS = TREE && D == 64 ? 6 : 3;
+  // Tiles whose scales are kept: a tile's are written when its codes have a place, so RAW_SLOTS + F16_SLOTS items behind
+  // what the products have done with; two more tiles may be under a softmax.
+  static constexpr int SCALES = TREE && D == 64 ? 16 : 8;
+  static_assert(SCALES >= (RAW_SLOTS + F16_SLOTS + 1) / 2 + 3, "scales");
   static constexpr int RAW = kKvManyTile * D;      // codes of K or V of a tile
   static constexpr int WIDE = 2 * RAW;             // the same in FP16; also 128 rows of Q
-  static constexpr int OFF_F16 = 2 * WIDE;
+  static constexpr int OFF_F16 = (ONE ? 1 : 2) * WIDE;
   static constexpr int OFF_RAW = OFF_F16 + F16_SLOTS * WIDE;
   static constexpr int OFF_SC = OFF_RAW + RAW_SLOTS * RAW;          // float2 [tiles][8 slices]: sK, log2 sV
-  static constexpr int OFF_MUL = OFF_SC + kKvManyScales * 8 * 8;    // float [128], for one row half
+  static constexpr int OFF_MUL = OFF_SC + SCALES * 8 * 8;    // float [128], for one row half
   static constexpr int OFF_NAN = OFF_MUL + 4 * 128;                 // int [tiles]
-  static constexpr int OFF_BAR = OFF_NAN + 4 * kKvManyScales;
-  static constexpr int BARS = 2 * RAW_SLOTS + 2 * F16_SLOTS + 4 * 2 + kKvManyScales + 2 * kKvManySegments + 3;
+  static constexpr int OFF_BAR = OFF_NAN + 4 * SCALES;
+  static constexpr int BARS = 2 * RAW_SLOTS + 2 * F16_SLOTS + 4 * 2 + SCALES + 2 * kKvManySegments + 3;
   static constexpr int OFF_SEG = (OFF_BAR + 8 * BARS + 15) / 16 * 16;  // KvSegment [segments]
   static constexpr int SMEM = OFF_SEG + 64 * kKvManySegments + 16 + 1024;
   static constexpr size_t SLOT = static_cast<size_t>(kKvManyRows) * (D + 2) * 4;
+  // warps that convert an item, and how many such groups there are
+  static constexpr int CONVERT = TREE ? 2 : 4, GROUPS = TREE ? 3 : 1;
   static constexpr size_t NAN_BYTES = 4 * kKvManyTile * (D / 8);    // u16 [4 tiles][128 tokens][D / 16] a CTA
 };
 
@@ -308,17 +316,46 @@ __device__ __forceinline__ uint64_t kv_add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// The items of a segment of n tiles, in the order in which the products take them: K and V of each tile; of a tree's one
+// row half, whose halves take alternate tiles, K0 K1 V0 K2 V1 .. V(n-1), so that a K's buffer is that of the V two
+// tiles before the one whose product comes first.
+__device__ __forceinline__ uint32_t kv_item_k(bool apart, uint32_t tile) { return apart && tile ? 2 * tile - 1 : 2 * tile; }
+__device__ __forceinline__ uint32_t kv_item_v(bool apart, uint32_t tile, uint32_t n) {
+  return apart && tile + 1 < n ? 2 * tile + 2 : 2 * tile + 1;
+}
+// the tile of item i, and whether it is a V
+__device__ __forceinline__ uint32_t kv_item_tile(bool apart, uint32_t i, uint32_t n, bool& is_v) {
+  is_v = apart ? i == 2 * n - 1 || (i && !(i & 1)) : i & 1;
+  return !apart || i == 2 * n - 1 ? i >> 1 : is_v ? (i >> 1) - 1 : (i + 1) >> 1;
+}
+
 // One lane's box of codes in place of a load.  (Rare.)
 __device__ __noinline__ void kv_fill_box(uint8_t* to, int bytes, uint32_t four) {
   for (int i = 0; i < bytes; i += 16) *reinterpret_cast<uint4*>(to + i) = make_uint4(four, four, four, four);
   fence_proxy_async_smem();  // (a copy may come to the same place next)
 }
 
-template <int FMT, int D, bool F16>
+// Which of the 16 tokens from t on a row of a tree sees, as bits: `nodes` is its row of the mask (null: none of the nodes),
+// first the first token that it sees of those in front of the nodes, n how many nodes there are.
+__device__ __forceinline__ uint32_t kv_tree_sees16(const uint64_t* nodes, int words, int n, int context, int first, int t) {
+  const int o = t - context;
+  uint32_t b = 0xFFFFu;
+  if (o > -16) {
+    const int w = o >> 6, sh = o & 63;  // (w = -1: what is in front of the nodes)
+    const uint64_t at = w < 0 ? ~0ull : nodes && w < words ? nodes[w] : 0;
+    const uint64_t behind = sh > 48 && nodes && w + 1 < words ? nodes[w + 1] : 0;
+    b &= static_cast<uint32_t>(at >> sh) | (sh > 48 ? static_cast<uint32_t>(behind << (64 - sh)) : 0);
+    if (n - o < 16) b &= (1u << max(n - o, 0)) - 1;
+  }
+  if (first > t) b &= ~0u << min(first - t, 16);
+  return b;
+}
+
+template <int FMT, int D, bool F16, bool TREE, bool ONE>
 __global__ void __launch_bounds__(kKvManyThreads, 1)
     kv_attention_many_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                              const KvAttnArgs a, int most_q, int planned, uint8_t* workspace) {
-  using Cfg = KvManyCfg<D>;
+  using Cfg = KvManyCfg<D, TREE, ONE>;
   extern __shared__ uint8_t kv_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(kv_smem_raw) + 1023) & ~uintptr_t(1023));
   float2* sSC = reinterpret_cast<float2*>(smem + Cfg::OFF_SC);
@@ -333,8 +370,8 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
   uint64_t* s_full = q_full + 2;
   uint64_t* p_full = s_full + 2;
   uint64_t* o_full = p_full + 2;
-  uint64_t* sc_full = o_full + 2;               // [kKvManyScales]
-  uint64_t* seg_full = sc_full + kKvManyScales; // [kKvManySegments]
+  uint64_t* sc_full = o_full + 2;               // [Cfg::SCALES]
+  uint64_t* seg_full = sc_full + Cfg::SCALES; // [kKvManySegments]
   uint64_t* seg_empty = seg_full + kKvManySegments;
   uint64_t* join_full = seg_empty + kKvManySegments;
   uint64_t* join_empty = join_full + 1;
@@ -346,10 +383,10 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < Cfg::RAW_SLOTS; ++i) {
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], 4);
+      mbar_init(&raw_empty[i], Cfg::CONVERT);
     }
     for (int i = 0; i < Cfg::F16_SLOTS; ++i) {
-      mbar_init(&f_full[i], 4);
+      mbar_init(&f_full[i], Cfg::CONVERT);
       mbar_init(&f_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -358,10 +395,10 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
       mbar_init(&p_full[i], 4);
       mbar_init(&o_full[i], 1);
     }
-    for (int i = 0; i < kKvManyScales; ++i) mbar_init(&sc_full[i], 1);
+    for (int i = 0; i < Cfg::SCALES; ++i) mbar_init(&sc_full[i], 1);
     for (int i = 0; i < kKvManySegments; ++i) {
       mbar_init(&seg_full[i], 1);
-      mbar_init(&seg_empty[i], 13);  // warps 0-11 and 13
+      mbar_init(&seg_empty[i], 9 + Cfg::CONVERT * Cfg::GROUPS);  // all that walk the segments but the loading warp
     }
     mbar_init(join_full, 4);
     mbar_init(join_empty, 4);
@@ -390,10 +427,10 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
     KvRequest req{};
     long long mine = 0;
     if (tid < a.requests) {
-      req = kv_request<false>(a, tid, most_q, blockIdx.x == 0);
+      req = kv_request<TREE>(a, tid, most_q, blockIdx.x == 0);
       const int units = kv_units_of(req, group);
 #pragma unroll 1
-      for (int i = 0; i < units; ++i) mine += kv_unit<false>(a, req, group, i).cost();
+      for (int i = 0; i < units; ++i) mine += kv_unit<TREE>(a, req, group, i).cost();
     }
     mine *= a.kv_heads;
     long long incl = mine;
@@ -412,7 +449,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
     }
     KvJob mine_job{kv_cut(total, blockIdx.x, gridDim.x), kv_cut(total, blockIdx.x + 1, gridDim.x), 0, 0, 0, 0, 0, 0, 0, 0};
     const bool here = mine_job.begin >= before && mine_job.begin < before + mine;
-    if (here) kv_first_unit<false>(a, req, tid, group, before, mine_job);
+    if (here) kv_first_unit<TREE>(a, req, tid, group, before, mine_job);
     if (here || (total == 0 && tid == 0)) {
       job = mine_job;
       reinterpret_cast<KvJob*>(workspace + kKvJobsAt)[blockIdx.x] = mine_job;
@@ -434,16 +471,35 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
   };
 
   if (warp == 12) {
-    // ------------------------------------------------------------------ loads: item 2i = K, 2i + 1 = V of tile i
+    // ------------------------------------------------------------------ loads
     KvManyWalk w;
-    kv_many_begin<false>(a, most_q, group, job, w);
+    kv_many_begin<TREE>(a, most_q, group, job, w);
     const long long range_start = w.pos;
     const int P = 1 << a.shift, rows_box = min(P, kKvTile), boxes = kKvManyTile / rows_box;
     const int most_tiles = 32 * P / kKvManyTile;
-    uint32_t tiles_done = 0, issued = 0;  // issued: items, for the end (a wait that gives up may leave a tile's second out)
-    bool ok = true;
+    uint32_t tiles_done = 0, issued = 0;  // issued: items
+    int row_before = -1, take_before = 0;  // this lane's box of the tile before
+    bool ok = true, odd_before = false;
+    // the next item: this lane's box from `row` on (-1: none), or codes that are taken as something else
+    auto load_item = [&](int v, int row, int taken, bool odd) {
+      const uint32_t slot = issued % Cfg::RAW_SLOTS;
+      ok = kv_wait(&raw_empty[slot], ((issued / Cfg::RAW_SLOTS) & 1) ^ 1, abort_flag, kSiteProducerEmpty);
+      if (!ok) return false;
+      uint8_t* dst = smem + Cfg::OFF_RAW + slot * Cfg::RAW + lane * rows_box * D;
+      const bool load = lane < boxes && row >= 0 && !taken;
+      const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, load)) * rows_box * D;
+      if (odd) {
+        if (lane < boxes && taken) kv_fill_box(dst, rows_box * D, kv_four_taken(taken));
+        __syncwarp();
+      }
+      ++issued;
+      if (lane == 0) mbar_arrive_expect_tx(&raw_full[slot], bytes);
+      __syncwarp();
+      if (load) tma_load_2d(dst, v ? &tmV : &tmK, &raw_full[slot], 0, row);
+      return true;
+    };
     while (ok) {
-      const bool more = kv_many_next<false>(a, most_q, group, w);
+      const bool more = kv_many_next<TREE>(a, most_q, group, w);
       const uint32_t sl = seg % kKvManySegments;
       if (!kv_wait(&seg_empty[sl], ((seg / kKvManySegments) & 1) ^ 1, abort_flag, kSiteProducerEmpty)) break;
       if (lane == 0) {
@@ -472,34 +528,23 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
           const int box_take = odd ? __shfl_sync(0xFFFFFFFFu, take, box_at) : 0;
           const int slice = ((lane & 7) * 16) >> a.shift;
           const float slice_k = __shfl_sync(0xFFFFFFFFu, sk, from + slice), slice_v = __shfl_sync(0xFFFFFFFFu, sv, from + slice);
-#pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            const uint32_t item = 2 * tiles_done + half, slot = item % Cfg::RAW_SLOTS;
-            if (!kv_wait(&raw_empty[slot], ((item / Cfg::RAW_SLOTS) & 1) ^ 1, abort_flag, kSiteProducerEmpty)) {
-              ok = false;
-              break;
-            }
-            uint8_t* dst = smem + Cfg::OFF_RAW + slot * Cfg::RAW + lane * rows_box * D;
-            const int taken = half ? box_take >> 8 : box_take & 0xFF;
-            const bool load = lane < boxes && box_block >= 0 && !taken;
-            const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, load)) * rows_box * D;
-            if (odd) {
-              if (lane < boxes && taken) kv_fill_box(dst, rows_box * D, kv_four_taken(taken));
-              __syncwarp();
-            }
-            ++issued;
-            if (lane == 0) mbar_arrive_expect_tx(&raw_full[slot], bytes);
-            __syncwarp();
-            if (load)
-              tma_load_2d(dst, half ? &tmV : &tmK, &raw_full[slot], 0,
-                          ((box_block * a.kv_heads + w.h) << a.shift) + (my & (P - 1)));
-            if (half == 0) {
-              const uint32_t st = tiles_done % kKvManyScales;
-              if (lane < 8) sSC[st * 8 + lane] = make_float2(slice_k, log2f(slice_v));
-              if (lane == 0) sNan[st] = 0;
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sc_full[st]);
-            }
+          const int box_row = box_block >= 0 ? ((box_block * a.kv_heads + w.h) << a.shift) + (my & (P - 1)) : -1;
+          const bool apart = TREE && (ONE || w.u.rows <= 128), last = i0 + i + 1 == w.count;
+          // K of this tile; V of this one, or of the one before
+          if (!load_item(0, box_row, box_take & 0xFF, odd)) break;
+          const uint32_t st = tiles_done % Cfg::SCALES;
+          if (lane < 8) sSC[st * 8 + lane] = make_float2(slice_k, log2f(slice_v));
+          if (lane == 0) sNan[st] = 0;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sc_full[st]);
+          if (!apart) {
+            load_item(1, box_row, box_take >> 8, odd);
+          } else {
+            if (i0 + i) load_item(1, row_before, take_before, odd || odd_before);
+            if (last && ok) load_item(1, box_row, box_take >> 8, odd);
+            row_before = box_row;
+            take_before = box_take >> 8;
+            odd_before = odd;
           }
         }
       }
@@ -518,14 +563,14 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
     KvSegment v;
     while (ok && next_segment(v)) {
       const int count = __shfl_sync(0xFFFFFFFFu, v.count, 0);
-      const bool single = v.rows <= 128;
+      const bool single = ONE || v.rows <= 128, apart = TREE && single;
       const int steps = single ? count + 2 : 2 * (count + 1);
       for (int step = 0; step < steps && ok; ++step) {
         // half h: V of an earlier tile, then K of the next.  Two row halves: both take every tile; one: every second.
         const int h = step & 1, pv = single ? step - 2 : (step >> 1) - 1, sc = single ? step : step >> 1;
         const bool frees = single || h == 1;
         if (pv >= 0) {
-          const uint32_t item = 2 * (tiles_done + pv) + 1, slot = item % Cfg::F16_SLOTS;
+          const uint32_t item = 2 * tiles_done + kv_item_v(apart, pv, count), slot = item % Cfg::F16_SLOTS;
           ok = kv_wait(&f_full[slot], (item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteMmaFull) &&
                kv_wait(&p_full[h], weights[h]++ & 1, abort_flag, kSiteMmaTmemEmpty);
           if (!ok) break;
@@ -543,7 +588,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
           __syncwarp();
         }
         if (sc < count) {
-          const uint32_t item = 2 * (tiles_done + sc), slot = item % Cfg::F16_SLOTS;
+          const uint32_t item = 2 * tiles_done + kv_item_k(apart, sc), slot = item % Cfg::F16_SLOTS;
           ok = kv_wait(&f_full[slot], (item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteMmaFull);
           if (ok && sc == 0) ok = kv_wait(&q_full[h], segments[h]++ & 1, abort_flag, kSiteMmaFull);
           if (!ok) break;
@@ -570,17 +615,21 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
       mbar_drain(drain_bar, 0, kWaitBudgetNs);
     }
     __syncwarp();
-  } else if (warp >= 8 && warp < 12) {
+  } else if (warp >= 8 && warp < (TREE ? 16 : 12)) {
     // ------------------------------------------------------------------ codes -> FP16
     constexpr int CH = D / 16;  // 16-code words of a token
-    const int wq = warp - 8, tl = lane & 7;
+    constexpr int WORDS = CH * 4 / Cfg::CONVERT, STEP = TREE ? 4 : 2;  // words of a lane, and those taken at once
+    const int wq = (warp - 8) % Cfg::CONVERT, tl = lane & 7;
+    const uint32_t mine = warp < 12 ? (warp - 8) / Cfg::CONVERT : 2;  // warps 14 and 15 are the last group
     uint32_t tiles_done = 0;
     bool ok = true;
     KvSegment v;
     while (ok && next_segment(v)) {
       const uint32_t items = 2 * (tiles_done + v.count);
+      const bool apart = TREE && (ONE || v.rows <= 128);
 #pragma unroll 1
       for (uint32_t item = 2 * tiles_done; item < items; ++item) {
+        if (Cfg::GROUPS > 1 && item % Cfg::GROUPS != mine) continue;
         const uint32_t slot = item % Cfg::RAW_SLOTS, fs = item % Cfg::F16_SLOTS;
         ok = kv_wait(&raw_full[slot], (item / Cfg::RAW_SLOTS) & 1, abort_flag, kSiteMmaFull) &&
              kv_wait(&f_empty[fs], ((item / Cfg::F16_SLOTS) & 1) ^ 1, abort_flag, kSiteProducerEmpty);
@@ -589,17 +638,19 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
         uint8_t* dst = smem + Cfg::OFF_F16 + fs * Cfg::WIDE;
         // lane: row tl of 8, word lane / 8 of 4; D = 128 has two groups of 4 words
         auto raw_at = [&](int n, int& row, int& word) {
-          row = 32 * wq + 8 * (n / (CH / 4)) + tl;
+          row = 128 / Cfg::CONVERT * wq + 8 * (n / (CH / 4)) + tl;
           word = (n % (CH / 4)) * 4 + (lane >> 3);
           return reinterpret_cast<uint4*>(src + (D == 128 ? row * 128 + ((word ^ (row & 7)) << 4)
                                                           : row * 64 + ((word ^ ((row >> 1) & 3)) << 4)));
         };
-        const int token = v.token + static_cast<int>(item / 2 - tiles_done) * kKvManyTile;
-        if ((item & 1) && (token < v.all_lo || token + kKvManyTile > v.all_hi)) {
+        bool is_v;
+        const uint32_t nth = kv_item_tile(apart, item - 2 * tiles_done, v.count, is_v), tile = tiles_done + nth;
+        const int token = v.token + static_cast<int>(nth) * kKvManyTile;
+        if (is_v && (token < v.all_lo || token + kKvManyTile > v.all_hi)) {
           // V of a tile that some row does not see whole: clear what no row sees; take NaN codes out and note them
           uint32_t any = 0;
 #pragma unroll 1
-          for (int n = 0; n < CH; ++n) {
+          for (int n = 0; n < WORDS; ++n) {
             int row, word;
             uint4* at = raw_at(n, row, word);
             const uint4 x = *at;
@@ -613,20 +664,20 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
               bits |= ((y >> 7 & 1) | (y >> 14 & 2) | (y >> 21 & 4) | (y >> 28 & 8)) << (4 * j);
             }
             *at = make_uint4(c[0], c[1], c[2], c[3]);
-            reinterpret_cast<uint16_t*>(nan_notes)[((item / 2 & 3) * kKvManyTile + row) * CH + word] = static_cast<uint16_t>(bits);
+            reinterpret_cast<uint16_t*>(nan_notes)[((tile & 3) * kKvManyTile + row) * CH + word] = static_cast<uint16_t>(bits);
             any |= bits;
           }
-          if (any) sNan[item / 2 % kKvManyScales] = 1;
+          if (any) sNan[tile % Cfg::SCALES] = 1;
           __threadfence_block();
         }
 #pragma unroll 1
-        for (int n0 = 0; n0 < CH; n0 += 2) {
-          uint4 x[2];
-          int row[2], word[2];
+        for (int n0 = 0; n0 < WORDS; n0 += STEP) {
+          uint4 x[STEP];
+          int row[STEP], word[STEP];
 #pragma unroll
-          for (int n = 0; n < 2; ++n) x[n] = *raw_at(n0 + n, row[n], word[n]);
+          for (int n = 0; n < STEP; ++n) x[n] = *raw_at(n0 + n, row[n], word[n]);
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
+          for (int n = 0; n < STEP; ++n) {
             const uint32_t c[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
             uint32_t f[8];
 #pragma unroll
@@ -652,8 +703,6 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + half * 128 + lanes, tO = tmem + 256 + half * 128 + lanes;
     uint8_t* sQ = smem + half * Cfg::WIDE;
-    float2* join_ml = reinterpret_cast<float2*>(smem + Cfg::WIDE);          // one row half: half 1's (m, l) and NaN notes
-    uint32_t* join_nan = reinterpret_cast<uint32_t*>(smem + Cfg::WIDE + 1024);  // (where its queries would be)
     uint32_t tiles_done = 0, my_tiles = 0, segments = 0, joins = 0;
     uint32_t other_segments = 0;  // half 1's segments with tiles, as half 0 counts them
     bool ok = true;
@@ -662,7 +711,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
     // loops: code that runs once a segment is not in the instruction cache, and costs by its length.)
     auto bring = [&](const KvSegment& v) {
       constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;
-      const bool single = v.rows <= 128;
+      const bool single = ONE || v.rows <= 128;
       if (single && half == 1) {  // half 0 brings the rows of both
         ok = kv_wait(&q_full[0], (seg - 1) & 1, abort_flag, kSiteEpiTmemFull);
         return sMul[row];
@@ -726,12 +775,14 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
     bool more = next_segment(v);
     float row_mul = more ? bring(v) : 0.f;
     while (ok && more) {
-      const bool single = v.rows <= 128;  // both halves work on the same rows, on every second tile
+      const bool single = ONE || v.rows <= 128;  // both halves work on the same rows, on every second tile
       const int my_row = single ? row : 128 * half + row;
       const bool live = my_row < v.rows;
       const int qi = (v.row0 + my_row) / group, hg = v.row0 + my_row - qi * group;
-      const int p = v.len - v.rows_q + qi;
-      const int lo = a.window ? max(0, p - a.window + 1) : 0, hi = a.causal ? min(v.len, p + 1) : v.len;
+      const int context = v.len - v.rows_q, p = context + qi;
+      const uint64_t* nodes = TREE && live ? a.tree_mask + static_cast<int64_t>(v.q0 + qi) * a.tree_words : nullptr;
+      const int lo = TREE ? (live ? kv_tree_first(a, v.q0 + qi, context, v.rows_q) : 0) : a.window ? max(0, p - a.window + 1) : 0;
+      const int hi = TREE ? context : a.causal ? min(v.len, p + 1) : v.len;
       const uint32_t width = static_cast<uint32_t>(max(hi - lo, 0));
       const int first = single ? half : 0;
       float m = -INFINITY, l = 0.f;
@@ -741,8 +792,8 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
 #pragma unroll 1
       for (int i = first; i < v.count; i += single ? 2 : 1, ++my_tiles) {
         const int token = v.token + i * kKvManyTile;
-        const uint32_t tile = tiles_done + i, st = tile % kKvManyScales;
-        ok = kv_wait(&sc_full[st], (tile / kKvManyScales) & 1, abort_flag, kSiteEpiTmemFull) &&
+        const uint32_t tile = tiles_done + i, st = tile % Cfg::SCALES;
+        ok = kv_wait(&sc_full[st], (tile / Cfg::SCALES) & 1, abort_flag, kSiteEpiTmemFull) &&
              kv_wait(&s_full[half], my_tiles & 1, abort_flag, kSiteEpiTmemFull);
         if (!ok) break;
         tc_fence_after();
@@ -757,9 +808,16 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
             tmem_ld_32x32b_x16(tS + 16 * g, x);
             tmem_ld_wait();
             tmem_regs_ready16(x);
+            if (TREE) {
+              const uint32_t seen = kv_tree_sees16(nodes, a.tree_words, v.rows_q, context, lo, t);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (static_cast<uint32_t>(token + 16 * g + j - lo) >= width) x[j] = 0xFF800000u;
+              for (int j = 0; j < 16; ++j)
+                if (!(seen >> j & 1)) x[j] = 0xFF800000u;
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (static_cast<uint32_t>(token + 16 * g + j - lo) >= width) x[j] = 0xFF800000u;
+            }
             tmem_st_32x32b_x16(tS + 16 * g, x);
           }
           tmem_st_wait();
@@ -838,12 +896,13 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         if (edge) {  // NaN codes of V in tokens that this row sees
-          const uint32_t v_item = 2 * tile + 1;
+          const uint32_t v_item = 2 * tiles_done + kv_item_v(TREE && single, i, v.count);
           ok = kv_wait(&f_full[v_item % Cfg::F16_SLOTS], (v_item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteEpiTmemFull);
           if (!ok) break;
           if (sNan[st]) {
-            const int j0 = max(lo - token, 0), j1 = min(hi - token, kKvManyTile);
+            const int j0 = max(lo - token, 0), j1 = min((TREE ? v.len : hi) - token, kKvManyTile);
             for (int j = j0; j < j1; ++j) {
+              if (TREE && !(kv_tree_sees16(nodes, a.tree_words, v.rows_q, context, lo, token + j) & 1)) continue;
               const volatile uint32_t* note =
                   reinterpret_cast<const volatile uint32_t*>(nan_notes + ((tile & 3) * kKvManyTile + j) * (D / 8));
 #pragma unroll
@@ -867,9 +926,14 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
       if (!ok) break;
       tc_fence_after();
       if (single && half == 1) {
-        join_ml[row] = make_float2(m, l);
+        uint32_t told[16];  // (m, l) and the NaN notes, where its scores were
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) join_nan[row * (D / 32) + j] = nan_d[j];
+        for (int j = 0; j < 16; ++j) told[j] = j >= 2 && j < 2 + D / 32 ? nan_d[j >= 2 && j < 2 + D / 32 ? j - 2 : 0] : 0;
+        told[0] = __float_as_uint(m);
+        told[1] = __float_as_uint(l);
+        tmem_st_32x32b_x16(tS, told);
+        tmem_st_wait();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(join_full);
         ok = kv_wait(join_empty, joins++ & 1, abort_flag, kSiteEpiTmemFull);
@@ -878,14 +942,19 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
         if (single) {
           ok = kv_wait(join_full, joins++ & 1, abort_flag, kSiteEpiTmemFull);
           if (ok && v.count > 1) {
-            const float2 other = join_ml[row];
+            tc_fence_after();
+            uint32_t told[16];
+            tmem_ld_32x32b_x16(tmem + 128 + lanes, told);
+            tmem_ld_wait();
+            tmem_regs_ready16(told);
+            const float2 other = make_float2(__uint_as_float(told[0]), __uint_as_float(told[1]));
             const float most = fmaxf(m, other.x), ref = most == -INFINITY ? 0.f : most;
             f0 = kv_exp2(m - ref);
             f1 = kv_exp2(other.x - ref);
             l = l * f0 + other.y * f1;
             m = most;
 #pragma unroll
-            for (int j = 0; j < D / 32; ++j) nan_d[j] |= join_nan[row * (D / 32) + j];
+            for (int j = 0; j < D / 32; ++j) nan_d[j] |= told[2 + j];
           }
         }
         if (!ok) break;

@@ -19,7 +19,6 @@
 #include "kv_cache.cuh"
 #include "kv_drafts.cuh"
 #include "kv_prefill.cuh"
-#include "kv_tree.cuh"
 #include "qk_norm.cuh"
 
 using namespace mxgb;

@@ -71,7 +71,7 @@ struct KvManyCfg {
   static constexpr int OFF_MUL = OFF_SC + SCALES * 8 * 8;    // float [128], for one row half
   static constexpr int OFF_NAN = OFF_MUL + 4 * 128;                 // int [tiles]
   static constexpr int OFF_BAR = OFF_NAN + 4 * SCALES;
-  static constexpr int BARS = 2 * RAW_SLOTS + 2 * F16_SLOTS + 4 * 2 + SCALES + 2 * kKvManySegments + 3;
+  static constexpr int BARS = 2 * RAW_SLOTS + 2 * F16_SLOTS + 4 * 2 + SCALES + 2 * kKvManySegments + 4;
   static constexpr int OFF_SEG = (OFF_BAR + 8 * BARS + 15) / 16 * 16;  // KvSegment [segments]
   static constexpr int SMEM = OFF_SEG + 64 * kKvManySegments + 16 + 1024;
   static constexpr size_t SLOT = static_cast<size_t>(kKvManyRows) * (D + 2) * 4;
@@ -335,20 +335,29 @@ __device__ __noinline__ void kv_fill_box(uint8_t* to, int bytes, uint32_t four) 
   fence_proxy_async_smem();  // (a copy may come to the same place next)
 }
 
-// Which of the 16 tokens from t on a row of a tree sees, as bits: `nodes` is its row of the mask (null: none of the nodes),
-// first the first token that it sees of those in front of the nodes, n how many nodes there are.
-__device__ __forceinline__ uint32_t kv_tree_sees16(const uint64_t* nodes, int words, int n, int context, int first, int t) {
-  const int o = t - context;
-  uint32_t b = 0xFFFFu;
-  if (o > -16) {
-    const int w = o >> 6, sh = o & 63;  // (w = -1: what is in front of the nodes)
-    const uint64_t at = w < 0 ? ~0ull : nodes && w < words ? nodes[w] : 0;
-    const uint64_t behind = sh > 48 && nodes && w + 1 < words ? nodes[w + 1] : 0;
-    b &= static_cast<uint32_t>(at >> sh) | (sh > 48 ? static_cast<uint32_t>(behind << (64 - sh)) : 0);
-    if (n - o < 16) b &= (1u << max(n - o, 0)) - 1;
+// Which of a tile's 128 tokens, from `token` on, a row of a tree sees, as bits: `nodes` is its row of the mask (null: none of
+// the nodes), first the first token that it sees of those in front of the nodes, n how many nodes there are.
+struct KvTreeBits {
+  uint64_t b[2];
+};
+__device__ __forceinline__ KvTreeBits kv_tree_bits(const uint64_t* nodes, int words, int n, int context, int first, int token) {
+  const int o = token - context, w0 = o >> 6, sh = o & 63;
+  uint64_t x[3];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const int w = w0 + k, left = n - 64 * w;  // (w < 0: what is in front of the nodes)
+    uint64_t word = w < 0 ? ~0ull : 0;
+    if (w >= 0 && left > 0 && w < words && nodes) word = nodes[w] & (left < 64 ? (1ull << left) - 1 : ~0ull);
+    x[k] = word;
   }
-  if (first > t) b &= ~0u << min(first - t, 16);
-  return b;
+  KvTreeBits v;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    v.b[k] = sh ? x[k] >> sh | x[k + 1] << (64 - sh) : x[k];
+    const int hidden = first - token - 64 * k;
+    if (hidden > 0) v.b[k] = hidden < 64 ? v.b[k] & (~0ull << hidden) : 0;
+  }
+  return v;
 }
 
 template <int FMT, int D, bool F16, bool TREE, bool ONE>
@@ -376,6 +385,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
   uint64_t* join_full = seg_empty + kKvManySegments;
   uint64_t* join_empty = join_full + 1;
   uint64_t* drain_bar = join_empty + 1;
+  uint64_t* turn = drain_bar + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_SEG + 64 * kKvManySegments);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
@@ -403,6 +413,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
     mbar_init(join_full, 4);
     mbar_init(join_empty, 4);
     mbar_init(drain_bar, 1);
+    mbar_init(turn, 4);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&tmK);
@@ -702,28 +713,30 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
     const int half = warp >> 2, row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + half * 128 + lanes, tO = tmem + 256 + half * 128 + lanes;
-    uint8_t* sQ = smem + half * Cfg::WIDE;
     uint32_t tiles_done = 0, my_tiles = 0, segments = 0, joins = 0;
     uint32_t other_segments = 0;  // half 1's segments with tiles, as half 0 counts them
     bool ok = true;
     // A segment's queries as FP16; returns what this thread's row of scores is to be multiplied with.  The rows
     // are copied to their places as they are, D / 8 lanes a row, and converted there, a row a thread.  (Short
     // loops: code that runs once a segment is not in the instruction cache, and costs by its length.)
-    auto bring = [&](const KvSegment& v) {
+    // Of one row half `by` brings the rows of both.
+    auto bring = [&](const KvSegment& v, int by) {
       constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;
       const bool single = ONE || v.rows <= 128;
-      if (single && half == 1) {  // half 0 brings the rows of both
+      uint8_t* sQ = smem + (single ? 0 : half) * Cfg::WIDE;
+      const int rows_at = single ? 0 : half * 128;
+      if (single && half != by) {
         ok = kv_wait(&q_full[0], (seg - 1) & 1, abort_flag, kSiteEpiTmemFull);
         return sMul[row];
       }
       const int word = lane % LANES, sub = lane / LANES, row0 = 32 * (warp & 3);
-      int r = row0 + sub, qi = (v.row0 + half * 128 + r) / group, hg = v.row0 + half * 128 + r - qi * group;
+      int r = row0 + sub, qi = (v.row0 + rows_at + r) / group, hg = v.row0 + rows_at + r - qi * group;
       const int qi_step = AT_ONCE / group, hg_step = AT_ONCE % group;
       const uint32_t to = smem_u32(sQ) + (word >> 3) * (128 * 128);
 #pragma unroll 1
       for (; r < row0 + 32; r += AT_ONCE) {
         const uint16_t* src = a.q + (v.q0 + qi) * a.stride_t + (v.head * group + hg) * a.stride_h + 8 * word;
-        const uint32_t bytes = half * 128 + r < v.rows ? 16 : 0;  // (the rest of the 16 is zeros)
+        const uint32_t bytes = rows_at + r < v.rows ? 16 : 0;  // (the rest of the 16 is zeros)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + r * 128 + (((word & 7) ^ (r & 7)) << 4)),
                      "l"(bytes ? src : a.q), "r"(bytes)
                      : "memory");
@@ -768,12 +781,12 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
       if (single) sMul[row] = row_mul;
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[half]);
+      if (lane == 0) mbar_arrive(&q_full[single ? 0 : half]);
       return row_mul;
     };
     KvSegment v;
     bool more = next_segment(v);
-    float row_mul = more ? bring(v) : 0.f;
+    float row_mul = more ? bring(v, 0) : 0.f;
     while (ok && more) {
       const bool single = ONE || v.rows <= 128;  // both halves work on the same rows, on every second tile
       const int my_row = single ? row : 128 * half + row;
@@ -793,6 +806,9 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
       for (int i = first; i < v.count; i += single ? 2 : 1, ++my_tiles) {
         const int token = v.token + i * kKvManyTile;
         const uint32_t tile = tiles_done + i, st = tile % Cfg::SCALES;
+        KvTreeBits seen{};
+        if (TREE && (token < v.all_lo || token + kKvManyTile > v.all_hi))
+          seen = kv_tree_bits(nodes, a.tree_words, v.rows_q, context, lo, token);
         ok = kv_wait(&sc_full[st], (tile / Cfg::SCALES) & 1, abort_flag, kSiteEpiTmemFull) &&
              kv_wait(&s_full[half], my_tiles & 1, abort_flag, kSiteEpiTmemFull);
         if (!ok) break;
@@ -803,16 +819,16 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
 #pragma unroll 1
           for (int g = 0; g < 8; ++g) {
             const int t = token + 16 * g;
-            if (!__any_sync(0xFFFFFFFFu, t < lo || t + 16 > hi)) continue;
+            const uint32_t bits = static_cast<uint32_t>((g < 4 ? seen.b[0] : seen.b[1]) >> (16 * (g & 3))) & 0xFFFFu;
+            if (!__any_sync(0xFFFFFFFFu, TREE ? bits != 0xFFFFu : t < lo || t + 16 > hi)) continue;
             uint32_t x[16];
             tmem_ld_32x32b_x16(tS + 16 * g, x);
             tmem_ld_wait();
             tmem_regs_ready16(x);
             if (TREE) {
-              const uint32_t seen = kv_tree_sees16(nodes, a.tree_words, v.rows_q, context, lo, t);
 #pragma unroll
               for (int j = 0; j < 16; ++j)
-                if (!(seen >> j & 1)) x[j] = 0xFF800000u;
+                if (!(bits >> j & 1)) x[j] = 0xFF800000u;
             } else {
 #pragma unroll
               for (int j = 0; j < 16; ++j)
@@ -902,7 +918,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
           if (sNan[st]) {
             const int j0 = max(lo - token, 0), j1 = min((TREE ? v.len : hi) - token, kKvManyTile);
             for (int j = j0; j < j1; ++j) {
-              if (TREE && !(kv_tree_sees16(nodes, a.tree_words, v.rows_q, context, lo, token + j) & 1)) continue;
+              if (TREE && !((j < 64 ? seen.b[0] : seen.b[1]) >> (j & 63) & 1)) continue;
               const volatile uint32_t* note =
                   reinterpret_cast<const volatile uint32_t*>(nan_notes + ((tile & 3) * kKvManyTile + j) * (D / 8));
 #pragma unroll
@@ -920,7 +936,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
       // products with the present ones have ended: its last scores have come.)
       KvSegment next;
       more = next_segment(next);
-      if (more && !single) row_mul = bring(next);
+      if (more && !single) row_mul = bring(next, 0);
       const bool any = first < v.count;  // whether this half had a tile
       if (any) ok = kv_wait(&o_full[half], segments++ & 1, abort_flag, kSiteEpiTmemFull);
       if (!ok) break;
@@ -936,6 +952,11 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(join_full);
+        if (TREE) {  // while half 0 joins and writes
+          ok = kv_wait(turn, joins & 1, abort_flag, kSiteEpiTmemFull);
+          if (!ok) break;
+          if (more) row_mul = bring(next, 1);
+        }
         ok = kv_wait(join_empty, joins++ & 1, abort_flag, kSiteEpiTmemFull);
       } else {
         float f0 = 1.f, f1 = 0.f;  // O = f0 O_half + f1 O_1
@@ -955,6 +976,11 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
             m = most;
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) nan_d[j] |= told[2 + j];
+            tc_fence_before();
+          }
+          if (TREE) {  // half 1 may bring the next queries: the last scores with these have come, and it is read what it told
+            __syncwarp();
+            if (lane == 0) mbar_arrive(turn);
           }
         }
         if (!ok) break;
@@ -1015,7 +1041,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
         }
       }
       if (!ok) break;
-      if (more && single) row_mul = bring(next);
+      if (more && single && !(TREE && half == 1)) row_mul = bring(next, TREE ? 1 : 0);
       v = next;
     }
   }

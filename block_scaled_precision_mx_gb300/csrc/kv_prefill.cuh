@@ -77,10 +77,6 @@ struct KvManyCfg {
   static constexpr size_t SLOT = static_cast<size_t>(kKvManyRows) * (D + 2) * 4;
   // warps that convert an item, and how many such groups there are
   static constexpr int CONVERT = TREE ? 2 : 4, GROUPS = TREE ? 3 : 1;
-  // Where tensor memory has room (a tree's D = 64), weights have a place of their own: the next scores then come while
-  // their product with V runs, not behind it.
-  static constexpr bool APART = TREE && D == 64;
-  static constexpr int O_AT = 256, O_STEP = APART ? 64 : 128, P_AT = APART ? 384 : 0, P_STEP = APART ? 64 : 128;
   static constexpr size_t NAN_BYTES = 4 * kKvManyTile * (D / 8);    // u16 [4 tiles][128 tokens][D / 16] a CTA
 };
 
@@ -581,33 +577,32 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
       const bool single = ONE || v.rows <= 128, apart = TREE && single;
       const int steps = single ? count + 2 : 2 * (count + 1);
       for (int step = 0; step < steps && ok; ++step) {
-        // half h: V of an earlier tile, then K of the next (weights apart: the other way round).  Two row halves: both take
-        // every tile; one: every second.
+        // half h: V of an earlier tile, then K of the next.  Two row halves: both take every tile; one: every second.
         const int h = step & 1, pv = single ? step - 2 : (step >> 1) - 1, sc = single ? step : step >> 1;
         const bool frees = single || h == 1;
-        auto output = [&]() {
+        if (pv >= 0) {
           const uint32_t item = 2 * tiles_done + kv_item_v(apart, pv, count), slot = item % Cfg::F16_SLOTS;
           ok = kv_wait(&f_full[slot], (item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteMmaFull) &&
-               (Cfg::APART || kv_wait(&p_full[h], weights[h]++ & 1, abort_flag, kSiteMmaTmemEmpty));
-          if (!ok) return;
+               kv_wait(&p_full[h], weights[h]++ & 1, abort_flag, kSiteMmaTmemEmpty);
+          if (!ok) break;
           tc_fence_after();
           const uint32_t v_lo = __shfl_sync(0xFFFFFFFFu, (f_lo + slot * (Cfg::WIDE / 16)) | kLoN, 0);
           const bool first = single ? pv < 2 : pv == 0;
           if (kv_elect()) {
 #pragma unroll
             for (int k = 0; k < kKvManyTile / 16; ++k)  // O_h += P_h V, 16 tokens at a time
-              umma_f16_ts(tmem + Cfg::O_AT + h * Cfg::O_STEP, tmem + Cfg::P_AT + h * Cfg::P_STEP + k * 8,
-                          desc_from_words(v_lo + k * (16 * 128 / 16), kHi), kIdO, !first || k > 0);
-            if (Cfg::APART || pv >= count - (single ? 2 : 1)) umma_commit(&o_full[h]);
+              umma_f16_ts(tmem + 256 + h * 128, tmem + h * 128 + k * 8, desc_from_words(v_lo + k * (16 * 128 / 16), kHi), kIdO,
+                          !first || k > 0);
+            if (pv >= count - (single ? 2 : 1)) umma_commit(&o_full[h]);
             if (frees) umma_commit(&f_empty[slot]);
           }
           __syncwarp();
-        };
-        auto scores = [&]() {
+        }
+        if (sc < count) {
           const uint32_t item = 2 * tiles_done + kv_item_k(apart, sc), slot = item % Cfg::F16_SLOTS;
           ok = kv_wait(&f_full[slot], (item / Cfg::F16_SLOTS) & 1, abort_flag, kSiteMmaFull);
           if (ok && sc == 0) ok = kv_wait(&q_full[h], segments[h]++ & 1, abort_flag, kSiteMmaFull);
-          if (!ok) return;
+          if (!ok) break;
           tc_fence_after();
           const uint32_t k_lo = __shfl_sync(0xFFFFFFFFu, (f_lo + slot * (Cfg::WIDE / 16)) | kLoK, 0);
           const uint32_t qh_lo = q_lo + (single ? 0 : h) * (Cfg::WIDE / 16);
@@ -621,14 +616,6 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
             if (frees) umma_commit(&f_empty[slot]);
           }
           __syncwarp();
-        };
-        if (Cfg::APART) {
-          if (pv >= 0) ok = kv_wait(&p_full[h], weights[h]++ & 1, abort_flag, kSiteMmaTmemEmpty);  // (the scores have been read, too)
-          if (ok && sc < count) scores();
-          if (ok && pv >= 0) output();
-        } else {
-          if (pv >= 0) output();
-          if (ok && sc < count) scores();
         }
       }
       tiles_done += count;
@@ -725,8 +712,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
     // ------------------------------------------------------------------ softmax, a row a thread
     const int half = warp >> 2, row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + half * 128 + lanes, tO = tmem + Cfg::O_AT + half * Cfg::O_STEP + lanes;
-    const uint32_t tP = tmem + Cfg::P_AT + half * Cfg::P_STEP + lanes;
+    const uint32_t tS = tmem + half * 128 + lanes, tO = tmem + 256 + half * 128 + lanes;
     uint32_t tiles_done = 0, my_tiles = 0, segments = 0, joins = 0;
     uint32_t other_segments = 0;  // half 1's segments with tiles, as half 0 counts them
     bool ok = true;
@@ -876,11 +862,6 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
             most = fmaxf(most, fmaf(fmaxf(y0, y1), row_mul * sc.x, sc.y));
           }
         }
-        if (Cfg::APART && i > first) {  // the product with the weights before these has ended
-          ok = kv_wait(&o_full[half], segments++ & 1, abort_flag, kSiteEpiTmemFull);
-          if (!ok) break;
-          tc_fence_after();
-        }
         const bool past = most > m + 8.f;
         if (__any_sync(0xFFFFFFFFu, past)) {
           const float keep = past && m > -INFINITY ? kv_exp2(m - most) : 1.f;  // (at m = -inf O and l are 0, or NaN)
@@ -926,7 +907,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
             unpack_f32x2(kv_add2(sum2[0], sum2[1]), sum0, sum1);
             l = fmaf(sum0 + sum1, kv_exp2(-sc.y), l);
           }
-          tmem_st_32x32b_x16(tP + 16 * g, packed);
+          tmem_st_32x32b_x16(tS + 16 * g, packed);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -950,8 +931,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
       }
       if (!ok) break;
       tiles_done += v.count;
-      if (Cfg::APART) other_segments += single ? v.count / 2 : v.count;
-      else if (!single) ++other_segments;
+      if (!single) ++other_segments;
       // The queries of the next segment, so that its first products run under this one's output.  (This half's
       // products with the present ones have ended: its last scores have come.)
       KvSegment next;
@@ -1012,7 +992,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
         const int64_t at_row = static_cast<int64_t>(v.q0 + qi) * a.heads + v.head * group + hg;
         float* part = reinterpret_cast<float*>(workspace + kv_many_slots_at(a.requests, D) + (2 * blockIdx.x + max(v.part - 1, 0)) * Cfg::SLOT);
         if (two) {
-          ok = kv_wait(&o_full[1], (Cfg::APART ? other_segments - 1 : other_segments++) & 1, abort_flag, kSiteEpiTmemFull);
+          ok = kv_wait(&o_full[1], (other_segments++) & 1, abort_flag, kSiteEpiTmemFull);
           if (!ok) break;
           tc_fence_after();
         }
@@ -1026,7 +1006,7 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
 #pragma unroll
           for (int k = 0; k < 16; ++k) f[k] = __uint_as_float(o[k]) * f0;
           if (two) {
-            tmem_ld_32x32b_x16(tO + Cfg::O_STEP + 16 * j, o);
+            tmem_ld_32x32b_x16(tO + 128 + 16 * j, o);
             tmem_ld_wait();
             tmem_regs_ready16(o);
 #pragma unroll

@@ -16,7 +16,7 @@ bool kv_drafts_ok(const int32_t* q_start, int64_t requests, int64_t num_tokens, 
 }
 
 // ------------------------------------------------------------------ norm and rotation
-constexpr int kQkMaxCtas = 608;  // of the backward pass: four a SM
+constexpr int kQkCtas = 456, kQkBackCtas = 304;  // three and two a SM
 
 // What the two passes share: shapes, types, table, positions.  Rows' addresses and strides by qk_rows_ok.
 bool qk_norm_ok(mx_half type, int64_t num_tokens, int64_t heads, int64_t kv_heads, int head_dim, const void* q_weight,
@@ -25,6 +25,7 @@ bool qk_norm_ok(mx_half type, int64_t num_tokens, int64_t heads, int64_t kv_head
   if (type != MX_HALF_BF16 && type != MX_HALF_F16) return false;
   if (num_tokens < 0 || num_tokens > kKvMostTokens || heads < 1 || heads > 65535 || kv_heads < 0 || kv_heads > 65535)
     return false;
+  if (num_tokens * (heads + kv_heads) > 0x7FFFFFFF) return false;
   if (head_dim < 8 || head_dim > 256 || head_dim % 8) return false;
   if (!q_weight || (kv_heads && !k_weight) || (weight_f32 != 0 && weight_f32 != 1)) return false;
   if (!aligned(q_weight, 16) || !aligned(k_weight, 16)) return false;
@@ -42,18 +43,17 @@ mx_status qk_norm_launch_as(const QkNormArgs& a, cudaStream_t st, int64_t* ctas)
   constexpr int kAtOnce = 32 / LANES * HEADS;
   const int64_t parts = (a.heads[0] + kAtOnce - 1) / kAtOnce + (a.heads[1] + kAtOnce - 1) / kAtOnce;
   int64_t grid = (a.tokens * parts + kQkThreads / 32 - 1) / (kQkThreads / 32);
-  if (BACK) grid = grid < kQkMaxCtas ? grid : kQkMaxCtas;
-  else if (grid > 0x7FFFFFFF) return MX_ERR_INVALID_ARG;
+  constexpr int64_t kMost = BACK ? kQkBackCtas : kQkCtas;
+  if (grid > kMost) grid = kMost;
   if (ctas) *ctas = grid;
   const auto kern = BACK ? qk_norm_rope_backward_kernel<LANES, F16, INTER, HEADS> : qk_norm_rope_kernel<LANES, F16, INTER, HEADS>;
   return pdl_launch(kern, static_cast<unsigned>(grid), kQkThreads, 0, st, a) == cudaSuccess ? launch_status() : MX_ERR_CUDA;
 }
 template <bool BACK, bool F16, bool INTER>
 mx_status qk_norm_launch_with(const QkNormArgs& a, cudaStream_t st, int64_t* ctas) {
-  constexpr int kHeads = BACK ? 2 : 4;
-  return a.dim <= 64    ? qk_norm_launch_as<BACK, 8, F16, INTER, kHeads>(a, st, ctas)
-         : a.dim <= 128 ? qk_norm_launch_as<BACK, 16, F16, INTER, kHeads>(a, st, ctas)
-                        : qk_norm_launch_as<BACK, 32, F16, INTER, kHeads>(a, st, ctas);
+  return a.dim <= 64    ? qk_norm_launch_as<BACK, 8, F16, INTER, 4>(a, st, ctas)
+         : a.dim <= 128 ? qk_norm_launch_as<BACK, 16, F16, INTER, 4>(a, st, ctas)
+                        : qk_norm_launch_as<BACK, 32, F16, INTER, 4>(a, st, ctas);
 }
 template <bool BACK>
 mx_status qk_norm_launch(const QkNormArgs& a, bool f16, cudaStream_t st, int64_t* ctas) {
@@ -98,7 +98,7 @@ mx_status qk_norm_rope(const void* q, const void* k, mx_half type, int64_t num_t
 }
 
 size_t qk_norm_rope_workspace_bytes(int head_dim) {
-  return head_dim < 8 || head_dim > 256 || head_dim % 8 ? 0 : static_cast<size_t>(kQkMaxCtas) * 2 * head_dim * 4;
+  return head_dim < 8 || head_dim > 256 || head_dim % 8 ? 0 : static_cast<size_t>(kQkBackCtas) * 2 * head_dim * 4;
 }
 
 mx_status qk_norm_rope_backward(const void* dq_out, const void* dk_out, const void* q, const void* k, mx_half type,

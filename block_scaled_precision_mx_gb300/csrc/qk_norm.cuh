@@ -133,50 +133,70 @@ __device__ __forceinline__ int qk_position(const QkNormArgs& a, int token) {
   return -1;
 }
 
-// LANES lanes have a head's row; a warp takes HEADS * 32 / LANES heads of a token's queries or of its keys, all loads
-// first.  Memory is the bound.
+// LANES lanes have a head's row; a warp takes HEADS * 32 / LANES heads of a token's queries or of its keys at a time, and
+// the next ones' rows are on their way while it works on these.  Memory is the bound: 16384 tokens of 40 heads of 128
+// 63.7 us, 5.4 TB/s, 0.80 of the measured copy rate.  (Three CTAs a SM, 85 registers: two 71 us, four 73; without the rows
+// ahead, a warp an item, 76; two heads at a time 74 to 89, eight 70 to 83.)
 template <int LANES, bool F16, bool INTER, int HEADS>
-__global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkNormArgs a) {
+__global__ void __launch_bounds__(kQkThreads, 3) qk_norm_rope_kernel(const QkNormArgs a) {
   pdl_prologue();
   constexpr int ROWS = 32 / LANES, AT_ONCE = ROWS * HEADS;
   const int sub = (threadIdx.x & 31) / LANES;
   const int parts0 = (a.heads[0] + AT_ONCE - 1) / AT_ONCE, parts = parts0 + (a.heads[1] + AT_ONCE - 1) / AT_ONCE;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kQkThreads / 32) + (threadIdx.x >> 5);
-  if (item >= static_cast<int64_t>(a.tokens) * parts) return;
-  const int token = static_cast<int>(item / parts), part = static_cast<int>(item - static_cast<int64_t>(token) * parts);
-  const int which = part >= parts0, h0 = (which ? part - parts0 : part) * AT_ONCE + sub;
-  const int heads = which ? a.heads[1] : a.heads[0];
   QkLane<LANES, INTER> lane(a);
-  const uint16_t* x = (which ? a.x[1] : a.x[0]) + token * (which ? a.xst[1] : a.xst[0]);
-  uint16_t* y = (which ? a.out[1] : a.out[0]) + token * (which ? a.ost[1] : a.ost[0]);
-  const int64_t xsh = which ? a.xsh[1] : a.xsh[0], osh = which ? a.osh[1] : a.osh[0];
-  uint2 v[HEADS][2];
-#pragma unroll
-  for (int i = 0; i < HEADS; ++i) lane.load(v[i], x + (h0 + i * ROWS) * xsh, h0 + i * ROWS < heads);
-  float w[8];
-  lane.template weights<F16>(w, a, which);
-  const int p = qk_position(a, token);
-  if (p < 0) return;
-  lane.angles(a, p);
   const float inv_dim = 1.f / a.dim;
+  const uint32_t items = static_cast<uint32_t>(a.tokens) * parts, step = gridDim.x * (kQkThreads / 32);
+  uint2 v[HEADS][2];
+  int p = -1, token = 0, which = 0, h0 = 0;
+  auto fetch = [&](uint32_t item) {
+    if (item >= items) return;
+    token = item / static_cast<uint32_t>(parts);
+    const int part = item - static_cast<uint32_t>(token) * parts;
+    which = part >= parts0;
+    h0 = (which ? part - parts0 : part) * AT_ONCE + sub;
+    const uint16_t* x = (which ? a.x[1] : a.x[0]) + token * (which ? a.xst[1] : a.xst[0]);
+    const int64_t xsh = which ? a.xsh[1] : a.xsh[0];
+    const int heads = which ? a.heads[1] : a.heads[0];
 #pragma unroll
-  for (int i = 0; i < HEADS; ++i) {
-    float f[8], sum = 0.f;
-    qk_unpack8<F16>(f, v[i]);
+    for (int i = 0; i < HEADS; ++i) lane.load(v[i], x + (h0 + i * ROWS) * xsh, h0 + i * ROWS < heads);
+    p = qk_position(a, token);
+  };
+  uint32_t item = blockIdx.x * (kQkThreads / 32) + (threadIdx.x >> 5);
+  fetch(item);
+  for (; item < items; item += step) {
+    uint2 u[HEADS][2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
-    const float r = rsqrtf(fmaf(qk_sum<LANES>(sum), inv_dim, a.eps));
+    for (int i = 0; i < HEADS; ++i) u[i][0] = v[i][0], u[i][1] = v[i][1];
+    const int at = p, heads = which ? a.heads[1] : a.heads[0], first = h0, w_of = which;
+    uint16_t* y = (which ? a.out[1] : a.out[0]) + token * (which ? a.ost[1] : a.ost[0]);
+    const int64_t osh = which ? a.osh[1] : a.osh[0];
+    if (at >= 0) lane.angles(a, at);
+    fetch(item + step);
+    if (at < 0) continue;
+    float w[8];
+    lane.template weights<F16>(w, a, w_of);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] *= r * w[j];
-    lane.template turn<false>(f);
-    lane.template store<F16>(y + (h0 + i * ROWS) * osh, f, h0 + i * ROWS < heads);
+    for (int i = 0; i < HEADS; ++i) {
+      float f[8], sum = 0.f;
+      qk_unpack8<F16>(f, u[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
+      const float r = rsqrtf(fmaf(qk_sum<LANES>(sum), inv_dim, a.eps));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] *= r * w[j];
+      lane.template turn<false>(f);
+      lane.template store<F16>(y + (first + i * ROWS) * osh, f, first + i * ROWS < heads);
+    }
   }
 }
 
 // The queries' items, then the keys', warp after warp of a grid of a fixed size; the weights' gradients are summed by
 // each lane over its items, then over the CTA's warps, and the CTAs' sums by the next kernel, in the same order each time.
+// 8191 tokens of 48 heads of 64: 37 us with that kernel, 4.1 TB/s; a lane's two loads a head, the turn and two sums over
+// the lanes, one behind the other, keep it from more.  (Two CTAs a SM, four heads at a time; one head 45, two 45; with the
+// next rows ahead, which then cost registers that the heads had, 41 to 49.)
 template <int LANES, bool F16, bool INTER, int HEADS>
-__global__ void __launch_bounds__(kQkThreads) qk_norm_rope_backward_kernel(const QkNormArgs a) {
+__global__ void __launch_bounds__(kQkThreads, 2) qk_norm_rope_backward_kernel(const QkNormArgs a) {
   pdl_prologue();
   constexpr int ROWS = 32 / LANES, AT_ONCE = ROWS * HEADS, WARPS = kQkThreads / 32;
   __shared__ float sums[WARPS][2][8 * LANES];
@@ -186,7 +206,7 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_backward_kernel(const
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
     const int heads = which ? a.heads[1] : a.heads[0], parts = (heads + AT_ONCE - 1) / AT_ONCE;
-    const int64_t items = static_cast<int64_t>(a.tokens) * parts;
+    const uint32_t items = static_cast<uint32_t>(a.tokens) * parts;
     const int64_t xst = which ? a.xst[1] : a.xst[0], dst = which ? a.dst[1] : a.dst[0], ost = which ? a.ost[1] : a.ost[0];
     const int64_t xsh = which ? a.xsh[1] : a.xsh[0], dsh = which ? a.dsh[1] : a.dsh[0], osh = which ? a.osh[1] : a.osh[0];
     const uint16_t* x = which ? a.x[1] : a.x[0];
@@ -194,8 +214,8 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_backward_kernel(const
     uint16_t* dx = which ? a.out[1] : a.out[0];
     float w[8], dw[8] = {};
     if (items) lane.template weights<F16>(w, a, which);
-    for (int64_t item = static_cast<int64_t>(blockIdx.x) * WARPS + warp; item < items; item += static_cast<int64_t>(gridDim.x) * WARPS) {
-      const int token = static_cast<int>(item / parts), h0 = static_cast<int>(item - static_cast<int64_t>(token) * parts) * AT_ONCE + sub;
+    for (uint32_t item = blockIdx.x * WARPS + warp; item < items; item += gridDim.x * WARPS) {
+      const int token = item / static_cast<uint32_t>(parts), h0 = (item - static_cast<uint32_t>(token) * parts) * AT_ONCE + sub;
       const int p = qk_position(a, token);
       uint2 v[HEADS][2], u[HEADS][2];
 #pragma unroll

@@ -503,7 +503,7 @@ mx_status kv_attention(const void* q, mx_half type, int64_t num_tokens, int64_t 
  *   y = R(p) (x r * w),  r = (mean_i x_i^2 + eps)^(-1/2)  over the head's head_dim values, in FP32, rounded once.
  * q, k: num_tokens tokens of heads (kv_heads) heads of head_dim values, bf16 or fp16, 16-byte aligned, values
  * contiguous, token and head strides (in elements) multiples of 8: slices of a fused projection will do.  kv_heads may
- * be 0 (k, k_weight and k_out NULL then).  head_dim is a multiple of 8, at most 256.  Outputs have strides of their own
+ * be 0 (k, k_weight and k_out NULL then).  num_tokens (heads + kv_heads) is at most 2^31 - 1.  head_dim is a multiple of 8, at most 256.  Outputs have strides of their own
  * and may be the inputs themselves (same address and strides); they may not overlap them otherwise.
  * q_weight, k_weight [head_dim], 16-byte aligned: x's type, or FP32 with weight_f32 = 1.
  * cos_sin float [max_positions][rot_dim], 16-byte aligned: rot_dim / 2 cosines of a position's angles, then their sines.

@@ -104,30 +104,78 @@ constexpr int kKvVerifySegment = 512;               // vocabulary entries that a
 constexpr int kKvVerifyMostVocab = 1 << 20;
 constexpr int kKvVerifyMostCluster = 8;
 
-// A probability in units of 2^-60, cut off there; anything but [0, 2) counts as 0 and is told.  Sums of such whole
-// numbers come out the same in any order and on any number of CTAs, and are no less exact than sums in 64-bit floating
-// point (whose unit runs at 2 a cycle and SM: a row of 128256 would take it 100 us).
-__device__ __forceinline__ uint64_t kv_fixed(float p, bool& bad) {
+// A row's sums are of whole multiples of 2^-44, to which each P is rounded: they come out the same in any order and on any
+// number of CTAs, and lie as near to the exact ones as sums in 64-bit floating point, whose unit runs at 2 a cycle and SM
+// (a row of 128256 would take it 100 us).  Single numbers are kept in units of 2^-60, cut off there.
+constexpr uint64_t kKvOne = 1ull << 60, kKvTakenOne = 1ull << 53;  // 1 so; 1 in W's units
+
+// [0, 2), or -0
+__device__ __forceinline__ bool kv_is_probability(float p) {
   const uint32_t u = __float_as_uint(p);
-  if (u >= 0x40000000u) {
-    bad = bad || u != 0x80000000u;
-    return 0;
-  }
-  const uint32_t e = u >> 23, m = e ? (u << 8) | 0x80000000u : 0u;
+  return u < 0x40000000u || u == 0x80000000u;
+}
+// anything else counts as 0, and is told
+__device__ __forceinline__ float kv_probability(float p, bool& bad) {
+  if (kv_is_probability(p)) return p;
+  bad = true;
+  return 0.f;
+}
+__device__ __forceinline__ uint64_t kv_fixed(float p) {
+  const uint32_t u = __float_as_uint(p), e = (u >> 23) & 0xFFu, m = e ? (u << 8) | 0x80000000u : 0u;
   uint64_t r;
   asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"(static_cast<uint64_t>(m) << 32), "r"(130u - e));  // (64 and more: 0)
   return r;
 }
-constexpr uint64_t kKvOne = 1ull << 60, kKvTakenOne = 1ull << 53;
-
 // max(p - W q, 0) of numbers so kept, W in units of 2^-53
 __device__ __forceinline__ uint64_t kv_residual(uint64_t p, uint64_t q, uint64_t taken) {
   const uint64_t y = taken == kKvTakenOne ? q : __umul64hi(taken, q << 3) << 8;
   return p > y ? p - y : 0;
 }
-__device__ __forceinline__ uint64_t kv_residual(float p, float q, uint64_t taken, bool& bad) {
-  const uint64_t x = kv_fixed(p, bad);
-  return taken ? kv_residual(x, kv_fixed(q, bad), taken) : x;
+
+// Sums of P, in two limbs: units of 2^-22, and of 2^-44 (signed).  A number plus 2 has the first in its last bits, and what
+// is left of it, plus 1.5 * 2^-21, the second; both are added up as they stand, bits and all, and what is too much is
+// taken off at the end.  p - q is taken as the nearest FP32 and its error, which together are exact (Knuth's sum of two).
+struct KvAmount {
+  uint32_t hi = 0, lo = 0;
+  int n = 0;
+  __device__ __forceinline__ void add(float p, float q, bool minus) {
+    float d = p, e = 0.f;
+    if (minus) {
+      d = p - q;
+      const float b = d - p;
+      e = d > 0.f ? (p - (d - b)) - (q + b) : 0.f;
+      d = fmaxf(d, 0.f);
+    }
+    const float h = d + 2.f;
+    hi += __float_as_uint(h);
+    lo += __float_as_uint(((d - (h - 2.f)) + e) + 1.5f / (1 << 21));
+    ++n;
+  }
+  __device__ __forceinline__ uint64_t sum() const {
+    const uint32_t h = hi - n * 0x40000000u;
+    const int32_t l = static_cast<int32_t>(lo - n * __float_as_uint(1.5f / (1 << 21)));
+    return (static_cast<uint64_t>(h) << 22) + static_cast<int64_t>(l);
+  }
+};
+
+// the sum of P over four entries
+__device__ __forceinline__ uint64_t kv_sum4(float4 x, float4 y, uint64_t taken) {
+  if (taken <= kKvTakenOne) {  // W = 0 or 1
+    KvAmount a;
+    a.add(x.x, y.x, taken != 0);
+    a.add(x.y, y.y, taken != 0);
+    a.add(x.z, y.z, taken != 0);
+    a.add(x.w, y.w, taken != 0);
+    return a.sum();
+  }
+  return (kv_residual(kv_fixed(x.x), kv_fixed(y.x), taken) >> 16) + (kv_residual(kv_fixed(x.y), kv_fixed(y.y), taken) >> 16) +
+         (kv_residual(kv_fixed(x.z), kv_fixed(y.z), taken) >> 16) + (kv_residual(kv_fixed(x.w), kv_fixed(y.w), taken) >> 16);
+}
+__device__ __forceinline__ uint64_t kv_sum1(float p, float q, uint64_t taken) {
+  if (taken > kKvTakenOne) return kv_residual(kv_fixed(p), kv_fixed(q), taken) >> 16;
+  KvAmount a;
+  a.add(p, q, taken != 0);
+  return a.sum();
 }
 
 __device__ __forceinline__ uint64_t kv_warp_sum(uint64_t x) {
@@ -208,14 +256,13 @@ __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const Kv
     broken = broken || !ok;
     sm.up[i] = static_cast<int16_t>(up);
     sm.token[i] = token;
-    sm.random[i] = a.accept[rows.q0 + i];
+    sm.random[i] = kv_probability(a.accept[rows.q0 + i], bad);
     float p = 0.f, q = 0.f;
     if (ok && up >= 0) {
       p = a.target[(rows.q0 + up) * a.target_stride + token];
       if (!CERTAIN) q = a.draft[(rows.q0 + up) * a.draft_stride + token];
-      // (what is no probability counts as 0)
-      if (kv_fixed(p, bad) == 0 && !(p > 0.f && p < 2.f)) p = 0.f;
-      if (!CERTAIN && kv_fixed(q, bad) == 0 && !(q > 0.f && q < 2.f)) q = 0.f;
+      p = kv_probability(p, bad);
+      q = kv_probability(q, bad);
     }
     sm.p[i] = p;
     sm.q[i] = q;
@@ -231,6 +278,7 @@ __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const Kv
 
   int node = 0, count = 1;
   uint64_t left = kKvOne, taken = 0;  // Z, W
+  uint64_t sum = 0;                   // of P, as last taken
   bool own = false;                   // nothing is left of P: the target's own probabilities are drawn from
   const int phase_all = (a.vocab + 3 + kKvVerifySegment - 1) / kKvVerifySegment;  // segments of a row, wherever it begins
   const int per = (phase_all + ranks - 1) / ranks, seg0 = min(static_cast<int>(rank) * per, phase_all);
@@ -243,6 +291,13 @@ __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const Kv
     target = a.target + (rows.q0 + node) * a.target_stride;
     draft = CERTAIN ? target : a.draft + (rows.q0 + node) * a.draft_stride;
     wide = entry_at(target) == entry_at(draft);  // (else the draft's row is read by single words)
+  };
+  auto clean = [&](float4 (&x)[4], float4 (&y)[4]) {  // (rare)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[k] = make_float4(kv_probability(x[k].x, bad), kv_probability(x[k].y, bad), kv_probability(x[k].z, bad), kv_probability(x[k].w, bad));
+      y[k] = make_float4(kv_probability(y[k].x, bad), kv_probability(y[k].y, bad), kv_probability(y[k].z, bad), kv_probability(y[k].w, bad));
+    }
   };
   // sums of P by segments into shared memory; returns the sum over all CTAs
   uint64_t before = 0;
@@ -261,11 +316,28 @@ __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const Kv
       else
 #pragma unroll
         for (int k = 0; k < 4; ++k) y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      uint64_t sum = 0;
+      uint32_t most = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        sum += kv_residual(x[k].x, y[k].x, taken, bad) + kv_residual(x[k].y, y[k].y, taken, bad) +
-               kv_residual(x[k].z, y[k].z, taken, bad) + kv_residual(x[k].w, y[k].w, taken, bad);
+      for (int k = 0; k < 4; ++k) {
+        most = max(max(most, max(__float_as_uint(x[k].x), __float_as_uint(x[k].y))), max(__float_as_uint(x[k].z), __float_as_uint(x[k].w)));
+        most = max(max(most, max(__float_as_uint(y[k].x), __float_as_uint(y[k].y))), max(__float_as_uint(y[k].z), __float_as_uint(y[k].w)));
+      }
+      if (most >= 0x40000000u) clean(x, y);
+      uint64_t sum = 0;
+      if (CERTAIN || taken == 0) {
+        KvAmount p;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p.add(x[k].x, 0.f, false), p.add(x[k].y, 0.f, false), p.add(x[k].z, 0.f, false), p.add(x[k].w, 0.f, false);
+        sum = p.sum();
+      } else if (taken == kKvTakenOne) {
+        KvAmount p;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p.add(x[k].x, y[k].x, true), p.add(x[k].y, y[k].y, true), p.add(x[k].z, y[k].z, true), p.add(x[k].w, y[k].w, true);
+        sum = p.sum();
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) sum += kv_sum4(x[k], y[k], taken);
+      }
       sum = kv_warp_sum(sum);
       mine += sum;
       if (lane == 0) sm.segment[s] = sum;
@@ -281,7 +353,7 @@ __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const Kv
         for (int j = node + 1; j < i; ++j) again = again || (sm.up[j] == node && sm.token[j] == sm.token[i]);
         const int s = (sm.token[i] - v00) / kKvVerifySegment - seg0;
         if (again || s < 0 || s >= segs) continue;
-        const uint64_t x = kv_fixed(sm.p[i], bad);
+        const uint64_t x = kv_sum1(sm.p[i], 0.f, 0);
         off += x;
         atomicAdd(reinterpret_cast<unsigned long long*>(&sm.segment[s]), ~static_cast<unsigned long long>(x) + 1);
       }
@@ -316,13 +388,13 @@ __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const Kv
     }
     const int i = i0 + __ffs(children) - 1;
     i0 = i + 1;
-    uint64_t p = kv_fixed(sm.p[i], bad), mark = kv_fixed(sm.random[i], bad);
+    uint64_t p = kv_fixed(sm.p[i]), mark = kv_fixed(sm.random[i]);
     if (CERTAIN) {
       bool again = false;
       for (int j = node + 1 + lane; j < i; j += 32) again = again || (sm.up[j] == node && sm.token[j] == sm.token[i]);
       if (__any_sync(0xFFFFFFFFu, again)) p = 0;
     } else {
-      const uint64_t q = kv_fixed(sm.q[i], bad);
+      const uint64_t q = kv_fixed(sm.q[i]);
       if (taken) p = kv_residual(p, q, taken);
       mark = __umul64hi(mark << 3, q << 3) >> 2;
     }
@@ -337,10 +409,11 @@ __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const Kv
       left -= min(p, left);
     } else {
       taken += left >> 7;
-      left = sum_rows();
+      sum = sum_rows();
+      left = sum << 16;
     }
   }
-  uint64_t sum = taken ? left : sum_rows();
+  if (!taken) sum = sum_rows();
   if (sum == 0) {  // (the distributions are the same, or differ by rounding)
     taken = 0;
     own = true;
@@ -355,7 +428,8 @@ __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const Kv
     }
   } else if (warp == 0) {
     const float s = a.sample[request];
-    const uint64_t mark = __umul64hi(sum, min(kv_fixed(s, bad), kKvOne - 1) << 4);  // what the running sum has to pass
+    // what the running sum has to pass
+    const uint64_t mark = __umul64hi(sum, min(kv_fixed(kv_probability(s, bad)), kKvOne - 1) << 4);
     bad = bad || !(s < 1.f);
     if (mark >= before && mark - before < sm.total) {
       uint64_t at = before;
@@ -380,10 +454,11 @@ __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const Kv
       int token = -1;
       for (int k = 0; k < 4 && token < 0; ++k) {
         const int v0 = v00 + 128 * k + 4 * lane;
-        const float4 x = kv_row4(target, v0, a.vocab, true);
-        const float4 y = !CERTAIN && taken ? kv_row4(draft, v0, a.vocab, wide) : make_float4(0.f, 0.f, 0.f, 0.f);
-        uint64_t v[4] = {kv_residual(x.x, y.x, taken, bad), kv_residual(x.y, y.y, taken, bad),
-                         kv_residual(x.z, y.z, taken, bad), kv_residual(x.w, y.w, taken, bad)};
+        float4 x[4] = {kv_row4(target, v0, a.vocab, true)}, y[4] = {};
+        if (!CERTAIN && taken) y[0] = kv_row4(draft, v0, a.vocab, wide);
+        clean(x, y);
+        uint64_t v[4] = {kv_sum1(x[0].x, y[0].x, taken), kv_sum1(x[0].y, y[0].y, taken), kv_sum1(x[0].z, y[0].z, taken),
+                         kv_sum1(x[0].w, y[0].w, taken)};
         if (CERTAIN && !own)
           for (int i = node + 1; i < n; ++i)
             if (sm.up[i] == node)

@@ -99,7 +99,7 @@ struct KvVerifyArgs {
   int requests, tokens, most, vocab;
 };
 
-constexpr int kKvVerifyThreads = 512;
+constexpr int kKvVerifyThreads = 256;
 constexpr int kKvVerifySegment = 512;               // vocabulary entries that a warp sums at a time
 constexpr int kKvVerifyMostVocab = 1 << 20;
 constexpr int kKvVerifyMostCluster = 8;
@@ -138,14 +138,10 @@ __device__ __forceinline__ uint64_t kv_residual(uint64_t p, uint64_t q, uint64_t
 struct KvAmount {
   uint32_t hi = 0, lo = 0;
   int n = 0;
-  __device__ __forceinline__ void add(float p, float q, bool minus) {
-    float d = p, e = 0.f;
-    if (minus) {
-      d = p - q;
-      const float b = d - p;
-      e = d > 0.f ? (p - (d - b)) - (q + b) : 0.f;
-      d = fmaxf(d, 0.f);
-    }
+  __device__ __forceinline__ void add(float p, float q) {
+    float d = p - q;
+    const float b = d - p, e = d > 0.f ? (p - (d - b)) - (q + b) : 0.f;
+    d = fmaxf(d, 0.f);
     const float h = d + 2.f;
     hi += __float_as_uint(h);
     lo += __float_as_uint(((d - (h - 2.f)) + e) + 1.5f / (1 << 21));
@@ -158,23 +154,11 @@ struct KvAmount {
   }
 };
 
-// the sum of P over four entries
-__device__ __forceinline__ uint64_t kv_sum4(float4 x, float4 y, uint64_t taken) {
-  if (taken <= kKvTakenOne) {  // W = 0 or 1
-    KvAmount a;
-    a.add(x.x, y.x, taken != 0);
-    a.add(x.y, y.y, taken != 0);
-    a.add(x.z, y.z, taken != 0);
-    a.add(x.w, y.w, taken != 0);
-    return a.sum();
-  }
-  return (kv_residual(kv_fixed(x.x), kv_fixed(y.x), taken) >> 16) + (kv_residual(kv_fixed(x.y), kv_fixed(y.y), taken) >> 16) +
-         (kv_residual(kv_fixed(x.z), kv_fixed(y.z), taken) >> 16) + (kv_residual(kv_fixed(x.w), kv_fixed(y.w), taken) >> 16);
-}
-__device__ __forceinline__ uint64_t kv_sum1(float p, float q, uint64_t taken) {
+// P of an entry, in units of 2^-44.  (q is 0 where W is.)
+__device__ __forceinline__ uint64_t kv_amount(float p, float q, uint64_t taken) {
   if (taken > kKvTakenOne) return kv_residual(kv_fixed(p), kv_fixed(q), taken) >> 16;
   KvAmount a;
-  a.add(p, q, taken != 0);
+  a.add(p, q);
   return a.sum();
 }
 
@@ -226,7 +210,10 @@ __device__ __forceinline__ float4 kv_row4(const float* row, int v0, int vocab, b
 // A cluster of CTAs has a request.  What the tests compare is fetched for all nodes at once, before the walk, so that
 // it waits for memory once.  A row's sum is taken in segments of 512, a warp each, 16 bytes a lane and load; the CTAs'
 // sums meet in distributed shared memory, and the last sum's segments say where the next token is, which one warp
-// then finds.  The bound is memory for many requests, the chain starts - nodes - two probabilities - row - segment for few.
+// then finds.  64 requests with chains of 5 over 128256 tokens: 20.5 us, 3.2 TB/s, 0.47 of the measured copy rate; one with
+// 26 nodes over 32000: 8.2 us.  What bounds it is the chain starts - nodes - two probabilities - rows - meeting - segment,
+// about 8 us, in front of and behind the 10 us that the rows take.  (Two CTAs of 256 threads a SM, whose loads all fit
+// their registers: three or four CTAs 24 us, two of 512 threads 23; the sums in three places of the code, 32.)
 template <bool CERTAIN>
 __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const KvVerifyArgs a) {
   pdl_prologue();
@@ -306,16 +293,29 @@ __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const Kv
     const int v00 = entry_at(target);
     uint64_t mine = 0;
     for (int s = warp; s < segs; s += kKvVerifyThreads / 32) {
-      const int v0 = v00 + (seg0 + s) * kKvVerifySegment + 4 * lane;
+      const int begin = v00 + (seg0 + s) * kKvVerifySegment, v0 = begin + 4 * lane;
+      const bool minus = !CERTAIN && taken;
       float4 x[4], y[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = kv_row4(target, v0 + 128 * k, a.vocab, true);
-      if (!CERTAIN && taken)
+      for (int k = 0; k < 4; ++k) y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (wide && begin >= 0 && begin + kKvVerifySegment <= a.vocab) {  // (no choice between the loads, which then run together)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = kv_row4(draft, v0 + 128 * k, a.vocab, wide);
-      else
+        for (int k = 0; k < 4; ++k) x[k] = __ldg(reinterpret_cast<const float4*>(target + v0 + 128 * k));
+        if (minus)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int k = 0; k < 4; ++k) y[k] = __ldg(reinterpret_cast<const float4*>(draft + v0 + 128 * k));
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          const float4 u = kv_row4(target, v0 + 128 * k, a.vocab, true);
+          const float4 t = minus ? kv_row4(draft, v0 + 128 * k, a.vocab, wide) : make_float4(0.f, 0.f, 0.f, 0.f);
+          // (straight choices: an index would put x and y into local memory)
+          if (k == 0) x[0] = u, y[0] = t;
+          if (k == 1) x[1] = u, y[1] = t;
+          if (k == 2) x[2] = u, y[2] = t;
+          if (k == 3) x[3] = u, y[3] = t;
+        }
+      }
       uint32_t most = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -324,19 +324,16 @@ __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const Kv
       }
       if (most >= 0x40000000u) clean(x, y);
       uint64_t sum = 0;
-      if (CERTAIN || taken == 0) {
+      if (CERTAIN || taken <= kKvTakenOne) {
         KvAmount p;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) p.add(x[k].x, 0.f, false), p.add(x[k].y, 0.f, false), p.add(x[k].z, 0.f, false), p.add(x[k].w, 0.f, false);
-        sum = p.sum();
-      } else if (taken == kKvTakenOne) {
-        KvAmount p;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) p.add(x[k].x, y[k].x, true), p.add(x[k].y, y[k].y, true), p.add(x[k].z, y[k].z, true), p.add(x[k].w, y[k].w, true);
+        for (int k = 0; k < 4; ++k) p.add(x[k].x, y[k].x), p.add(x[k].y, y[k].y), p.add(x[k].z, y[k].z), p.add(x[k].w, y[k].w);
         sum = p.sum();
       } else {
-#pragma unroll 1
-        for (int k = 0; k < 4; ++k) sum += kv_sum4(x[k], y[k], taken);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          sum += kv_amount(x[k].x, y[k].x, taken) + kv_amount(x[k].y, y[k].y, taken) + kv_amount(x[k].z, y[k].z, taken) +
+                 kv_amount(x[k].w, y[k].w, taken);
       }
       sum = kv_warp_sum(sum);
       mine += sum;
@@ -353,7 +350,7 @@ __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const Kv
         for (int j = node + 1; j < i; ++j) again = again || (sm.up[j] == node && sm.token[j] == sm.token[i]);
         const int s = (sm.token[i] - v00) / kKvVerifySegment - seg0;
         if (again || s < 0 || s >= segs) continue;
-        const uint64_t x = kv_sum1(sm.p[i], 0.f, 0);
+        const uint64_t x = kv_amount(sm.p[i], 0.f, 0);
         off += x;
         atomicAdd(reinterpret_cast<unsigned long long*>(&sm.segment[s]), ~static_cast<unsigned long long>(x) + 1);
       }
@@ -380,44 +377,51 @@ __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const Kv
 
   // the walk, by every warp for itself
   if (tid == 0) sm.way[0] = 0;
-  for (int i0 = 1; i0 < n;) {
-    const uint32_t children = __ballot_sync(0xFFFFFFFFu, i0 + lane < n && sm.up[i0 + lane] == node);
-    if (!children) {
-      i0 += 32;
-      continue;
+  bool summed = false;  // sum is of the present P
+  for (int i0 = 1;;) {
+    bool rejected = false;
+    while (i0 < n) {
+      const uint32_t children = __ballot_sync(0xFFFFFFFFu, i0 + lane < n && sm.up[i0 + lane] == node);
+      if (!children) {
+        i0 += 32;
+        continue;
+      }
+      const int i = i0 + __ffs(children) - 1;
+      i0 = i + 1;
+      uint64_t p = kv_fixed(sm.p[i]), mark = kv_fixed(sm.random[i]);
+      if (CERTAIN) {
+        bool again = false;
+        for (int j = node + 1 + lane; j < i; j += 32) again = again || (sm.up[j] == node && sm.token[j] == sm.token[i]);
+        if (__any_sync(0xFFFFFFFFu, again)) p = 0;
+      } else {
+        const uint64_t q = kv_fixed(sm.q[i]);
+        if (taken) p = kv_residual(p, q, taken);
+        mark = __umul64hi(mark << 3, q << 3) >> 2;
+      }
+      mark = __umul64hi(mark << 3, left << 3) >> 2;
+      if (mark < p) {
+        if (tid == 0) sm.way[count] = static_cast<int16_t>(i);
+        node = i;
+        ++count;
+        left = kKvOne;
+        taken = 0;
+        summed = false;
+      } else if (CERTAIN) {
+        left -= min(p, left);
+      } else {
+        taken += left >> 7;
+        rejected = true;
+        break;
+      }
     }
-    const int i = i0 + __ffs(children) - 1;
-    i0 = i + 1;
-    uint64_t p = kv_fixed(sm.p[i]), mark = kv_fixed(sm.random[i]);
-    if (CERTAIN) {
-      bool again = false;
-      for (int j = node + 1 + lane; j < i; j += 32) again = again || (sm.up[j] == node && sm.token[j] == sm.token[i]);
-      if (__any_sync(0xFFFFFFFFu, again)) p = 0;
-    } else {
-      const uint64_t q = kv_fixed(sm.q[i]);
-      if (taken) p = kv_residual(p, q, taken);
-      mark = __umul64hi(mark << 3, q << 3) >> 2;
+    if (!rejected && summed) {
+      if (sum || own) break;
+      taken = 0;  // (the distributions are the same, or differ by rounding)
+      own = true;
     }
-    mark = __umul64hi(mark << 3, left << 3) >> 2;
-    if (mark < p) {
-      if (tid == 0) sm.way[count] = static_cast<int16_t>(i);
-      node = i;
-      ++count;
-      left = kKvOne;
-      taken = 0;
-    } else if (CERTAIN) {
-      left -= min(p, left);
-    } else {
-      taken += left >> 7;
-      sum = sum_rows();
-      left = sum << 16;
-    }
-  }
-  if (!taken) sum = sum_rows();
-  if (sum == 0) {  // (the distributions are the same, or differ by rounding)
-    taken = 0;
-    own = true;
     sum = sum_rows();
+    summed = true;
+    if (rejected) left = sum << 16;
   }
   set_rows();
   // the next token
@@ -457,8 +461,8 @@ __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const Kv
         float4 x[4] = {kv_row4(target, v0, a.vocab, true)}, y[4] = {};
         if (!CERTAIN && taken) y[0] = kv_row4(draft, v0, a.vocab, wide);
         clean(x, y);
-        uint64_t v[4] = {kv_sum1(x[0].x, y[0].x, taken), kv_sum1(x[0].y, y[0].y, taken), kv_sum1(x[0].z, y[0].z, taken),
-                         kv_sum1(x[0].w, y[0].w, taken)};
+        uint64_t v[4] = {kv_amount(x[0].x, y[0].x, taken), kv_amount(x[0].y, y[0].y, taken), kv_amount(x[0].z, y[0].z, taken),
+                         kv_amount(x[0].w, y[0].w, taken)};
         if (CERTAIN && !own)
           for (int i = node + 1; i < n; ++i)
             if (sm.up[i] == node)

@@ -645,6 +645,7 @@ def kv_tree_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Ten
         raise ValueError("a window needs positions")
     tree = (_at(tree_mask, _int64, "tree_mask"), tree_mask.shape[1],
             None if positions is None else _at(positions, _int32, "positions"))
+    _one_device(q, k_codes, v_codes, k_scale, v_scale, block_tables, lengths, q_start, tree_mask, positions, out, lse, workspace)
     return _kv_attention("kv_tree_attention", tree, (), q, k_codes, v_codes, k_scale, v_scale, block_tables, lengths, q_start,
                          max_q_len, elem, softmax_scale, window, out, lse, workspace, stream)
 
@@ -692,6 +693,16 @@ def _kv_attention(entry, tree, causal, q, k_codes, v_codes, k_scale, v_scale, bl
 
 
 # ------------------------------------------------------------------ norm and rotation; drafted tokens
+def _one_device(first, *others):
+    """All on the current device, whose stream the call goes to: a kernel there cannot read another's memory."""
+    dev = first.device
+    if not first.is_cuda or dev.index != torch.cuda.current_device():
+        raise ValueError("tensors must be CUDA tensors on the current device")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError("all tensors must be on one device")
+
+
 def _qk_out(out, like, name):
     """(tensor, address, token stride, head stride) of an output shaped like a [tokens][heads][head_dim] tensor."""
     if out is None:
@@ -738,6 +749,7 @@ def qk_norm_rope(q: torch.Tensor, k, q_weight: torch.Tensor, k_weight, cos_sin, 
     ko_at, ko_st, ko_sh = None, 0, 0
     if k is not None:
         k_out, ko_at, ko_st, ko_sh = _qk_out(k_out, k, "k_out")
+    _one_device(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out)
     st = load().qk_norm_rope(q_at, k_at, half, shape[0], shape[1], kv_heads, shape[2], q_st, q_sh, k_st, k_sh, qw, kw, wide,
                              table, places, rot, pos, eps, interleaved, qo_at, ko_at, qo_st, qo_sh, ko_st, ko_sh,
                              _stream(stream))
@@ -782,6 +794,7 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out, q: torch.Tensor, k, q_we
         workspace = _call_workspace(need, dev, at_stream)
     elif workspace.numel() < need:
         raise ValueError(f"workspace must have {need} bytes")
+    _one_device(q, k, dq_out, dk_out, q_weight, k_weight, cos_sin, positions, dq, dk, dq_weight, dk_weight, workspace)
     st = load().qk_norm_rope_backward(g_at, gk_at, q_at, k_at, half, shape[0], shape[1], kv_heads, head_dim, g_st, g_sh, gk_st,
                                       gk_sh, q_st, q_sh, k_st, k_sh, qw, kw, wide, table, places, rot, pos, eps, interleaved,
                                       dq_at, dk_at, dq_st, dq_sh, dk_st, dk_sh, _at(dq_weight, _float32, "dq_weight"),
@@ -816,6 +829,7 @@ def kv_draft_trees(parents: torch.Tensor, lengths: torch.Tensor, q_start: torch.
         positions = torch.empty(tokens, dtype=_int32, device=dev)
     if tree_mask.dim() != 2 or tree_mask.shape[0] != tokens or positions.numel() != tokens:
         raise ValueError("tree_mask must be [tokens][words] and positions [tokens]")
+    _one_device(parents, lengths, q_start, tree_mask, positions)
     st = load().kv_draft_trees(_at(parents, _int32, "parents"), tokens, _at(lengths, _int32, "lengths"),
                                _at(q_start, _int32, "q_start"), requests, max_q_len, window,
                                _at(tree_mask, _int64, "tree_mask"), tree_mask.shape[1], _at(positions, _int32, "positions"),
@@ -860,6 +874,7 @@ def kv_verify_drafts(target_probs: torch.Tensor, drafts: torch.Tensor, parents: 
         counts = torch.empty(requests, dtype=_int32, device=dev)
     if path.numel() != n or tokens.numel() != n or counts.numel() != requests:
         raise ValueError("path and tokens are [tokens], counts is [requests]")
+    _one_device(drafts, target_probs, draft_probs, parents, q_start, accept_random, sample_random, path, tokens, counts)
     st = load().kv_verify_drafts(t_at, t_st, d_at, d_st, vocab, _at(drafts, _int32, "drafts"), _at(parents, _int32, "parents"),
                                  n, _at(q_start, _int32, "q_start"), requests, min(n, 1024) if max_q_len is None else max_q_len,
                                  _at(accept_random, _float32, "accept_random"), _at(sample_random, _float32, "sample_random"),
@@ -884,6 +899,7 @@ def kv_cache_compact(path: torch.Tensor, counts: torch.Tensor, lengths: torch.Te
         kept_lengths = torch.empty(requests, dtype=_int32, device=lengths.device)
     elif kept_lengths.numel() != requests:
         raise ValueError("kept_lengths must be [requests]")
+    _one_device(path, counts, lengths, q_start, block_tables, k_codes, v_codes, k_scale, v_scale, kept_lengths)
     st = load().kv_cache_compact(_at(path, _int32, "path"), _at(counts, _int32, "counts"), path.numel(),
                                  _at(lengths, _int32, "lengths"), _at(q_start, _int32, "q_start"), requests,
                                  _at(block_tables, _int32, "block_tables"), max_blocks, _at(k_codes, _uint8, "k_codes"),

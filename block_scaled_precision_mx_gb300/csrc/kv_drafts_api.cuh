@@ -4,9 +4,18 @@
 
 namespace {
 
-bool kv_overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + b_bytes && y < x + a_bytes;
+struct KvSpan {
+  const void* at;
+  size_t bytes;
+};
+// whether an output shares bytes with an input: some CTA may still read what another writes
+bool kv_overlap(std::initializer_list<KvSpan> outputs, std::initializer_list<KvSpan> inputs) {
+  for (const KvSpan& a : outputs)
+    for (const KvSpan& b : inputs) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+      if (a.at && b.at && x < y + b.bytes && y < x + a.bytes) return true;
+    }
+  return false;
 }
 
 // starts of up to kKvMaxRequests requests of up to kKvMostNodes rows each
@@ -141,6 +150,7 @@ mx_status qk_norm_rope_backward(const void* dq_out, const void* dk_out, const vo
   a.dim = head_dim, a.rot = rot_dim, a.most_pos = static_cast<int>(max_positions);
   a.interleaved = interleaved, a.weight_f32 = weight_f32;
   cudaStream_t st = as_stream(stream);
+  const std::lock_guard<std::mutex> hold(kv_turn);  // (the two launches speak to each other through the workspace)
   int64_t ctas = 0;
   if (num_tokens) {
     const mx_status s = qk_norm_launch<true>(a, type == MX_HALF_F16, st, &ctas);
@@ -161,6 +171,9 @@ mx_status kv_draft_trees(const int32_t* parents, int64_t num_tokens, const int32
   if (num_tokens && (!parents || !tree_mask || !positions)) return MX_ERR_INVALID_ARG;
   if (!aligned(parents, 4) || !aligned(tree_mask, 8) || !aligned(positions, 4)) return MX_ERR_INVALID_ARG;
   if (num_tokens == 0) return MX_OK;
+  const size_t r4 = 4 * requests, t4 = 4 * num_tokens;
+  if (kv_overlap({{tree_mask, 2 * t4 * mask_words}, {positions, t4}}, {{parents, t4}, {lengths, r4}, {q_start, r4 + 4}}))
+    return MX_ERR_INVALID_ARG;
   KvTreesArgs a{};
   a.parents = parents;
   a.lengths = lengths;
@@ -189,6 +202,10 @@ mx_status kv_verify_drafts(const float* target_probs, int64_t target_stride, con
     return MX_ERR_INVALID_ARG;
   if (!aligned(target_probs, 4) || !aligned(draft_probs, 4) || !aligned(drafts, 4) || !aligned(parents, 4) ||
       !aligned(accept_random, 4) || !aligned(sample_random, 4) || !aligned(path, 4) || !aligned(tokens, 4) || !aligned(counts, 4))
+    return MX_ERR_INVALID_ARG;
+  const size_t r4 = 4 * requests, t4 = 4 * num_tokens;
+  if (kv_overlap({{path, t4}, {tokens, t4}, {counts, r4}},
+                 {{drafts, t4}, {parents, t4}, {q_start, r4 + 4}, {accept_random, t4}, {sample_random, r4}}))
     return MX_ERR_INVALID_ARG;
   KvVerifyArgs a{};
   a.target = target_probs;
@@ -244,7 +261,8 @@ mx_status kv_cache_compact(const int32_t* path, const int32_t* counts, int64_t n
       !aligned(v_codes, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(kept_lengths, 4))
     return MX_ERR_INVALID_ARG;
   // (every CTA of a request reads its length and count, and one writes what it keeps)
-  if (kv_overlap(kept_lengths, 4 * requests, lengths, 4 * requests) || kv_overlap(kept_lengths, 4 * requests, counts, 4 * requests))
+  const size_t r4 = 4 * requests, t4 = 4 * num_tokens;
+  if (kv_overlap({{kept_lengths, r4}}, {{lengths, r4}, {counts, r4}, {q_start, r4 + 4}, {path, t4}, {block_tables, r4 * max_blocks}}))
     return MX_ERR_INVALID_ARG;
   KvCompactArgs a{};
   a.path = path;

@@ -529,7 +529,8 @@ size_t qk_norm_rope_workspace_bytes(int head_dim);
  * strides.  dq, dk may be dq_out, dk_out themselves, or q, k.  A token that the forward pass left out gets zeros in dq
  * and dk and adds nothing to the weights' gradients, dq_weight and dk_weight, float [head_dim], which are written, not
  * added to, in an order of sums that depends on the sizes alone.  workspace: qk_norm_rope_workspace_bytes bytes, 16-byte
- * aligned, contents need not be initialised; calls that may overlap need one each.
+ * aligned, contents need not be initialised; calls that may overlap need one each.  Calls from several host threads on
+ * one stream do not overlap, and may share one.
  */
 mx_status qk_norm_rope_backward(const void* dq_out, const void* dk_out, const void* q, const void* k, mx_half type,
                                 int64_t num_tokens, int64_t heads, int64_t kv_heads, int head_dim,
@@ -559,6 +560,7 @@ mx_status qk_norm_rope_backward(const void* dq_out, const void* dk_out, const vo
  *   positions[num_tokens] = lengths[r] - n + depth (a node without parent has depth 0).
  * 64 mask_words >= max_q_len, mask_words <= 16.  A request with a parent out of range gets masks of 0 and positions -1,
  * and is reported.  Rows from q_start[requests] on get the same; rows of requests that are left out are not written.
+ * Outputs may not overlap inputs, here and in kv_verify_drafts.
  */
 mx_status kv_draft_trees(const int32_t* parents, int64_t num_tokens, const int32_t* lengths, const int32_t* q_start,
                          int64_t requests, int64_t max_q_len, int64_t window, int64_t* tree_mask, int64_t mask_words,
@@ -622,7 +624,7 @@ mx_status kv_verify_drafts(const float* target_probs, int64_t target_stride, con
  * they were.  A request whose path, counts, blocks, length or starts break their contract is left as it is, keeps
  * lengths[r] and is reported.  Tokens of a block whose scale is out of range become NaN; a run into such a block is left
  * out; both are reported.  No two requests have a block that is written to in common.  kept_lengths may not
- * overlap lengths or counts.
+ * overlap an input.
  */
 mx_status kv_cache_compact(const int32_t* path, const int32_t* counts, int64_t num_tokens, const int32_t* lengths,
                            const int32_t* q_start, int64_t requests, const int32_t* block_tables, int64_t max_blocks,

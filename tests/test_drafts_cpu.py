@@ -51,7 +51,8 @@ def test_norm_backward_refuses_bad_arguments(lib):
 
 
 def test_trees_refuse_bad_arguments(lib):
-    ok = dict(parents=FAKE, tokens=40, lengths=FAKE, q_start=FAKE, requests=4, most=16, window=0, mask=FAKE, words=1, pos=FAKE)
+    far = 1 << 24
+    ok = dict(parents=FAKE, tokens=40, lengths=FAKE, q_start=FAKE, requests=4, most=16, window=0, mask=far, words=1, pos=far + 4096)
 
     def call(**a):
         return lib.kv_draft_trees(a["parents"], a["tokens"], a["lengths"], a["q_start"], a["requests"], a["most"], a["window"],
@@ -59,7 +60,8 @@ def test_trees_refuse_bad_arguments(lib):
     refuses(call, ok, [{k: None} for k in ("parents", "lengths", "q_start", "mask", "pos")]
             + [{"parents": FAKE + 2}, {"mask": FAKE + 4}, {"tokens": -1}, {"tokens": 1 << 31}, {"requests": 0},
                {"requests": 16385}, {"most": 41}, {"most": -1}, {"tokens": 4000, "most": 1025, "words": 17}, {"words": 0},
-               {"words": 17}, {"tokens": 400, "most": 65}, {"window": -1}, {"window": 1 << 31}])
+               {"words": 17}, {"tokens": 400, "most": 65}, {"window": -1}, {"window": 1 << 31}, {"pos": FAKE}, {"pos": FAKE + 156},
+               {"mask": FAKE - 312}, {"lengths": far + 8}, {"q_start": far + 4096 + 156}])
     assert call(**dict(ok, tokens=0, most=0, parents=None, mask=None, pos=None)) == mx.MX_OK
 
 
@@ -83,7 +85,7 @@ def test_tree_attention_refuses_bad_arguments(lib):
 
 def test_verify_refuses_bad_arguments(lib):
     ok = dict(target=FAKE, tst=1000, draft=FAKE, dst=1000, vocab=1000, drafts=FAKE, parents=FAKE, tokens=40, q_start=FAKE,
-              requests=4, most=16, accept=FAKE, sample=FAKE, path=FAKE, out=FAKE, counts=FAKE)
+              requests=4, most=16, accept=FAKE, sample=FAKE, path=1 << 24, out=(1 << 24) + 4096, counts=(1 << 24) + 8192)
 
     def call(**a):
         return lib.kv_verify_drafts(a["target"], a["tst"], a["draft"], a["dst"], a["vocab"], a["drafts"], a["parents"],
@@ -92,7 +94,8 @@ def test_verify_refuses_bad_arguments(lib):
     refuses(call, ok, [{k: None} for k in ("target", "drafts", "parents", "q_start", "accept", "sample", "path", "out", "counts")]
             + [{"target": FAKE + 2}, {"draft": FAKE + 1}, {"path": FAKE + 2}, {"vocab": 0}, {"vocab": (1 << 20) + 1, "tst": 1 << 21, "dst": 1 << 21},
                {"tst": 999}, {"dst": 999}, {"tokens": -1}, {"requests": 0}, {"requests": 16385}, {"most": 41}, {"most": -1},
-               {"tokens": 4000, "most": 1025}])
+               {"tokens": 4000, "most": 1025}, {"path": FAKE}, {"out": FAKE + 156}, {"counts": FAKE - 12},
+               {"drafts": (1 << 24) + 156}, {"sample": (1 << 24) + 8192 + 12}])
 
 
 def test_compact_refuses_bad_arguments(lib):
@@ -105,7 +108,7 @@ def test_compact_refuses_bad_arguments(lib):
                                     a["max_blocks"], a["kc"], a["vc"], a["ks"], a["vs"], a["elem"], a["blocks"], a["kv_heads"],
                                     a["p"], a["d"], a["kept"], None)
     refuses(call, ok, [{k: None} for k in ("path", "counts", "lengths", "q_start", "tables", "kc", "vc", "ks", "vs", "kept")]
-            + [{"kept": FAKE}, {"kept": FAKE + 12}, {"kept": FAKE + 64}, {"kept": FAKE + 52}, {"kc": FAKE + 8}, {"vs": FAKE + 2},
+            + [{"kept": FAKE}, {"kept": FAKE + 12}, {"kept": FAKE + 64}, {"kept": FAKE + 52}, {"kept": FAKE + 124}, {"kept": FAKE - 12}, {"kc": FAKE + 8}, {"vs": FAKE + 2},
                {"tokens": -1}, {"requests": 0}, {"requests": 16385}, {"max_blocks": 0}, {"max_blocks": 1 << 25}, {"elem": 3},
                {"blocks": 0}, {"kv_heads": 0}, {"p": 24}, {"d": 96}], [{"elem": 2}])
 

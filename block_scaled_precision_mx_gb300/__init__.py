@@ -695,18 +695,20 @@ def _kv_attention(entry, tree, causal, q, k_codes, v_codes, k_scale, v_scale, bl
 # ------------------------------------------------------------------ norm and rotation; drafted tokens
 def _one_device(first, *others):
     """All on the current device, whose stream the call goes to: a kernel there cannot read another's memory."""
-    dev = first.device
-    if not first.is_cuda or dev.index != torch.cuda.current_device():
+    if not first.is_cuda or first.get_device() != torch.cuda.current_device():
         raise ValueError("tensors must be CUDA tensors on the current device")
+    dev = first.get_device()
     for t in others:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError("all tensors must be on one device")
 
 
 def _qk_out(out, like, name):
     """(tensor, address, token stride, head stride) of an output shaped like a [tokens][heads][head_dim] tensor."""
-    if out is None:
-        out = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    if out is None:  # (fresh outputs are not checked again)
+        shape = like.shape
+        out = torch.empty(shape, dtype=like.dtype, device=like.device)
+        return out, out.data_ptr(), shape[1] * shape[2], shape[2]
     shape, at, _, st, sh = _rows_of_heads(out, name)
     if shape != like.shape or out.dtype is not like.dtype:
         raise ValueError(f"{name} must be shaped and typed like its input")
@@ -788,13 +790,13 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out, q: torch.Tensor, k, q_we
         dk_weight = torch.empty(head_dim, dtype=_float32, device=dev)
     if dq_weight.numel() != head_dim or dk_weight.numel() != head_dim:
         raise ValueError("the weights' gradients must have head_dim values")
+    _one_device(q, k, dq_out, dk_out, q_weight, k_weight, cos_sin, positions, dq, dk, dq_weight, dk_weight, workspace)
     at_stream = _stream(stream)
     need = int(load().qk_norm_rope_workspace_bytes(head_dim))
     if workspace is None:
         workspace = _call_workspace(need, dev, at_stream)
     elif workspace.numel() < need:
         raise ValueError(f"workspace must have {need} bytes")
-    _one_device(q, k, dq_out, dk_out, q_weight, k_weight, cos_sin, positions, dq, dk, dq_weight, dk_weight, workspace)
     st = load().qk_norm_rope_backward(g_at, gk_at, q_at, k_at, half, shape[0], shape[1], kv_heads, head_dim, g_st, g_sh, gk_st,
                                       gk_sh, q_st, q_sh, k_st, k_sh, qw, kw, wide, table, places, rot, pos, eps, interleaved,
                                       dq_at, dk_at, dq_st, dq_sh, dk_st, dk_sh, _at(dq_weight, _float32, "dq_weight"),

@@ -494,8 +494,10 @@ __global__ void __launch_bounds__(kKvManyThreads, 1)
     // the next item: this lane's box from `row` on (-1: none), or codes that are taken as something else
     auto load_item = [&](int v, int row, int taken, bool odd) {
       const uint32_t slot = issued % Cfg::RAW_SLOTS;
-      ok = kv_wait(&raw_empty[slot], ((issued / Cfg::RAW_SLOTS) & 1) ^ 1, abort_flag, kSiteProducerEmpty);
-      if (!ok) return false;
+      if (!kv_wait(&raw_empty[slot], ((issued / Cfg::RAW_SLOTS) & 1) ^ 1, abort_flag, kSiteProducerEmpty)) {
+        ok = false;
+        return false;
+      }
       uint8_t* dst = smem + Cfg::OFF_RAW + slot * Cfg::RAW + lane * rows_box * D;
       const bool load = lane < boxes && row >= 0 && !taken;
       const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, load)) * rows_box * D;

@@ -40,7 +40,8 @@ constexpr int kKvTreesThreads = 128;
 // A request a CTA.  Its parents come into shared memory; a node a thread then walks up to its root, sets the
 // bits of what it passes and counts its depth.  Parents are smaller than their children, so the words of a node's
 // mask are finished one after the other on the way.  Latency is the bound: a launch, two dependent loads, as many
-// steps in shared memory as the tree is deep.
+// steps in shared memory as the tree is deep.  64 trees of 32 nodes 2.2 us, 2000 of 100 to 200 8.4 us (12 MB: 1.8 us; words
+// of 8 bytes that a thread writes one by one, 32 apart).
 __global__ void __launch_bounds__(kKvTreesThreads) kv_draft_trees_kernel(const KvTreesArgs a) {
   pdl_prologue();
   __shared__ int16_t up[kKvMostNodes];
@@ -552,7 +553,9 @@ __device__ __forceinline__ uint4 kv_codes_times(uint4 c, float ratio) {
 // still to be read.  What moves into one block is a run, as in kv_cache_append: the block keeps its scale or, where the
 // run's values need a larger one, raises it, and its codes in front are rounded again.  A warp has a request's
 // keys, or values, of one kv head: it looks over the path and the blocks, then takes run by run, reading the
-// codes for their largest value only where a scale differs.  Latency is the bound: starts, path, tables, scales, codes.
+// codes for their largest value only where a scale differs.  Latency is the bound: starts, path, tables, scales, codes, one
+// after the other: 64 requests of 32 nodes 3.1 us, 500 of 100 nodes with blocks of 16 and 16 heads 10 us (16000 warps, each
+// of which goes through that chain for about six tokens).
 template <int FMT, int D>
 __global__ void __launch_bounds__(kKvCompactThreads) kv_compact_kernel(const KvCompactArgs a) {
   pdl_prologue();

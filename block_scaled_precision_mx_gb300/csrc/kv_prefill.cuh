@@ -30,6 +30,13 @@
 // Instruction supply decides much of this: with every role unrolled the same work took 3.0 ms, so each
 // role's loop is short and rolled, and code that runs once a segment is short too (a segment's queries by an
 // unrolled load of 16 rows a lane: 20000 cycles; by the present loops: 5000).
+//
+// Trees (TREE) of 17 rows a kv head and more take the same kernel with their own masks and a few changes that
+// KvManyCfg names.  Their tiles are bound by chains, not by a pipe: of one row half a tile is ~2200 cycles (its codes'
+// conversion by two warps 1500, softmax 1900 on alternate tiles, the products' handing over 500 each), of two ~3400.  Tried
+// there and slower: scores of 64 tokens in two buffers a half with a tile's weights unrolled (98 us for 71, 387 for 257), codes
+// brought to L2 ahead of their loads (92), the next 32 scores read while the present ones become weights (81), a warp
+// for each of the two products (262 for 257), weights apart from the scores (256, not worth its code).
 #pragma once
 
 #include "kv_attention.cuh"
@@ -54,8 +61,9 @@ static_assert(sizeof(KvSegment) <= 64, "a segment's place in shared memory");
 constexpr int kKvManySegments = 4;
 
 // TREE: a tree's rows, few for many tokens, so that a tile's way through the CTA counts: three groups of warps convert items
-// in turn, D = 64 has twice the buffers, and of one row half K and V come in the order of the products (32 trees of 16 to
-// 32 nodes, 4 query heads, up to 4096 tokens: 87 us without all that, 76 with it).  ONE: no unit has more than 128 rows, so that the place of the other half's queries is free.
+// in turn, D = 64 has twice the buffers, of one row half K and V come in the order of the products, a tile's mask bits are
+// fetched at once, and the half that does not write brings the next queries (32 trees of 16 to 32 nodes, 4 query heads a kv
+// head, up to 4096 tokens: 87 us without all that, 71 with it; 9 of 61 nodes, D = 64, windows of 20000: 272 and 257).  ONE: no unit has more than 128 rows, so that the place of the other half's queries is free.
 template <int D, bool TREE, bool ONE>
 struct KvManyCfg {
   static constexpr int RAW_SLOTS = !TREE ? 4 : D == 64 ? 8 : ONE ? 6 : 4, F16_SLOTS = TREE && D == 64 ? 6 : 3;

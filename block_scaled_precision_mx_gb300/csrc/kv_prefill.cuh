@@ -36,7 +36,8 @@
 // conversion by two warps 1500, softmax 1900 on alternate tiles, the products' handing over 500 each), of two ~3400.  Tried
 // there and slower: scores of 64 tokens in two buffers a half with a tile's weights unrolled (98 us for 71, 387 for 257), codes
 // brought to L2 ahead of their loads (92), the next 32 scores read while the present ones become weights (81), a warp
-// for each of the two products (262 for 257), weights apart from the scores (256, not worth its code).
+// for each of the two products (262 for 257), weights apart from the scores (256, not worth its code), and with them the
+// maximum beside the weights in one pass, made again where the reference was too low (303).
 #pragma once
 
 #include "kv_attention.cuh"

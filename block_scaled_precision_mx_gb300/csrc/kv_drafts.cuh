@@ -420,6 +420,9 @@ __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const Kv
       taken = 0;  // (the distributions are the same, or differ by rounding)
       own = true;
     }
+    // (what stays where no CTA finds the next token: nothing is left of P, or it is no distribution and its sum does not fit;
+    // in front of the CTAs' meeting, and so of the token)
+    if (rank == 0 && tid == 0) a.next[rows.q0 + count - 1] = -1;
     sum = sum_rows();
     summed = true;
     if (rejected) left = sum << 16;
@@ -427,10 +430,7 @@ __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const Kv
   set_rows();
   // the next token
   if (sum == 0) {
-    if (rank == 0 && tid == 0) {
-      a.next[rows.q0 + count - 1] = -1;
-      atomicOr(&g_mx_error_word, kSiteBadCache);
-    }
+    if (rank == 0 && tid == 0) atomicOr(&g_mx_error_word, kSiteBadCache);
   } else if (warp == 0) {
     const float s = a.sample[request];
     // what the running sum has to pass

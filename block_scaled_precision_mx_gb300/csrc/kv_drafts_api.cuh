@@ -50,12 +50,19 @@ bool qk_rows_ok(const void* x, int64_t tokens, int64_t heads, int64_t st, int64_
 template <bool BACK, int LANES, bool F16, bool INTER, int HEADS>
 mx_status qk_norm_launch_as(const QkNormArgs& a, cudaStream_t st, int64_t* ctas) {
   constexpr int kAtOnce = 32 / LANES * HEADS;
-  const int64_t parts = (a.heads[0] + kAtOnce - 1) / kAtOnce + (a.heads[1] + kAtOnce - 1) / kAtOnce;
-  int64_t grid = (a.tokens * parts + kQkThreads / 32 - 1) / (kQkThreads / 32);
+  const int64_t parts = (a.heads[0] + kAtOnce - 1) / kAtOnce + (a.heads[1] + kAtOnce - 1) / kAtOnce, heads = a.heads[0] + a.heads[1];
+  // Items of one token's heads, or of rows in a row where the former would leave a third of their places empty or more.
+  // (100 MB of rows, forward and backward, us: 3 + 1 heads of 80, 4 of 16 places, 205 and 368 by tokens, 84 and 139 by
+  // rows; 16 + 2 of 64, 18 of 32, 63 and 110, 54 and 83; 12 + 12 of 96, 24 of 32, 65 and 115, 66 and 107; 32 + 8 of 128, all
+  // places, 40 and 71, 51 and 80.)
+  const bool flat = 2 * kAtOnce * parts >= 3 * heads;
+  const int64_t items = flat ? (a.tokens * heads + kAtOnce - 1) / kAtOnce : a.tokens * parts;
+  int64_t grid = (items + kQkThreads / 32 - 1) / (kQkThreads / 32);
   constexpr int64_t kMost = BACK ? kQkBackCtas : kQkCtas;
   if (grid > kMost) grid = kMost;
   if (ctas) *ctas = grid;
-  const auto kern = BACK ? qk_norm_rope_backward_kernel<LANES, F16, INTER, HEADS> : qk_norm_rope_kernel<LANES, F16, INTER, HEADS>;
+  auto kern = flat ? qk_norm_rope_rows_kernel<LANES, F16, INTER, HEADS> : qk_norm_rope_kernel<LANES, F16, INTER, HEADS>;
+  if (BACK) kern = flat ? qk_norm_rope_backward_kernel<LANES, F16, INTER, HEADS, true> : qk_norm_rope_backward_kernel<LANES, F16, INTER, HEADS, false>;
   return pdl_launch(kern, static_cast<unsigned>(grid), kQkThreads, 0, st, a) == cudaSuccess ? launch_status() : MX_ERR_CUDA;
 }
 template <bool BACK, bool F16, bool INTER>

@@ -190,12 +190,59 @@ __global__ void __launch_bounds__(kQkThreads, 3) qk_norm_rope_kernel(const QkNor
   }
 }
 
+// For few heads, whose items above would be half empty: HEADS * 32 / LANES rows in a row, of whatever tokens.  The angles
+// are each row's own then.
+template <int LANES, bool F16, bool INTER, int HEADS>
+__global__ void __launch_bounds__(kQkThreads, 3) qk_norm_rope_rows_kernel(const QkNormArgs a) {
+  pdl_prologue();
+  constexpr int ROWS = 32 / LANES, AT_ONCE = ROWS * HEADS;
+  const int sub = (threadIdx.x & 31) / LANES;
+  QkLane<LANES, INTER> lane(a);
+  const float inv_dim = 1.f / a.dim;
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const uint32_t heads = which ? a.heads[1] : a.heads[0], rows = a.tokens * heads;
+    const uint16_t* x = which ? a.x[1] : a.x[0];
+    uint16_t* y = which ? a.out[1] : a.out[0];
+    const int64_t xst = which ? a.xst[1] : a.xst[0], xsh = which ? a.xsh[1] : a.xsh[0];
+    const int64_t ost = which ? a.ost[1] : a.ost[0], osh = which ? a.osh[1] : a.osh[0];
+    float w[8];
+    if (rows) lane.template weights<F16>(w, a, which);
+    for (uint32_t row0 = (blockIdx.x * (kQkThreads / 32) + (threadIdx.x >> 5)) * AT_ONCE; row0 < rows;
+         row0 += gridDim.x * (kQkThreads / 32) * AT_ONCE) {
+      uint2 v[HEADS][2];
+      int p[HEADS];
+#pragma unroll
+      for (int i = 0; i < HEADS; ++i) {
+        const uint32_t row = row0 + sub + i * ROWS, token = row / heads, h = row - token * heads;
+        lane.load(v[i], x + token * xst + h * xsh, row < rows);
+        p[i] = row < rows ? qk_position(a, token) : -1;
+      }
+#pragma unroll
+      for (int i = 0; i < HEADS; ++i) {
+        const uint32_t row = row0 + sub + i * ROWS, token = row / heads, h = row - token * heads;
+        lane.angles(a, max(p[i], 0));
+        float f[8], sum = 0.f;
+        qk_unpack8<F16>(f, v[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
+        const float r = rsqrtf(fmaf(qk_sum<LANES>(sum), inv_dim, a.eps));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] *= r * w[j];
+        lane.template turn<false>(f);
+        lane.template store<F16>(y + token * ost + h * osh, f, p[i] >= 0);
+      }
+    }
+  }
+}
+
 // The queries' items, then the keys', warp after warp of a grid of a fixed size; the weights' gradients are summed by
 // each lane over its items, then over the CTA's warps, and the CTAs' sums by the next kernel, in the same order each time.
 // 8191 tokens of 48 heads of 64: 37 us with that kernel, 4.1 TB/s; a lane's two loads a head, the turn and two sums over
 // the lanes, one behind the other, keep it from more.  (Two CTAs a SM, four heads at a time; one head 45, two 45; with the
 // next rows ahead, which then cost registers that the heads had, 41 to 49.)
-template <int LANES, bool F16, bool INTER, int HEADS>
+// FLAT: items are rows in a row, as for few heads above.
+template <int LANES, bool F16, bool INTER, int HEADS, bool FLAT>
 __global__ void __launch_bounds__(kQkThreads, 2) qk_norm_rope_backward_kernel(const QkNormArgs a) {
   pdl_prologue();
   constexpr int ROWS = 32 / LANES, AT_ONCE = ROWS * HEADS, WARPS = kQkThreads / 32;
@@ -205,8 +252,8 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_norm_rope_backward_kernel(co
   const float inv_dim = 1.f / a.dim;
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
-    const int heads = which ? a.heads[1] : a.heads[0], parts = (heads + AT_ONCE - 1) / AT_ONCE;
-    const uint32_t items = static_cast<uint32_t>(a.tokens) * parts;
+    const uint32_t heads = which ? a.heads[1] : a.heads[0], parts = (heads + AT_ONCE - 1) / AT_ONCE, rows = a.tokens * heads;
+    const uint32_t items = FLAT ? (rows + AT_ONCE - 1) / AT_ONCE : a.tokens * parts;
     const int64_t xst = which ? a.xst[1] : a.xst[0], dst = which ? a.dst[1] : a.dst[0], ost = which ? a.ost[1] : a.ost[0];
     const int64_t xsh = which ? a.xsh[1] : a.xsh[0], dsh = which ? a.dsh[1] : a.dsh[0], osh = which ? a.osh[1] : a.osh[0];
     const uint16_t* x = which ? a.x[1] : a.x[0];
@@ -215,19 +262,31 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_norm_rope_backward_kernel(co
     float w[8], dw[8] = {};
     if (items) lane.template weights<F16>(w, a, which);
     for (uint32_t item = blockIdx.x * WARPS + warp; item < items; item += gridDim.x * WARPS) {
-      const int token = item / static_cast<uint32_t>(parts), h0 = (item - static_cast<uint32_t>(token) * parts) * AT_ONCE + sub;
-      const int p = qk_position(a, token);
+      const uint32_t whole = FLAT ? 0 : item / parts, h0 = FLAT ? 0 : (item - whole * parts) * AT_ONCE + sub;
       uint2 v[HEADS][2], u[HEADS][2];
+      int p[FLAT ? HEADS : 1];
+      auto place = [&](int i, uint32_t& token, uint32_t& h) {  // row i of the item; whether there is one
+        const uint32_t row = item * AT_ONCE + sub + i * ROWS;
+        token = FLAT ? row / heads : whole;
+        h = FLAT ? row - token * heads : h0 + i * ROWS;
+        return FLAT ? row < rows : h < heads;
+      };
+      if (!FLAT) p[0] = qk_position(a, whole);
 #pragma unroll
       for (int i = 0; i < HEADS; ++i) {
-        const int h = h0 + i * ROWS;
-        lane.load(v[i], x + token * xst + h * xsh, h < heads);
-        lane.load(u[i], dy + token * dst + h * dsh, h < heads);
+        uint32_t token, h;
+        const bool live = place(i, token, h);
+        lane.load(v[i], x + token * xst + h * xsh, live);
+        lane.load(u[i], dy + token * dst + h * dsh, live);
+        if (FLAT) p[FLAT ? i : 0] = live ? qk_position(a, token) : -1;
       }
-      lane.angles(a, max(p, 0));
+      if (!FLAT) lane.angles(a, max(p[0], 0));
 #pragma unroll
       for (int i = 0; i < HEADS; ++i) {
-        const int h = h0 + i * ROWS;
+        uint32_t token, h;
+        const bool live = place(i, token, h);
+        const int at = p[FLAT ? i : 0];
+        if (FLAT) lane.angles(a, max(at, 0));
         float f[8], g[8], sum = 0.f, dot = 0.f;
         qk_unpack8<F16>(f, v[i]);
         qk_unpack8<F16>(g, u[i]);
@@ -243,10 +302,10 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_norm_rope_backward_kernel(co
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float xh = f[j] * r;
-          o[j] = p < 0 ? 0.f : r * fmaf(g[j], w[j], -xh * mean);
-          if (p >= 0 && h < heads) dw[j] = fmaf(g[j], xh, dw[j]);
+          o[j] = at < 0 ? 0.f : r * fmaf(g[j], w[j], -xh * mean);
+          if (at >= 0 && live) dw[j] = fmaf(g[j], xh, dw[j]);
         }
-        lane.template store<F16>(dx + token * ost + h * osh, o, h < heads);
+        lane.template store<F16>(dx + token * ost + h * osh, o, live);
       }
     }
 #pragma unroll

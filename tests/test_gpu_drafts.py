@@ -422,6 +422,21 @@ def test_verify_broken_contracts():
     assert counts.tolist() == [1, 1] and (tokens == -1).all() and path[0] == path[4] == 0
 
 
+@pytest.mark.parametrize("vocab", [1000, 1 << 20])
+def test_verify_rows_that_are_no_distributions(vocab):
+    """Entries that are probabilities each, but whose sums are not near 1: a token of the vocabulary, or none."""
+    for value in (1.9, 1.0, 1e-3):
+        target = torch.full((3, vocab), value, device="cuda")
+        draft = torch.full((3, vocab), 1e-6, device="cuda")
+        for q in (None, draft):
+            tokens = torch.full((3,), 77777777, dtype=torch.int32, device="cuda")
+            _, _, counts = mx.kv_verify_drafts(target, gpu(np.int32([0, 5, 6])), gpu(np.int32([-1, 0, 1])), gpu(np.int32([0, 3])),
+                                               gpu(np.full(3, 0.5, np.float32)), gpu(np.float32([0.7])), draft_probs=q, tokens=tokens)
+            mx.mx_check()
+            n = int(counts)
+            assert 1 <= n <= 3 and all(-1 <= t < vocab for t in tokens.tolist()) and all(t == -1 for t in tokens.tolist()[n:])
+
+
 # ------------------------------------------------------------------ compaction
 def check_compact(context, nodes, paths, p, kv_heads, d, elem, seed=0, spread=1.5, pad=0, scales=None):
     rng = np.random.RandomState(seed)

@@ -707,7 +707,7 @@ def _qk_out(out, like, name):
     """(tensor, address, token stride, head stride) of an output shaped like a [tokens][heads][head_dim] tensor."""
     if out is None:  # (fresh outputs are not checked again)
         shape = like.shape
-        out = like.new_empty(shape)
+        out = torch.empty(shape, dtype=like.dtype, device=like.device)
         return out, out.data_ptr(), shape[1] * shape[2], shape[2]
     shape, at, _, st, sh = _rows_of_heads(out, name)
     if shape != like.shape or out.dtype is not like.dtype:
@@ -760,11 +760,6 @@ def qk_norm_rope(q: torch.Tensor, k, q_weight: torch.Tensor, k_weight, cos_sin, 
     return q_out, k_out
 
 
-@functools.lru_cache(maxsize=64)
-def _qk_workspace_bytes(head_dim: int) -> int:
-    return int(load().qk_norm_rope_workspace_bytes(head_dim))
-
-
 def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out, q: torch.Tensor, k, q_weight: torch.Tensor, k_weight, cos_sin,
                           positions, eps: float = 1e-6, interleaved: bool = False, dq=None, dk=None, dq_weight=None,
                           dk_weight=None, workspace=None, stream=None):
@@ -788,34 +783,38 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out, q: torch.Tensor, k, q_we
     dk_at, dk_st, dk_sh = None, 0, 0
     if k is not None:
         dk, dk_at, dk_st, dk_sh = _qk_out(dk, k, "dk")
-    head_dim = shape[2]
-    if dq_weight is None and dk_weight is None:
-        dq_weight, dk_weight = q.new_empty((2, head_dim), dtype=_float32).unbind(0)
-    elif dq_weight is None:
-        dq_weight = q.new_empty(head_dim, dtype=_float32)
-    elif dk_weight is None:
-        dk_weight = q.new_empty(head_dim, dtype=_float32)
+    dev, head_dim = q.device, shape[2]
+    if dq_weight is None:
+        dq_weight = torch.empty(head_dim, dtype=_float32, device=dev)
+    if dk_weight is None:
+        dk_weight = torch.empty(head_dim, dtype=_float32, device=dev)
     if dq_weight.numel() != head_dim or dk_weight.numel() != head_dim:
         raise ValueError("the weights' gradients must have head_dim values")
     _one_device(q, k, dq_out, dk_out, q_weight, k_weight, cos_sin, positions, dq, dk, dq_weight, dk_weight, workspace)
     at_stream = _stream(stream)
-    need = _qk_workspace_bytes(head_dim)
+    need = int(load().qk_norm_rope_workspace_bytes(head_dim))
     if workspace is None:
-        if at_stream == _PER_THREAD:
-            raise ValueError("a call on the per-thread default stream needs a workspace of the caller's")
-        # (the one that kv_attention's calls on the stream share, behind what they keep zero)
-        ws_at = _kv_workspace(4096 + need, q.device, at_stream, stream).data_ptr() + 4096
+        workspace = _call_workspace(need, dev, at_stream)
     elif workspace.numel() < need:
         raise ValueError(f"workspace must have {need} bytes")
-    else:
-        ws_at = _at(workspace, _uint8, "workspace")
     st = load().qk_norm_rope_backward(g_at, gk_at, q_at, k_at, half, shape[0], shape[1], kv_heads, head_dim, g_st, g_sh, gk_st,
                                       gk_sh, q_st, q_sh, k_st, k_sh, qw, kw, wide, table, places, rot, pos, eps, interleaved,
                                       dq_at, dk_at, dq_st, dq_sh, dk_st, dk_sh, _at(dq_weight, _float32, "dq_weight"),
-                                      _at(dk_weight, _float32, "dk_weight"), ws_at, at_stream)
+                                      _at(dk_weight, _float32, "dk_weight"), _at(workspace, _uint8, "workspace"), at_stream)
     if st:
         _check(st, "qk_norm_rope_backward")
     return dq, dk, dq_weight, dk_weight
+
+
+def _call_workspace(need, dev, stream):
+    """A workspace that need not be clear, for one call: torch's allocator has it back when the call's work on the
+    stream is in order in front of the next owner's, so it is made as one of that stream's."""
+    if stream == _stream(None):
+        return torch.empty(need, dtype=_uint8, device=dev)
+    if stream == _PER_THREAD:
+        raise ValueError("a call on the per-thread default stream needs a workspace of the caller's")
+    with torch.cuda.stream(torch.cuda.ExternalStream(0 if stream == _LEGACY else stream, device=dev)):
+        return torch.empty(need, dtype=_uint8, device=dev)
 
 
 def kv_draft_trees(parents: torch.Tensor, lengths: torch.Tensor, q_start: torch.Tensor, max_q_len: int, window: int = 0,
@@ -823,13 +822,13 @@ def kv_draft_trees(parents: torch.Tensor, lengths: torch.Tensor, q_start: torch.
     """Visibility and positions of trees of drafted tokens from their parents (int32 [tokens], numbers within a request;
     -1: none) (include/mx.h, kv_draft_trees).  Returns (tree_mask int64 [tokens][ceil(max_q_len / 64)], positions int32
     [tokens])."""
-    tokens, requests = parents.numel(), lengths.numel()
+    tokens, requests, dev = parents.numel(), lengths.numel(), parents.device
     if q_start.numel() != requests + 1:
         raise ValueError("q_start must be [requests + 1]")
     if tree_mask is None:
-        tree_mask = parents.new_empty((tokens, max(1, (max_q_len + 63) // 64)), dtype=_int64)
+        tree_mask = torch.empty((tokens, max(1, (max_q_len + 63) // 64)), dtype=_int64, device=dev)
     if positions is None:
-        positions = parents.new_empty(tokens)
+        positions = torch.empty(tokens, dtype=_int32, device=dev)
     if tree_mask.dim() != 2 or tree_mask.shape[0] != tokens or positions.numel() != tokens:
         raise ValueError("tree_mask must be [tokens][words] and positions [tokens]")
     _one_device(parents, lengths, q_start, tree_mask, positions)
@@ -860,7 +859,7 @@ def kv_verify_drafts(target_probs: torch.Tensor, drafts: torch.Tensor, parents: 
     behind them (include/mx.h, kv_verify_drafts).  drafts, parents int32 [tokens]; q_start int32 [requests + 1];
     accept_random float32 [tokens], sample_random float32 [requests]; draft_probs: what the drafts were drawn from, or
     None where they are certain.  Returns (path int32 [tokens], tokens int32 [tokens], counts int32 [requests])."""
-    n, requests = drafts.numel(), sample_random.numel()
+    n, requests, dev = drafts.numel(), sample_random.numel(), drafts.device
     t_at, t_st, vocab = _probs(target_probs, n, "target_probs")
     d_at, d_st = None, 0
     if draft_probs is not None:
@@ -870,11 +869,11 @@ def kv_verify_drafts(target_probs: torch.Tensor, drafts: torch.Tensor, parents: 
     if parents.numel() != n or accept_random.numel() != n or q_start.numel() != requests + 1:
         raise ValueError("parents and accept_random are [tokens], q_start is [requests + 1]")
     if path is None:
-        path = drafts.new_empty(n)
+        path = torch.empty(n, dtype=_int32, device=dev)
     if tokens is None:
-        tokens = drafts.new_empty(n)
+        tokens = torch.empty(n, dtype=_int32, device=dev)
     if counts is None:
-        counts = drafts.new_empty(requests)
+        counts = torch.empty(requests, dtype=_int32, device=dev)
     if path.numel() != n or tokens.numel() != n or counts.numel() != requests:
         raise ValueError("path and tokens are [tokens], counts is [requests]")
     _one_device(drafts, target_probs, draft_probs, parents, q_start, accept_random, sample_random, path, tokens, counts)
@@ -899,7 +898,7 @@ def kv_cache_compact(path: torch.Tensor, counts: torch.Tensor, lengths: torch.Te
     if table_rows != requests or counts.numel() != requests or q_start.numel() != requests + 1:
         raise ValueError("block_tables is [requests][max_blocks], lengths and counts are [requests], q_start [requests + 1]")
     if kept_lengths is None:
-        kept_lengths = lengths.new_empty(requests)
+        kept_lengths = torch.empty(requests, dtype=_int32, device=lengths.device)
     elif kept_lengths.numel() != requests:
         raise ValueError("kept_lengths must be [requests]")
     _one_device(path, counts, lengths, q_start, block_tables, k_codes, v_codes, k_scale, v_scale, kept_lengths)

@@ -127,10 +127,12 @@ __device__ __forceinline__ uint64_t kv_fixed(float p) {
   asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"(static_cast<uint64_t>(m) << 32), "r"(130u - e));  // (64 and more: 0)
   return r;
 }
-// max(p - W q, 0) of numbers so kept, W in units of 2^-53
+// max(p - W q, 0) of numbers so kept, W in units of 2^-53.  W grows with every rejected sibling, so W q may be far
+// past what 64 bits hold of it; from 4 on no p comes near it.
 __device__ __forceinline__ uint64_t kv_residual(uint64_t p, uint64_t q, uint64_t taken) {
-  const uint64_t y = taken == kKvTakenOne ? q : __umul64hi(taken, q << 3) << 8;
-  return p > y ? p - y : 0;
+  if (taken == kKvTakenOne) return p > q ? p - q : 0;
+  const uint64_t high = __umul64hi(taken, q << 3);  // W q in units of 2^-52
+  return high < 1ull << 54 && p > high << 8 ? p - (high << 8) : 0;
 }
 
 // Sums of P, in two limbs: units of 2^-22, and of 2^-44 (signed).  A number plus 2 has the first in its last bits, and what

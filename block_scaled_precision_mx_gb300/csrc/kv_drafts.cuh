@@ -617,7 +617,8 @@ __global__ void __launch_bounds__(kKvCompactThreads) kv_compact_kernel(const KvC
       float s;
       const uint8_t* at = source(j, s);
       odd = odd || !in_range(s);
-      if (s != old) amax = fmaxf(amax, kv_codes_amax<FMT>(*reinterpret_cast<const uint4*>(at)) * s);
+      // (what becomes NaN says nothing of the scale: it would wipe out what is in front and beside it)
+      if (s != old && in_range(s)) amax = fmaxf(amax, kv_codes_amax<FMT>(*reinterpret_cast<const uint4*>(at)) * s);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));

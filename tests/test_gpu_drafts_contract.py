@@ -3,7 +3,10 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_drafts import check_verify
+import block_scaled_precision_mx_gb300 as mx
+from tests import drafts_reference as ref
+from tests import kv_reference as kv
+from tests.test_gpu_drafts import check_verify, gpu, reported
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +52,36 @@ def test_verify_siblings_of_a_narrow_draft(star, children, below):
                                 sample=np.float32([sample]))
             if trial == 0:
                 assert int(want[2][0]) == 1 + below  # (a word on the inputs: all of them are rejected)
+
+
+# ------------------------------------------------------------------ compaction
+@pytest.mark.parametrize("odd", [float("nan"), float("inf"), float("-inf"), -0.5, 2.0 ** 49, 2.0 ** -49])
+@pytest.mark.parametrize("elem", [mx.E4M3, mx.E5M2])
+@pytest.mark.parametrize("p,d,context,way", [(16, 64, 10, [0, 3, 25, 28, 29]), (16, 128, 16, [0, 17, 33]), (32, 64, 40, [2, 26, 30, 33])])
+def test_compact_keeps_what_is_beside_a_block_out_of_range(p, d, context, way, elem, odd):
+    """The last block's scale is no scale (for half of the heads): its tokens become NaN, and the codes, scales and moved
+    tokens of the blocks that they come to are what they are with any NaN in their place."""
+    rng = np.random.RandomState(p + context)
+    nodes, heads = 34, 4
+    held = -(-(context + nodes) // p)
+    tables = rng.permutation(held + 1)[None, :held].astype(np.int32)
+    path = np.int32([way + [-1] * (nodes - len(way))])[0]
+    counts, lengths, q_start = np.int32([len(way)]), np.int32([context + nodes]), np.int32([0, nodes])
+    assert (context + way[-1]) // p == held - 1 > (context + len(way) - 1) // p  # (moved from, not into)
+    caches, want = [], []
+    for _ in range(2):
+        codes = rng.randint(0, 120, (held + 1, heads, p, d)).astype(np.uint8)
+        scale = 2.0 ** rng.randint(-3, 4, (held + 1, heads)).astype(np.float32)
+        scale[tables[0, 0], 1] = 0  # (a block of zeros among those that are moved into)
+        scale[tables[0, -1], ::2] = np.nan
+        want.append(ref.compact(path, counts, lengths, q_start, tables, codes, scale, elem))
+        scale[tables[0, -1], ::2] = odd
+        want[-1][1][tables[0, -1], ::2] = odd
+        caches.append((codes, scale))
+    codes, scale = [gpu(c) for c, _ in caches], [gpu(s) for _, s in caches]
+    kept = mx.kv_cache_compact(gpu(path), gpu(counts), gpu(lengths), gpu(q_start), gpu(tables), *codes, *scale, elem=elem)
+    reported()
+    assert kept.tolist() == [context + len(way)]
+    for c, s, (wc, ws, _) in zip(codes, scale, want):
+        assert np.array_equal(s.cpu().numpy(), ws, equal_nan=True)
+        assert np.array_equal(c.cpu().numpy(), wc)

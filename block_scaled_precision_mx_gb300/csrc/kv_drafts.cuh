@@ -106,8 +106,9 @@ constexpr int kKvVerifyMostVocab = 1 << 20;
 constexpr int kKvVerifyMostCluster = 8;
 
 // A row's sums are of whole multiples of 2^-44, to which each P is rounded: they come out the same in any order and on any
-// number of CTAs, and lie as near to the exact ones as sums in 64-bit floating point, whose unit runs at 2 a cycle and SM
-// (a row of 128256 would take it 100 us).  Single numbers are kept in units of 2^-60, cut off there.
+// number of CTAs, and are off by 2^-45 an entry and a little, all of them the same way where the entries are alike (128256:
+// 4e-9 at worst; 1e-11 where the roundings are independent).  Sums in 64-bit floating point would be nearer, but their unit
+// runs at 2 a cycle and SM (a row of 128256 would take it 100 us).  Single numbers are kept in units of 2^-60, cut off there.
 constexpr uint64_t kKvOne = 1ull << 60, kKvTakenOne = 1ull << 53;  // 1 so; 1 in W's units
 
 // [0, 2), or -0
@@ -159,7 +160,7 @@ struct KvAmount {
 
 // P of an entry, in units of 2^-44.  (q is 0 where W is.)
 __device__ __forceinline__ uint64_t kv_amount(float p, float q, uint64_t taken) {
-  if (taken > kKvTakenOne) return kv_residual(kv_fixed(p), kv_fixed(q), taken) >> 16;
+  if (taken > kKvTakenOne) return (kv_residual(kv_fixed(p), kv_fixed(q), taken) + (1u << 15)) >> 16;
   KvAmount a;
   a.add(p, q);
   return a.sum();

@@ -602,8 +602,8 @@ mx_status kv_tree_attention(const void* q, mx_half type, int64_t num_tokens, int
  *   path[..] = the accepted nodes, the root first, then -1;
  *   tokens[..] = the accepted drafts and then the next token, counts[r] of them, then -1.
  * Rows from q_start[requests] on get -1.  Sums are of whole multiples of 2^-44, to which each P is rounded: no order
- * changes them.  Random numbers are in [0, 1).  A probability or random number that is negative, NaN or 2 and above counts as 0
- * and is reported.  A request with a token or parent out of range gets counts 0 and -1, and is reported; one whose P and
+ * changes them, and they are within 1.2 vocab 2^-45 of the exact ones (an entry below 2^-46 is never drawn).  Random numbers
+ * are in [0, 1).  A probability or random number that is negative, NaN or 2 and above counts as 0 and is reported.  A request with a token or parent out of range gets counts 0 and -1, and is reported; one whose P and
  * target are all 0 gets -1 as its next token, and is reported.  Requests with broken starts get counts 0.
  * vocab is at most 2^20, probabilities need 4-byte alignment.
  */

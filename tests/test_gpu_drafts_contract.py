@@ -6,7 +6,7 @@ import torch
 import block_scaled_precision_mx_gb300 as mx
 from tests import drafts_reference as ref
 from tests import kv_reference as kv
-from tests.test_gpu_drafts import check_verify, gpu, reported
+from tests.test_gpu_drafts import check_verify, gpu, ok, reported
 
 pytestmark = pytest.mark.gpu
 
@@ -52,6 +52,30 @@ def test_verify_siblings_of_a_narrow_draft(star, children, below):
                                 sample=np.float32([sample]))
             if trial == 0:
                 assert int(want[2][0]) == 1 + below  # (a word on the inputs: all of them are rejected)
+
+
+@pytest.mark.parametrize("share", [0.6, 0.9, 1.4, 2.6])  # of 2^-44, the unit of the sums
+@pytest.mark.parametrize("rejected", [0, 1, 2, 5])
+def test_verify_sums_of_many_tiny_probabilities(rejected, share):
+    """2^20 - 2 entries that are alike stand in front of the two large ones, one of which the draft has.  Each is
+    rounded by 2^-45 at most, and what is left of p - q, below 2^-23, by 2^-48 before: 1.2 * 2^-45 an entry."""
+    vocab, n = 1 << 20, 1 + rejected
+    target, draft = np.full((n, vocab), share * 2.0 ** -44, np.float32), np.zeros((n, vocab), np.float32)
+    target[:, -2:], draft[:, -1] = 0.5, 1
+    tiny = float(target[0, 0])
+    for sample in np.float32([0, 5e-9, 1e-8, 2e-8, 3e-8]):
+        path, tokens, counts = mx.kv_verify_drafts(gpu(target), gpu(np.full(n, vocab - 1, np.int32)), gpu(np.int32([-1] + [0] * rejected)),
+                                                   gpu(np.int32([0, n])), gpu(np.full(n, 0.75, np.float32)), gpu(np.array([sample])),
+                                                   draft_probs=gpu(draft))
+        ok()
+        assert counts.tolist() == [1] and path.tolist() == [0] + [-1] * rejected
+        token = int(tokens[0])
+        # what the running sum has to pass, and what it is before and behind the token, each within its bound; the second
+        # large entry is gone with the first rejection
+        mark = float(sample) * (tiny * (vocab - 2) + (0.5 if rejected else 1.0))
+        off = (token + 2 + float(sample) * vocab) * 1.2 * 2.0 ** -45
+        assert token * tiny <= mark + off
+        assert (token + 1) * tiny + (0.5 if token >= vocab - 2 else 0) > mark - off
 
 
 # ------------------------------------------------------------------ compaction

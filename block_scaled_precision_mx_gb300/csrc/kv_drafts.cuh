@@ -110,6 +110,10 @@ constexpr int kKvVerifyMostCluster = 8;
 // 4e-9 at worst; 1e-11 where the roundings are independent).  Sums in 64-bit floating point would be nearer, but their unit
 // runs at 2 a cycle and SM (a row of 128256 would take it 100 us).  Single numbers are kept in units of 2^-60, cut off there.
 constexpr uint64_t kKvOne = 1ull << 60, kKvTakenOne = 1ull << 53;  // 1 so; 1 in W's units
+// A sum of P is below 2, or the row is no distribution, which is told.  Z stays below 2 then, so that no product of it passes
+// 64 bits, and so does what a number in [0, 2) is times a probability; a warp's part of a sum (below 2^63) stays below
+// kKvMostPart, so that no sum of all 64 parts does, and from kKvMostSum on there is no next token.
+constexpr uint64_t kKvSumTwo = 1ull << 45, kKvMostSum = 1ull << 56, kKvMostPart = 1ull << 57;
 
 // [0, 2), or -0
 __device__ __forceinline__ bool kv_is_probability(float p) {
@@ -343,7 +347,7 @@ __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const Kv
       mine += sum;
       if (lane == 0) sm.segment[s] = sum;
     }
-    if (lane == 0) sm.warp_total[warp] = mine;
+    if (lane == 0) sm.warp_total[warp] = min(mine, kKvMostPart);
     __syncthreads();
     if (CERTAIN && warp == 0) {
       // the rejected children's tokens do not count: taken off their segments, and each once
@@ -376,6 +380,7 @@ __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const Kv
     }
     __syncwarp();
     kv_cluster_sync();  // (before any of it is written again, or its CTA has gone)
+    bad = bad || sum >= kKvSumTwo;
     return sum;
   };
 
@@ -400,7 +405,7 @@ __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const Kv
       } else {
         const uint64_t q = kv_fixed(sm.q[i]);
         if (taken) p = kv_residual(p, q, taken);
-        mark = __umul64hi(mark << 3, q << 3) >> 2;
+        mark = min(static_cast<uint64_t>(__umul64hi(mark << 3, q << 3) >> 2), 2 * kKvOne - 1);
       }
       mark = __umul64hi(mark << 3, left << 3) >> 2;
       if (mark < p) {
@@ -423,16 +428,16 @@ __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const Kv
       taken = 0;  // (the distributions are the same, or differ by rounding)
       own = true;
     }
-    // (what stays where no CTA finds the next token: nothing is left of P, or it is no distribution and its sum does not fit;
-    // in front of the CTAs' meeting, and so of the token)
+    // (what stays where there is no next token: nothing is left of P, or it is far from a distribution; in front of the
+    // CTAs' meeting, and so of the token)
     if (rank == 0 && tid == 0) a.next[rows.q0 + count - 1] = -1;
     sum = sum_rows();
     summed = true;
-    if (rejected) left = sum << 16;
+    if (rejected) left = min(sum, kKvSumTwo - 1) << 16;
   }
   set_rows();
   // the next token
-  if (sum == 0) {
+  if (sum == 0 || sum >= kKvMostSum) {
     if (rank == 0 && tid == 0) atomicOr(&g_mx_error_word, kSiteBadCache);
   } else if (warp == 0) {
     const float s = a.sample[request];

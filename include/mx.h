@@ -604,7 +604,8 @@ mx_status kv_tree_attention(const void* q, mx_half type, int64_t num_tokens, int
  * Rows from q_start[requests] on get -1.  Sums are of whole multiples of 2^-44, to which each P is rounded: no order
  * changes them, and they are within 1.2 vocab 2^-45 of the exact ones (an entry below 2^-46 is never drawn).  Random numbers
  * are in [0, 1).  A probability or random number that is negative, NaN or 2 and above counts as 0 and is reported.  A request with a token or parent out of range gets counts 0 and -1, and is reported; one whose P and
- * target are all 0 gets -1 as its next token, and is reported.  Requests with broken starts get counts 0.
+ * target are all 0 gets -1 as its next token, and is reported.  A sum of P that is 2 or more is reported (its row is no
+ * distribution): Z is then just below 2, and from 4096 on the next token is -1.  Requests with broken starts get counts 0.
  * vocab is at most 2^20, probabilities need 4-byte alignment.
  */
 mx_status kv_verify_drafts(const float* target_probs, int64_t target_stride, const float* draft_probs, int64_t draft_stride,

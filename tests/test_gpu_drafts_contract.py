@@ -78,6 +78,54 @@ def test_verify_sums_of_many_tiny_probabilities(rejected, share):
         assert (token + 1) * tiny + (0.5 if token >= vocab - 2 else 0) > mark - off
 
 
+def one_request(target, drafts, accept, sample, draft=None):
+    """(path, tokens, count) of one root whose other nodes are its children."""
+    n = len(drafts)
+    out = mx.kv_verify_drafts(gpu(np.float32(target)), gpu(np.int32(drafts)), gpu(np.int32([-1] + [0] * (n - 1))), gpu(np.int32([0, n])),
+                              gpu(np.float32(accept)), gpu(np.float32([sample])), draft_probs=None if draft is None else gpu(np.float32(draft)))
+    return out[0].tolist(), out[1].tolist(), int(out[2])
+
+
+@pytest.mark.parametrize("value,vocab,drawn", [(1.0, 1000, True), (1.0, 2, True), (1.0, 3, True), (1.9, 2, True), (1.0, 4095, True), (1.0, 4096, False),
+                                               (1.5, 4000, False), (2.0 ** -10, 1 << 20, True), (1.0, 1 << 20, False), (1.9, 1 << 20, False)])
+def test_verify_reports_sums_of_two_and_above(value, vocab, drawn):
+    """The next token is still drawn as the formula says, up to a sum of 4096."""
+    for sample in (0.0, 0.5, 0.75):
+        path, tokens, count = one_request(np.full((1, vocab), value), [0], [0], sample)
+        reported()
+        assert (path, count) == ([0], 1)
+        assert tokens == [int(sample * vocab) if drawn else -1]
+
+
+def test_verify_does_not_report_sums_below_two():
+    for row in ([1.9375], [1.0, 0.96875], [2.0 ** -10] * 2047, [2.0 ** -19] * ((1 << 20) - 1)):
+        for rejected in (0, 3):  # (sums of the whole row, and of what is behind its first token's whole draft)
+            n, draft = 1 + rejected, np.zeros((1 + rejected, len(row)))
+            draft[:, 0] = 1.96875
+            one_request(np.tile(row, (n, 1)), [0] * n, [1 - 2.0 ** -24] * n, 0.5, draft if rejected else None)
+            ok()
+
+
+@pytest.mark.parametrize("heavy", [2, 9, 500, 60000])
+def test_verify_z_stays_below_two(heavy):
+    """Target 1/4, 1/2 and many of 1.9, draft 3/4 and 1/4: behind the first child's rejection Z is as good as 2, and the second
+    child is accepted below 1/4 / (1/4 2) = 1/2."""
+    target, draft = np.full((3, 2 + heavy), 1.9), np.zeros((3, 2 + heavy))
+    target[:, :2], draft[:, :2] = [0.25, 0.5], [0.75, 0.25]
+    for second in (0.0, 0.2, 0.4, 0.4999, 0.5001, 0.6, 0.9):
+        path, _, _ = one_request(target, [0, 0, 1], [0, 0.5, second], 0.5, draft)
+        reported()
+        assert path == ([0, 2, -1] if second < 0.5 else [0, -1, -1])
+
+
+def test_verify_random_numbers_of_one_and_above_accept_nothing_more():
+    """(Out of contract; with q above 1 as well they passed 64 bits and accepted what a smaller number rejects.)"""
+    for number in (1.0, 1.25, 1.5, 1.9375):
+        path, _, _ = one_request([[0.5, 0.25]] * 2, [0, 0], [0, number], 0.25, [[1.9375, 0]] * 2)
+        assert path == [0, -1]
+    mx.mx_check()
+
+
 # ------------------------------------------------------------------ compaction
 @pytest.mark.parametrize("odd", [float("nan"), float("inf"), float("-inf"), -0.5, 2.0 ** 49, 2.0 ** -49])
 @pytest.mark.parametrize("elem", [mx.E4M3, mx.E5M2])

@@ -4,17 +4,14 @@
 
 namespace {
 
-struct KvSpan {
-  const void* at;
-  size_t bytes;
-};
-// whether an output shares bytes with an input: some CTA may still read what another writes
-bool kv_overlap(std::initializer_list<KvSpan> outputs, std::initializer_list<KvSpan> inputs) {
-  for (const KvSpan& a : outputs)
-    for (const KvSpan& b : inputs) {
-      const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
-      if (a.at && b.at && x < y + b.bytes && y < x + a.bytes) return true;
-    }
+// whether an output shares bytes with an input or with another output: some CTA may still read what another writes
+bool kv_overlap(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
+  for (const Span* a = outputs.begin(); a != outputs.end(); ++a) {
+    for (const Span& b : inputs)
+      if (spans_meet(*a, b)) return true;
+    for (const Span* b = outputs.begin(); b != a; ++b)
+      if (spans_meet(*a, *b)) return true;
+  }
   return false;
 }
 
@@ -178,8 +175,9 @@ mx_status kv_draft_trees(const int32_t* parents, int64_t num_tokens, const int32
   if (num_tokens && (!parents || !tree_mask || !positions)) return MX_ERR_INVALID_ARG;
   if (!aligned(parents, 4) || !aligned(tree_mask, 8) || !aligned(positions, 4)) return MX_ERR_INVALID_ARG;
   if (num_tokens == 0) return MX_OK;
-  const size_t r4 = 4 * requests, t4 = 4 * num_tokens;
-  if (kv_overlap({{tree_mask, 2 * t4 * mask_words}, {positions, t4}}, {{parents, t4}, {lengths, r4}, {q_start, r4 + 4}}))
+  const int64_t r4 = 4 * requests, t4 = 4 * num_tokens;
+  if (kv_overlap({span(tree_mask, 2 * t4 * mask_words), span(positions, t4)},
+                 {span(parents, t4), span(lengths, r4), span(q_start, r4 + 4)}))
     return MX_ERR_INVALID_ARG;
   KvTreesArgs a{};
   a.parents = parents;
@@ -210,9 +208,11 @@ mx_status kv_verify_drafts(const float* target_probs, int64_t target_stride, con
   if (!aligned(target_probs, 4) || !aligned(draft_probs, 4) || !aligned(drafts, 4) || !aligned(parents, 4) ||
       !aligned(accept_random, 4) || !aligned(sample_random, 4) || !aligned(path, 4) || !aligned(tokens, 4) || !aligned(counts, 4))
     return MX_ERR_INVALID_ARG;
-  const size_t r4 = 4 * requests, t4 = 4 * num_tokens;
-  if (kv_overlap({{path, t4}, {tokens, t4}, {counts, r4}},
-                 {{drafts, t4}, {parents, t4}, {q_start, r4 + 4}, {accept_random, t4}, {sample_random, r4}}))
+  const int64_t r4 = 4 * requests, t4 = 4 * num_tokens;
+  if (kv_overlap({span(path, t4), span(tokens, t4), span(counts, r4)},
+                 {span(drafts, t4), span(parents, t4), span(q_start, r4 + 4), span(accept_random, t4), span(sample_random, r4),
+                  span(target_probs, 4 * vocab, num_tokens, 4 * target_stride),
+                  span(draft_probs, 4 * vocab, num_tokens, 4 * draft_stride)}))
     return MX_ERR_INVALID_ARG;
   KvVerifyArgs a{};
   a.target = target_probs;
@@ -268,8 +268,9 @@ mx_status kv_cache_compact(const int32_t* path, const int32_t* counts, int64_t n
       !aligned(v_codes, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(kept_lengths, 4))
     return MX_ERR_INVALID_ARG;
   // (every CTA of a request reads its length and count, and one writes what it keeps)
-  const size_t r4 = 4 * requests, t4 = 4 * num_tokens;
-  if (kv_overlap({{kept_lengths, r4}}, {{lengths, r4}, {counts, r4}, {q_start, r4 + 4}, {path, t4}, {block_tables, r4 * max_blocks}}))
+  const int64_t r4 = 4 * requests, t4 = 4 * num_tokens;
+  if (kv_overlap({span(kept_lengths, r4)}, {span(lengths, r4), span(counts, r4), span(q_start, r4 + 4), span(path, t4),
+                                            span(block_tables, r4 * max_blocks)}))
     return MX_ERR_INVALID_ARG;
   KvCompactArgs a{};
   a.path = path;

@@ -21,6 +21,7 @@
 #include "kv_drafts.cuh"
 #include "kv_prefill.cuh"
 #include "qk_norm.cuh"
+#include "spans.cuh"
 
 using namespace mxgb;
 

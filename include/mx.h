@@ -560,7 +560,7 @@ mx_status qk_norm_rope_backward(const void* dq_out, const void* dk_out, const vo
  *   positions[num_tokens] = lengths[r] - n + depth (a node without parent has depth 0).
  * 64 mask_words >= max_q_len, mask_words <= 16.  A request with a parent out of range gets masks of 0 and positions -1,
  * and is reported.  Rows from q_start[requests] on get the same; rows of requests that are left out are not written.
- * Outputs may not overlap inputs, here and in kv_verify_drafts.
+ * Outputs may not overlap inputs or each other, here and in kv_verify_drafts.
  */
 mx_status kv_draft_trees(const int32_t* parents, int64_t num_tokens, const int32_t* lengths, const int32_t* q_start,
                          int64_t requests, int64_t max_q_len, int64_t window, int64_t* tree_mask, int64_t mask_words,

@@ -6,7 +6,7 @@ import torch
 import block_scaled_precision_mx_gb300 as mx
 from tests import drafts_reference as ref
 from tests import kv_reference as kv
-from tests.test_gpu_drafts import check_verify, gpu, ok, reported
+from tests.test_gpu_drafts import check_verify, gpu, ok, probs, reported
 
 pytestmark = pytest.mark.gpu
 
@@ -124,6 +124,32 @@ def test_verify_random_numbers_of_one_and_above_accept_nothing_more():
         path, _, _ = one_request([[0.5, 0.25]] * 2, [0, 0], [0, number], 0.25, [[1.9375, 0]] * 2)
         assert path == [0, -1]
     mx.mx_check()
+
+
+@pytest.mark.parametrize("certain", [True, False])
+def test_verify_outputs_between_rows_of_probabilities(certain):
+    """Rows apart leave room, which is no input: outputs there are no overlap, and those a row further are."""
+    rng = np.random.RandomState(7)
+    t, vocab, pad = 9, 601, 200
+    base = [torch.zeros(t, vocab + pad, device="cuda") for _ in range(2)]
+    for b in base:
+        b[:, :vocab] = gpu(probs(rng, t, vocab))
+    target, draft = (b[:, :vocab] for b in base)
+    rest = (gpu(rng.randint(0, vocab, t), torch.int32), gpu(np.int32([-1, 0, 0, 1, 2, 0, 1, 5, 3])), gpu(np.int32([0, t])),
+            gpu(rng.rand(t).astype(np.float32)), gpu(rng.rand(1).astype(np.float32)))
+    draft = None if certain else draft
+    want = mx.kv_verify_drafts(target, *rest, draft_probs=draft)
+    words = [b.view(torch.int32) for b in base]
+    got = mx.kv_verify_drafts(target, *rest, draft_probs=draft, path=words[0][3, vocab:vocab + t], tokens=words[1][0, vocab + pad - t:],
+                              counts=words[0][3, vocab + t:vocab + t + 1])
+    ok()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for place in (words[0][3, vocab - 1:vocab - 1 + t], words[0].view(-1)[vocab + pad - 1:vocab + pad - 1 + t]):
+        with pytest.raises(mx.MxError):
+            mx.kv_verify_drafts(target, *rest, draft_probs=draft, tokens=place)
+    with pytest.raises(mx.MxError):
+        mx.kv_verify_drafts(target, *rest, draft_probs=draft, path=got[0], tokens=got[0])
+    ok()
 
 
 # ------------------------------------------------------------------ compaction

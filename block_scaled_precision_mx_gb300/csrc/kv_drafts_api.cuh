@@ -44,6 +44,40 @@ bool qk_norm_ok(mx_half type, int64_t num_tokens, int64_t heads, int64_t kv_head
 bool qk_rows_ok(const void* x, int64_t tokens, int64_t heads, int64_t st, int64_t sh) {
   return tokens == 0 || heads == 0 || (x && aligned(x, 16) && st % 8 == 0 && sh % 8 == 0);
 }
+// Rows of 16-bit values: queries, keys, their results or gradients.
+struct QkRows {
+  const void* at;
+  int64_t heads, st, sh;
+};
+// Outputs i = 0, 1 (queries, keys) may be their own inputs, which the same lanes read in front of that; else no output
+// shares bytes with an input or another output, nor its rows with each other.
+bool qk_apart(int64_t tokens, int head_dim, const QkRows (&out)[2], std::initializer_list<QkRows> in0, std::initializer_list<QkRows> in1,
+              std::initializer_list<Span> more_out, std::initializer_list<Span> more_in) {
+  auto rows = [&](const QkRows& r) { return span(r.at, 2 * head_dim, tokens, 2 * r.st, r.heads, 2 * r.sh); };
+  auto same = [&](const QkRows& a, const QkRows& b) {
+    return a.at == b.at && (tokens == 1 || a.st == b.st) && (a.heads == 1 || a.sh == b.sh);
+  };
+  const Span spans[2] = {rows(out[0]), rows(out[1])};
+  for (int i = 0; i < 2; ++i) {
+    if (spans[i].n[0] == 0) continue;
+    if (!rows_apart(2 * head_dim, tokens, 2 * out[i].st, out[i].heads, 2 * out[i].sh)) return false;
+    for (const QkRows& r : in0)
+      if ((i || !same(out[i], r)) && spans_meet(spans[i], rows(r))) return false;
+    for (const QkRows& r : in1)
+      if ((!i || !same(out[i], r)) && spans_meet(spans[i], rows(r))) return false;
+    for (const Span& x : more_in)
+      if (spans_meet(spans[i], x)) return false;
+    for (const Span& x : more_out)
+      if (spans_meet(spans[i], x)) return false;
+  }
+  for (const Span& o : more_out) {
+    for (const QkRows& r : in0)
+      if (spans_meet(o, rows(r))) return false;
+    for (const QkRows& r : in1)
+      if (spans_meet(o, rows(r))) return false;
+  }
+  return !spans_meet(spans[0], spans[1]) && !kv_overlap(more_out, more_in);
+}
 template <bool BACK, int LANES, bool F16, bool INTER, int HEADS>
 mx_status qk_norm_launch_as(const QkNormArgs& a, cudaStream_t st, int64_t* ctas) {
   constexpr int kAtOnce = 32 / LANES * HEADS;
@@ -92,6 +126,13 @@ mx_status qk_norm_rope(const void* q, const void* k, mx_half type, int64_t num_t
       !qk_rows_ok(k_out, num_tokens, kv_heads, k_out_stride_token, k_out_stride_head))
     return MX_ERR_INVALID_ARG;
   if (num_tokens == 0) return MX_OK;
+  const int64_t weight_bytes = (weight_f32 ? 4 : 2) * static_cast<int64_t>(head_dim);
+  if (!qk_apart(num_tokens, head_dim,
+                {{q_out, heads, q_out_stride_token, q_out_stride_head}, {k_out, kv_heads, k_out_stride_token, k_out_stride_head}},
+                {{q, heads, q_stride_token, q_stride_head}}, {{k, kv_heads, k_stride_token, k_stride_head}}, {},
+                {span(q_weight, weight_bytes), span(kv_heads ? k_weight : nullptr, weight_bytes),
+                 span(rot_dim ? cos_sin : nullptr, 4 * max_positions * rot_dim), span(positions, 4 * num_tokens)}))
+    return MX_ERR_INVALID_ARG;
   QkNormArgs a{};
   a.x[0] = static_cast<const uint16_t*>(q);
   a.x[1] = static_cast<const uint16_t*>(k);
@@ -133,6 +174,15 @@ mx_status qk_norm_rope_backward(const void* dq_out, const void* dk_out, const vo
       !qk_rows_ok(dk, num_tokens, kv_heads, dk_stride_token, dk_stride_head))
     return MX_ERR_INVALID_ARG;
   if (!dq_weight || !dk_weight || !workspace || !aligned(dq_weight, 4) || !aligned(dk_weight, 4) || !aligned(workspace, 16))
+    return MX_ERR_INVALID_ARG;
+  const int64_t weight_bytes = (weight_f32 ? 4 : 2) * static_cast<int64_t>(head_dim);
+  if (!qk_apart(num_tokens, head_dim, {{dq, heads, dq_stride_token, dq_stride_head}, {dk, kv_heads, dk_stride_token, dk_stride_head}},
+                {{dq_out, heads, dq_out_stride_token, dq_out_stride_head}, {q, heads, q_stride_token, q_stride_head}},
+                {{dk_out, kv_heads, dk_out_stride_token, dk_out_stride_head}, {k, kv_heads, k_stride_token, k_stride_head}},
+                {span(dq_weight, 4 * static_cast<int64_t>(head_dim)), span(dk_weight, 4 * static_cast<int64_t>(head_dim)),
+                 span(workspace, static_cast<int64_t>(qk_norm_rope_workspace_bytes(head_dim)))},
+                {span(q_weight, weight_bytes), span(kv_heads ? k_weight : nullptr, weight_bytes),
+                 span(rot_dim ? cos_sin : nullptr, 4 * max_positions * rot_dim), span(positions, 4 * num_tokens)}))
     return MX_ERR_INVALID_ARG;
   QkNormArgs a{};
   a.x[0] = static_cast<const uint16_t*>(q);

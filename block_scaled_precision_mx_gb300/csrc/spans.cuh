@@ -66,6 +66,23 @@ inline bool spans_meet_in_step(const Span& a, const Span& b, int64_t step0, int6
   return false;
 }
 
+// Whether rows of one tensor share no bytes with each other (n and steps as span takes them).
+inline bool rows_apart(int64_t bytes, int64_t n0, int64_t step0, int64_t n1, int64_t step1) {
+  if ((n0 > 1 && step0 == 0) || (n1 > 1 && step1 == 0)) return n0 < 1 || n1 < 1;
+  const Span s = span(reinterpret_cast<const void*>(uintptr_t(1) << 62), bytes, n0, step0, n1, step1);
+  if (s.n[0] == 0) return true;
+  if (s.n[1] > 1 && s.step[1] < bytes) return false;
+  const int64_t lo1 = (s.n[1] - 1) * s.step[1];
+  for (int64_t i = 1; i < s.n[0] && i * s.step[0] - lo1 < bytes; ++i) {  // i rows on, and up to lo1 back
+    if (i * s.step[0] < bytes) return false;
+    if (s.n[1] > 1 && span_floor(i * s.step[0] + bytes - 1, s.step[1]) >= span_ceil(i * s.step[0] - bytes + 1, s.step[1])) {
+      const int64_t j = span_ceil(i * s.step[0] - bytes + 1, s.step[1]);  // the least number of steps back that meets
+      if (j <= s.n[1] - 1) return false;
+    }
+  }
+  return true;
+}
+
 // Whether a and b share a byte.
 inline bool spans_meet(const Span& a, const Span& b) {
   if (a.n[0] == 0 || b.n[0] == 0) return false;

@@ -504,7 +504,8 @@ mx_status kv_attention(const void* q, mx_half type, int64_t num_tokens, int64_t 
  * q, k: num_tokens tokens of heads (kv_heads) heads of head_dim values, bf16 or fp16, 16-byte aligned, values
  * contiguous, token and head strides (in elements) multiples of 8: slices of a fused projection will do.  kv_heads may
  * be 0 (k, k_weight and k_out NULL then).  num_tokens (heads + kv_heads) is at most 2^31 - 1.  head_dim is a multiple of 8, at most 256.  Outputs have strides of their own
- * and may be the inputs themselves (same address and strides); they may not overlap them otherwise.
+ * and may be the inputs themselves (q_out q, k_out k: same address and strides); otherwise they may not overlap an input,
+ * each other or themselves (slices of one buffer do not).
  * q_weight, k_weight [head_dim], 16-byte aligned: x's type, or FP32 with weight_f32 = 1.
  * cos_sin float [max_positions][rot_dim], 16-byte aligned: rot_dim / 2 cosines of a position's angles, then their sines.
  * R turns the first rot_dim values of a head (a multiple of 16; 0: none, and cos_sin may be NULL), as pairs
@@ -526,7 +527,8 @@ size_t qk_norm_rope_workspace_bytes(int head_dim);
  * qk_norm_rope_backward -- gradients of qk_norm_rope with respect to q, k and the weights.  With g = R(p)^T dy, xh = x r:
  *   dx = r (w g - xh mean(w g xh)),   dw = sum over tokens and heads of g xh.
  * dq_out, dk_out: the results' gradients; q, k: the forward pass's inputs (not its results); all as there, with their own
- * strides.  dq, dk may be dq_out, dk_out themselves, or q, k.  A token that the forward pass left out gets zeros in dq
+ * strides.  dq, dk may be dq_out, dk_out themselves, or q, k; otherwise no output, nor the workspace, may overlap an
+ * input, another output or itself.  A token that the forward pass left out gets zeros in dq
  * and dk and adds nothing to the weights' gradients, dq_weight and dk_weight, float [head_dim], which are written, not
  * added to, in an order of sums that depends on the sizes alone.  workspace: qk_norm_rope_workspace_bytes bytes, 16-byte
  * aligned, contents need not be initialised; calls that may overlap need one each.  Calls from several host threads on

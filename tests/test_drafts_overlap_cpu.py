@@ -45,3 +45,37 @@ def test_trees(lib):
         return lib.kv_draft_trees(a["parents"], 40, a["lengths"], a["q_start"], 4, 16, 0, a["mask"], 2, a["pos"], None)
     refused(call, ok, [{"pos": ok["mask"]}, {"pos": ok["mask"] + 636}, {"mask": ok["pos"] - 632}, {"mask": ok["pos"] + 152},
                        {"pos": ok["parents"] + 156}, {"mask": ok["q_start"] + 16}])
+
+
+# tokens 4, 32 + 8 heads of 128, contiguous: 32768 and 8192 bytes; 100 positions of 128 angles
+NORM = dict(tokens=4, heads=32, kv_heads=8, d=128, wf32=0, qst=4096, kst=1024, qost=4096, kost=1024)
+
+
+def test_norm(lib):
+    ok = dict(NORM, **apart(["q", "k", "qw", "kw", "table", "pos", "qo", "ko"]))
+
+    def call(**a):
+        return lib.qk_norm_rope(a["q"], a["k"], 0, a["tokens"], a["heads"], a["kv_heads"], a["d"], a["qst"], 128, a["kst"], 128, a["qw"],
+                                a["kw"], a["wf32"], a["table"], 100, 128, a["pos"], 1e-6, 0, a["qo"], a["ko"], a["qost"], 128,
+                                a["kost"], 128, None)
+    refused(call, ok, [{"qo": ok[i]} for i in ("k", "qw", "kw", "table", "pos", "ko")] + [{"ko": ok[i]} for i in ("q", "qw", "kw", "table", "pos")]
+            + [{"qo": ok["q"] + 16}, {"qo": ok["q"] - 16}, {"qo": ok["q"] + 32768 - 16}, {"qo": ok["q"], "qost": 5120},
+               {"qst": 5120, "qo": ok["q"] + 256}, {"ko": ok["k"], "kost": 2048}, {"qo": ok["table"] + 4 * 100 * 128 - 16},
+               {"qo": ok["qw"] + 240}, {"wf32": 1, "qo": ok["qw"] + 496}, {"k": ok["q"], "qo": ok["q"]},
+               {"qo": ok["ko"] - 32768 + 16}, {"qost": 4088}, {"qost": 0}, {"kost": 8}])
+
+
+def test_norm_backward(lib):
+    ok = dict(NORM, **apart(["gq", "gk", "q", "k", "qw", "kw", "table", "pos", "qo", "ko", "dqw", "dkw", "ws"]))
+
+    def call(**a):
+        return lib.qk_norm_rope_backward(a["gq"], a["gk"], a["q"], a["k"], 0, a["tokens"], a["heads"], a["kv_heads"], a["d"], 4096, 128,
+                                         1024, 128, a["qst"], 128, a["kst"], 128, a["qw"], a["kw"], a["wf32"], a["table"], 100, 128,
+                                         a["pos"], 1e-6, 0, a["qo"], a["ko"], a["qost"], 128, a["kost"], 128, a["dqw"], a["dkw"], a["ws"],
+                                         None)
+    inputs = ("gq", "gk", "q", "k", "qw", "kw", "table", "pos")
+    refused(call, ok, [{o: ok[i]} for o in ("dqw", "dkw", "ws") for i in inputs + ("qo", "ko")]
+            + [{"qo": ok[i]} for i in ("gk", "k", "qw", "kw", "table", "pos", "ko")] + [{"ko": ok[i]} for i in ("gq", "q", "qw", "table", "pos")]
+            + [{"qo": ok["gq"] + 16}, {"qo": ok["q"] - 16}, {"qo": ok["gq"], "qost": 5120}, {"ko": ok["gk"], "kost": 2048},
+               {"dqw": ok["dkw"]}, {"dqw": ok["dkw"] - 508}, {"dqw": ok["ws"] + 64}, {"dkw": ok["ws"] + mx.load().qk_norm_rope_workspace_bytes(128) - 4},
+               {"gk": ok["gq"], "qo": ok["gq"]}, {"qost": 0}, {"kost": 8}, {"tokens": 0, "dqw": ok["dkw"]}])

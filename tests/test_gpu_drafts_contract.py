@@ -6,7 +6,7 @@ import torch
 import block_scaled_precision_mx_gb300 as mx
 from tests import drafts_reference as ref
 from tests import kv_reference as kv
-from tests.test_gpu_drafts import check_verify, gpu, ok, probs, reported
+from tests.test_gpu_drafts import check_verify, gpu, ok, probs, reported, rotation, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -16,6 +16,47 @@ def built():
     import __graft_entry__
     __graft_entry__.build()
     torch.cuda.set_device(0)
+
+
+# ------------------------------------------------------------------ norm and rotation
+@pytest.mark.parametrize("tokens,heads,kv_heads", [(1, 4, 2), (5, 1, 1), (37, 8, 1), (130, 3, 3)])
+@pytest.mark.parametrize("order", ["tokens", "heads"])
+def test_norm_in_place_and_between_each_other(order, tokens, heads, kv_heads):
+    """Queries, keys and others in one buffer, by tokens or by heads first: over themselves, over the place of others, and
+    over the results' gradients, which all give what separate tensors do; anything else that shares bytes is refused."""
+    rng = np.random.RandomState(tokens)
+    d, all_heads = 64, 2 * (heads + kv_heads) + 1
+    buf = rows(rng, (tokens, all_heads, d) if order == "tokens" else (all_heads, tokens, d), torch.bfloat16).cuda()
+
+    def split(b):
+        return (b if order == "tokens" else b.transpose(0, 1)).split([heads, kv_heads, heads, kv_heads, 1], dim=1)
+    q, k, q2, k2, _ = split(buf)
+    w, table, positions = torch.ones(d, device="cuda"), gpu(rotation(50, d)), gpu(rng.randint(0, 50, tokens), torch.int32)
+    want = mx.qk_norm_rope(q.contiguous(), k.contiguous(), w, w, table, positions)
+    back = mx.qk_norm_rope_backward(q2.contiguous(), k2.contiguous(), q.contiguous(), k.contiguous(), w, w, table, positions)
+
+    def same(got, expected):
+        ok()
+        assert all(torch.equal(a, b) for a, b in zip(got, expected))
+    for places in ((0, 1), (2, 3), (0, 3), (2, 1)):  # (what the results may lie over: queries on queries, keys on keys)
+        parts = split(buf.clone())
+        same(mx.qk_norm_rope(parts[0], parts[1], w, w, table, positions, q_out=parts[places[0]], k_out=parts[places[1]]), want)
+        assert torch.equal(parts[4], split(buf)[4])
+        parts = split(buf.clone())
+        same(mx.qk_norm_rope_backward(parts[2], parts[3], parts[0], parts[1], w, w, table, positions, dq=parts[places[0]], dk=parts[places[1]]), back)
+        assert torch.equal(parts[4], split(buf)[4])
+    narrow = q[:, :1], k[:, :1]
+    with pytest.raises(mx.MxError):
+        mx.qk_norm_rope(*narrow, w, w, table, positions, q_out=narrow[1], k_out=narrow[0])
+    with pytest.raises(mx.MxError):
+        mx.qk_norm_rope(*narrow, w, w, table, positions, q_out=narrow[0], k_out=narrow[0])
+    with pytest.raises(mx.MxError):
+        mx.qk_norm_rope(*narrow, w, w, table, positions, q_out=torch.empty(1, 1, d, dtype=q.dtype, device="cuda").expand(tokens, 1, d)
+                        if tokens > 1 else narrow[1])
+    with pytest.raises(mx.MxError):
+        mx.qk_norm_rope_backward(q, k, q, k, w, w, table, positions, dq_weight=w)
+    ok()
+    assert torch.equal(mx.qk_norm_rope(q, k, w, w, table, positions)[0], want[0])  # (nothing was written)
 
 
 # ------------------------------------------------------------------ verification

@@ -19,6 +19,7 @@ using mxgb::span;
 extern "C" int meet(const int64_t* a, const int64_t* b) {
   return mxgb::spans_meet(span((const void*)a[0], a[1], a[2], a[3], a[4], a[5]), span((const void*)b[0], b[1], b[2], b[3], b[4], b[5]));
 }
+extern "C" int apart(const int64_t* a) { return mxgb::rows_apart(a[1], a[2], a[3], a[4], a[5]); }
 """)
     lib = str(d / "spans.so")
     subprocess.check_call(["g++", "-O1", "-std=c++17", "-fPIC", "-shared", "-I", CSRC, str(d / "spans.cc"), "-o", lib])
@@ -60,6 +61,15 @@ def test_slices_of_a_projection(lib):
         for (h0, n0), (h1, n1) in itertools.product(parts, parts):
             a, b = ((AT + h * steps[1], size, tokens, steps[0], n, steps[1]) for h, n in ((h0, n0), (h1, n1)))
             assert asked(lib, a, b) == (h0 < h1 + n1 and h1 < h0 + n0)
+
+
+def test_rows_of_one_tensor(lib):
+    rng, found = np.random.RandomState(1), []
+    for _ in range(30000):
+        s = (AT, int(rng.randint(1, 9)), int(rng.randint(0, 5)), int(rng.randint(-30, 31)), int(rng.randint(0, 5)), int(rng.randint(-30, 31)))
+        found.append(len(covered(s)) == s[1] * s[2] * s[4])
+        assert bool(lib.apart((ctypes.c_int64 * 6)(*s))) == found[-1], s
+    assert 0.2 < np.mean(found) < 0.9
 
 
 def test_none_and_empty_ones_meet_nothing(lib):

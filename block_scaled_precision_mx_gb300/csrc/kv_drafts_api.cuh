@@ -319,8 +319,11 @@ mx_status kv_cache_compact(const int32_t* path, const int32_t* counts, int64_t n
     return MX_ERR_INVALID_ARG;
   // (every CTA of a request reads its length and count, and one writes what it keeps)
   const int64_t r4 = 4 * requests, t4 = 4 * num_tokens;
-  if (kv_overlap({span(kept_lengths, r4)}, {span(lengths, r4), span(counts, r4), span(q_start, r4 + 4), span(path, t4),
-                                            span(block_tables, r4 * max_blocks)}))
+  // (and keys' and values' warps move without looking at each other)
+  const int64_t heads_of_blocks = num_blocks * kv_heads, code_bytes = heads_of_blocks * block_tokens * head_dim;
+  if (kv_overlap({span(kept_lengths, r4), span(k_codes, code_bytes), span(v_codes, code_bytes), span(k_scale, 4 * heads_of_blocks),
+                  span(v_scale, 4 * heads_of_blocks)},
+                 {span(lengths, r4), span(counts, r4), span(q_start, r4 + 4), span(path, t4), span(block_tables, r4 * max_blocks)}))
     return MX_ERR_INVALID_ARG;
   KvCompactArgs a{};
   a.path = path;

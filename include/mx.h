@@ -626,8 +626,8 @@ mx_status kv_verify_drafts(const float* target_probs, int64_t target_stride, con
  * same scale move as they are.  A block of scale 0 takes the run's own.  Codes from kept_lengths[r] on are left as
  * they were.  A request whose path, counts, blocks, length or starts break their contract is left as it is, keeps
  * lengths[r] and is reported.  Tokens of a block whose scale is out of range become NaN, and have no part in the scale
- * of the block that they move to; a run into such a block is left out; both are reported.  No two requests have a block that is written to in common.  kept_lengths may not
- * overlap an input.
+ * of the block that they move to; a run into such a block is left out; both are reported.  No two requests have a block that is written to in common.  kept_lengths and the keys',
+ * values' and scales' tensors may not overlap each other or an input.
  */
 mx_status kv_cache_compact(const int32_t* path, const int32_t* counts, int64_t num_tokens, const int32_t* lengths,
                            const int32_t* q_start, int64_t requests, const int32_t* block_tables, int64_t max_blocks,

@@ -79,3 +79,16 @@ def test_norm_backward(lib):
             + [{"qo": ok["gq"] + 16}, {"qo": ok["q"] - 16}, {"qo": ok["gq"], "qost": 5120}, {"ko": ok["gk"], "kost": 2048},
                {"dqw": ok["dkw"]}, {"dqw": ok["dkw"] - 508}, {"dqw": ok["ws"] + 64}, {"dkw": ok["ws"] + mx.load().qk_norm_rope_workspace_bytes(128) - 4},
                {"gk": ok["gq"], "qo": ok["gq"]}, {"qost": 0}, {"kost": 8}, {"tokens": 0, "dqw": ok["dkw"]}])
+
+
+def test_compact(lib):
+    inputs, outputs = ("path", "counts", "lengths", "q_start", "tables"), ("kc", "vc", "ks", "vs", "kept")
+    ok = apart(inputs + outputs)
+    codes, scales = 16 * 8 * 64 * 128, 4 * 16 * 8
+
+    def call(**a):
+        return lib.kv_cache_compact(a["path"], a["counts"], 40, a["lengths"], a["q_start"], 4, a["tables"], 8, a["kc"], a["vc"], a["ks"],
+                                    a["vs"], 0, 16, 8, 64, 128, a["kept"], None)
+    refused(call, ok, [{o: ok[i]} for o in outputs for i in inputs] + [{a: ok[b]} for a in outputs for b in outputs if a != b]
+            + [{"kc": ok["vc"] + codes - 16}, {"kc": ok["vc"] - codes + 16}, {"ks": ok["vs"] + scales - 4}, {"ks": ok["vc"] + codes - 4},
+               {"kept": ok["vs"] + scales - 4}, {"kept": ok["kc"] - 12}])

@@ -108,7 +108,8 @@ constexpr int kKvVerifyMostCluster = 8;
 // A row's sums are of whole multiples of 2^-44, to which each P is rounded: they come out the same in any order and on any
 // number of CTAs, and are off by 2^-45 an entry and a little, all of them the same way where the entries are alike (128256:
 // 4e-9 at worst; 1e-11 where the roundings are independent).  Sums in 64-bit floating point would be nearer, but their unit
-// runs at 2 a cycle and SM (a row of 128256 would take it 100 us).  Single numbers are kept in units of 2^-60, cut off there.
+// runs at 2 a cycle and SM (a row of 128256 would take it 100 us).  Single numbers are kept in units of 2^-60, cut off there:
+// of 1 in sums, of the larger of p and q in a test.
 constexpr uint64_t kKvOne = 1ull << 60, kKvTakenOne = 1ull << 53;  // 1 so; 1 in W's units
 // A sum of P is below 2, or the row is no distribution, which is told.  Z stays below 2 then, so that no product of it passes
 // 64 bits, and so does what a number in [0, 2) is times a probability; a warp's part of a sum (below 2^63) stays below
@@ -131,6 +132,11 @@ __device__ __forceinline__ uint64_t kv_fixed(float p) {
   uint64_t r;
   asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"(static_cast<uint64_t>(m) << 32), "r"(130u - e));  // (64 and more: 0)
   return r;
+}
+// the power of two that brings the larger of two into [1, 2) (of two below 2^-126, near to it)
+__device__ __forceinline__ float kv_near_one(float p, float q) {
+  const uint32_t e = __float_as_uint(fmaxf(fabsf(p), fabsf(q))) >> 23;
+  return __uint_as_float((e ? 254 - e : 253) << 23);
 }
 // max(p - W q, 0) of numbers so kept, W in units of 2^-53.  W grows with every rejected sibling, so W q may be far
 // past what 64 bits hold of it; from 4 on no p comes near it.
@@ -397,15 +403,18 @@ __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const Kv
       }
       const int i = i0 + __ffs(children) - 1;
       i0 = i + 1;
-      uint64_t p = kv_fixed(sm.p[i]), mark = kv_fixed(sm.random[i]);
+      // r q Z < max(p - W q, 0) holds as well for p and q times a power of two (r and p, of a certain draft): so large that
+      // 2^-60 of the larger one is what is cut off, for tokens that are next to impossible too
+      const float r = sm.random[i], by = CERTAIN ? r : sm.q[i], up = kv_near_one(sm.p[i], by);
+      uint64_t p = kv_fixed(sm.p[i] * up), mark = kv_fixed(by * up);
       if (CERTAIN) {
         bool again = false;
         for (int j = node + 1 + lane; j < i; j += 32) again = again || (sm.up[j] == node && sm.token[j] == sm.token[i]);
         if (__any_sync(0xFFFFFFFFu, again)) p = 0;
       } else {
-        const uint64_t q = kv_fixed(sm.q[i]);
-        if (taken) p = kv_residual(p, q, taken);
-        mark = min(static_cast<uint64_t>(__umul64hi(mark << 3, q << 3) >> 2), 2 * kKvOne - 1);
+        if (taken) p = kv_residual(p, mark, taken);
+        else if (sm.p[i] > 0.f) p = max(p, static_cast<uint64_t>(1));  // (more than r = 0)
+        mark = min(static_cast<uint64_t>(__umul64hi(mark << 3, kv_fixed(r) << 3) >> 2), 2 * kKvOne - 1);
       }
       mark = __umul64hi(mark << 3, left << 3) >> 2;
       if (mark < p) {
@@ -416,7 +425,7 @@ __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const Kv
         taken = 0;
         summed = false;
       } else if (CERTAIN) {
-        left -= min(p, left);
+        if (p) left -= min(kv_fixed(sm.p[i]), left);
       } else {
         taken += left >> 7;
         rejected = true;

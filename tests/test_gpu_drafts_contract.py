@@ -119,6 +119,29 @@ def test_verify_sums_of_many_tiny_probabilities(rejected, share):
         assert (token + 1) * tiny + (0.5 if token >= vocab - 2 else 0) > mark - off
 
 
+@pytest.mark.parametrize("certain", [True, False])
+@pytest.mark.parametrize("power", [-30, -70, -100, -130])
+def test_verify_tokens_that_are_next_to_impossible(power, certain):
+    """Probabilities of a few times 2^power beside one large: the test is of their ratio, however small both are, and exactly
+    so (of certain drafts: of the random number and the probability)."""
+    rng = np.random.RandomState(-power)
+    vocab, n, kept = 6, 9, []
+    for trial in range(200):
+        target, draft = (rng.randint(0, 64, (n, vocab)) * 2.0 ** power for _ in range(2))
+        target[:, -1], draft[:, -1] = 1, 0.5
+        drafts = rng.randint(0, vocab, n).astype(np.int32)
+        if not certain and trial % 2:
+            drafts[1] = vocab - 2  # rejected: its W leaves p - W q of the others
+            target[0, vocab - 2] = 0
+        accept = rng.randint(0, 64, n) * 2.0 ** (power if certain else -6)
+        accept[rng.rand(n) < 0.1] = 0
+        parents = np.array([-1] + [min(i - 1, rng.randint(0, 3)) for i in range(1, n)], np.int32)
+        want = check_verify([n], vocab, certain, target=target.astype(np.float32), draft=None if certain else draft.astype(np.float32), drafts=drafts,
+                            parents=parents, accept=accept.astype(np.float32), sample=np.float32([rng.randint(8, 64) / 64]))
+        kept.append(int(want[2][0]))
+    assert len(set(kept)) > 2  # (a word on the inputs)
+
+
 def one_request(target, drafts, accept, sample, draft=None):
     """(path, tokens, count) of one root whose other nodes are its children."""
     n = len(drafts)

@@ -139,11 +139,11 @@ __device__ __forceinline__ float kv_near_one(float p, float q) {
   return __uint_as_float((e ? 254 - e : 253) << 23);
 }
 // max(p - W q, 0) of numbers so kept, W in units of 2^-53.  W grows with every rejected sibling, so W q may be far
-// past what 64 bits hold of it; from 4 on no p comes near it.
+// past what 64 bits hold of it: it is compared before it is shifted.
 __device__ __forceinline__ uint64_t kv_residual(uint64_t p, uint64_t q, uint64_t taken) {
   if (taken == kKvTakenOne) return p > q ? p - q : 0;
   const uint64_t high = __umul64hi(taken, q << 3);  // W q in units of 2^-52
-  return high < 1ull << 54 && p > high << 8 ? p - (high << 8) : 0;
+  return p >> 8 >= high ? p - (high << 8) : 0;
 }
 
 // Sums of P, in two limbs: units of 2^-22, and of 2^-44 (signed).  A number plus 2 has the first in its last bits, and what

@@ -9,6 +9,8 @@
 //
 // With a tree of drafted tokens (the kernels' TREE) the Q newest tokens are a tree's nodes: a query sees, of the
 // C = L - Q tokens in front of them, j > position - window, and of the nodes those whose bits its row of the mask has.
+// (64 requests over 4096 tokens, D = 128, 8 kv heads, trees against chains: 4 rows a kv head 91.5 and 90.8 us, 16 rows 115 and
+// 113; floor 79.)
 #pragma once
 
 #include <cmath>

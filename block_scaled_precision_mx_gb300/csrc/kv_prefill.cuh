@@ -20,7 +20,7 @@
 // folded into the exponent, and the reference m is renewed only when a score passes it by 8; the row's O in
 // tensor memory is then rescaled by its own thread, between two products.
 //
-// Measured (D = 128, 32 query and 8 kv heads, E4M3): 4096 queries over 32768 tokens 1.59 ms, 1.29 PFLOP/s, 0.66 of the
+// Measured (D = 128, 32 query and 8 kv heads, E4M3): 4096 queries over 32768 tokens 1.60 ms, 1.29 PFLOP/s, 0.66 of the
 // measured bf16 rate; 6 prompts of 711 to 1500 tokens 193 us (872 units of 11 tiles; 75 us of products).
 // What bounds it: a tile's products are 2048 cycles, but a half's chain of softmax (~2300 cycles: maximum 560,
 // weights 1260, waits), its P V and its next S is ~3700, because S and P share tensor memory (O and S of two halves fill it) and S(i + 1) has to follow P(i) V; and shared memory carries 320 KB a tile (2560

@@ -161,6 +161,19 @@ def test_verify_reports_sums_of_two_and_above(value, vocab, drawn):
         assert tokens == [int(sample * vocab) if drawn else -1]
 
 
+@pytest.mark.parametrize("requests", [39, 77, 153, 400])
+def test_verify_far_sums_of_many_requests(requests):
+    """(With fewer CTAs a request each sums more of a row.)"""
+    for vocab, value in ((1 << 20, 1.9375), (1 << 20, 2.0 ** -9), (2048, 1.9375)):
+        target = torch.full((requests, vocab), value, device="cuda")
+        none = gpu(np.full(requests, -1, np.int32))
+        path, tokens, counts = mx.kv_verify_drafts(target, none, none, gpu(np.arange(requests + 1, dtype=np.int32)),
+                                                   torch.zeros(requests, device="cuda"), torch.full((requests,), 0.5, device="cuda"))
+        reported()
+        assert (counts == 1).all() and (path == 0).all()
+        assert (tokens == (vocab // 2 if value * vocab < 4096 else -1)).all()
+
+
 def test_verify_does_not_report_sums_below_two():
     for row in ([1.9375], [1.0, 0.96875], [2.0 ** -10] * 2047, [2.0 ** -19] * ((1 << 20) - 1)):
         for rejected in (0, 3):  # (sums of the whole row, and of what is behind its first token's whole draft)

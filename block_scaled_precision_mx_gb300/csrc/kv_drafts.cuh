@@ -225,9 +225,10 @@ __device__ __forceinline__ float4 kv_row4(const float* row, int v0, int vocab, b
 // it waits for memory once.  A row's sum is taken in segments of 512, a warp each, 16 bytes a lane and load; the CTAs'
 // sums meet in distributed shared memory, and the last sum's segments say where the next token is, which one warp
 // then finds.  64 requests with chains of 5 over 128256 tokens: 20.6 us, 3.2 TB/s, 0.47 of the measured copy rate; one with
-// 26 nodes over 32000: 8.3 us; 16 with 60 nodes, most of them rejected, 25.1 us.  What bounds it is the chain starts - nodes - two probabilities - rows - meeting - segment,
-// about 8 us, in front of and behind the 10 us that the rows take.  (Two CTAs of 256 threads a SM, whose loads all fit
-// their registers: three or four CTAs 24 us, two of 512 threads 23; the sums in three places of the code, 32.)
+// 26 nodes over 32000: 8.3 us; 16 with 60 nodes, most of them rejected, 25.1 us.  What bounds it is the chain starts
+// - nodes - two probabilities - rows - meeting - segment, about 8 us, in front of and behind the 10 us that the rows
+// take.  (Two CTAs of 256 threads a SM, whose loads all fit their registers: three or four CTAs 24 us, two of 512
+// threads 23; the sums in three places of the code, 32.)
 template <bool CERTAIN>
 __global__ void __launch_bounds__(kKvVerifyThreads, 2) kv_verify_kernel(const KvVerifyArgs a) {
   pdl_prologue();

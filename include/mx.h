@@ -526,13 +526,13 @@ size_t qk_norm_rope_workspace_bytes(int head_dim);
 /*
  * qk_norm_rope_backward -- gradients of qk_norm_rope with respect to q, k and the weights.  With g = R(p)^T dy, xh = x r:
  *   dx = r (w g - xh mean(w g xh)),   dw = sum over tokens and heads of g xh.
- * dq_out, dk_out: the results' gradients; q, k: the forward pass's inputs (not its results); all as there, with their own
- * strides.  dq, dk may be dq_out, dk_out themselves, or q, k; otherwise no output, nor the workspace, may overlap an
- * input, another output or itself.  A token that the forward pass left out gets zeros in dq
- * and dk and adds nothing to the weights' gradients, dq_weight and dk_weight, float [head_dim], which are written, not
- * added to, in an order of sums that depends on the sizes alone.  workspace: qk_norm_rope_workspace_bytes bytes, 16-byte
- * aligned, contents need not be initialised; calls that may overlap need one each.  Calls from several host threads on
- * one stream do not overlap, and may share one.
+ * dq_out, dk_out: the results' gradients; q, k: the forward pass's inputs (not its results); all as there, with their
+ * own strides.  dq, dk may be dq_out, dk_out themselves, or q, k; otherwise no output, nor the workspace, may overlap
+ * an input, another output or itself.  A token that the forward pass left out gets zeros in dq and dk and adds nothing
+ * to the weights' gradients, dq_weight and dk_weight, float [head_dim], which are written, not added to, in an order of
+ * sums that depends on the sizes alone.  workspace: qk_norm_rope_workspace_bytes bytes, 16-byte aligned, contents need
+ * not be initialised; calls that may overlap need one each.  Calls from several host threads on one stream do not
+ * overlap, and may share one.
  */
 mx_status qk_norm_rope_backward(const void* dq_out, const void* dk_out, const void* q, const void* k, mx_half type,
                                 int64_t num_tokens, int64_t heads, int64_t kv_heads, int head_dim,
@@ -604,10 +604,11 @@ mx_status kv_tree_attention(const void* q, mx_half type, int64_t num_tokens, int
  *   path[..] = the accepted nodes, the root first, then -1;
  *   tokens[..] = the accepted drafts and then the next token, counts[r] of them, then -1.
  * Rows from q_start[requests] on get -1.  Sums are of whole multiples of 2^-44, to which each P is rounded: no order
- * changes them, and they are within 1.2 vocab 2^-45 of the exact ones (an entry below 2^-46 is never drawn).  Random numbers
- * are in [0, 1).  A probability or random number that is negative, NaN or 2 and above counts as 0 and is reported.  A request with a token or parent out of range gets counts 0 and -1, and is reported; one whose P and
- * target are all 0 gets -1 as its next token, and is reported.  A sum of P that is 2 or more is reported (its row is no
- * distribution): Z is then just below 2, and from 4096 on the next token is -1.  Requests with broken starts get counts 0.
+ * changes them, and they are within 1.2 vocab 2^-45 of the exact ones (an entry below 2^-46 is never drawn).  Random
+ * numbers are in [0, 1).  A probability or random number that is negative, NaN or 2 and above counts as 0 and is reported.
+ * A request with a token or parent out of range gets counts 0 and -1, and is reported; one whose P and target are all 0
+ * gets -1 as its next token, and is reported.  A sum of P that is 2 or more is reported (its row is no distribution): Z is
+ * then just below 2, and from 4096 on the next token is -1.  Requests with broken starts get counts 0.
  * vocab is at most 2^20, probabilities need 4-byte alignment.
  */
 mx_status kv_verify_drafts(const float* target_probs, int64_t target_stride, const float* draft_probs, int64_t draft_stride,
@@ -620,14 +621,15 @@ mx_status kv_verify_drafts(const float* target_probs, int64_t target_stride, con
  *
  * Node path[q_start[r] + i] of request r, i < counts[r], moves to place lengths[r] - n + i; kept_lengths[r] becomes
  * lengths[r] - n + counts[r], the request's length from then on (give it to kv_block_tables, which takes the blocks
- * behind it back).  path rises and counts[r] <= n <= 1024 (as kv_verify_drafts gives them).  What moves into one block is
- * a run: the block keeps its scale or, where a value would not fit (|value| > MAX scale), raises it to the smallest
- * 2^k that does, and the codes in front of the run are rounded again, as kv_cache_append does; codes whose block has the
- * same scale move as they are.  A block of scale 0 takes the run's own.  Codes from kept_lengths[r] on are left as
+ * behind it back).  path rises and counts[r] <= n <= 1024 (as kv_verify_drafts gives them).  What moves into one block
+ * is a run: the block keeps its scale or, where a value would not fit (|value| > MAX scale), raises it to the smallest
+ * 2^k that does, and the codes in front of the run are rounded again, as kv_cache_append does; codes whose block has
+ * the same scale move as they are.  A block of scale 0 takes the run's own.  Codes from kept_lengths[r] on are left as
  * they were.  A request whose path, counts, blocks, length or starts break their contract is left as it is, keeps
  * lengths[r] and is reported.  Tokens of a block whose scale is out of range become NaN, and have no part in the scale
- * of the block that they move to; a run into such a block is left out; both are reported.  No two requests have a block that is written to in common.  kept_lengths and the keys',
- * values' and scales' tensors may not overlap each other or an input.
+ * of the block that they move to; a run into such a block is left out; both are reported.  No two requests have a block
+ * that is written to in common.  kept_lengths and the keys', values' and scales' tensors may not overlap each other or
+ * an input.
  */
 mx_status kv_cache_compact(const int32_t* path, const int32_t* counts, int64_t num_tokens, const int32_t* lengths,
                            const int32_t* q_start, int64_t requests, const int32_t* block_tables, int64_t max_blocks,

@@ -598,7 +598,8 @@ mx_status kv_tree_attention(const void* q, mx_half type, int64_t num_tokens, int
  * child x (accept_random its number) is accepted if accept_random q(x) Z < P(x), where q = draft(u), and then its
  * children are tried; else W += Z, P = max(target(u) - W q, 0), Z = sum P.  Certain drafts have q(x) = 1: accepted if
  * accept_random Z < P(x), else P(x) = 0 and Z -= P(x).  Behind the last accepted node the next token is the first whose
- * running sum of P is above sample_random[r] sum P; where nothing is left of P, target(u) is drawn from instead.
+ * running sum of P is above sample_random[r] sum P; where nothing is left of P (all of it rounds to 0, below), target(u)
+ * is drawn from instead.
  * For each request, at its rows from q_start[r] on:
  *   counts[r] = accepted nodes, the root among them (0 for a request without rows);
  *   path[..] = the accepted nodes, the root first, then -1;
